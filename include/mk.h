@@ -473,6 +473,178 @@ int mk_launch_probe(int num_workers, int cooperative, void *stream);
  * reused for hundreds of forward passes). */
 void mk_free(mk_plan_t plan);
 
+/* ======================================================================
+ * Serving operators: an 8-bit paged KV cache (attention over it, storing
+ * into it, loading from it, copying its pages, accounting for them) and
+ * sampling.  Asynchronous launches on `stream` of the current device; the
+ * caller owns every buffer, no call allocates, and none synchronises except
+ * mk_cache_status.  They may be captured into CUDA graphs.  (The source
+ * pages describe a bf16 cache, one buffer per sequence, and greedy decoding:
+ * these have no counterpart there.)
+ *
+ * Cache layout, N pages of P tokens (P = 32 or 64) for L layers:
+ *   K codes  e4m3 [L, N, Hkv, P, D]
+ *   V codes  e4m3 [L, N, Hkv, D, P]     (transposed inside the page, so that
+ *                                        the tokens P.V contracts lie together)
+ *   scales   fp32 [L, N, Hkv], one array for K and one for V
+ * An element is code x scale; a scale is a power of two between 2^-120 and
+ * 2^120, or 0 for a page and head whose stored values are all zero.  Token j
+ * of sequence b lives in slot j % P of page table[b, j / P] (table int32
+ * [batch, width], the same pages in every layer; entries behind a sequence's
+ * last page are never used, -1 by custom).
+ *
+ * Device-side checks: a page number outside [0, N), a sequence longer than
+ * its table row, a negative or inconsistent length or offset is never
+ * followed.  The first one is recorded in the cache's status words
+ * (mk_cache_status); what happens to the sequence is said at each call. */
+typedef struct {
+    uint64_t k_codes, v_codes;    /* device, 16-byte aligned */
+    uint64_t k_scales, v_scales;  /* device fp32 */
+    uint64_t status;              /* device int32 [4], zeroed by the caller: the first failed check, as MK_ERR_*,
+                                     sequence, position, page (mk_cache_status) */
+    int layers, pages, kv_heads;
+    int page_tokens;              /* P: 32 or 64 */
+    int head_dim;                 /* D: 64 or 128 */
+} mk_cache_desc;
+
+/* Token rows outside the cache, bf16, K and V: element (layer l, sequence b,
+ * token t, head h, d) at base + l s[0] + b s[1] + (row0[b] + t) s[2] + h s[3]
+ * + d (strides in elements, multiples of 8; bases 16-byte aligned).  Packed
+ * ragged tokens: s[1] = 0 and row0 = each sequence's first row. */
+typedef struct {
+    uint64_t k, v;
+    int64_t k_stride[4], v_stride[4];
+    int rows;                     /* extent of the token axis: row0[b] + t must stay below it */
+    uint64_t row0;                /* device int32 [batch], or 0: rows start at 0 */
+} mk_cache_rows;
+
+/* Store tokens start[b] .. start[b] + count[b] - 1 of every sequence, all
+ * layers, quantised (no counterpart on the pages).  Per layer, page and head the scale is the least power of
+ * two s with amax / s <= 448 over the finite new values; a page that already
+ * holds earlier tokens (start[b] inside it) keeps max(that, its scale), and
+ * where this grows, the codes of its other slots are rounded again to the
+ * new scale.  Codes are value / s rounded to nearest even, +-448 beyond;
+ * infinities become +-448, NaN stays NaN.  A page whose first slot is stored
+ * has its remaining slots set to zero.  The pages written must belong to one
+ * sequence only (a shared page is copied first: mk_cache_copy).
+ * table int32 [batch, table_width], start and count int32 [batch] are device
+ * arrays; max_count bounds count (a longer count is a failed check).  A
+ * sequence that fails a check stores nothing on the pages concerned. */
+int mk_cache_store(const mk_cache_desc *cache, const mk_cache_rows *rows, const int32_t *table, int table_width,
+                   const int32_t *start, const int32_t *count, int batch, int max_count, void *stream);
+
+/* The inverse (no counterpart on the pages): tokens start[b] .. start[b] +
+ * count[b] - 1 of every sequence, all layers, as bf16(code x scale) into
+ * rows.  Rows outside those are left as they were, also where a check failed. */
+int mk_cache_load(const mk_cache_desc *cache, const mk_cache_rows *rows, const int32_t *table, int table_width,
+                  const int32_t *start, const int32_t *count, int batch, int max_count, void *stream);
+
+/* Attention of new tokens over one layer of the cache.  Sequence b has T_b
+ * query tokens, at positions len[b] - T_b + i (their K/V already stored):
+ *   s_j = scale q . k_j,  max(0, pos - window + 1) <= j <= pos (window 0: from 0)
+ *   out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
+ * A query that sees no token gets out = 0, lse = -inf, and so do all queries
+ * of a sequence whose length fails its check (offsets that fail: its rows are
+ * left alone); a page number that fails is skipped, as if its tokens were
+ * masked.  One that sees a NaN, or holds a value that is not finite, gets
+ * NaN.  q head h uses kv head h / (q_heads / kv_heads). */
+typedef struct {
+    uint64_t q;                   /* device bf16 [tokens, q_heads, D], strides below, D contiguous */
+    uint64_t out;                 /* device bf16, the same shape */
+    uint64_t lse;                 /* device fp32 [tokens, q_heads] contiguous, or 0 */
+    int64_t q_stride[2], out_stride[2];  /* token, head; in elements, multiples of 8 */
+    uint64_t table;               /* device int32 [batch, table_width] */
+    uint64_t lens;                /* device int32 [batch]: tokens in the cache, the new ones among them */
+    uint64_t q_start;             /* device int32 [batch + 1]: sequence b's queries are rows q_start[b] ..
+                                     q_start[b + 1] - 1 (other rows are left as they were); 0: T_b = max_tokens each */
+    int batch, table_width, q_heads;
+    int tokens;                   /* rows of q */
+    int max_tokens;               /* most query tokens of a sequence (with q_start: a hint for the tile height) */
+    int window;
+    float scale;                  /* >= 0; usually 1 / sqrt(D) */
+    int num_sms;                  /* SMs to plan for; 0 = all of the current device */
+} mk_attend_desc;
+
+/* Device bytes of workspace mk_cache_attend needs (contents need no
+ * initialising; calls that may overlap in time need workspaces of their own;
+ * no counterpart on the pages). */
+int mk_cache_attend_workspace(const mk_cache_desc *cache, const mk_attend_desc *attend, uint64_t *bytes);
+
+/* See mk_attend_desc (split-KV attention with a log-sum-exp merge: "MegaRTP
+ * megakernel article", sections 1-2, attention; the 8-bit paged form has no
+ * counterpart there). */
+int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc *attend, void *workspace,
+                    uint64_t workspace_bytes, void *stream);
+
+/* Copy pages src[i] -> dst[i], all layers, codes and scales (no counterpart
+ * on the pages).  src and dst are host arrays of n page numbers, read before
+ * the call returns; no dst may repeat or be a src (MK_ERR_INVALID).  With a
+ * table (device int32 [table_entries]), every entry that names a src is
+ * renamed to its dst (to the first one listed, if a src repeats). */
+int mk_cache_copy(const mk_cache_desc *cache, const int32_t *src, const int32_t *dst, int n, int32_t *table,
+                  int64_t table_entries, void *stream);
+
+/* Synchronise `stream`, read the cache's status words into status[4] (may be
+ * NULL) and return status[0]: MK_OK, MK_ERR_DEVICE_CHECK or MK_ERR_TIMEOUT;
+ * clear: set them to zero again (no counterpart on the pages). */
+int mk_cache_status(const mk_cache_desc *cache, int clear, int32_t *status, void *stream);
+
+/* Host accounting of a cache's pages with reference counts (no counterpart
+ * on the pages): no device work.  Not thread-safe. */
+typedef struct mk_pages_s *mk_pages_t;
+int mk_pages_create(int num_pages, mk_pages_t *out);
+/* Take n pages, the lowest-numbered free ones, each with one reference; MK_ERR_INVALID, and none
+ * taken, if fewer are free (no counterpart on the pages). */
+int mk_pages_alloc(mk_pages_t pages, int n, int32_t *ids);
+/* Add one reference to each page (a fork shares its full pages); all must be
+ * in use, else MK_ERR_INVALID and nothing changes (no counterpart on the pages). */
+int mk_pages_share(mk_pages_t pages, const int32_t *ids, int n);
+/* Drop one reference of each; a page without references is free.  All or
+ * nothing, like mk_pages_share (no counterpart on the pages). */
+int mk_pages_release(mk_pages_t pages, const int32_t *ids, int n);
+/* Moves that pack the pages in use into the lowest numbers: src[i] -> dst[i]
+ * (room for num_pages each), *n of them, applied to the counts; the caller
+ * copies the pages and renames them in its tables (mk_cache_copy does both;
+ * no counterpart on the pages). */
+int mk_pages_compact(mk_pages_t pages, int32_t *src, int32_t *dst, int *n);
+/* Reference counts int32 [num_pages] (may be NULL) and the number of free
+ * pages (may be NULL; no counterpart on the pages). */
+int mk_pages_info(mk_pages_t pages, int32_t *refs, int *free_pages);
+/* NULL-safe (no counterpart on the pages). */
+void mk_pages_free(mk_pages_t pages);
+
+/* Sampling (no counterpart on the pages, which decode greedily).  Per row of
+ * logits z:
+ *   order by z, largest first, the lower index first on ties;
+ *   w_i = exp((z_i - max z) / temperature)
+ *   keep the first top_k;  of those the shortest prefix whose w sum to at
+ *   least top_p of theirs (one at least);  of those the i with w_i >= min_p
+ *   token = the least kept i with sum of the kept w_0 .. w_i > u * their sum
+ *   logprob = log(w_token / their sum)
+ * temperature <= 0 (or NaN): the largest logit, lowest index on ties,
+ * logprob 0.  top_k <= 0, top_p >= 1 (or NaN) and min_p <= 0 (or NaN) switch
+ * a filter off.  NaN logits count as -inf; a row with no logit above -inf
+ * gives token 0 and logprob -inf.  Each setting is one value for all rows,
+ * or, where its pointer is not 0, one per row. */
+typedef struct {
+    uint64_t logits;              /* device, [batch, vocab], row stride below */
+    int64_t row_stride;           /* elements, >= vocab */
+    int batch, vocab;             /* vocab at most 688128 */
+    int bf16;                     /* 1: bf16 logits, 0: fp32 */
+    uint64_t u;                   /* device fp32 [batch], uniform in [0, 1) (held to that range) */
+    uint64_t tokens;              /* device int32 [batch]: out */
+    uint64_t logprob;             /* device fp32 [batch]: out, or 0 */
+    uint64_t temperature_rows, top_k_rows, top_p_rows, min_p_rows;  /* device fp32 / int32 [batch], or 0 */
+    float temperature;
+    int top_k;
+    float top_p, min_p;
+} mk_sample_desc;
+
+/* See mk_sample_desc (greedy decoding is the pages' rule; sampling has no
+ * counterpart there).  tokens may be a row of MK_BIND_TOKENS, which the next
+ * MK_RUN_HOST_TOKENS step reads. */
+int mk_sample(const mk_sample_desc *sample, void *stream);
+
 /* Thread-local description of the last non-zero status (no counterpart on
  * the pages: the error string of this C ABI). */
 const char *mk_last_error(void);

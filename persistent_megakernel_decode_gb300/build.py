@@ -16,8 +16,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIB_DIR, "libmk.so")
-SOURCES = ["interp.cu", "api.cpp", "planner.cpp"]
-HEADERS = ["mk_internal.h", "planner.h", "dev_common.cuh", "dev_ops.cuh", "dev_glm.cuh", "dev_tc.cuh", "dev_glm_tc.cuh"]
+SOURCES = ["interp.cu", "api.cpp", "planner.cpp", "cache.cu", "attend.cu", "sample.cu", "pages.cpp"]
+HEADERS = ["mk_internal.h", "planner.h", "dev_common.cuh", "dev_ops.cuh", "dev_glm.cuh", "dev_tc.cuh", "dev_glm_tc.cuh",
+           "dev_serve.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,592 @@
+// Sampling: temperature, top-k, top-p and min-p over the logits of a decode
+// step, without sorting them.
+//
+// Mathematics.  Tokens are ordered by the 64-bit key (logit descending, index
+// ascending), unique per token, so top-k and top-p each keep the keys up to a
+// cut.  A cut is found by counting: a histogram over bins that follow the
+// order, the bin in which the running count (or weight) reaches its target,
+// then the same inside that bin, until few enough candidates are left to rank
+// them by comparing each with all.  The first bins are 1/64 octave of weight
+// wide (linear in the logit), later ones split the bin's range of keys.
+//
+// Weights 2^-d, d = (max - z) log2(e) / temperature, are 64-bit fixed point
+// (2^44 for d = 0), relative accuracy 2^-30: d is carried as a pair of fp32
+// numbers, 2^-d as integers (32-entry table times a polynomial of exp(-a), a <
+// ln 2 / 32).  Integer sums do not depend on their order, so neither does the
+// token, and the cumulative sums keep the accuracy that a 150,000-token
+// vocabulary asks for (fp32 sums would move a boundary by more than a token's
+// probability).
+//
+// Work split.  One cluster of CTAs per row (up to 16: a row of 0.5 MB is
+// spread over 16 SMs), each CTA keeping its share of the row in shared
+// memory; histograms are joined through distributed shared memory.  What
+// bounds it is latency: the row is read once, then cluster barriers follow.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "dev_serve.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace mk {
+
+constexpr int SMP_THREADS = 512, SMP_WARPS = SMP_THREADS / 32;
+constexpr int SMP_BINS = 2048, SMP_SUB = 64;     // first-level bins; bins per octave of weight
+constexpr int SMP_CAP = 1024;                    // candidates ranked directly
+constexpr int SMP_MAXCTAS = 16;
+constexpr int SMP_CHUNK = 43008;                 // logits per CTA at most (168 KB)
+constexpr int SMP_ROW = 128;                     // logits per warp pass
+constexpr uint64_t KEY_NONE = ~0ull;
+
+struct SmpParams {
+    const void *logits;
+    int64_t row_stride;
+    int vocab, chunk;
+    const float *u;
+    int *tokens;
+    float *logprob;
+    const float *temperature_rows, *top_p_rows, *min_p_rows;
+    const int *top_k_rows;
+    float temperature, top_p, min_p;
+    int top_k;
+};
+
+struct SmpBin {  // sums over a bin or a prefix of bins
+    unsigned long long w;
+    uint32_t n;
+};
+
+struct alignas(16) SmpShared {  // the logits behind it are read 16 bytes at a time
+    uint32_t table[32];                             // 2^31 2^(-i/32)
+    unsigned long long best[SMP_MAXCTAS];           // every CTA's largest (ordered logit, index)
+    unsigned long long slice_w[SMP_MAXCTAS];        // every CTA's slice of the histogram
+    uint32_t slice_n[SMP_MAXCTAS];
+    unsigned long long lo[SMP_MAXCTAS], hi[SMP_MAXCTAS];  // every CTA's least and largest key in the bin
+    unsigned long long kept[SMP_MAXCTAS];           // every CTA's kept weight
+    unsigned long long before_w, bin_w;             // the bin found: weight before it and in it
+    uint32_t before_n, bin_n;
+    int bin;
+    unsigned long long cut, cut_w;                  // the cut found and the weight up to it
+    uint32_t cands;
+    unsigned long long red[SMP_WARPS];
+    uint32_t red_n[SMP_WARPS];
+    uint32_t hist[4][SMP_BINS];                     // count; weight in 16-bit pieces
+    unsigned long long ckey[SMP_CAP], cw[SMP_CAP];  // candidates (in CTA 0)
+};
+
+// Keys rise in sampling order: the larger logit first, then the lower index.
+DEV uint32_t ordered_bits(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+DEV unsigned long long sample_key(float x, int i) {
+    return ((unsigned long long)(~ordered_bits(x)) << 32) | (uint32_t)i;
+}
+
+struct Weigher {
+    float top, ch, cl;  // the row's maximum; log2(e) / temperature as a pair of fp32
+    const uint32_t *table;
+    DEV float octaves(float x) const { return (top - x) * ch; }  // d in fp32: monotone in x
+    // 2^44 2^-d
+    DEV unsigned long long operator()(float x) const {
+        if (x == top) return 1ull << 44;
+        const float dh = top - x;
+        const float bp = dh - top;
+        const float dl = (top - (dh - bp)) + (-x - bp);  // dh + dl = top - x exactly
+        const float t = dh * ch;
+        if (!(t < 45.f)) return 0;  // less than half a unit (or not finite)
+        const float te = fmaf(dh, ch, -t) + fmaf(dh, cl, dl * ch);
+        const float n = floorf(t);
+        // d in 32.32 fixed point; t - n is exact, te below 2^-17
+        const long long d = max(0ll, ((long long)n << 32) + (long long)(uint32_t)((t - n) * 4294967296.f) +
+                                         (long long)__float2int_rn(te * 4294967296.f));
+        const uint32_t f = (uint32_t)d;
+        // 2^-f = table x exp(-a), a = (f mod 1/32) ln 2 < 0.0217: terms to a^4 / 24 leave 4e-11
+        const uint32_t a = __umulhi(f & 0x07ffffffu, 2977044472u);  // ln 2 in 0.32
+        uint32_t q = 715827883u - __umulhi(a, 178956971u);         // 1/6 - a/24
+        q = 0x80000000u - __umulhi(a, q);                          // 1/2 - a q
+        q = 0xffffffffu - __umulhi(a, q);                          // 1 - a q
+        const uint32_t e = 0x80000000u - (__umulhi(a, q) >> 1);    // 1 - a q, in 1.31
+        const unsigned long long prod = (unsigned long long)table[f >> 27] * e;  // 2.62
+        const int s = 18 + (int)(d >> 32);
+        return s < 64 ? prod >> s : 0;
+    }
+};
+
+DEV unsigned long long warp_sum64(unsigned long long v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+DEV unsigned long long warp_min64(unsigned long long v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = min(v, __shfl_xor_sync(FULL, v, o));
+    return v;
+}
+
+// One row per cluster.  Every CTA keeps logits [rank * chunk, ...) in shared
+// memory; `x` behind the row's end are -inf.
+struct Sampler {
+    const SmpParams &p;
+    SmpShared &s;
+    float *x;
+    unsigned long long *rows;  // kept weight of each 128-logit pass
+    cg::cluster_group cl;
+    int rank, ctas, first, n;  // n: multiple of 128
+    Weigher w;
+
+    DEV float4 four(int i) const { return *reinterpret_cast<const float4 *>(x + i); }
+
+    // The first key position at which the running count reaches `need_n` (by
+    // count) or the running weight reaches `need_w`, over keys <= limit, all
+    // of which hold `limit`; returns that key, and the weight up to it.
+    DEV unsigned long long find(bool by_weight, unsigned long long need, unsigned long long limit,
+                                unsigned long long &upto) {
+        const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+        unsigned long long lo = 0, hi = limit, w_before = 0;
+        uint32_t n_before = 0;
+        bool octave = true;  // bins: octaves of weight first, then keys
+        int shift = 0;
+        while (true) {
+            for (int i = tid; i < 4 * SMP_BINS; i += SMP_THREADS) s.hist[0][i] = 0;
+            __syncthreads();
+            for (int i = tid * 4; i < n; i += SMP_THREADS * 4) {
+                const float4 v = four(i);
+                const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const unsigned long long key = sample_key(e[j], first + i + j);
+                    if (e[j] == -INFINITY || key < lo || key > hi) continue;
+                    const int bin = octave ? bin_of(e[j]) : (int)((key - lo) >> shift);
+                    const unsigned long long ww = w(e[j]);
+                    atomicAdd(&s.hist[0][bin], 1u);
+                    atomicAdd(&s.hist[1][bin], (uint32_t)ww & 0xffffu);
+                    atomicAdd(&s.hist[2][bin], (uint32_t)(ww >> 16) & 0xffffu);
+                    atomicAdd(&s.hist[3][bin], (uint32_t)(ww >> 32));
+                }
+            }
+            cl.sync();
+            // this CTA's slice of the bins over all CTAs
+            const int per = SMP_BINS / ctas;
+            unsigned long long bw = 0;
+            uint32_t bn = 0;
+            // threads hold consecutive bins of the slice (per <= 2048: up to 4 each)
+            constexpr int M = SMP_BINS / SMP_THREADS;
+            unsigned long long tw[M];
+            uint32_t tn[M];
+#pragma unroll
+            for (int k = 0; k < M; ++k) {
+                tw[k] = 0;
+                tn[k] = 0;
+                const int i = tid * M + k;
+                if (i < per)
+                    for (int r = 0; r < ctas; ++r) {
+                        const uint32_t *h = cl.map_shared_rank(&s.hist[0][0], r) + rank * per + i;
+                        tn[k] += h[0];
+                        tw[k] += (unsigned long long)h[SMP_BINS] + ((unsigned long long)h[2 * SMP_BINS] << 16) +
+                                 ((unsigned long long)h[3 * SMP_BINS] << 32);
+                    }
+                bn += tn[k];
+                bw += tw[k];
+            }
+            // exclusive prefix over the block
+            unsigned long long pw = bw;
+            uint32_t pn = bn;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long a = __shfl_up_sync(FULL, pw, o);
+                const uint32_t b = __shfl_up_sync(FULL, pn, o);
+                if (lane >= o) {
+                    pw += a;
+                    pn += b;
+                }
+            }
+            if (lane == 31) {
+                s.red[warp] = pw;
+                s.red_n[warp] = pn;
+            }
+            __syncthreads();
+            unsigned long long all_w = 0;
+            uint32_t all_n = 0;
+            unsigned long long my_w = pw - bw;
+            uint32_t my_n = pn - bn;
+#pragma unroll
+            for (int i = 0; i < SMP_WARPS; ++i) {
+                if (i < warp) {
+                    my_w += s.red[i];
+                    my_n += s.red_n[i];
+                }
+                all_w += s.red[i];
+                all_n += s.red_n[i];
+            }
+            if (tid < ctas) {
+                *cl.map_shared_rank(&s.slice_w[rank], tid) = all_w;
+                *cl.map_shared_rank(&s.slice_n[rank], tid) = all_n;
+            }
+            cl.sync();
+            unsigned long long sw = w_before;
+            uint32_t sn = n_before;
+            for (int r = 0; r < rank; ++r) {
+                sw += s.slice_w[r];
+                sn += s.slice_n[r];
+            }
+            my_w += sw;
+            my_n += sn;
+#pragma unroll
+            for (int k = 0; k < M; ++k) {
+                const bool hit = by_weight ? (my_w < need && my_w + tw[k] >= need) : (my_n < need && my_n + tn[k] >= need);
+                if (hit)
+                    for (int r = 0; r < ctas; ++r) {
+                        SmpShared *o = cl.map_shared_rank(&s, r);
+                        o->bin = rank * per + tid * M + k;
+                        o->before_w = my_w;
+                        o->before_n = my_n;
+                        o->bin_n = tn[k];
+                    }
+                my_w += tw[k];
+                my_n += tn[k];
+            }
+            if (tid == 0) s.cands = 0;
+            cl.sync();
+            const int bin = s.bin;
+            w_before = s.before_w;
+            n_before = s.before_n;
+            const uint32_t count = s.bin_n;
+            // the bin's keys: gathered in CTA 0 if few, else their range for the next level
+            unsigned long long mn = KEY_NONE, mx = 0;
+            SmpShared *lead = cl.map_shared_rank(&s, 0);
+            for (int i = tid * 4; i < n; i += SMP_THREADS * 4) {
+                const float4 v = four(i);
+                const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const unsigned long long key = sample_key(e[j], first + i + j);
+                    if (e[j] == -INFINITY || key < lo || key > hi) continue;
+                    if ((octave ? bin_of(e[j]) : (int)((key - lo) >> shift)) != bin) continue;
+                    if (count <= SMP_CAP) {
+                        const uint32_t at = atomicAdd(&lead->cands, 1u);
+                        lead->ckey[at] = key;
+                        lead->cw[at] = w(e[j]);
+                    } else {
+                        mn = min(mn, key);
+                        mx = max(mx, key);
+                    }
+                }
+            }
+            if (count <= SMP_CAP) break;
+            mn = warp_min64(mn);
+            mx = ~warp_min64(~mx);
+            __syncthreads();  // s.red was read
+            if (lane == 0) {
+                s.red[warp] = mn;
+                s.ckey[warp] = mx;
+            }
+            __syncthreads();
+            if (tid < ctas) {
+                for (int i = 0; i < SMP_WARPS; ++i) {
+                    mn = min(mn, s.red[i]);
+                    mx = max(mx, s.ckey[i]);
+                }
+                *cl.map_shared_rank(&s.lo[rank], tid) = mn;
+                *cl.map_shared_rank(&s.hi[rank], tid) = mx;
+            }
+            cl.sync();
+            lo = KEY_NONE;
+            hi = 0;
+            for (int r = 0; r < ctas; ++r) {
+                lo = min(lo, s.lo[r]);
+                hi = max(hi, s.hi[r]);
+            }
+            octave = false;
+            shift = max(0, 64 - __clzll(hi - lo) - 11);
+        }
+        cl.sync();
+        if (rank == 0) {
+            // rank every candidate by comparing it with all: count and weight of those up to it
+            const int count = (int)s.bin_n;
+            for (int i = tid; i < count; i += SMP_THREADS) {
+                const unsigned long long key = s.ckey[i];
+                unsigned long long before = w_before;
+                uint32_t rk = n_before;
+                for (int j = 0; j < count; ++j)
+                    if (s.ckey[j] < key) {
+                        before += s.cw[j];
+                        ++rk;
+                    }
+                const unsigned long long with = before + s.cw[i];
+                if (by_weight ? (before < need && with >= need) : rk + 1 == need)
+                    for (int r = 0; r < ctas; ++r) {
+                        SmpShared *o = cl.map_shared_rank(&s, r);
+                        o->cut = key;
+                        o->cut_w = with;
+                    }
+            }
+        }
+        cl.sync();
+        upto = s.cut_w;
+        return s.cut;
+    }
+
+    DEV int bin_of(float v) const { return (int)fminf((float)(SMP_BINS - 1), w.octaves(v) * (float)SMP_SUB); }
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) {
+    SmpShared &s = *reinterpret_cast<SmpShared *>(mk_smem);
+    float *x = reinterpret_cast<float *>(mk_smem + sizeof(SmpShared));
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank(), ctas = (int)cl.num_blocks();
+    const int row = blockIdx.x / ctas, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int first = rank * p.chunk, have = min(p.chunk, p.vocab - first), n = p.chunk;
+    unsigned long long *rows = reinterpret_cast<unsigned long long *>(x + p.chunk);
+
+    // the row's share into shared memory, and its largest (logit, index)
+    float top = -INFINITY;
+    int at = 0;
+    const auto put = [&](int i, float v) {
+        v = v != v ? -INFINITY : v + 0.f;  // -0 counts as 0
+        x[i] = v;
+        if (v > top || (v == top && first + i < at)) {
+            top = v;
+            at = first + i;
+        }
+    };
+    constexpr int VEC = BF16 ? 8 : 4;
+    const char *src = static_cast<const char *>(p.logits) + (row * p.row_stride + first) * (BF16 ? 2 : 4);
+    const int vecs = have > 0 && (uintptr_t)src % 16 == 0 ? have / VEC : 0;
+#pragma unroll 4
+    for (int i = tid; i < vecs; i += SMP_THREADS) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
+        const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (BF16) {
+                put(8 * i + 2 * j, __uint_as_float(e[j] << 16));
+                put(8 * i + 2 * j + 1, __uint_as_float(e[j] & 0xffff0000u));
+            } else {
+                put(4 * i + j, __uint_as_float(e[j]));
+            }
+        }
+    }
+    for (int i = vecs * VEC + tid; i < n; i += SMP_THREADS) {
+        float v = -INFINITY;
+        if (i < have)
+            v = BF16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(src)[i] << 16)
+                     : reinterpret_cast<const float *>(src)[i];
+        put(i, v);
+    }
+    // largest (ordered logit, ~index) of the block, then of the cluster
+    unsigned long long best = ((unsigned long long)ordered_bits(top) << 32) | (uint32_t)~at;
+    best = ~warp_min64(~best);
+    if (lane == 0) s.red[warp] = best;
+    if (tid < 32) s.table[tid] = (uint32_t)(exp2(-tid / 32.0) * 2147483648.0 + 0.5);
+    __syncthreads();
+    if (tid < ctas) {
+        for (int i = 0; i < SMP_WARPS; ++i) best = max(best, s.red[i]);
+        *cl.map_shared_rank(&s.best[rank], tid) = best;
+    }
+    cl.sync();
+    best = 0;
+    for (int r = 0; r < ctas; ++r) best = max(best, s.best[r]);
+    const int arg = (int)~(uint32_t)best;
+    const uint32_t ob = (uint32_t)(best >> 32);
+    top = __uint_as_float(ob & 0x80000000u ? ob & 0x7fffffffu : ~ob);
+
+    const float temp = p.temperature_rows ? p.temperature_rows[row] : p.temperature;
+    const int top_k = p.top_k_rows ? p.top_k_rows[row] : p.top_k;
+    const float top_p = p.top_p_rows ? p.top_p_rows[row] : p.top_p;
+    const float min_p = p.min_p_rows ? p.min_p_rows[row] : p.min_p;
+    if (!(temp > 0.f) || top_k == 1 || top == -INFINITY) {  // the same in the whole cluster
+        if (rank == 0 && tid == 0) {
+            p.tokens[row] = top == -INFINITY ? 0 : arg;
+            if (p.logprob) p.logprob[row] = top == -INFINITY ? -INFINITY : 0.f;
+        }
+        cl.sync();
+        return;
+    }
+    const double c = 1.4426950408889634 / (double)temp;
+    const float ch = (float)c;
+    Sampler k{p, s, x, rows, cl, rank, ctas, first, n, {top, ch, ch < INFINITY ? (float)(c - (double)ch) : 0.f, s.table}};
+
+    unsigned long long cut = sample_key(-3.402823466e38f, 0x7fffffff), cut_w = 0;  // every finite logit
+    bool have_w = false;
+    if (top_k > 0 && top_k < p.vocab) {
+        // no cut if fewer than top_k logits are above -inf
+        uint32_t live = 0;
+        for (int i = tid * 4; i < n; i += SMP_THREADS * 4) {
+            const float4 v = k.four(i);
+            live += (v.x > -INFINITY) + (v.y > -INFINITY) + (v.z > -INFINITY) + (v.w > -INFINITY);
+        }
+        live = __reduce_add_sync(FULL, live);
+        if (lane == 0) s.red_n[warp] = live;
+        __syncthreads();
+        if (tid < ctas) {
+            uint32_t sum = 0;
+            for (int i = 0; i < SMP_WARPS; ++i) sum += s.red_n[i];
+            *cl.map_shared_rank(&s.slice_n[rank], tid) = sum;
+        }
+        cl.sync();
+        live = 0;
+        for (int r = 0; r < ctas; ++r) live += s.slice_n[r];
+        cl.sync();
+        if (live > (uint32_t)top_k) {
+            cut = k.find(false, top_k, cut, cut_w);
+            have_w = true;
+        }
+    }
+    // weight of what a pass keeps: per 128 logits (rows), per CTA, per cluster
+    float least = -INFINITY;
+    const auto keeps = [&](float v, int i) { return v >= least && sample_key(v, first + i) <= cut; };
+    const auto kept_weight = [&]() {
+        for (int r = warp; r < n / SMP_ROW; r += SMP_WARPS) {
+            const int i = r * SMP_ROW + lane * 4;
+            const float4 v = k.four(i);
+            unsigned long long sum = 0;
+            if (keeps(v.x, i)) sum += k.w(v.x);
+            if (keeps(v.y, i + 1)) sum += k.w(v.y);
+            if (keeps(v.z, i + 2)) sum += k.w(v.z);
+            if (keeps(v.w, i + 3)) sum += k.w(v.w);
+            sum = warp_sum64(sum);
+            if (lane == 0) rows[r] = sum;
+        }
+        __syncthreads();
+        unsigned long long sum = 0;
+        for (int r = tid; r < n / SMP_ROW; r += SMP_THREADS) sum += rows[r];
+        sum = warp_sum64(sum);
+        if (lane == 0) s.red[warp] = sum;
+        __syncthreads();
+        if (tid < ctas) {
+            unsigned long long a = 0;
+            for (int i = 0; i < SMP_WARPS; ++i) a += s.red[i];
+            *cl.map_shared_rank(&s.kept[rank], tid) = a;
+        }
+        cl.sync();
+        unsigned long long all = 0;
+        for (int r = 0; r < ctas; ++r) all += s.kept[r];
+        return all;
+    };
+    if (top_p < 1.f) {
+        if (!have_w) {
+            cut_w = kept_weight();
+            cl.sync();
+        }
+        const double want = ceil((double)fmaxf(top_p, 0.f) * (double)cut_w);
+        const unsigned long long need = min(max((unsigned long long)want, 1ull), cut_w);
+        cut = k.find(true, need, cut, cut_w);
+    }
+    if (min_p > 0.f) {
+        // w >= min_p  <=>  z >= max + temperature ln(min_p): the least fp32 number that is
+        const double edge = (double)top + (double)temp * log((double)min_p);
+        least = __double2float_ru(edge);
+        if (min_p >= 1.f) least = top;
+    }
+    const unsigned long long total = kept_weight();
+    const float u = fminf(fmaxf(p.u[row], 0.f), 0x1.fffffep-1f);
+    const unsigned long long target = min((unsigned long long)((double)u * (double)total), total - 1);
+    unsigned long long before = 0;
+    for (int r = 0; r < rank; ++r) before += s.kept[r];
+    if (warp == 0 && before <= target && target < before + s.kept[rank]) {
+        // the pass, then the lane, then the logit in which the running sum passes the target
+        int r = 0;
+        for (int r0 = 0; r0 < n / SMP_ROW; r0 += 32) {
+            unsigned long long v = r0 + lane < n / SMP_ROW ? rows[r0 + lane] : 0, q = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long a = __shfl_up_sync(FULL, q, o);
+                if (lane >= o) q += a;
+            }
+            const unsigned hit = __ballot_sync(FULL, before + q > target);
+            if (hit) {
+                const int j = __ffs(hit) - 1;
+                r = r0 + j;
+                before += __shfl_sync(FULL, q, j) - __shfl_sync(FULL, v, j);
+                break;
+            }
+            before += __shfl_sync(FULL, q, 31);
+        }
+        const int i = r * SMP_ROW + lane * 4;
+        const float4 v = k.four(i);
+        const float e[4] = {v.x, v.y, v.z, v.w};
+        unsigned long long ww[4], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            ww[j] = keeps(e[j], i + j) ? k.w(e[j]) : 0;
+            sum += ww[j];
+        }
+        unsigned long long q = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long a = __shfl_up_sync(FULL, q, o);
+            if (lane >= o) q += a;
+        }
+        before += q - sum;
+        if (before <= target && target < before + sum) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (before <= target && target < before + ww[j]) {
+                    p.tokens[row] = first + i + j;
+                    // log(w / total) through the rest: exact near 0, where the rest is small
+                    if (p.logprob) p.logprob[row] = (float)-log1p((double)(total - ww[j]) / (double)ww[j]);
+                }
+                before += ww[j];
+            }
+        }
+    }
+    cl.sync();
+}
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" int mk_sample(const mk_sample_desc *d, void *stream) {
+    if (!d) return set_error(MK_ERR_INVALID, "null descriptor");
+    if (d->batch < 0 || d->vocab <= 0 || (d->batch > 1 && d->row_stride < d->vocab))
+        return set_error(MK_ERR_INVALID, "batch negative, vocab not positive, or rows overlap");
+    if (d->vocab > SMP_MAXCTAS * SMP_CHUNK) return set_error(MK_ERR_UNSUPPORTED, "vocab above 688128");
+    if (d->batch == 0) return MK_OK;
+    if (!d->logits || !d->u || !d->tokens) return set_error(MK_ERR_INVALID, "null argument");
+    if (d->logits % (d->bf16 ? 2 : 4) || (d->u | d->tokens | d->logprob) % 4)
+        return set_error(MK_ERR_INVALID, "a pointer is not aligned to its type");
+    // CTAs per row: as many SMs as a row can use while rows are few; at least
+    // what its share of shared memory asks for
+    int ctas = d->batch <= 8 ? 16 : d->batch <= 16 ? 8 : d->batch <= 40 ? 4 : 2;
+    while (ctas < SMP_MAXCTAS && (d->vocab + ctas - 1) / ctas > SMP_CHUNK) ctas *= 2;
+    while (ctas > 1 && d->vocab < ctas * 1024) ctas /= 2;
+    if (d->batch > INT32_MAX / SMP_MAXCTAS) return set_error(MK_ERR_UNSUPPORTED, "too many rows");
+    SmpParams p{};
+    p.logits = reinterpret_cast<const void *>(d->logits);
+    p.row_stride = d->row_stride;
+    p.vocab = d->vocab;
+    p.chunk = ((d->vocab + ctas - 1) / ctas + SMP_ROW - 1) / SMP_ROW * SMP_ROW;
+    p.u = reinterpret_cast<const float *>(d->u);
+    p.tokens = reinterpret_cast<int *>(d->tokens);
+    p.logprob = reinterpret_cast<float *>(d->logprob);
+    p.temperature_rows = reinterpret_cast<const float *>(d->temperature_rows);
+    p.top_k_rows = reinterpret_cast<const int *>(d->top_k_rows);
+    p.top_p_rows = reinterpret_cast<const float *>(d->top_p_rows);
+    p.min_p_rows = reinterpret_cast<const float *>(d->min_p_rows);
+    p.temperature = d->temperature;
+    p.top_k = d->top_k;
+    p.top_p = d->top_p;
+    p.min_p = d->min_p;
+    const int smem = (int)sizeof(SmpShared) + p.chunk * 4 + p.chunk / SMP_ROW * 8;
+    void (*f)(const SmpParams) = d->bf16 ? sample_kernel<true> : sample_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return serve_cuda_fail(e, "cudaFuncSetAttribute");
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(d->batch * ctas));
+    cfg.blockDim = dim3(SMP_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, f, (const SmpParams)p);
+    return e == cudaSuccess ? MK_OK : serve_cuda_fail(e, "sampling launch");
+}

@@ -1,0 +1,263 @@
+"""8-bit paged KV cache: attention over it, storing, loading, copying pages, and the accounting of pages.
+
+Binding of the ``mk_cache_*`` and ``mk_pages_*`` calls of ``include/mk.h``, which has the definitions (layout, scales,
+masks, what a failed check does); this module checks arguments and marshals them.  Every call is asynchronous on
+``stream`` (default: the current torch stream of the cache's device) and may be captured into a CUDA graph, except
+``Kv8Cache.check``, which synchronises.
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+from typing import List, Optional, Sequence, Tuple
+
+import numpy as np
+import torch
+
+from . import runtime as rt
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+class Kv8Cache:
+    """e4m3 K codes [L, N, Hkv, P, D], V codes [L, N, Hkv, D, P] and their fp32 scales [L, N, Hkv] (contiguous CUDA
+    tensors, codes as float8_e4m3fn or uint8); P 32 or 64, D 64 or 128.  The tensors stay the caller's: nothing is
+    copied.  ``table`` arguments are int32 [B, width]: sequence b's token j lies in page table[b, j // P]."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if not k.is_cuda:
+            raise ValueError("the cache must be CUDA tensors")
+        rt.check_tensor("k", k, k.device, _CODES, (None,) * 5)
+        L, N, H, P, D = k.shape
+        rt.check_tensor("v", v, k.device, _CODES, (L, N, H, D, P))
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            rt.check_tensor(name, t, k.device, (torch.float32,), (L, N, H))
+        if not all(t.is_contiguous() for t in (k, v, k_scale, v_scale)):
+            raise ValueError("the cache's tensors must be contiguous")
+        if P not in (32, 64) or D not in (64, 128):
+            raise ValueError(f"pages of {P} tokens with head_dim {D}: 32 or 64 tokens, 64 or 128 dims are supported")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.layers, self.pages, self.kv_heads, self.page_tokens, self.head_dim = L, N, H, P, D
+        self.device = k.device
+        self.status = torch.zeros(4, dtype=torch.int32, device=k.device)
+        self._desc = rt.CacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                  self.status.data_ptr(), L, N, H, P, D)
+        self._lib = rt.load()
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
+        """A cache of zeroed pages."""
+        dev = torch.device(device)
+        codes = lambda *s: torch.zeros((layers, pages, kv_heads) + s, dtype=torch.uint8, device=dev)  # noqa: E731
+        scale = lambda: torch.zeros((layers, pages, kv_heads), dtype=torch.float32, device=dev)  # noqa: E731
+        return cls(codes(page_tokens, head_dim).view(torch.float8_e4m3fn),
+                   codes(head_dim, page_tokens).view(torch.float8_e4m3fn), scale(), scale())
+
+    # ---- moving tokens ----
+    def _move(self, call, k, v, table, start, count, row0, max_count, stream, writes):
+        dev, i32 = self.device, (torch.int32,)
+        for name, t in (("k", k), ("v", v)):
+            rt.check_tensor(name, t, dev, (torch.bfloat16,), (self.layers, None, None, self.kv_heads, self.head_dim))
+            if t.stride(4) != 1 or t.data_ptr() % 16 or any(s % 8 for s in t.stride()[:4]):
+                raise ValueError(f"{name}: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8")
+            if writes and any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)) and row0 is None:
+                raise ValueError(f"{name}: rows that overlap cannot be written")
+        b, rows = k.shape[1], k.shape[2]
+        if tuple(v.shape) != tuple(k.shape):
+            raise ValueError("k and v must have the same shape")
+        rt.check_tensor("table", table, dev, i32, (b, None))
+        for name, t in (("start", start), ("count", count)) + ((("row0", row0),) if row0 is not None else ()):
+            rt.check_tensor(name, t, dev, i32, (b,))
+        if not all(t.is_contiguous() for t in (table, start, count) + ((row0,) if row0 is not None else ())):
+            raise ValueError("table, start, count and row0 must be contiguous")
+        if b == 0 or rows == 0:
+            return
+        r = rt.CacheRows(k.data_ptr(), v.data_ptr(), (C.c_int64 * 4)(*k.stride()[:4]), (C.c_int64 * 4)(*v.stride()[:4]),
+                         rows, row0.data_ptr() if row0 is not None else 0)
+        ctx, st = rt.on_device(k, stream)
+        with ctx:
+            rt._check(call(C.byref(self._desc), C.byref(r), table.data_ptr(), table.shape[1], start.data_ptr(),
+                           count.data_ptr(), b, rows if max_count is None else max_count, st))
+
+    def store(self, k, v, table, start, count, row0=None, max_count: Optional[int] = None, stream=None):
+        """Quantise new tokens into the cache, all layers: row ``row0[b] + i`` (default 0 + i) of sequence b in ``k`` and
+        ``v`` (bf16 [L, B, T, Hkv, D], any strides with D contiguous; packed ragged tokens [L, total, Hkv, D] are
+        ``x[:, None].expand(L, B, total, Hkv, D)`` with ``row0``) becomes cache position ``start[b] + i``, i <
+        ``count[b]``.  ``max_count`` (default T) bounds the counts.  Pages written must belong to one sequence only."""
+        self._move(self._lib.mk_cache_store, k, v, table, start, count, row0, max_count, stream, False)
+
+    def load(self, k, v, table, start, count, row0=None, max_count: Optional[int] = None, stream=None):
+        """The inverse of :meth:`store`: cache positions ``start[b] + i`` into rows ``row0[b] + i``; other rows stay."""
+        self._move(self._lib.mk_cache_load, k, v, table, start, count, row0, max_count, stream, True)
+
+    # ---- attention ----
+    def attend(self, q, table, lens, layer: int = 0, q_start=None, max_tokens: Optional[int] = None,
+               scale: Optional[float] = None, window: int = 0, out=None, lse=None, workspace=None,
+               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """Attention of new tokens over ``layer`` of the cache (their K/V stored before): ``lens[b]`` tokens are cached,
+        the last T of them are the queries.  ``q`` is bf16 [B, T, Hq, D], or with ``q_start`` (int32 [B + 1]) packed
+        [total, Hq, D], sequence b's queries being rows q_start[b] .. q_start[b + 1] - 1 (``max_tokens``: the most of
+        one sequence, a hint).  ``window`` > 0: a query sees that many last tokens, itself among them.  Returns (out
+        bf16 like q, lse fp32 without the last axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8
+        tensor of at least :meth:`attend_workspace` bytes; by default one is allocated per call."""
+        dev, D = self.device, self.head_dim
+        packed = q_start is not None
+        rt.check_tensor("q", q, dev, (torch.bfloat16,), (None,) * (2 if packed else 3) + (D,))
+        hq = q.shape[-2]
+        if packed:
+            b = q_start.numel() - 1
+            rt.check_tensor("q_start", q_start, dev, (torch.int32,), (max(b, 0) + 1,))
+            total, most = q.shape[0], q.shape[0] if max_tokens is None else max_tokens
+        else:
+            b, most = q.shape[0], q.shape[1]
+            total = b * most
+            if max_tokens is not None and max_tokens != most:
+                raise ValueError("max_tokens is q's second axis without q_start")
+        rt.check_tensor("table", table, dev, (torch.int32,), (b, None))
+        rt.check_tensor("lens", lens, dev, (torch.int32,), (b,))
+        if not (table.is_contiguous() and lens.is_contiguous() and (not packed or q_start.is_contiguous())):
+            raise ValueError("table, lens and q_start must be contiguous")
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        else:
+            rt.check_tensor("out", out, dev, (torch.bfloat16,), tuple(q.shape))
+        if lse is None:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        else:
+            rt.check_tensor("lse", lse, dev, (torch.float32,), tuple(q.shape[:-1]))
+            if not lse.is_contiguous():
+                raise ValueError("lse must be contiguous")
+        a = rt.AttendDesc()
+        for name, t in (("q", q), ("out", out)):
+            s = t.stride()
+            if total and (s[-1] != 1 or t.data_ptr() % 16 or s[-2] % 8 or s[-3] % 8
+                          or (not packed and b > 1 and s[0] != s[1] * most)):
+                raise ValueError(f"{name}: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8 "
+                                 "elements, and sequences evenly spaced rows")
+        a.q, a.out, a.lse = q.data_ptr(), out.data_ptr(), lse.data_ptr()
+        a.q_stride[0], a.q_stride[1] = q.stride(-3), q.stride(-2)
+        a.out_stride[0], a.out_stride[1] = out.stride(-3), out.stride(-2)
+        a.table, a.lens, a.q_start = table.data_ptr(), lens.data_ptr(), q_start.data_ptr() if packed else 0
+        a.batch, a.table_width, a.q_heads, a.tokens, a.max_tokens = b, table.shape[1], hq, total, most
+        a.window, a.scale = window, 1.0 / math.sqrt(D) if scale is None else scale
+        ctx, st = rt.on_device(q, stream)
+        with ctx:
+            need = self._workspace(a)
+            own = workspace is None
+            if own:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            else:
+                rt.check_tensor("workspace", workspace, dev, (torch.uint8,), (None,))
+            rt._check(self._lib.mk_cache_attend(C.byref(self._desc), layer, C.byref(a), workspace.data_ptr(),
+                                                workspace.numel(), st))
+        if stream is not None:
+            for t in (out, lse) + ((workspace,) if own else ()):  # made on the current stream, used on `stream`
+                t.record_stream(stream)
+        return out, lse
+
+    def _workspace(self, a) -> int:
+        n = C.c_uint64()
+        rt._check(self._lib.mk_cache_attend_workspace(C.byref(self._desc), C.byref(a), C.byref(n)))
+        return n.value
+
+    def attend_workspace(self, batch: int, q_heads: int, max_tokens: int = 1) -> int:
+        """Bytes of workspace :meth:`attend` needs for up to ``batch`` sequences of up to ``max_tokens`` queries."""
+        a = rt.AttendDesc()
+        a.batch, a.q_heads, a.tokens, a.max_tokens, a.table_width = batch, q_heads, batch * max_tokens, max_tokens, 1
+        with torch.cuda.device(self.device):
+            return self._workspace(a)
+
+    # ---- pages ----
+    def copy_pages(self, src: Sequence[int], dst: Sequence[int], table=None, stream=None):
+        """Copy pages ``src[i]`` -> ``dst[i]`` in all layers (codes and scales); no dst may repeat or be a src.  With
+        ``table`` (a contiguous int32 tensor) its entries that name a src are renamed to the dst."""
+        s, d = np.ascontiguousarray(src, dtype=np.int32), np.ascontiguousarray(dst, dtype=np.int32)
+        if s.ndim != 1 or s.shape != d.shape:
+            raise ValueError("src and dst must be lists of the same length")
+        if table is not None:
+            rt.check_tensor("table", table, self.device, (torch.int32,))
+            if not table.is_contiguous():
+                raise ValueError("table must be contiguous")
+        ctx, st = rt.on_device(self.k, stream)
+        with ctx:
+            rt._check(self._lib.mk_cache_copy(C.byref(self._desc), s.ctypes.data, d.ctypes.data, len(s),
+                                              table.data_ptr() if table is not None else None,
+                                              table.numel() if table is not None else 0, st))
+
+    def check(self, stream=None):
+        """Wait for ``stream`` and raise ``MkError`` if a device-side check has failed since the last call."""
+        ctx, st = rt.on_device(self.k, stream)
+        with ctx:
+            rt._check(self._lib.mk_cache_status(C.byref(self._desc), 1, None, st))
+
+
+class PagePool:
+    """Which pages of a cache are in use, with reference counts (host only; not thread-safe).  Sequences are lists of
+    page numbers in token order."""
+
+    def __init__(self, num_pages: int):
+        self.num_pages = num_pages
+        self._lib = rt.load()
+        self.h = C.c_void_p()
+        rt._check(self._lib.mk_pages_create(num_pages, C.byref(self.h)))
+
+    def alloc(self, n: int) -> List[int]:
+        """Take ``n`` free pages, the lowest-numbered first; ``MkError`` (and none taken) if there are fewer."""
+        ids = np.zeros(max(n, 1), np.int32)
+        rt._check(self._lib.mk_pages_alloc(self.h, n, ids.ctypes.data))
+        return ids[:n].tolist()
+
+    def share(self, pages: Sequence[int]):
+        """One more reference to each page."""
+        a = np.ascontiguousarray(pages, dtype=np.int32)
+        rt._check(self._lib.mk_pages_share(self.h, a.ctypes.data, len(a)))
+
+    def release(self, pages: Sequence[int]):
+        """Drop one reference to each page; one that nobody holds is free."""
+        a = np.ascontiguousarray(pages, dtype=np.int32)
+        rt._check(self._lib.mk_pages_release(self.h, a.ctypes.data, len(a)))
+
+    def fork(self, pages: Sequence[int], length: int, page_tokens: int) -> Tuple[List[int], List[int], List[int]]:
+        """A child of a sequence of ``length`` tokens: its full pages are shared, a last page that is not full gets a page
+        of its own.  Returns (child's pages, src, dst): copy src -> dst with ``Kv8Cache.copy_pages``."""
+        used = -(-length // page_tokens)
+        if length < 0 or used > len(pages):
+            raise ValueError(f"{len(pages)} pages do not hold {length} tokens")
+        full = length // page_tokens
+        fresh = self.alloc(used - full)
+        try:
+            self.share(pages[:full])
+        except rt.MkError:
+            self.release(fresh)
+            raise
+        return list(pages[:full]) + fresh, list(pages[full:used]), fresh
+
+    def compact(self) -> Tuple[List[int], List[int]]:
+        """Renumber the pages in use to 0 .. used - 1; returns the moves (src, dst): pass them, with the page tables, to
+        ``Kv8Cache.copy_pages``."""
+        s, d, n = np.zeros(self.num_pages, np.int32), np.zeros(self.num_pages, np.int32), C.c_int()
+        rt._check(self._lib.mk_pages_compact(self.h, s.ctypes.data, d.ctypes.data, C.byref(n)))
+        return s[:n.value].tolist(), d[:n.value].tolist()
+
+    def refs(self) -> np.ndarray:
+        """Reference counts, int32 [num_pages]."""
+        out = np.zeros(self.num_pages, np.int32)
+        rt._check(self._lib.mk_pages_info(self.h, out.ctypes.data, None))
+        return out
+
+    @property
+    def free_pages(self) -> int:
+        n = C.c_int()
+        rt._check(self._lib.mk_pages_info(self.h, None, C.byref(n)))
+        return n.value
+
+    def free(self):
+        if self.h and self.h.value:
+            self._lib.mk_pages_free(self.h)
+            self.h = C.c_void_p()
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass

@@ -42,7 +42,10 @@ PER_LAYER = ("wq", "wk", "wv", "wo", "wg", "wu", "wd", "norm_attn", "norm_mlp", 
 
 EXPORTED = ["mk_plan", "mk_plan_graph", "mk_plan_info_get", "mk_plan_export", "mk_bind", "mk_run",
             "mk_sync_status", "mk_read_counters", "mk_read_trace", "mk_free", "mk_last_error", "mk_argmax_index",
-            "mk_run_static", "mk_plan_glm", "mk_launch_probe", "mk_plan_export_attn_table"]
+            "mk_run_static", "mk_plan_glm", "mk_launch_probe", "mk_plan_export_attn_table",
+            "mk_cache_store", "mk_cache_load", "mk_cache_attend", "mk_cache_attend_workspace", "mk_cache_copy",
+            "mk_cache_status", "mk_pages_create", "mk_pages_alloc", "mk_pages_share", "mk_pages_release",
+            "mk_pages_compact", "mk_pages_info", "mk_pages_free", "mk_sample"]
 STATIC_WORKSPACE_BYTES = 64 << 20
 
 
@@ -109,6 +112,30 @@ class ErrorRecord(C.Structure):
                 ("observed", C.c_uint32), ("needed", C.c_uint32), ("opcode", C.c_int32), ("role", C.c_int32)]
 
 
+class CacheDesc(C.Structure):
+    _fields_ = [(n, C.c_uint64) for n in ("k_codes", "v_codes", "k_scales", "v_scales", "status")] + [
+        (n, C.c_int) for n in ("layers", "pages", "kv_heads", "page_tokens", "head_dim")]
+
+
+class CacheRows(C.Structure):
+    _fields_ = [("k", C.c_uint64), ("v", C.c_uint64), ("k_stride", C.c_int64 * 4), ("v_stride", C.c_int64 * 4),
+                ("rows", C.c_int), ("row0", C.c_uint64)]
+
+
+class AttendDesc(C.Structure):
+    _fields_ = [("q", C.c_uint64), ("out", C.c_uint64), ("lse", C.c_uint64), ("q_stride", C.c_int64 * 2),
+                ("out_stride", C.c_int64 * 2), ("table", C.c_uint64), ("lens", C.c_uint64), ("q_start", C.c_uint64)] + [
+        (n, C.c_int) for n in ("batch", "table_width", "q_heads", "tokens", "max_tokens", "window")] + [
+        ("scale", C.c_float), ("num_sms", C.c_int)]
+
+
+class SampleDesc(C.Structure):
+    _fields_ = [("logits", C.c_uint64), ("row_stride", C.c_int64), ("batch", C.c_int), ("vocab", C.c_int),
+                ("bf16", C.c_int)] + [(n, C.c_uint64) for n in (
+                    "u", "tokens", "logprob", "temperature_rows", "top_k_rows", "top_p_rows", "min_p_rows")] + [
+        ("temperature", C.c_float), ("top_k", C.c_int), ("top_p", C.c_float), ("min_p", C.c_float)]
+
+
 _lib = None
 
 
@@ -135,6 +162,20 @@ def load():
     lib.mk_read_counters.argtypes = [P, P, P]
     lib.mk_read_trace.argtypes = [P, P, P]
     lib.mk_launch_probe.argtypes = [C.c_int, C.c_int, P]
+    lib.mk_cache_store.argtypes = lib.mk_cache_load.argtypes = [C.POINTER(CacheDesc), C.POINTER(CacheRows), P, C.c_int,
+                                                                P, P, C.c_int, C.c_int, P]
+    lib.mk_cache_attend.argtypes = [C.POINTER(CacheDesc), C.c_int, C.POINTER(AttendDesc), P, C.c_uint64, P]
+    lib.mk_cache_attend_workspace.argtypes = [C.POINTER(CacheDesc), C.POINTER(AttendDesc), C.POINTER(C.c_uint64)]
+    lib.mk_cache_copy.argtypes = [C.POINTER(CacheDesc), P, P, C.c_int, P, C.c_int64, P]
+    lib.mk_cache_status.argtypes = [C.POINTER(CacheDesc), C.c_int, P, P]
+    lib.mk_pages_create.argtypes = [C.c_int, C.POINTER(P)]
+    lib.mk_pages_alloc.argtypes = [P, C.c_int, P]
+    lib.mk_pages_share.argtypes = lib.mk_pages_release.argtypes = [P, P, C.c_int]
+    lib.mk_pages_compact.argtypes = [P, P, P, P]
+    lib.mk_pages_info.argtypes = [P, P, P]
+    lib.mk_pages_free.argtypes = [P]
+    lib.mk_pages_free.restype = None
+    lib.mk_sample.argtypes = [C.POINTER(SampleDesc), P]
     lib.mk_free.argtypes = [P]
     lib.mk_free.restype = None
     lib.mk_last_error.restype = C.c_char_p
@@ -168,6 +209,82 @@ def _target(num_sms=0, smem_per_cta=0, mode=MODE_MEGAKERNEL, **knobs) -> TargetD
 def launch_probe(num_workers: int, cooperative: bool, stream) -> None:
     """Launch the empty probe kernel (see ``mk_launch_probe``) on a torch stream."""
     _check(load().mk_launch_probe(int(num_workers), int(cooperative), C.c_void_p(stream.cuda_stream)))
+
+
+def on_device(t, stream=None):
+    """(context that makes ``t``'s device current, stream handle): the launch goes to ``stream``, or to that
+    device's current torch stream."""
+    import torch
+    st = stream if stream is not None else torch.cuda.current_stream(t.device)
+    if st.device != t.device:
+        raise ValueError(f"stream of {st.device}, tensors of {t.device}")
+    return torch.cuda.device(t.device), st.cuda_stream
+
+
+def check_tensor(name, t, device, dtypes, shape=None):
+    """``t`` must lie on ``device``, have one of ``dtypes`` and the shape (None entries: any extent)."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape))):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}")
+
+
+def _row_setting(desc, name, value, batch, device, dtype, off):
+    """One sampling setting: None (off), a number for all rows, or a tensor with one value per row."""
+    import torch
+    if value is None:
+        setattr(desc, name, off)
+        return None
+    if isinstance(value, torch.Tensor):
+        check_tensor(name, value, device, (dtype,), (batch,))
+        value = value.contiguous()
+        setattr(desc, name + "_rows", value.data_ptr())
+        return value  # kept alive until the launch is queued
+    setattr(desc, name, value)
+    return None
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, stream=None):
+    """Draw one token per row of ``logits`` [B, V] (fp32 or bf16 CUDA tensor, any row stride) with the uniforms ``u``
+    [B] (fp32, [0, 1)): temperature, then top-k, top-p, min-p, in this order (``mk_sample`` in ``include/mk.h`` has the
+    definitions).  Each setting is None (off; temperature 1), a number, or a CUDA tensor of one value per row (fp32;
+    int32 for ``top_k``); a temperature of 0 takes the largest logit.  Returns (tokens int32 [B], logprob fp32 [B]: the
+    log probability under the filtered distribution); ``tokens``: an int32 [B] tensor to write into.  Asynchronous; may
+    be captured into a CUDA graph."""
+    import torch
+    check_tensor("logits", logits, logits.device, (torch.float32, torch.bfloat16), (None, None))
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    b, v = logits.shape
+    if b and logits.stride(1) != 1:
+        raise ValueError("logits must be contiguous along the vocabulary")
+    check_tensor("u", u, logits.device, (torch.float32,), (b,))
+    d = SampleDesc()
+    d.logits, d.row_stride, d.batch, d.vocab = logits.data_ptr(), max(logits.stride(0), v) if b < 2 else logits.stride(0), b, v
+    d.bf16 = int(logits.dtype == torch.bfloat16)
+    u = u.contiguous()
+    keep = (_row_setting(d, "temperature", temperature, b, logits.device, torch.float32, 1.0),
+            _row_setting(d, "top_k", top_k, b, logits.device, torch.int32, 0),
+            _row_setting(d, "top_p", top_p, b, logits.device, torch.float32, 1.0),
+            _row_setting(d, "min_p", min_p, b, logits.device, torch.float32, 0.0))
+    if tokens is None:
+        tokens = torch.empty((b,), dtype=torch.int32, device=logits.device)
+    else:
+        check_tensor("tokens", tokens, logits.device, (torch.int32,), (b,))
+        if not tokens.is_contiguous():
+            raise ValueError("tokens must be contiguous")
+    logprob = torch.empty((b,), dtype=torch.float32, device=logits.device)
+    d.u, d.tokens, d.logprob = u.data_ptr(), tokens.data_ptr(), logprob.data_ptr()
+    dev, st = on_device(logits, stream)
+    with dev:
+        _check(load().mk_sample(C.byref(d), st))
+    if stream is not None:
+        for t in (u, logprob, *keep):  # made on the current stream, used on `stream`
+            if t is not None:
+                t.record_stream(stream)
+    return tokens, logprob
 
 
 class Plan:
@@ -341,6 +458,39 @@ class Session:
         if rc != MK_OK:
             raise MkError(rc, load().mk_last_error().decode())
         return rec
+
+    def sample(self, step: int, u, temperature=None, top_k=None, top_p=None, min_p=None):
+        """Sample the tokens that follow ``step`` from its logits (see :func:`sample`; ``u`` [B]) into ``tokens[step +
+        1]``, where step ``step + 1`` run with ``host_tokens`` reads them.  Returns (tokens, logprob), both [B]."""
+        if not 0 <= step < self.max_steps:
+            raise ValueError(f"step {step} outside the planned {self.max_steps}")
+        return sample(self.logits, u, temperature, top_k, top_p, min_p, tokens=self.tokens[step + 1], stream=self.stream)
+
+    def generate(self, first_step: int, num_steps: int, u, temperature=None, top_k=None, top_p=None, min_p=None,
+                 timeout_ns: int = 0):
+        """Decode ``num_steps`` steps from ``tokens[first_step]`` on, each next token sampled with the settings of
+        :func:`sample` and the uniforms ``u[i]`` (fp32 [num_steps, B]) instead of taken by argmax.  Returns the sampled
+        tokens int32 [num_steps, B] (a view of ``tokens``) and their log probabilities; asynchronous."""
+        check_tensor("u", u, self.logits.device, (self.torch.float32,), (num_steps, self.B))
+        logs = []
+        for i in range(num_steps):
+            self.run(first_step + i, 1, host_tokens=True, timeout_ns=timeout_ns)
+            logs.append(self.sample(first_step + i, u[i], temperature, top_k, top_p, min_p)[1])
+        with self.torch.cuda.stream(self.stream):
+            logprob = self.torch.stack(logs) if logs else u.new_empty((0, self.B))
+        return self.tokens[first_step + 1: first_step + 1 + num_steps], logprob
+
+    def store_kv(self, cache, table, start, count, max_count: Optional[int] = None):
+        """Park K/V in an 8-bit paged cache (``kvcache.Kv8Cache`` with this model's layers, heads and head_dim):
+        positions ``start[b]`` .. ``start[b] + count[b] - 1`` of every sequence, all layers, into the pages of ``table``
+        (int32 CUDA tensors [B, width], [B], [B])."""
+        cache.store(self.kcache.transpose(2, 3), self.vcache.transpose(2, 3), table, start, count, row0=start,
+                    max_count=max_count, stream=self.stream)
+
+    def load_kv(self, cache, table, start, count, max_count: Optional[int] = None):
+        """The inverse of :meth:`store_kv`: bring those positions back from the 8-bit cache."""
+        cache.load(self.kcache.transpose(2, 3), self.vcache.transpose(2, 3), table, start, count, row0=start,
+                   max_count=max_count, stream=self.stream)
 
     def step_tokens(self, step: int) -> np.ndarray:
         """Argmax token of every sequence at ``step`` (after sync)."""
