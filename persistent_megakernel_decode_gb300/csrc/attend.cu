@@ -7,23 +7,23 @@
 // What bounds it: the cache's bytes, 2 D per token and kv head, each read
 // once; a group of q heads (and of new tokens) shares them.
 //
-// Matrix products.  Codes go to the tensor cores as they lie in memory
-// (mma.sync m16n8k32, e4m3 x e4m3 -> fp32): converting them to f16 first
-// would cost as many conversions as the SM can issue at the HBM rate.  A
-// bf16 query is exactly the sum of two e4m3 numbers at scales 1 and 1/16 (8
-// significant bits = 4 + 4; its row is scaled by a power of two into e4m3's
-// range), and a probability is one to 2^-8 of its value; the two halves are
-// rows g and g + 8 of the 16-row tile, so that both products of a row land
-// in the same thread: c[0..1] + c[2..3] / 16.  The 8 rows of a tile are q
-// heads of one kv head, then new tokens.  Against tcgen05: its least tile is
-// 64 rows, a decode step fills 4 to 8 of them, and the kernel is bound by
-// bytes either way.
+// Matrix products.  mma.sync m16n8k16 in f16 with fp32 sums, the cache as the
+// 16-row operand: scores are K q^T (16 tokens x 8 query rows), outputs V^T
+// p^T (16 dims x 8 rows), so that the 8 rows of a decode step's kv head (q
+// heads, then new tokens) fill the tile.  Codes become f16 in registers
+// (exact).  A query row is scaled by a power of two into f16's range, which
+// holds bf16's 8 bits exactly; probabilities are f16 times 2^14, 2^-11 of
+// their value.  Against m16n8k32 in e4m3 (rows split into two e4m3 halves, no
+// conversions in the source): that form runs as conversions and f16 products
+// all the same: 1460 instructions a page and warp against about 1000 here.  Against tcgen05: its
+// least tile is 64 query rows wide or needs the scores to cross TMEM between
+// the products; the kernel is bound by bytes either way.
 //
-// Token order.  A contraction may run over tokens in any order, so column n
-// of score tile j is token (P/4)(n/2) + 2j + n%2 of the page: then thread t
-// of a quad owns the P/4 tokens from (P/4) t on, its probabilities already
-// are the second product's A fragment, and its V operand is one P/4-byte run
-// of a transposed V row.
+// Token order.  A contraction may run over tokens in any order, so row (m, u,
+// g) of the score tile (16-row step m, half u, row g) is token (P/4)(g/2) + 4m
+// + 2u + g%2 of the page: after an 8 x 8 transpose in registers (movmatrix),
+// thread t of a quad holds the probabilities of the P/4 tokens from (P/4) t
+// on, and its V operand is one P/4-byte run of a transposed V row.
 //
 // Work split.  The pages of all (sequence, row tile, kv head) form one axis,
 // cut into equal ranges, one per CTA (one CTA per SM): ragged batches and
@@ -43,7 +43,7 @@ namespace mk {
 constexpr int ATT_WARPS = 8;                        // consumer warps
 constexpr int ATT_THREADS = (ATT_WARPS + 1) * 32;   // + the producer
 constexpr int ATT_MAXB = 1024;                      // sequences per call
-constexpr int ATT_MAXSTAGES = 32;
+constexpr int ATT_MAXRING = 32;                     // pages in the ring (one producer lane each)
 
 struct AttParams {
     CacheView c;  // of the layer: k, v, ks, vs point at it
@@ -52,12 +52,17 @@ struct AttParams {
     float *lse;
     int64_t qs_t, qs_h, os_t, os_h;
     const int *table, *lens, *q_start;
-    int batch, width, group, tokens, max_tokens, window, stages, ctas;
+    int batch, width, group, tokens, max_tokens, window, ring, ctas;
     float scale_log2;
     // workspace: prefix int64 [batch + 1]; partial (m, l) [ctas][2][RT][2]; partial O [ctas][2][RT][D]
     long long *prefix;
     float *part_ml, *part_o;
 };
+
+// ln of the sum of exponentials: maximum in log2 units, sum times 2^14.
+DEV float att_lse(float big, float sum) {
+    return sum == 0.f ? -INFINITY : (big - 14.f + log2f(sum)) * 0.6931471805599453f;
+}
 
 // What a sequence asks for: its query rows, its pages [lo, hi) that any row sees.
 struct AttSeq {
@@ -90,110 +95,141 @@ DEV int att_used(long long total, int ctas) { return (int)min((long long)ctas, t
 // CTA of work item x when `total` items are cut into `ctas` <= total ranges [c total / ctas, (c + 1) total / ctas).
 DEV int att_owner(long long x, long long total, int ctas) { return (int)(((x + 1) * ctas - 1) / total); }
 
-// One range of pages of one unit, as every warp of the CTA walks them.
+struct AttShared {
+    long long *prefix;  // [batch + 1]: pages of all units before each sequence
+    int4 *seq;          // [batch]: AttSeq without hi
+    float2 *scale;      // [ring]: (K scale, V scale), K scale < 0: page not loaded
+    uint64_t *full_k, *full_v, *empty_k, *empty_v;
+    int *has_k, *has_v; // [ring]: number of the page that the slot was last asked to load
+    float *merge;       // [8 warps][8 NT rows][D + 4]
+    float *ml;          // [8 warps][8 NT rows][2]
+    int *ctrl;          // [0] abort
+    uint8_t *ring;      // [ring][K page, V page]
+};
+
+// Tiles of rt rows: 8 NT rows a warp, rt / (8 NT) warps side by side
+__host__ __device__ constexpr int att_nt(int rt) { return rt == 8 ? 1 : 2; }
+
+__host__ __device__ constexpr int att_fixed_bytes(int D, int nt) {
+    return ATT_WARPS * 8 * nt * (D + 4) * 4 + ATT_WARPS * 8 * nt * 2 * 4 + ATT_MAXRING * (8 + 32 + 8) + 16;
+}
+__host__ __device__ constexpr int att_seq_bytes(int batch) { return batch * 16 + (batch + 1) * 8; }
+
+template <int D, int NT>
+DEV AttShared att_shared(const AttParams &p) {
+    AttShared s;
+    uint8_t *at = mk_smem;
+    s.full_k = reinterpret_cast<uint64_t *>(at);
+    s.full_v = s.full_k + ATT_MAXRING;
+    s.empty_k = s.full_v + ATT_MAXRING;
+    s.empty_v = s.empty_k + ATT_MAXRING;
+    at += ATT_MAXRING * 32;
+    s.scale = reinterpret_cast<float2 *>(at);
+    at += ATT_MAXRING * 8;
+    s.has_k = reinterpret_cast<int *>(at);
+    s.has_v = s.has_k + ATT_MAXRING;
+    at += ATT_MAXRING * 8;
+    s.ctrl = reinterpret_cast<int *>(at);
+    at += 16;
+    s.ml = reinterpret_cast<float *>(at);
+    at += ATT_WARPS * 8 * NT * 2 * 4;
+    s.merge = reinterpret_cast<float *>(at);
+    at += ATT_WARPS * 8 * NT * (D + 4) * 4;
+    s.seq = reinterpret_cast<int4 *>(at);
+    s.prefix = reinterpret_cast<long long *>(s.seq + p.batch);
+    const uint32_t used = (uint32_t)(at - mk_smem) + att_seq_bytes(p.batch);
+    s.ring = mk_smem + ((used + 127) & ~127u);
+    return s;
+}
+
+// Work item x (a page of a unit) belongs to the last sequence b with prefix[b] <= x that has any.
+DEV int att_find(const long long *prefix, int batch, long long x) {
+    int a = 0, z = batch;
+    while (z - a > 1) {
+        const int mid = (a + z) / 2;
+        if (prefix[mid] <= x) a = mid;
+        else z = mid;
+    }
+    return a;
+}
+// A quotient that mostly fits 32 bits.
+DEV long long att_div(long long a, int b) { return a <= 0xffffffffll ? (long long)((uint32_t)a / (uint32_t)b) : a / b; }
+
+// The pages of a sequence that the rows of one of its tiles see: [lo, hi).
+template <int P, int RT>
+DEV void att_tile_pages(const AttParams &p, const int4 &q, int tile, int &lo, int &hi) {
+    const int rows = q.y * p.group;
+    const int i0 = tile * RT / p.group, i1 = (min((tile + 1) * RT, rows) - 1) / p.group;
+    const int top = q.z - q.y + i1, bottom = q.z - q.y + i0;
+    hi = top < 0 ? 0 : top / P + 1;
+    lo = p.window > 0 ? max(0, bottom - p.window + 1) / P : 0;
+}
+
+// One range of pages of one unit, as the consumer warps walk them.
 struct AttSeg {
-    int b, tile, h, p0, p1;   // pages [p0, p1)
+    int tile, h, pg, n;       // pages [pg, pg + n) of the sequence
     int q0, cnt, len;
     bool whole;               // the unit's every page
     bool first;               // the CTA's first range
 };
 
-struct AttShared {
-    long long *prefix;  // [batch + 1]
-    float2 *scale;      // [stages]: (K scale, V scale), K scale < 0: page not loaded
-    uint64_t *full, *empty;
-    float *merge;       // [8 warps][8 rows][D + 8]
-    float *ml;          // [8 warps][8 rows][2]
-    int *ctrl;          // [0] abort
-    uint8_t *ring;
-};
-
-template <int D>
-__host__ __device__ constexpr int att_fixed_bytes() {
-    return ATT_WARPS * 8 * (D + 8) * 4 + ATT_WARPS * 8 * 2 * 4 + ATT_MAXSTAGES * (8 + 16) + 16;
+DEV void att_range(const AttParams &p, long long total, long long &x, long long &end) {
+    const int ctas = max(1, att_used(total, p.ctas));
+    x = end = 0;
+    if ((int)blockIdx.x < ctas) {
+        x = (long long)blockIdx.x * total / ctas;
+        end = (long long)(blockIdx.x + 1) * total / ctas;
+    }
 }
 
-template <int D>
-DEV AttShared att_shared(const AttParams &p) {
-    AttShared s;
-    uint8_t *at = mk_smem;
-    s.full = reinterpret_cast<uint64_t *>(at);
-    s.empty = s.full + ATT_MAXSTAGES;
-    at += ATT_MAXSTAGES * 16;
-    s.scale = reinterpret_cast<float2 *>(at);
-    at += ATT_MAXSTAGES * 8;
-    s.ctrl = reinterpret_cast<int *>(at);
-    at += 16;
-    s.ml = reinterpret_cast<float *>(at);
-    at += ATT_WARPS * 8 * 2 * 4;
-    s.merge = reinterpret_cast<float *>(at);
-    at += ATT_WARPS * 8 * (D + 8) * 4;
-    s.prefix = reinterpret_cast<long long *>(at);
-    const uint32_t used = (uint32_t)(at - mk_smem) + (p.batch + 1) * 8;
-    s.ring = mk_smem + ((used + 127) & ~127u);
-    return s;
-}
-
-// Walks the ranges of this CTA; the same in every warp.
-template <int P, int RT>
+template <int P>
 struct AttWalk {
     const AttParams &p;
-    const long long *prefix;
+    const AttShared &s;
     long long x, end;
     int b;
     bool first = true;
-    DEV AttWalk(const AttParams &p_, const long long *pre) : p(p_), prefix(pre) {
-        const long long total = pre[p.batch];
-        const int ctas = max(1, att_used(total, p.ctas));
-        x = end = 0;
-        if ((int)blockIdx.x < ctas) {
-            x = (long long)blockIdx.x * total / ctas;
-            end = (long long)(blockIdx.x + 1) * total / ctas;
-        }
-        int a = 0, z = p.batch;  // the last b with prefix[b] <= x
-        while (z - a > 1) {
-            const int mid = (a + z) / 2;
-            if (pre[mid] <= x) a = mid;
-            else z = mid;
-        }
-        b = a;
+    DEV AttWalk(const AttParams &p_, const AttShared &s_) : p(p_), s(s_) {
+        att_range(p, s.prefix[p.batch], x, end);
+        b = att_find(s.prefix, p.batch, x);
     }
     DEV bool next(AttSeg &g) {
         if (x >= end) return false;
-        while (prefix[b + 1] <= x) ++b;
-        const AttSeq s = att_seq<P>(p, b, false);
-        const int np = s.hi - s.lo;
-        const long long r = x - prefix[b];
-        const int unit = (int)(r / np), pg = (int)(r % np);
-        const int n = (int)min((long long)(np - pg), end - x);
-        x += n;
-        g.b = b;
+        while (s.prefix[b + 1] <= x) ++b;
+        const int4 q = s.seq[b];
+        const int np = (q.z + P - 1) / P - q.w;
+        const long long r = x - s.prefix[b];
+        const int unit = (int)att_div(r, np), pg = (int)(r - (long long)unit * np);
+        g.n = (int)min((long long)(np - pg), end - x);
+        x += g.n;
         g.tile = unit / p.c.hkv;
-        g.h = unit % p.c.hkv;
-        g.q0 = s.q0;
-        g.cnt = s.cnt;
-        g.len = s.len;
-        g.whole = n == np;
+        g.h = unit - g.tile * p.c.hkv;
+        g.pg = q.w + pg;
+        g.q0 = q.x;
+        g.cnt = q.y;
+        g.len = q.z;
+        g.whole = g.n == np;
         g.first = first;
         first = false;
-        // the tile's own rows may see fewer pages than the sequence's
-        const int rows = s.cnt * p.group;
-        const int i0 = g.tile * RT / p.group, i1 = (min((g.tile + 1) * RT, rows) - 1) / p.group;
-        const int top = s.len - s.cnt + i1, bottom = s.len - s.cnt + i0;
-        const int seen_hi = top < 0 ? 0 : top / P + 1;
-        const int seen_lo = p.window > 0 ? max(0, bottom - p.window + 1) / P : 0;
-        g.p0 = max(s.lo + pg, seen_lo);
-        g.p1 = min(s.lo + pg + n, seen_hi);
         return true;
     }
 };
 
-// Bounded wait on a ring barrier (a few seconds): false if it ran out or
-// another warp gave up.
-DEV bool att_wait(const AttParams &p, const AttShared &s, uint64_t *bar, uint32_t parity) {
-    if (mbar_test(bar, parity)) return true;
-    for (int i = 0; i < 4000; ++i) {
-        if (mbar_wait_hint(bar, parity, 1000000)) return true;
+// Wait until a slot holds page `number`, bounded (a few seconds): false if it
+// ran out or another warp gave up.  The barrier's parity alone does not say
+// which page landed: a slot's pages belong to different warps, and one that
+// is ahead could take the landing before last for its own.
+DEV bool att_wait(const AttParams &p, const AttShared &s, int *has, int number, uint64_t *bar, uint32_t parity) {
+    bool asked = ld_acquire_cta(has) == number;
+    if (asked && mbar_test(bar, parity)) return true;
+    for (int i = 0; i < 4000000; ++i) {
+        if (!asked) {
+            asked = ld_acquire_cta(has) == number;
+            if (!asked && i > 1000) __nanosleep(1000);
+        } else {
+            if (mbar_wait_hint(bar, parity, 100000)) return true;
+            i += 1000;
+        }
         if (*reinterpret_cast<volatile int *>(s.ctrl)) return false;
     }
     note_failure(p.c.status, MK_ERR_TIMEOUT, -1, blockIdx.x, -1);
@@ -201,69 +237,118 @@ DEV bool att_wait(const AttParams &p, const AttShared &s, uint64_t *bar, uint32_
     return false;
 }
 
-template <int D, int P, int MT>
+// The producer warp.  Lane i of a batch of `ring` pages looks up and loads the
+// i-th: a loop over pages in one thread took 850 clocks a page, all of them
+// instruction latency.  All lanes poll their slots at once; those that are
+// free are filled.
+template <int D, int P, int RT>
 DEV void att_produce(const AttParams &p, const AttShared &s) {
-    constexpr int RT = 8 * MT, PAGE = P * D;
+    constexpr int PAGE = P * D;
     const int lane = threadIdx.x % 32;
-    AttWalk<P, RT> walk(p, s.prefix);
-    AttSeg g;
-    int it = 0;
+    long long x, end;
+    att_range(p, s.prefix[p.batch], x, end);
+    const bool mine = lane < p.ring;
+    uint8_t *dst = s.ring + (size_t)lane * 2 * PAGE;
+    // page number (-1: not loaded) and kv head of this lane's next page
+    const auto look = [&](long long i, int &id, int &h) {
+        id = -1;
+        h = 0;
+        if (!mine || i >= end) return;
+        int b = att_find(s.prefix, p.batch, i);
+        while (s.prefix[b + 1] <= i) ++b;
+        const int4 q = s.seq[b];
+        const int np = (q.z + P - 1) / P - q.w;
+        const long long r = i - s.prefix[b];
+        const int unit = (int)att_div(r, np), pg = q.w + (int)(r - (long long)unit * np);
+        const int tile = unit / p.c.hkv;
+        h = unit - tile * p.c.hkv;
+        int lo, hi;
+        att_tile_pages<P, RT>(p, q, tile, lo, hi);
+        if (pg < lo || pg >= hi) return;
+        id = p.table[(size_t)b * p.width + pg];
+        if ((unsigned)id >= (unsigned)p.c.pages) {
+            note_failure(p.c.status, MK_ERR_DEVICE_CHECK, b, pg * P, id);
+            id = -1;
+        }
+    };
+    int id, h;
+    look(x + lane, id, h);
+    uint32_t turn = 0, k_fills = 0, v_fills = 0;
     bool ok = true;
-    while (ok && walk.next(g)) {
-        for (int base = g.p0; ok && base < g.p1; base += 32) {
-            const int n = min(32, g.p1 - base);
-            int id = -1;
-            float ks = -1.f, vs = 0.f;
-            if (lane < n) {
-                id = p.table[(size_t)g.b * p.width + base + lane];
-                if ((unsigned)id < (unsigned)p.c.pages) {
-                    ks = p.c.ks[(size_t)id * p.c.hkv + g.h];
-                    vs = p.c.vs[(size_t)id * p.c.hkv + g.h];
-                } else {
-                    note_failure(p.c.status, MK_ERR_DEVICE_CHECK, g.b, (base + lane) * P, id);
-                    id = -1;
-                }
+    for (; x < end && ok; x += p.ring, ++turn) {
+        const bool want = mine && x + lane < end;
+        const size_t at = (size_t)(id < 0 ? 0 : id) * p.c.hkv + h;
+        float2 sc = make_float2(-1.f, 0.f);
+        if (want && id >= 0) sc = make_float2(p.c.ks[at], p.c.vs[at]);
+        const int now = id;
+        bool k_todo = want, v_todo = want;
+        const uint32_t ph = (turn & 1) ^ 1;
+        for (int spin = 0; __any_sync(FULL, k_todo || v_todo); ++spin) {
+            const bool k = k_todo && (turn == 0 || mbar_test(&s.empty_k[lane], ph));
+            if (k && now >= 0) {
+                mbar_expect_tx(&s.full_k[lane], PAGE);
+                bulk_g2s_plain(dst, p.c.k + at * PAGE, PAGE, &s.full_k[lane]);
             }
-            for (int i = 0; i < n; ++i, ++it) {
-                const int page = __shfl_sync(FULL, id, i);
-                const float k1 = __shfl_sync(FULL, ks, i), v1 = __shfl_sync(FULL, vs, i);
-                const int st = it % p.stages;
-                if (it >= p.stages) ok = att_wait(p, s, &s.empty[st], ((it / p.stages) & 1) ^ 1);
-                ok = __shfl_sync(FULL, ok, 0);
-                if (!ok) break;
-                if (lane == 0) {
-                    s.scale[st] = make_float2(page < 0 ? -1.f : k1, v1);
-                    if (page < 0) {
-                        mbar_arrive(&s.full[st]);
-                    } else {
-                        mbar_expect_tx(&s.full[st], 2 * PAGE);
-                        const size_t off = ((size_t)page * p.c.hkv + g.h) * PAGE;
-                        bulk_g2s_plain(s.ring + (size_t)st * 2 * PAGE, p.c.k + off, PAGE, &s.full[st]);
-                        bulk_g2s_plain(s.ring + (size_t)st * 2 * PAGE + PAGE, p.c.v + off, PAGE, &s.full[st]);
-                    }
+            const bool v = v_todo && (turn == 0 || mbar_test(&s.empty_v[lane], ph));
+            if (v) st_release_cta(&s.has_v[lane], (int)turn * p.ring + lane);
+            if (v && now >= 0) {
+                mbar_expect_tx(&s.full_v[lane], PAGE);
+                bulk_g2s_plain(dst + PAGE, p.c.v + at * PAGE, PAGE, &s.full_v[lane]);
+            }
+            if (k) {  // full_k counts two arrivals: the scales come with the second
+                s.scale[lane] = sc;
+                st_release_cta(&s.has_k[lane], (int)turn * p.ring + lane);
+                mbar_arrive(&s.full_k[lane]);
+                if (now < 0) mbar_arrive(&s.full_k[lane]);
+            }
+            if (v && now < 0) mbar_arrive(&s.full_v[lane]);
+            k_todo = k_todo && !k;
+            v_todo = v_todo && !v;
+            k_fills += k;
+            v_fills += v;
+            if (spin == 0) look(x + p.ring + lane, id, h);  // the next turn's pages, while this one's slots come free
+            if (spin > 256) {
+                __nanosleep(spin > 4096 ? 1000 : 100);
+                const bool give_up = spin > 4000000 || *reinterpret_cast<volatile int *>(s.ctrl);  // a few seconds
+                if (__any_sync(FULL, give_up)) {
+                    ok = false;
+                    break;
                 }
-                __syncwarp();
             }
         }
     }
-    if (!ok && lane == 0) {  // given up: let the copies in flight land before the CTA ends
-        for (int k = max(0, it - p.stages); k < it; ++k)
-            for (int i = 0; i < 200 && !mbar_wait_hint(&s.full[k % p.stages], (k / p.stages) & 1, 1000000); ++i) {
-            }
+    if (!ok) {  // let the copies in flight land before the CTA ends
+        if (lane == 0) note_failure(p.c.status, MK_ERR_TIMEOUT, -1, blockIdx.x, -1);
+        *reinterpret_cast<volatile int *>(s.ctrl) = 1;
+        for (int i = 0; i < 200 && k_fills && !mbar_wait_hint(&s.full_k[lane], (k_fills - 1) & 1, 1000000); ++i) {
+        }
+        for (int i = 0; i < 200 && v_fills && !mbar_wait_hint(&s.full_v[lane], (v_fills - 1) & 1, 1000000); ++i) {
+        }
     }
 }
 
-DEV void att_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+DEV void att_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit values, two a thread (row lane / 4), transposed.
+DEV uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 DEV float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+DEV uint32_t half2_of(float lo, float hi) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+    return h;
 }
 // Bytes of w that are e4m3's NaN codes (0x7f, 0xff), as a byte mask.
 DEV uint32_t nan_bytes(uint32_t w) {
@@ -271,10 +356,10 @@ DEV uint32_t nan_bytes(uint32_t w) {
     return m * 0xffu;
 }
 
-// The query fragment of one row: dims h2 * 64 + 16 t .. + 15, split into e4m3
-// halves; returns 2^-k of the row's scaling (NaN if the row is not finite).
+// One row of the query operand: f16 pairs of dims h2 * 64 + 16 t .. + 15;
+// returns 2^-k of the row's scaling (NaN if the row is not finite).
 template <int D>
-DEV float att_load_q(const uint16_t *row, int t, uint32_t (&qa)[D / 32][4]) {
+DEV float att_load_q(const uint16_t *row, int t, uint32_t (&qb)[D / 64][8]) {
     float f[D / 64][16];
     uint32_t big = 0;
 #pragma unroll
@@ -297,204 +382,268 @@ DEV float att_load_q(const uint16_t *row, int t, uint32_t (&qa)[D / 32][4]) {
     }
     big = max(big, __shfl_xor_sync(FULL, big, 1));
     big = max(big, __shfl_xor_sync(FULL, big, 2));
-    // times 2^(7 - exponent) (bits 127 + 7 - (field - 127)): the row's largest value lands in [128, 256)
-    const int up = min(max(261 - (int)(big >> 23), 1), 253);
+    // times 2^(14 - exponent) (bits 127 + 14 - (field - 127)): the row's largest value lands in [2^14, 2^15)
+    const int up = min(max(268 - (int)(big >> 23), 1), 253);
     const float sc = __uint_as_float((uint32_t)up << 23);
 #pragma unroll
     for (int h2 = 0; h2 < D / 64; ++h2)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // 4 dims: a register of hi codes and one of lo codes
-            uint32_t hi = 0, lo = 0;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float a = f[h2][4 * i + 2 * j] * sc, b = f[h2][4 * i + 2 * j + 1] * sc;
-                const uint32_t e = to_e4m3x2(a, b);
-                float ea, eb;
-                half2_floats(e4m3x2_to_half2(e), ea, eb);
-                hi |= e << (16 * j);
-                lo |= to_e4m3x2((a - ea) * 16.f, (b - eb) * 16.f) << (16 * j);
-            }
-            qa[2 * h2 + i / 2][(i % 2) * 2] = hi;
-            qa[2 * h2 + i / 2][(i % 2) * 2 + 1] = lo;
-        }
+        for (int i = 0; i < 8; ++i) qb[h2][i] = half2_of(f[h2][2 * i] * sc, f[h2][2 * i + 1] * sc);
     return big >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(254 - up) << 23);
 }
 
 DEV void att_consumer_bar() { asm volatile("bar.sync 1, %0;" ::"n"(ATT_WARPS * 32) : "memory"); }
 
-template <int D, int P, int MT>
+template <int D, int P, int RT>
 DEV void att_consume(const AttParams &p, const AttShared &s) {
-    constexpr int RT = 8 * MT, NG = ATT_WARPS / MT, PAGE = P * D, NJ = P / 8, RUN = P / 4;
+    constexpr int NT = att_nt(RT), WT = RT / (8 * NT), NG = ATT_WARPS / WT;  // row tiles a warp, warps a tile, page groups
+    constexpr int PAGE = P * D, RUN = P / 4, NM = P / 16, ND = D / 16, LD = D + 4;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g8 = lane / 4, t = lane % 4;
-    const int mt = warp % MT, grp = warp / MT;
-    AttWalk<P, RT> walk(p, s.prefix);
+    const int wt = warp % WT, grp = warp / WT;
+    AttWalk<P> walk(p, s);
     AttSeg g;
-    int it = 0;
     bool ok = true;
+    // this warp's pages are those of the CTA's ranges with number grp, grp + NG, ...; `mine` is the next one's, in
+    // ring slot st at phase ph; `before` counts the pages of the ranges done
+    int mine = grp, before = 0, st = grp;
+    uint32_t ph = 0;
+    const auto settle = [&] {
+        while (st >= p.ring) {
+            st -= p.ring;
+            ph ^= 1;
+        }
+    };
+    settle();
     while (walk.next(g)) {
-        const int rows = g.cnt * p.group;
-        const int r = g.tile * RT + mt * 8 + g8;                    // this thread's row
-        const int tok = r / p.group, head = g.h * p.group + r % p.group;
-        const int pos = r < rows ? g.len - g.cnt + tok : -1;        // it sees [least, pos]
-        const int least = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-        uint32_t qa[D / 32][4];
-        const uint16_t *qrow = r < rows ? p.q + (int64_t)(g.q0 + tok) * p.qs_t + (int64_t)head * p.qs_h : nullptr;
-        const float qf = att_load_q<D>(qrow, t, qa) * p.scale_log2;
-        // pages that every row of the warp's tile sees whole need no masks
-        const int all_hi = __reduce_min_sync(FULL, r < rows ? pos : INT_MAX);
-        const int all_lo = __reduce_max_sync(FULL, r < rows ? least : 0);
-        float m = -INFINITY, l = 0.f, o[D / 8][2];
+        const int rows = g.cnt * p.group, row0 = g.tile * RT + wt * 8 * NT, base = g.len - g.cnt;
+        const auto pos_of = [&](int r) { return r < rows ? base + r / p.group : -1; };  // a row sees [least, pos]
+        const auto least_of = [&](int pos) { return p.window > 0 ? max(0, pos - p.window + 1) : 0; };
+        uint32_t qb[NT][D / 64][8];
+        float f[NT][2], m[NT][2], l[NT][2], o[NT][ND][4];
+        int pos[NT][2];
+        int all_hi = INT_MAX, all_lo = 0;  // pages within need no masks
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = 0.f;
-        for (int pg = g.p0; pg < g.p1; ++pg, ++it) {
-            if (it % NG != grp || !ok) continue;
-            const int st = it % p.stages;
-            ok = att_wait(p, s, &s.full[st], (it / p.stages) & 1);
+        for (int n = 0; n < NT; ++n) {
+            const int r = row0 + 8 * n + g8;  // this thread's row of the operand
+            const uint16_t *qrow = nullptr;
+            if (r < rows) {
+                const int tok = r / p.group;
+                qrow = p.q + (int64_t)(g.q0 + tok) * p.qs_t + (int64_t)(g.h * p.group + r - tok * p.group) * p.qs_h;
+                all_hi = min(all_hi, base + tok);
+                all_lo = max(all_lo, least_of(base + tok));
+            }
+            const float qf = att_load_q<D>(qrow, t, qb[n]) * p.scale_log2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // its columns of the products
+                f[n][e] = __shfl_sync(FULL, qf, 8 * t + 4 * e);
+                pos[n][e] = pos_of(row0 + 8 * n + 2 * t + e);
+                m[n][e] = -INFINITY;
+                l[n][e] = 0.f;
+            }
+#pragma unroll
+            for (int d = 0; d < ND; ++d) o[n][d][0] = o[n][d][1] = o[n][d][2] = o[n][d][3] = 0.f;
+        }
+        all_hi = __reduce_min_sync(FULL, all_hi);
+        all_lo = __reduce_max_sync(FULL, all_lo);
+        for (; mine < before + g.n; mine += NG, st += NG, settle()) {
+            const int pg = g.pg + mine - before;
+            if (ok) ok = att_wait(p, s, &s.has_k[st], mine, &s.full_k[st], ph);
             ok = __all_sync(FULL, ok);
             if (!ok) continue;
             const float2 sc = s.scale[st];
+            const bool there = sc.x >= 0.f || sc.x != sc.x;
             const uint8_t *kp = s.ring + (size_t)st * 2 * PAGE, *vp = kp + PAGE;
-            if (sc.x >= 0.f || sc.x != sc.x) {
-                float c[NJ][4];
+            if (there) {
+                const bool edge = pg * P < all_lo || pg * P + P - 1 > all_hi;
+                float c[NT][NM][4];
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < NM; ++i) c[n][i][0] = c[n][i][1] = c[n][i][2] = c[n][i][3] = 0.f;
+                const uint8_t *kr = kp + (RUN * (g8 >> 1) + (g8 & 1)) * D + 16 * t;
+                // 32 dims at a time, so that consecutive products go to different sums
 #pragma unroll
                 for (int h2 = 0; h2 < D / 64; ++h2)
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const int row = RUN * (g8 >> 1) + 2 * j + (g8 & 1);
-                        const uint4 kk = *reinterpret_cast<const uint4 *>(kp + row * D + h2 * 64 + 16 * t);
-                        att_mma(c[j], qa[2 * h2], kk.x, kk.y);
-                        att_mma(c[j], qa[2 * h2 + 1], kk.z, kk.w);
-                    }
-                const float f = sc.x * qf;
-                const int first = pg * P + RUN * t;  // token of c[0][0]
-                const bool edge = pg * P < all_lo || pg * P + P - 1 > all_hi;
-                float mx = -INFINITY;
+                    for (int jj = 0; jj < 2; ++jj) {
+                        uint2 x[NM], y[NM];
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
+                        for (int i = 0; i < NM; ++i) {
+                            x[i] = *reinterpret_cast<const uint2 *>(kr + 4 * i * D + h2 * 64 + 8 * jj);
+                            y[i] = *reinterpret_cast<const uint2 *>(kr + (4 * i + 2) * D + h2 * 64 + 8 * jj);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int i = 0; i < NM; ++i) {
+                                const uint32_t xw = j ? x[i].y : x[i].x, yw = j ? y[i].y : y[i].x;
+                                uint32_t a0, a1, a2, a3;
+                                e4m3x4_to_half2(xw, a0, a2);
+                                e4m3x4_to_half2(yw, a1, a3);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    att_mma(c[n][i], a0, a1, a2, a3, qb[n][h2][4 * jj + 2 * j], qb[n][h2][4 * jj + 2 * j + 1]);
+                            }
+                    }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.empty_k[st]);  // K is read: the next one loads during the rest
+                const int first = pg * P + RUN * (g8 >> 1) + (g8 & 1);  // token of c[.][0][0]; [i][2u + e]: + 4 i + 2 u
+                float alpha[NT][2];
+                uint32_t pb[NT][NM][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float z = fmaf(c[j][e + 2], 0.0625f, c[j][e]) * f;
-                        if (edge && (first + 2 * j + e > pos || first + 2 * j + e < least)) z = -INFINITY;
-                        c[j][e] = z;
-                        mx = fmaxf(mx, z);
+                        const float fk = f[n][e] * sc.x;
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < NM; ++i)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                float z = c[n][i][2 * u + e] * fk;
+                                if (edge) {
+                                    const int x = first + 4 * i + 2 * u;
+                                    if (x > pos[n][e] || x < least_of(pos[n][e])) z = -INFINITY;
+                                }
+                                c[n][i][2 * u + e] = z;
+                                mx = fmaxf(mx, z);
+                            }
+                        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
+                        const float mn = fmaxf(m[n][e], mx), mu = mn == -INFINITY ? 0.f : mn;
+                        alpha[n][e] = exp2_fast(m[n][e] - mu);
+                        m[n][e] = mn;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int i = 0; i < NM; ++i)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const float x = exp2_fast(c[n][i][2 * u + e] - mu + 14.f);
+                                c[n][i][2 * u + e] = x;
+                                sum += x;
+                            }
+                        l[n][e] = fmaf(l[n][e], alpha[n][e], sum);
                     }
-                mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
-                const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
-                const float alpha = exp2_fast(m - mu);
-                m = mn;
-                // probabilities x 2^8 (e4m3's upper range), in e4m3 halves
-                uint32_t pa[P / 32][4];
-                float sum = 0.f;
 #pragma unroll
-                for (int k = 0; k < P / 32; ++k)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t hi = 0, lo = 0;
+                    for (int i = 0; i < NM; ++i)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int j = 4 * k + 2 * q + i;
-                            const float a = exp2_fast(c[j][0] - mu + 8.f), b = exp2_fast(c[j][1] - mu + 8.f);
-                            sum += a + b;
-                            uint32_t h2;
-                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(b), "f"(a));
-                            const uint32_t e = half2_to_e4m3x2(h2);
-                            hi |= e << (16 * i);
-                            // the remainder is exact in f16; x 16
-                            lo |= half2_to_e4m3x2(half2_mul(half2_sub(h2, e4m3x2_to_half2(e)), 0x4c004c00u)) << (16 * i);
-                        }
-                        pa[k][2 * q] = hi;
-                        pa[k][2 * q + 1] = lo;
-                    }
-                l = fmaf(l, alpha, sum);
-                if (!edge) {
+                        for (int u = 0; u < 2; ++u) pb[n][i][u] = transpose8(half2_of(c[n][i][2 * u], c[n][i][2 * u + 1]));
+                ok = att_wait(p, s, &s.has_v[st], mine, &s.full_v[st], ph);
+                ok = __all_sync(FULL, ok);
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        float a[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int d = 0; d < ND; ++d) {
+                    uint32_t w[2][RUN / 4];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint8_t *vr = vp + (d * 16 + 8 * u + g8) * P + RUN * t;
                         if constexpr (P == 64) {
-                            const uint4 vv = *reinterpret_cast<const uint4 *>(vp + (n * 8 + g8) * P + RUN * t);
-                            att_mma(a, pa[0], vv.x, vv.y);
-                            att_mma(a, pa[1], vv.z, vv.w);
+                            const uint4 x = *reinterpret_cast<const uint4 *>(vr);
+                            w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w;
                         } else {
-                            const uint2 vv = *reinterpret_cast<const uint2 *>(vp + (n * 8 + g8) * P + RUN * t);
-                            att_mma(a, pa[0], vv.x, vv.y);
+                            const uint2 x = *reinterpret_cast<const uint2 *>(vr);
+                            w[u][0] = x.x, w[u][1] = x.y;
                         }
-                        o[n][0] = fmaf(fmaf(a[2], 0.0625f, a[0]), sc.y, o[n][0] * alpha);
-                        o[n][1] = fmaf(fmaf(a[3], 0.0625f, a[1]), sc.y, o[n][1] * alpha);
                     }
-                } else {
-                    // A masked token's weight is 0, but 0 x NaN is NaN: NaN
-                    // codes are taken out, and a second product of the mask
-                    // with their places says which sums really contain one.
-                    uint32_t see[P / 32][4];
+                    if (edge) {
+                        // A masked token's weight is 0, but 0 x NaN is NaN: NaN
+                        // codes are taken out, and a product of the mask with
+                        // their places says which sums really contain one.
+                        uint32_t bad = 0;
 #pragma unroll
-                    for (int k = 0; k < P / 32; ++k)
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t w = 0;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int x = first + 8 * k + 4 * q + i;
-                                if (x <= pos && x >= least) w |= 0x38u << (8 * i);  // 1.0
-                            }
-                            see[k][2 * q] = w;
-                            see[k][2 * q + 1] = 0;
-                        }
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        uint32_t vv[RUN / 4], bad = 0;
-#pragma unroll
-                        for (int i = 0; i < RUN / 4; ++i) {
-                            vv[i] = *reinterpret_cast<const uint32_t *>(vp + (n * 8 + g8) * P + RUN * t + 4 * i);
-                            bad |= nan_bytes(vv[i]);
-                        }
-                        float a[4] = {0.f, 0.f, 0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
+                        for (int i = 0; i < RUN / 4; ++i) bad |= nan_bytes(w[0][i]) | nan_bytes(w[1][i]);
                         if (__any_sync(FULL, bad != 0)) {
-                            uint32_t at[RUN / 4];
+                            uint32_t at[2][RUN / 4];
 #pragma unroll
-                            for (int i = 0; i < RUN / 4; ++i) {
-                                const uint32_t nb = nan_bytes(vv[i]);
-                                vv[i] &= ~nb;
-                                at[i] = nb & 0x38383838u;
+                            for (int i = 0; i < RUN / 4; ++i)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const uint32_t nb = nan_bytes(w[u][i]);
+                                    w[u][i] &= ~nb;
+                                    at[u][i] = nb & 0x38383838u;  // 1.0
+                                }
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                const int ps = pos_of(row0 + 8 * n + g8), ls = least_of(ps);
+                                float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                for (int i = 0; i < RUN / 4; ++i) {
+                                    uint32_t see[2];
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k) {
+                                        const int x = pg * P + RUN * t + 4 * i + 2 * k;
+                                        see[k] = (x <= ps && x >= ls ? 0x3c00u : 0u) |
+                                                 (x + 1 <= ps && x + 1 >= ls ? 0x3c000000u : 0u);
+                                    }
+                                    att_mma(z, e4m3x2_to_half2(at[0][i]), e4m3x2_to_half2(at[1][i]),
+                                            e4m3x2_to_half2(at[0][i] >> 16), e4m3x2_to_half2(at[1][i] >> 16), see[0], see[1]);
+                                }
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (z[k] > 0.f) o[n][d][k] = __uint_as_float(0x7fc00000u);
                             }
-#pragma unroll
-                            for (int k = 0; k < P / 32; ++k) att_mma(z, see[k], at[2 * k], at[2 * k + 1]);
                         }
-#pragma unroll
-                        for (int k = 0; k < P / 32; ++k) att_mma(a, pa[k], vv[2 * k], vv[2 * k + 1]);
-                        const float nan = __uint_as_float(0x7fc00000u);
-                        o[n][0] = fmaf(fmaf(a[2], 0.0625f, a[0]), sc.y, o[n][0] * alpha) + (z[0] > 0.f ? nan : 0.f);
-                        o[n][1] = fmaf(fmaf(a[3], 0.0625f, a[1]), sc.y, o[n][1] * alpha) + (z[1] > 0.f ? nan : 0.f);
                     }
+                    float a[NT][4];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) a[n][0] = a[n][1] = a[n][2] = a[n][3] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < RUN / 4; ++i) {
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_to_half2(w[0][i], a0, a2);
+                        e4m3x4_to_half2(w[1][i], a1, a3);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) att_mma(a[n], a0, a1, a2, a3, pb[n][i][0], pb[n][i][1]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[n][d][k] = fmaf(a[n][k], sc.y, o[n][d][k] * alpha[n][k % 2]);
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.empty[st]);
+            if (lane == 0) {
+                if (!there) mbar_arrive(&s.empty_k[st]);
+                mbar_arrive(&s.empty_v[st]);
+            }
         }
-        l += __shfl_xor_sync(FULL, l, 1);
-        l += __shfl_xor_sync(FULL, l, 2);
+        before += g.n;
         // merge the NG warps of each tile
-        float *mo = s.merge + (warp * 8 + g8) * (D + 8);
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) *reinterpret_cast<float2 *>(mo + 8 * n + 2 * t) = make_float2(o[n][0], o[n][1]);
-        if (t == 0) *reinterpret_cast<float2 *>(s.ml + (warp * 8 + g8) * 2) = make_float2(m, l);
+        for (int n = 0; n < NT; ++n) {
+            float *mo = s.merge + ((warp * NT + n) * 8 + 2 * t) * LD + g8;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[n][e];
+                sum += __shfl_xor_sync(FULL, sum, 4);
+                sum += __shfl_xor_sync(FULL, sum, 8);
+                sum += __shfl_xor_sync(FULL, sum, 16);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    mo[e * LD + 16 * d] = o[n][d][e];
+                    mo[e * LD + 16 * d + 8] = o[n][d][2 + e];
+                }
+                if (g8 == 0) *reinterpret_cast<float2 *>(s.ml + ((warp * NT + n) * 8 + 2 * t + e) * 2) = make_float2(m[n][e], sum);
+            }
+        }
         att_consumer_bar();
         for (int i = threadIdx.x; i < RT * (D / 4); i += ATT_WARPS * 32) {
             const int row = i / (D / 4), d4 = i % (D / 4);
+            // row of the tile -> (warp side by side, row of the warp); group k is WT warps further
+            const auto at = [&](int k) { return (k * WT + row / (8 * NT)) * 8 * NT + row % (8 * NT); };
             float big = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < NG; ++k) big = fmaxf(big, s.ml[((k * MT + row / 8) * 8 + row % 8) * 2]);
+            for (int k = 0; k < NG; ++k) big = fmaxf(big, s.ml[at(k) * 2]);
             const float mu = big == -INFINITY ? 0.f : big;
             float sum = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < NG; ++k) {
-                const int w = (k * MT + row / 8) * 8 + row % 8;
-                const float a = exp2_fast(s.ml[w * 2] - mu);
-                const float4 x = *reinterpret_cast<const float4 *>(s.merge + w * (D + 8) + 4 * d4);
-                sum = fmaf(a, s.ml[w * 2 + 1], sum);
+                const float a = exp2_fast(s.ml[at(k) * 2] - mu);
+                const float4 x = *reinterpret_cast<const float4 *>(s.merge + at(k) * LD + 4 * d4);
+                sum = fmaf(a, s.ml[at(k) * 2 + 1], sum);
                 acc.x = fmaf(a, x.x, acc.x);
                 acc.y = fmaf(a, x.y, acc.y);
                 acc.z = fmaf(a, x.z, acc.z);
@@ -509,8 +658,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                 *reinterpret_cast<uint2 *>(p.out + token * p.os_t + (int64_t)hd * p.os_h + 4 * d4) =
                     make_uint2(bf16_pair(acc.x * inv, acc.y * inv), bf16_pair(acc.z * inv, acc.w * inv));
                 if (p.lse && d4 == 0)
-                    p.lse[token * (p.group * p.c.hkv) + hd] =
-                        sum == 0.f ? -INFINITY : (big - 8.f + log2f(sum)) * 0.6931471805599453f;
+                    p.lse[token * (p.group * p.c.hkv) + hd] = att_lse(big, sum);
             } else {
                 const size_t slot = ((size_t)blockIdx.x * 2 + (g.first ? 0 : 1)) * RT + row;
                 *reinterpret_cast<float4 *>(p.part_o + slot * D + 4 * d4) = acc;
@@ -521,24 +669,28 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
     }
 }
 
-template <int D, int P, int MT>
+template <int D, int P, int RT>
 __global__ void __launch_bounds__(ATT_THREADS, 1) cache_attend_kernel(const AttParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
-    const AttShared s = att_shared<D>(p);
+    const AttShared s = att_shared<D, att_nt(RT)>(p);
     const int tid = threadIdx.x;
-    constexpr int RT = 8 * MT;
     for (int b = tid; b < p.batch; b += ATT_THREADS) {
         const AttSeq q = att_seq<P>(p, b, blockIdx.x == 0);
         s.prefix[b + 1] = (long long)((q.cnt * p.group + RT - 1) / RT) * (q.hi - q.lo) * p.c.hkv;
+        s.seq[b] = make_int4(q.q0, q.cnt, q.len, q.lo);
+    }
+    if (tid >= ATT_THREADS - 32 && tid - (ATT_THREADS - 32) < p.ring) {
+        const int i = tid - (ATT_THREADS - 32);
+        s.has_k[i] = s.has_v[i] = -1;
+        mbar_init(&s.full_k[i], 2);
+        mbar_init(&s.full_v[i], 1);
+        mbar_init(&s.empty_k[i], RT / (8 * att_nt(RT)));
+        mbar_init(&s.empty_v[i], RT / (8 * att_nt(RT)));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0) {
         s.prefix[0] = 0;
         s.ctrl[0] = 0;
-        for (int i = 0; i < p.stages; ++i) {
-            mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], MT);
-        }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
     if (tid < 32) {  // running sums, 32 sequences at a time
@@ -559,8 +711,8 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) cache_attend_kernel(const AttP
     __syncthreads();
     if (blockIdx.x == 0)
         for (int b = tid; b <= p.batch; b += ATT_THREADS) p.prefix[b] = s.prefix[b];
-    if (tid >= ATT_WARPS * 32) att_produce<D, P, MT>(p, s);
-    else att_consume<D, P, MT>(p, s);
+    if (tid >= ATT_WARPS * 32) att_produce<D, P, RT>(p, s);
+    else att_consume<D, P, RT>(p, s);
 }
 
 // One warp per query row: rows that see nothing get zeros, rows whose pages
@@ -616,8 +768,7 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p, int
     uint16_t *dst = p.out + (int64_t)token * p.os_t + (int64_t)head * p.os_h + lane * V;
 #pragma unroll
     for (int i = 0; i < V; i += 2) *reinterpret_cast<uint32_t *>(dst + i) = bf16_pair(acc[i] * inv, acc[i + 1] * inv);
-    if (p.lse && lane == 0)
-        p.lse[w] = sum == 0.f ? -INFINITY : (big - 8.f + log2f(sum)) * 0.6931471805599453f;
+    if (p.lse && lane == 0) p.lse[w] = att_lse(big, sum);
 }
 
 struct AttPlan {
@@ -656,8 +807,8 @@ static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, AttPlan &pl
 using AttFn = void (*)(const AttParams);
 template <int D, int P>
 static AttFn att_kernel(int rt) {
-    return rt == 8 ? cache_attend_kernel<D, P, 1> : rt == 16 ? cache_attend_kernel<D, P, 2>
-         : rt == 32 ? cache_attend_kernel<D, P, 4> : cache_attend_kernel<D, P, 8>;
+    return rt == 8 ? cache_attend_kernel<D, P, 8> : rt == 16 ? cache_attend_kernel<D, P, 16>
+         : rt == 32 ? cache_attend_kernel<D, P, 32> : cache_attend_kernel<D, P, 64>;
 }
 
 }  // namespace mk
@@ -719,10 +870,10 @@ int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc 
     p.prefix = reinterpret_cast<long long *>(ws);
     p.part_ml = reinterpret_cast<float *>(ws + pl.prefix_bytes);
     p.part_o = reinterpret_cast<float *>(ws + pl.prefix_bytes + pl.ml_bytes);
-    const int fixed = (D == 64 ? att_fixed_bytes<64>() : att_fixed_bytes<128>()) + (p.batch + 1) * 8 + 128;
+    const int fixed = att_fixed_bytes(D, att_nt(pl.rt)) + att_seq_bytes(p.batch) + 128;
     constexpr int kSmem = 227 * 1024;
-    p.stages = std::min(ATT_MAXSTAGES, (kSmem - fixed) / (2 * P * D));
-    const int smem = fixed + p.stages * 2 * P * D;
+    p.ring = std::min(ATT_MAXRING, (kSmem - fixed) / (2 * P * D));
+    const int smem = fixed + p.ring * 2 * P * D;
     AttFn f = D == 64 ? (P == 32 ? att_kernel<64, 32>(pl.rt) : att_kernel<64, 64>(pl.rt))
                       : (P == 32 ? att_kernel<128, 32>(pl.rt) : att_kernel<128, 64>(pl.rt));
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);

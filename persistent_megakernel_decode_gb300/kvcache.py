@@ -40,6 +40,7 @@ class Kv8Cache:
         self.layers, self.pages, self.kv_heads, self.page_tokens, self.head_dim = L, N, H, P, D
         self.device = k.device
         self.status = torch.zeros(4, dtype=torch.int32, device=k.device)
+        self.num_sms = 0  # SMs that attend plans for; 0: all of the device
         self._desc = rt.CacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   self.status.data_ptr(), L, N, H, P, D)
         self._lib = rt.load()
@@ -139,7 +140,7 @@ class Kv8Cache:
         a.out_stride[0], a.out_stride[1] = out.stride(-3), out.stride(-2)
         a.table, a.lens, a.q_start = table.data_ptr(), lens.data_ptr(), q_start.data_ptr() if packed else 0
         a.batch, a.table_width, a.q_heads, a.tokens, a.max_tokens = b, table.shape[1], hq, total, most
-        a.window, a.scale = window, 1.0 / math.sqrt(D) if scale is None else scale
+        a.window, a.scale, a.num_sms = window, 1.0 / math.sqrt(D) if scale is None else scale, self.num_sms
         ctx, st = rt.on_device(q, stream)
         with ctx:
             need = self._workspace(a)
@@ -164,6 +165,7 @@ class Kv8Cache:
         """Bytes of workspace :meth:`attend` needs for up to ``batch`` sequences of up to ``max_tokens`` queries."""
         a = rt.AttendDesc()
         a.batch, a.q_heads, a.tokens, a.max_tokens, a.table_width = batch, q_heads, batch * max_tokens, max_tokens, 1
+        a.num_sms = self.num_sms
         with torch.cuda.device(self.device):
             return self._workspace(a)
 
