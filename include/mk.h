@@ -629,7 +629,7 @@ void mk_pages_free(mk_pages_t pages);
 typedef struct {
     uint64_t logits;              /* device, [batch, vocab], row stride below */
     int64_t row_stride;           /* elements, >= vocab */
-    int batch, vocab;             /* vocab at most 688128 */
+    int batch, vocab;             /* vocab at most 622592 */
     int bf16;                     /* 1: bf16 logits, 0: fp32 */
     uint64_t u;                   /* device fp32 [batch], uniform in [0, 1) (held to that range) */
     uint64_t tokens;              /* device int32 [batch]: out */

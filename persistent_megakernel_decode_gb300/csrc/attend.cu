@@ -871,16 +871,16 @@ int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc 
     p.part_ml = reinterpret_cast<float *>(ws + pl.prefix_bytes);
     p.part_o = reinterpret_cast<float *>(ws + pl.prefix_bytes + pl.ml_bytes);
     const int fixed = att_fixed_bytes(D, att_nt(pl.rt)) + att_seq_bytes(p.batch) + 128;
-    constexpr int kSmem = 227 * 1024;
-    p.ring = std::min(ATT_MAXRING, (kSmem - fixed) / (2 * P * D));
+    p.ring = std::min(ATT_MAXRING, (SERVE_SMEM - fixed) / (2 * P * D));
     const int smem = fixed + p.ring * 2 * P * D;
     AttFn f = D == 64 ? (P == 32 ? att_kernel<64, 32>(pl.rt) : att_kernel<64, 64>(pl.rt))
                       : (P == 32 ? att_kernel<128, 32>(pl.rt) : att_kernel<128, 64>(pl.rt));
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return serve_cuda_fail(e, "cudaFuncSetAttribute");
+    static std::atomic<uint32_t> ready[SERVE_MAX_DEVICES];
+    const int variant = (D == 128 ? 8 : 0) + (P == 64 ? 4 : 0) + (pl.rt == 8 ? 0 : pl.rt == 16 ? 1 : pl.rt == 32 ? 2 : 3);
+    if (int rc = serve_prepare(reinterpret_cast<const void *>(f), ready, variant, false)) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     f<<<pl.ctas, ATT_THREADS, smem, st>>>(p);
-    e = cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return serve_cuda_fail(e, "attention launch");
     cudaLaunchAttribute dep{};
     dep.id = cudaLaunchAttributeProgrammaticStreamSerialization;

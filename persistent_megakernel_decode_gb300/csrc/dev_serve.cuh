@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "dev_common.cuh"
@@ -15,7 +16,21 @@ inline int serve_cuda_fail(cudaError_t e, const char *what) {
     return set_error(MK_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
-constexpr int CACHE_MAX_DIM = 128;
+// Function attributes are set once per device and kernel: `ready` has a bit
+// per kernel for each device (setting them twice at once does no harm).
+constexpr int SERVE_MAX_DEVICES = 64, SERVE_SMEM = 227 * 1024;
+inline int serve_prepare(const void *f, std::atomic<uint32_t> (&ready)[SERVE_MAX_DEVICES], int bit, bool large_clusters) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return serve_cuda_fail(e, "cudaGetDevice");
+    if (dev < 0 || dev >= SERVE_MAX_DEVICES) return set_error(MK_ERR_INVALID, "device ordinal out of range");
+    if (ready[dev].load(std::memory_order_acquire) >> bit & 1u) return MK_OK;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SERVE_SMEM);
+    if (e == cudaSuccess && large_clusters) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return serve_cuda_fail(e, "cudaFuncSetAttribute");
+    ready[dev].fetch_or(1u << bit, std::memory_order_release);
+    return MK_OK;
+}
 
 // The cache's arrays with typed pointers, by value in kernel parameters.
 struct CacheView {

@@ -17,6 +17,11 @@
 // vocabulary asks for (fp32 sums would move a boundary by more than a token's
 // probability).
 //
+// Short cut.  Where the candidates up to the bin that holds the cut are at most
+// 1024 (any usual top-k; top-p of a peaked distribution), they are gathered in
+// one CTA, which does the rest alone: every filter keeps a prefix of the order,
+// so ranks and running weights among the candidates decide all three.
+//
 // Work split.  One cluster of CTAs per row (up to 16: a row of 0.5 MB is
 // spread over 16 SMs), each CTA keeping its share of the row in shared
 // memory; histograms are joined through distributed shared memory.  What
@@ -33,9 +38,10 @@ namespace mk {
 
 constexpr int SMP_THREADS = 512, SMP_WARPS = SMP_THREADS / 32;
 constexpr int SMP_BINS = 2048, SMP_SUB = 64;     // first-level bins; bins per octave of weight
+constexpr int SMP_COARSE = 64, SMP_FINE = SMP_BINS / SMP_COARSE;  // first-level bins are searched in two steps
 constexpr int SMP_CAP = 1024;                    // candidates ranked directly
 constexpr int SMP_MAXCTAS = 16;
-constexpr int SMP_CHUNK = 43008;                 // logits per CTA at most (168 KB)
+constexpr int SMP_CHUNK = 38912;                 // logits per CTA at most (152 KB)
 constexpr int SMP_ROW = 128;                     // logits per warp pass
 constexpr uint64_t KEY_NONE = ~0ull;
 
@@ -52,11 +58,6 @@ struct SmpParams {
     int top_k;
 };
 
-struct SmpBin {  // sums over a bin or a prefix of bins
-    unsigned long long w;
-    uint32_t n;
-};
-
 struct alignas(16) SmpShared {  // the logits behind it are read 16 bytes at a time
     uint32_t table[32];                             // 2^31 2^(-i/32)
     unsigned long long best[SMP_MAXCTAS];           // every CTA's largest (ordered logit, index)
@@ -64,13 +65,15 @@ struct alignas(16) SmpShared {  // the logits behind it are read 16 bytes at a t
     uint32_t slice_n[SMP_MAXCTAS];
     unsigned long long lo[SMP_MAXCTAS], hi[SMP_MAXCTAS];  // every CTA's least and largest key in the bin
     unsigned long long kept[SMP_MAXCTAS];           // every CTA's kept weight
-    unsigned long long before_w, bin_w;             // the bin found: weight before it and in it
+    unsigned long long before_w, need, total;       // the bin found: weight before it; what was looked for
     uint32_t before_n, bin_n;
     int bin;
     unsigned long long cut, cut_w;                  // the cut found and the weight up to it
     uint32_t cands;
     unsigned long long red[SMP_WARPS];
     uint32_t red_n[SMP_WARPS];
+    unsigned long long coarse_w[SMP_MAXCTAS][SMP_COARSE], fine_w[SMP_MAXCTAS][SMP_FINE];  // every CTA's
+    uint32_t coarse_n[SMP_MAXCTAS][SMP_COARSE], fine_n[SMP_MAXCTAS][SMP_FINE];
     uint32_t hist[4][SMP_BINS];                     // count; weight in 16-bit pieces
     unsigned long long ckey[SMP_CAP], cw[SMP_CAP];  // candidates (in CTA 0)
 };
@@ -114,6 +117,8 @@ struct Weigher {
     }
 };
 
+// log(w / total) through the rest: exact near 0, where the rest is small.
+DEV float log_share(unsigned long long w, unsigned long long total) { return (float)-log1p((double)(total - w) / (double)w); }
 DEV unsigned long long warp_sum64(unsigned long long v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
@@ -328,8 +333,233 @@ struct Sampler {
         return s.cut;
     }
 
+    // First-level histogram of every logit above -inf, joined over the cluster.
+    // Finds the bin in which the running count (by_weight: weight) reaches its
+    // target: `need` of the count, or the fraction `share` of the weight.
+    // s.bin (-1: there are fewer than `need`), s.before_n / before_w, s.bin_n,
+    // and the total weight are the same in every CTA afterwards.
+    DEV void first_bin(bool by_weight, uint32_t need_n, float share, unsigned long long &need, unsigned long long &total) {
+        const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+        for (int i = tid; i < (by_weight ? 4 : 1) * SMP_BINS; i += SMP_THREADS) s.hist[0][i] = 0;
+        if (tid == 0) s.cands = 0;  // before any CTA's gather: a cluster barrier comes first
+        __syncthreads();
+        for (int i = tid * 4; i < n; i += SMP_THREADS * 4) {
+            const float4 v = four(i);
+            const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (e[j] == -INFINITY) continue;
+                const int bin = bin_of(e[j]);
+                atomicAdd(&s.hist[0][bin], 1u);
+                if (by_weight) {
+                    const unsigned long long ww = w(e[j]);
+                    atomicAdd(&s.hist[1][bin], (uint32_t)ww & 0xffffu);
+                    atomicAdd(&s.hist[2][bin], (uint32_t)(ww >> 16) & 0xffffu);
+                    atomicAdd(&s.hist[3][bin], (uint32_t)(ww >> 32));
+                }
+            }
+        }
+        __syncthreads();
+        {   // coarse sums to every CTA: 8 threads a coarse bin
+            constexpr int T = SMP_THREADS / SMP_COARSE, M = SMP_FINE / T;
+            const int c = tid / T;
+            uint32_t cn = 0;
+            unsigned long long cw = 0;
+#pragma unroll
+            for (int k = 0; k < M; ++k) {
+                const int i = c * SMP_FINE + tid % T * M + k;
+                cn += s.hist[0][i];
+                if (by_weight) cw += hist_weight(&s.hist[0][i]);
+            }
+#pragma unroll
+            for (int o = 1; o < T; o <<= 1) {
+                cn += __shfl_xor_sync(FULL, cn, o);
+                cw += __shfl_xor_sync(FULL, cw, o);
+            }
+            for (int r = tid % T; r < ctas; r += T) {
+                SmpShared *q = cl.map_shared_rank(&s, r);
+                q->coarse_n[rank][c] = cn;
+                q->coarse_w[rank][c] = cw;
+            }
+        }
+        cl.sync();
+        if (warp == 0) {  // lane: coarse bins 2 lane, 2 lane + 1
+            uint32_t cn[2] = {0, 0};
+            unsigned long long cw[2] = {0, 0};
+            for (int r = 0; r < ctas; ++r)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    cn[k] += s.coarse_n[r][2 * lane + k];
+                    cw[k] += s.coarse_w[r][2 * lane + k];
+                }
+            uint32_t pn = cn[0] + cn[1];
+            unsigned long long pw = cw[0] + cw[1];
+            running(lane, pn, pw);
+            const unsigned long long all = __shfl_sync(FULL, pw, 31);
+            const double want = ceil((double)fmaxf(share, 0.f) * (double)all);
+            const unsigned long long goal = by_weight ? min(max((unsigned long long)want, 1ull), all) : need_n;
+            if (lane == 0) {
+                s.bin = -1;
+                s.need = goal;
+                s.total = all;
+            }
+            __syncwarp();
+            unsigned long long bw = pw - cw[0] - cw[1];
+            uint32_t bn = pn - cn[0] - cn[1];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (by_weight ? bw < goal && bw + cw[k] >= goal : bn < goal && bn + cn[k] >= goal) {
+                    s.bin = 2 * lane + k;
+                    s.before_w = bw;
+                    s.before_n = bn;
+                }
+                bw += cw[k];
+                bn += cn[k];
+            }
+        }
+        __syncthreads();
+        need = s.need;
+        total = s.total;
+        const int c = s.bin;
+        if (c >= 0) {
+            if (warp < ctas) {
+                const uint32_t *h = cl.map_shared_rank(&s.hist[0][c * SMP_FINE + lane], warp);
+                s.fine_n[warp][lane] = h[0];
+                s.fine_w[warp][lane] = by_weight ? hist_weight(h) : 0;
+            }
+            __syncthreads();
+            if (warp == 0) {
+                uint32_t fn = 0;
+                unsigned long long fw = 0;
+                for (int r = 0; r < ctas; ++r) {
+                    fn += s.fine_n[r][lane];
+                    fw += s.fine_w[r][lane];
+                }
+                uint32_t pn = fn;
+                unsigned long long pw = fw;
+                running(lane, pn, pw);
+                const unsigned long long bw = s.before_w + pw - fw;
+                const uint32_t bn = s.before_n + pn - fn;
+                __syncwarp();
+                if (by_weight ? bw < need && bw + fw >= need : bn < need && bn + fn >= need) {
+                    s.bin = c * SMP_FINE + lane;
+                    s.before_w = bw;
+                    s.before_n = bn;
+                    s.bin_n = fn;
+                }
+            }
+            __syncthreads();
+        }
+    }
+    DEV static unsigned long long hist_weight(const uint32_t *h) {
+        return (unsigned long long)h[SMP_BINS] + ((unsigned long long)h[2 * SMP_BINS] << 16) +
+               ((unsigned long long)h[3 * SMP_BINS] << 32);
+    }
+    // inclusive sums over the warp
+    DEV static void running(int lane, uint32_t &pn, unsigned long long &pw) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t a = __shfl_up_sync(FULL, pn, o);
+            const unsigned long long b = __shfl_up_sync(FULL, pw, o);
+            if (lane >= o) {
+                pn += a;
+                pw += b;
+            }
+        }
+    }
+
+    // Logits of bins lo .. hi into CTA 0's list (ends with a cluster barrier).
+    DEV void gather(int lo, int hi) {
+        SmpShared *lead = cl.map_shared_rank(&s, 0);
+        for (int i = threadIdx.x * 4; i < n; i += SMP_THREADS * 4) {
+            const float4 v = four(i);
+            const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (e[j] == -INFINITY) continue;
+                const int bin = bin_of(e[j]);
+                if (bin < lo || bin > hi) continue;
+                const uint32_t at = atomicAdd(&lead->cands, 1u);
+                lead->ckey[at] = sample_key(e[j], first + i + j);
+                lead->cw[at] = w(e[j]);
+            }
+        }
+        cl.sync();
+    }
+
+    // Calls f(i, count, weight) for every candidate i: how many others `before(j,
+    // i)` holds for, and their weight.  512 threads share the n^2 comparisons.
+    template <class B, class F>
+    DEV void each_before(int count, B before, F f) const {
+        int per = SMP_THREADS;  // candidates a round: a power of two, 32 threads each at most
+        while (per > SMP_THREADS / 32 && per / 2 >= count) per /= 2;
+        const int g = SMP_THREADS / per;
+        for (int i0 = 0; i0 < count; i0 += per) {
+            const int i = i0 + (int)threadIdx.x / g;
+            uint32_t c = 0;
+            unsigned long long sum = 0;
+            if (i < count)
+                for (int j = threadIdx.x % g; j < count; j += g)
+                    if (before(j, i)) {
+                        ++c;
+                        sum += s.cw[j];
+                    }
+            for (int o = 1; o < g; o <<= 1) {
+                c += __shfl_xor_sync(FULL, c, o);
+                sum += __shfl_xor_sync(FULL, sum, o);
+            }
+            if (i < count && threadIdx.x % g == 0) f(i, c, sum);
+        }
+        __syncthreads();
+    }
+
     DEV int bin_of(float v) const { return (int)fminf((float)(SMP_BINS - 1), w.octaves(v) * (float)SMP_SUB); }
 };
+
+// The rest of a row among the candidates of CTA 0's list, which hold every
+// logit up to the cuts: top_k of them (or all), then top-p (`need` of the
+// weight if it is known, else top_p of the top_k's), then those >= least.
+static __device__ __noinline__ void finish_few(const Sampler &k, int count, int top_k, float top_p, unsigned long long need,
+                                               float least, float u, int *token, float *logprob) {
+    SmpShared &s = k.s;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    // rank and weight before each candidate, over the histogram (done with)
+    unsigned long long *cb = reinterpret_cast<unsigned long long *>(s.hist[2]);
+    static_assert(SMP_CAP * 8 <= 2 * sizeof s.hist[0] && SMP_CAP <= SMP_BINS, "fits");
+    k.each_before(count, [&](int j, int i) { return s.ckey[j] < s.ckey[i]; },
+                  [&](int i, uint32_t c, unsigned long long sum) {
+                      cb[i] = sum;
+                      s.hist[0][i] = c;  // the rank
+                      if ((int)c == top_k - 1) s.cut_w = sum + s.cw[i];
+                  });
+    if (need == 0) {
+        need = s.cut_w;
+        if (top_p < 1.f)
+            need = min(max((unsigned long long)ceil((double)fmaxf(top_p, 0.f) * (double)s.cut_w), 1ull), s.cut_w);
+    }
+    // what is kept, by weight: the others' becomes 0
+    unsigned long long sum = 0;
+    for (int i = tid; i < count; i += SMP_THREADS) {
+        const uint32_t ob = ~(uint32_t)(s.ckey[i] >> 32);
+        const float z = __uint_as_float(ob & 0x80000000u ? ob & 0x7fffffffu : ~ob);
+        if ((int)s.hist[0][i] >= top_k || cb[i] >= need || z < least) s.cw[i] = 0;
+        sum += s.cw[i];
+    }
+    sum = warp_sum64(sum);
+    __syncthreads();
+    if (lane == 0) s.red[warp] = sum;
+    __syncthreads();
+    unsigned long long total = 0;
+    for (int i = 0; i < SMP_WARPS; ++i) total += s.red[i];
+    const unsigned long long target = min((unsigned long long)((double)u * (double)total), total - 1);
+    k.each_before(count, [&](int j, int i) { return (uint32_t)s.ckey[j] < (uint32_t)s.ckey[i]; },  // by index
+                  [&](int i, uint32_t, unsigned long long before) {
+                      if (before <= target && target < before + s.cw[i]) {
+                          *token = (int)(uint32_t)s.ckey[i];
+                          if (logprob) *logprob = log_share(s.cw[i], total);
+                      }
+                  });
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) {
@@ -402,41 +632,63 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
             p.tokens[row] = top == -INFINITY ? 0 : arg;
             if (p.logprob) p.logprob[row] = top == -INFINITY ? -INFINITY : 0.f;
         }
-        cl.sync();
         return;
     }
     const double c = 1.4426950408889634 / (double)temp;
     const float ch = (float)c;
     Sampler k{p, s, x, rows, cl, rank, ctas, first, n, {top, ch, ch < INFINITY ? (float)(c - (double)ch) : 0.f, s.table}};
 
+    const float u = fminf(fmaxf(p.u[row], 0.f), 0x1.fffffep-1f);
+    float least = -INFINITY;
+    if (min_p > 0.f) {
+        // w >= min_p  <=>  z >= max + temperature ln(min_p): the least fp32 number that is
+        least = min_p >= 1.f ? top : __double2float_ru((double)top + (double)temp * log((double)min_p));
+    }
     unsigned long long cut = sample_key(-3.402823466e38f, 0x7fffffff), cut_w = 0;  // every finite logit
-    bool have_w = false;
-    if (top_k > 0 && top_k < p.vocab) {
-        // no cut if fewer than top_k logits are above -inf
-        uint32_t live = 0;
-        for (int i = tid * 4; i < n; i += SMP_THREADS * 4) {
-            const float4 v = k.four(i);
-            live += (v.x > -INFINITY) + (v.y > -INFINITY) + (v.z > -INFINITY) + (v.w > -INFINITY);
+    bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.f;
+    if (by_k || by_p) {
+        unsigned long long need, all;
+        k.first_bin(!by_k, top_k, top_p, need, all);
+        if (by_k && s.bin < 0) {  // fewer than top_k logits above -inf: no cut there
+            by_k = false;
+            cl.sync();  // the bins were read
+            if (by_p) k.first_bin(true, 0, top_p, need, all);
         }
-        live = __reduce_add_sync(FULL, live);
-        if (lane == 0) s.red_n[warp] = live;
-        __syncthreads();
-        if (tid < ctas) {
-            uint32_t sum = 0;
-            for (int i = 0; i < SMP_WARPS; ++i) sum += s.red_n[i];
-            *cl.map_shared_rank(&s.slice_n[rank], tid) = sum;
+        const int bin = s.bin;
+        const uint32_t upto = s.before_n + s.bin_n;
+        if ((by_k || by_p) && upto <= SMP_CAP) {
+            k.gather(0, bin);
+            if (rank != 0) return;
+            finish_few(k, upto, by_k ? top_k : (int)upto, by_p ? top_p : 1.f, by_p && !by_k ? need : 0, least, u,
+                       p.tokens + row, p.logprob ? p.logprob + row : nullptr);
+            return;
         }
-        cl.sync();
-        live = 0;
-        for (int r = 0; r < ctas; ++r) live += s.slice_n[r];
-        cl.sync();
-        if (live > (uint32_t)top_k) {
+        if (by_k) {
+            cl.sync();  // the bins were read
             cut = k.find(false, top_k, cut, cut_w);
-            have_w = true;
+            if (by_p) {
+                const double want = ceil((double)fmaxf(top_p, 0.f) * (double)cut_w);
+                need = min(max((unsigned long long)want, 1ull), cut_w);
+                cut = k.find(true, need, cut, cut_w);
+            }
+        } else if (by_p && s.bin_n <= SMP_CAP) {
+            const uint32_t count = s.bin_n;
+            const unsigned long long before = s.before_w;
+            k.gather(bin, bin);
+            if (rank == 0)
+                k.each_before((int)count, [&](int j, int i) { return s.ckey[j] < s.ckey[i]; },
+                              [&](int i, uint32_t, unsigned long long sum) {
+                                  if (before + sum < need && before + sum + s.cw[i] >= need)
+                                      for (int r = 0; r < ctas; ++r) cl.map_shared_rank(&s, r)->cut = s.ckey[i];
+                              });
+            cl.sync();
+            cut = s.cut;
+        } else if (by_p) {
+            cl.sync();  // the bins were read
+            cut = k.find(true, need, cut, cut_w);
         }
     }
     // weight of what a pass keeps: per 128 logits (rows), per CTA, per cluster
-    float least = -INFINITY;
     const auto keeps = [&](float v, int i) { return v >= least && sample_key(v, first + i) <= cut; };
     const auto kept_weight = [&]() {
         for (int r = warp; r < n / SMP_ROW; r += SMP_WARPS) {
@@ -466,23 +718,7 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
         for (int r = 0; r < ctas; ++r) all += s.kept[r];
         return all;
     };
-    if (top_p < 1.f) {
-        if (!have_w) {
-            cut_w = kept_weight();
-            cl.sync();
-        }
-        const double want = ceil((double)fmaxf(top_p, 0.f) * (double)cut_w);
-        const unsigned long long need = min(max((unsigned long long)want, 1ull), cut_w);
-        cut = k.find(true, need, cut, cut_w);
-    }
-    if (min_p > 0.f) {
-        // w >= min_p  <=>  z >= max + temperature ln(min_p): the least fp32 number that is
-        const double edge = (double)top + (double)temp * log((double)min_p);
-        least = __double2float_ru(edge);
-        if (min_p >= 1.f) least = top;
-    }
     const unsigned long long total = kept_weight();
-    const float u = fminf(fmaxf(p.u[row], 0.f), 0x1.fffffep-1f);
     const unsigned long long target = min((unsigned long long)((double)u * (double)total), total - 1);
     unsigned long long before = 0;
     for (int r = 0; r < rank; ++r) before += s.kept[r];
@@ -526,14 +762,12 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
             for (int j = 0; j < 4; ++j) {
                 if (before <= target && target < before + ww[j]) {
                     p.tokens[row] = first + i + j;
-                    // log(w / total) through the rest: exact near 0, where the rest is small
-                    if (p.logprob) p.logprob[row] = (float)-log1p((double)(total - ww[j]) / (double)ww[j]);
+                    if (p.logprob) p.logprob[row] = log_share(ww[j], total);
                 }
                 before += ww[j];
             }
         }
     }
-    cl.sync();
 }
 
 }  // namespace mk
@@ -544,7 +778,7 @@ extern "C" int mk_sample(const mk_sample_desc *d, void *stream) {
     if (!d) return set_error(MK_ERR_INVALID, "null descriptor");
     if (d->batch < 0 || d->vocab <= 0 || (d->batch > 1 && d->row_stride < d->vocab))
         return set_error(MK_ERR_INVALID, "batch negative, vocab not positive, or rows overlap");
-    if (d->vocab > SMP_MAXCTAS * SMP_CHUNK) return set_error(MK_ERR_UNSUPPORTED, "vocab above 688128");
+    if (d->vocab > SMP_MAXCTAS * SMP_CHUNK) return set_error(MK_ERR_UNSUPPORTED, "vocab above 622592");
     if (d->batch == 0) return MK_OK;
     if (!d->logits || !d->u || !d->tokens) return set_error(MK_ERR_INVALID, "null argument");
     if (d->logits % (d->bf16 ? 2 : 4) || (d->u | d->tokens | d->logprob) % 4)
@@ -573,9 +807,9 @@ extern "C" int mk_sample(const mk_sample_desc *d, void *stream) {
     p.min_p = d->min_p;
     const int smem = (int)sizeof(SmpShared) + p.chunk * 4 + p.chunk / SMP_ROW * 8;
     void (*f)(const SmpParams) = d->bf16 ? sample_kernel<true> : sample_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return serve_cuda_fail(e, "cudaFuncSetAttribute");
+    static std::atomic<uint32_t> ready[SERVE_MAX_DEVICES];
+    if (int rc = serve_prepare(reinterpret_cast<const void *>(f), ready, d->bf16 ? 1 : 0, true)) return rc;
+    cudaError_t e;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = ctas;

@@ -8,7 +8,7 @@ masks, what a failed check does); this module checks arguments and marshals them
 from __future__ import annotations
 
 import ctypes as C
-import math
+from array import array
 from typing import List, Optional, Sequence, Tuple
 
 import numpy as np
@@ -27,11 +27,13 @@ class Kv8Cache:
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         if not k.is_cuda:
             raise ValueError("the cache must be CUDA tensors")
-        rt.check_tensor("k", k, k.device, _CODES, (None,) * 5)
+        if k.dim() != 5 or k.dtype not in _CODES:
+            raise ValueError(f"k must be e4m3 codes [L, N, Hkv, P, D], got {k.dtype} {tuple(k.shape)}")
         L, N, H, P, D = k.shape
-        rt.check_tensor("v", v, k.device, _CODES, (L, N, H, D, P))
+        self.index = k.get_device()
+        rt.check_tensor("v", v, self.index, k.dtype, (L, N, H, D, P))
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            rt.check_tensor(name, t, k.device, (torch.float32,), (L, N, H))
+            rt.check_tensor(name, t, self.index, torch.float32, (L, N, H))
         if not all(t.is_contiguous() for t in (k, v, k_scale, v_scale)):
             raise ValueError("the cache's tensors must be contiguous")
         if P not in (32, 64) or D not in (64, 128):
@@ -43,7 +45,9 @@ class Kv8Cache:
         self.num_sms = 0  # SMs that attend plans for; 0: all of the device
         self._desc = rt.CacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   self.status.data_ptr(), L, N, H, P, D)
+        self._ref = C.byref(self._desc)  # never changed after this
         self._lib = rt.load()
+        self._sizes = {}  # workspace bytes by (batch, q heads, tokens, most tokens of a sequence, num_sms)
 
     @classmethod
     def empty(cls, layers: int, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
@@ -54,31 +58,42 @@ class Kv8Cache:
         return cls(codes(page_tokens, head_dim).view(torch.float8_e4m3fn),
                    codes(head_dim, page_tokens).view(torch.float8_e4m3fn), scale(), scale())
 
+    def _ints(self, b, **tensors):
+        """int32 [b] device arrays, contiguous."""
+        for name, t in tensors.items():
+            if t is not None and (t.dtype is not torch.int32 or t.get_device() != self.index or t.shape != (b,)
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous int32 [{b}] tensor on cuda:{self.index}, got {t.dtype} "
+                                 f"{tuple(t.shape)} on {t.device}")
+
+    def _table(self, table, b):
+        if (table.dtype is not torch.int32 or table.get_device() != self.index or table.dim() != 2
+                or table.shape[0] != b or not table.is_contiguous()):
+            raise ValueError(f"table must be a contiguous int32 [{b}, width] tensor on cuda:{self.index}, got "
+                             f"{table.dtype} {tuple(table.shape)} on {table.device}")
+        return table.shape[1]
+
     # ---- moving tokens ----
     def _move(self, call, k, v, table, start, count, row0, max_count, stream, writes):
-        dev, i32 = self.device, (torch.int32,)
+        shape = k.shape
+        if len(shape) != 5 or shape[0] != self.layers or shape[3] != self.kv_heads or shape[4] != self.head_dim:
+            raise ValueError(f"k has shape {tuple(shape)}, expected ({self.layers}, B, T, {self.kv_heads}, {self.head_dim})")
+        ks, vs, kp, vp = k.stride(), v.stride(), k.data_ptr(), v.data_ptr()
         for name, t in (("k", k), ("v", v)):
-            rt.check_tensor(name, t, dev, (torch.bfloat16,), (self.layers, None, None, self.kv_heads, self.head_dim))
-            if t.stride(4) != 1 or t.data_ptr() % 16 or any(s % 8 for s in t.stride()[:4]):
-                raise ValueError(f"{name}: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8")
-            if writes and any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)) and row0 is None:
-                raise ValueError(f"{name}: rows that overlap cannot be written")
-        b, rows = k.shape[1], k.shape[2]
-        if tuple(v.shape) != tuple(k.shape):
-            raise ValueError("k and v must have the same shape")
-        rt.check_tensor("table", table, dev, i32, (b, None))
-        for name, t in (("start", start), ("count", count)) + ((("row0", row0),) if row0 is not None else ()):
-            rt.check_tensor(name, t, dev, i32, (b,))
-        if not all(t.is_contiguous() for t in (table, start, count) + ((row0,) if row0 is not None else ())):
-            raise ValueError("table, start, count and row0 must be contiguous")
+            rt.check_tensor(name, t, self.index, torch.bfloat16, shape)
+        if (ks[4] != 1 or vs[4] != 1 or (kp | vp) % 16
+                or (ks[0] | ks[1] | ks[2] | ks[3] | vs[0] | vs[1] | vs[2] | vs[3]) % 8):
+            raise ValueError("k and v: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8 elements")
+        if writes and any(s[i] == 0 and shape[i] > 1 for s in (ks, vs) for i in ((0, 2, 3) if row0 is not None else (0, 1, 2, 3))):
+            raise ValueError("rows that overlap cannot be written")
+        b, rows = shape[1], shape[2]
+        width = self._table(table, b)
+        self._ints(b, start=start, count=count, row0=row0)
         if b == 0 or rows == 0:
             return
-        r = rt.CacheRows(k.data_ptr(), v.data_ptr(), (C.c_int64 * 4)(*k.stride()[:4]), (C.c_int64 * 4)(*v.stride()[:4]),
-                         rows, row0.data_ptr() if row0 is not None else 0)
-        ctx, st = rt.on_device(k, stream)
-        with ctx:
-            rt._check(call(C.byref(self._desc), C.byref(r), table.data_ptr(), table.shape[1], start.data_ptr(),
-                           count.data_ptr(), b, rows if max_count is None else max_count, st))
+        r = rt.CacheRows(kp, vp, ks[:4], vs[:4], rows, row0.data_ptr() if row0 is not None else 0)
+        rt.launch(self.index, stream, call, self._ref, C.byref(r), table.data_ptr(), width, start.data_ptr(),
+                  count.data_ptr(), b, rows if max_count is None else max_count)
 
     def store(self, k, v, table, start, count, row0=None, max_count: Optional[int] = None, stream=None):
         """Quantise new tokens into the cache, all layers: row ``row0[b] + i`` (default 0 + i) of sequence b in ``k`` and
@@ -88,7 +103,8 @@ class Kv8Cache:
         self._move(self._lib.mk_cache_store, k, v, table, start, count, row0, max_count, stream, False)
 
     def load(self, k, v, table, start, count, row0=None, max_count: Optional[int] = None, stream=None):
-        """The inverse of :meth:`store`: cache positions ``start[b] + i`` into rows ``row0[b] + i``; other rows stay."""
+        """The inverse of :meth:`store`: cache positions ``start[b] + i`` into rows ``row0[b] + i``; other rows stay.
+        (Packed rows as in :meth:`store`: the sequences' rows must not overlap.)"""
         self._move(self._lib.mk_cache_load, k, v, table, start, count, row0, max_count, stream, True)
 
     # ---- attention ----
@@ -100,97 +116,93 @@ class Kv8Cache:
         [total, Hq, D], sequence b's queries being rows q_start[b] .. q_start[b + 1] - 1 (``max_tokens``: the most of
         one sequence, a hint).  ``window`` > 0: a query sees that many last tokens, itself among them.  Returns (out
         bf16 like q, lse fp32 without the last axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8
-        tensor of at least :meth:`attend_workspace` bytes; by default one is allocated per call."""
-        dev, D = self.device, self.head_dim
-        packed = q_start is not None
-        rt.check_tensor("q", q, dev, (torch.bfloat16,), (None,) * (2 if packed else 3) + (D,))
-        hq = q.shape[-2]
+        tensor of at least :meth:`attend_workspace` bytes, used by one call at a time; by default one is allocated per
+        call."""
+        D, packed, shape = self.head_dim, q_start is not None, q.shape
+        if (q.dtype is not torch.bfloat16 or q.get_device() != self.index or len(shape) != (3 if packed else 4)
+                or shape[-1] != D):
+            raise ValueError(f"q must be bf16 {'[total, Hq' if packed else '[B, T, Hq'}, {D}] on cuda:{self.index}, got "
+                             f"{q.dtype} {tuple(shape)} on {q.device}")
+        hq = shape[-2]
         if packed:
             b = q_start.numel() - 1
-            rt.check_tensor("q_start", q_start, dev, (torch.int32,), (max(b, 0) + 1,))
-            total, most = q.shape[0], q.shape[0] if max_tokens is None else max_tokens
+            self._ints(max(b, 0) + 1, q_start=q_start)
+            total, most = shape[0], shape[0] if max_tokens is None else max_tokens
         else:
-            b, most = q.shape[0], q.shape[1]
+            b, most = shape[0], shape[1]
             total = b * most
             if max_tokens is not None and max_tokens != most:
                 raise ValueError("max_tokens is q's second axis without q_start")
-        rt.check_tensor("table", table, dev, (torch.int32,), (b, None))
-        rt.check_tensor("lens", lens, dev, (torch.int32,), (b,))
-        if not (table.is_contiguous() and lens.is_contiguous() and (not packed or q_start.is_contiguous())):
-            raise ValueError("table, lens and q_start must be contiguous")
+        width = self._table(table, b)
+        self._ints(b, lens=lens)
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         else:
-            rt.check_tensor("out", out, dev, (torch.bfloat16,), tuple(q.shape))
+            rt.check_tensor("out", out, self.index, torch.bfloat16, shape)
         if lse is None:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+            lse = torch.empty(shape[:-1], dtype=torch.float32, device=self.device)
         else:
-            rt.check_tensor("lse", lse, dev, (torch.float32,), tuple(q.shape[:-1]))
+            rt.check_tensor("lse", lse, self.index, torch.float32, shape[:-1])
             if not lse.is_contiguous():
                 raise ValueError("lse must be contiguous")
-        a = rt.AttendDesc()
-        for name, t in (("q", q), ("out", out)):
-            s = t.stride()
-            if total and (s[-1] != 1 or t.data_ptr() % 16 or s[-2] % 8 or s[-3] % 8
-                          or (not packed and b > 1 and s[0] != s[1] * most)):
-                raise ValueError(f"{name}: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8 "
-                                 "elements, and sequences evenly spaced rows")
-        a.q, a.out, a.lse = q.data_ptr(), out.data_ptr(), lse.data_ptr()
-        a.q_stride[0], a.q_stride[1] = q.stride(-3), q.stride(-2)
-        a.out_stride[0], a.out_stride[1] = out.stride(-3), out.stride(-2)
-        a.table, a.lens, a.q_start = table.data_ptr(), lens.data_ptr(), q_start.data_ptr() if packed else 0
-        a.batch, a.table_width, a.q_heads, a.tokens, a.max_tokens = b, table.shape[1], hq, total, most
-        a.window, a.scale, a.num_sms = window, 1.0 / math.sqrt(D) if scale is None else scale, self.num_sms
-        ctx, st = rt.on_device(q, stream)
-        with ctx:
-            need = self._workspace(a)
-            own = workspace is None
-            if own:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            else:
-                rt.check_tensor("workspace", workspace, dev, (torch.uint8,), (None,))
-            rt._check(self._lib.mk_cache_attend(C.byref(self._desc), layer, C.byref(a), workspace.data_ptr(),
-                                                workspace.numel(), st))
+        qs, os, qp, op = q.stride(), out.stride(), q.data_ptr(), out.data_ptr()
+        if total and (qs[-1] != 1 or os[-1] != 1 or (qp | op) % 16 or (qs[-2] | qs[-3] | os[-2] | os[-3]) % 8
+                      or (not packed and b > 1 and (qs[0] != qs[1] * most or os[0] != os[1] * most))):
+            raise ValueError("q and out: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8 "
+                             "elements, and sequences evenly spaced rows")
+        a = rt.AttendDesc(qp, op, lse.data_ptr(), qs[-3], qs[-2], os[-3], os[-2], table.data_ptr(), lens.data_ptr(),
+                          q_start.data_ptr() if packed else 0, b, width, hq, total, most, window,
+                          D ** -0.5 if scale is None else scale, self.num_sms)
+        own = workspace is None
+        if own:
+            workspace = torch.empty(self._workspace(a), dtype=torch.uint8, device=self.device)
+        else:
+            rt.check_tensor("workspace", workspace, self.index, torch.uint8)
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+        rt.launch(self.index, stream, self._lib.mk_cache_attend, self._ref, layer, C.byref(a), workspace.data_ptr(),
+                  workspace.numel())
         if stream is not None:
             for t in (out, lse) + ((workspace,) if own else ()):  # made on the current stream, used on `stream`
                 t.record_stream(stream)
         return out, lse
 
     def _workspace(self, a) -> int:
-        n = C.c_uint64()
-        rt._check(self._lib.mk_cache_attend_workspace(C.byref(self._desc), C.byref(a), C.byref(n)))
-        return n.value
+        key = (a.batch, a.q_heads, a.tokens, a.max_tokens, a.num_sms)
+        size = self._sizes.get(key)
+        if size is None:
+            n = C.c_uint64()
+            with torch.cuda.device(self.index):
+                rt._check(self._lib.mk_cache_attend_workspace(self._ref, C.byref(a), C.byref(n)))
+            if len(self._sizes) >= 1024:
+                self._sizes.clear()
+            size = self._sizes[key] = n.value
+        return size
 
     def attend_workspace(self, batch: int, q_heads: int, max_tokens: int = 1) -> int:
         """Bytes of workspace :meth:`attend` needs for up to ``batch`` sequences of up to ``max_tokens`` queries."""
         a = rt.AttendDesc()
         a.batch, a.q_heads, a.tokens, a.max_tokens, a.table_width = batch, q_heads, batch * max_tokens, max_tokens, 1
         a.num_sms = self.num_sms
-        with torch.cuda.device(self.device):
-            return self._workspace(a)
+        return self._workspace(a)
 
     # ---- pages ----
     def copy_pages(self, src: Sequence[int], dst: Sequence[int], table=None, stream=None):
         """Copy pages ``src[i]`` -> ``dst[i]`` in all layers (codes and scales); no dst may repeat or be a src.  With
         ``table`` (a contiguous int32 tensor) its entries that name a src are renamed to the dst."""
-        s, d = np.ascontiguousarray(src, dtype=np.int32), np.ascontiguousarray(dst, dtype=np.int32)
-        if s.ndim != 1 or s.shape != d.shape:
+        s, d = array("i", src), array("i", dst)
+        if len(s) != len(d):
             raise ValueError("src and dst must be lists of the same length")
         if table is not None:
-            rt.check_tensor("table", table, self.device, (torch.int32,))
+            rt.check_tensor("table", table, self.index, torch.int32)
             if not table.is_contiguous():
                 raise ValueError("table must be contiguous")
-        ctx, st = rt.on_device(self.k, stream)
-        with ctx:
-            rt._check(self._lib.mk_cache_copy(C.byref(self._desc), s.ctypes.data, d.ctypes.data, len(s),
-                                              table.data_ptr() if table is not None else None,
-                                              table.numel() if table is not None else 0, st))
+        rt.launch(self.index, stream, self._lib.mk_cache_copy, self._ref, s.buffer_info()[0], d.buffer_info()[0], len(s),
+                  table.data_ptr() if table is not None else None, table.numel() if table is not None else 0)
 
     def check(self, stream=None):
         """Wait for ``stream`` and raise ``MkError`` if a device-side check has failed since the last call."""
-        ctx, st = rt.on_device(self.k, stream)
-        with ctx:
-            rt._check(self._lib.mk_cache_status(C.byref(self._desc), 1, None, st))
+        rt.launch(self.index, stream, self._lib.mk_cache_status, self._ref, 1, None)
 
 
 class PagePool:

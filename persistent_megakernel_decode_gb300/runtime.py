@@ -13,6 +13,7 @@ from dataclasses import dataclass
 from typing import Dict, List, Optional, Sequence
 
 import numpy as np
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmk.so")
@@ -123,8 +124,9 @@ class CacheRows(C.Structure):
 
 
 class AttendDesc(C.Structure):
-    _fields_ = [("q", C.c_uint64), ("out", C.c_uint64), ("lse", C.c_uint64), ("q_stride", C.c_int64 * 2),
-                ("out_stride", C.c_int64 * 2), ("table", C.c_uint64), ("lens", C.c_uint64), ("q_start", C.c_uint64)] + [
+    _fields_ = [(n, C.c_uint64) for n in ("q", "out", "lse")] + [
+        (n, C.c_int64) for n in ("q_token_stride", "q_head_stride", "out_token_stride", "out_head_stride")] + [
+        (n, C.c_uint64) for n in ("table", "lens", "q_start")] + [
         (n, C.c_int) for n in ("batch", "table_width", "q_heads", "tokens", "max_tokens", "window")] + [
         ("scale", C.c_float), ("num_sms", C.c_int)]
 
@@ -211,39 +213,32 @@ def launch_probe(num_workers: int, cooperative: bool, stream) -> None:
     _check(load().mk_launch_probe(int(num_workers), int(cooperative), C.c_void_p(stream.cuda_stream)))
 
 
-def on_device(t, stream=None):
-    """(context that makes ``t``'s device current, stream handle): the launch goes to ``stream``, or to that
-    device's current torch stream."""
-    import torch
-    st = stream if stream is not None else torch.cuda.current_stream(t.device)
-    if st.device != t.device:
-        raise ValueError(f"stream of {st.device}, tensors of {t.device}")
-    return torch.cuda.device(t.device), st.cuda_stream
+def check_tensor(name, t, index: int, dtype, shape=None):
+    """``t`` must lie on CUDA device ``index`` and have the type and the shape."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has type {t.dtype}, expected {dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def check_tensor(name, t, device, dtypes, shape=None):
-    """``t`` must lie on ``device``, have one of ``dtypes`` and the shape (None entries: any extent)."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} has type {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape))):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('*' if w is None else w for w in shape)}")
-
-
-def _row_setting(desc, name, value, batch, device, dtype, off):
-    """One sampling setting: None (off), a number for all rows, or a tensor with one value per row."""
-    import torch
-    if value is None:
-        setattr(desc, name, off)
-        return None
-    if isinstance(value, torch.Tensor):
-        check_tensor(name, value, device, (dtype,), (batch,))
-        value = value.contiguous()
-        setattr(desc, name + "_rows", value.data_ptr())
-        return value  # kept alive until the launch is queued
-    setattr(desc, name, value)
-    return None
+def launch(index: int, stream, call, *args):
+    """``call(*args, stream handle)`` with CUDA device ``index`` current, on ``stream`` (a torch stream of that device) or
+    on the device's current torch stream; raises ``MkError`` on a status."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index != index:
+        raise ValueError(f"a stream of cuda:{stream.device_index} for tensors of cuda:{index}")
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        rc = call(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = call(*args, handle)
+    if rc != MK_OK:
+        raise MkError(rc, load().mk_last_error().decode())
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, stream=None):
@@ -253,37 +248,43 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     int32 for ``top_k``); a temperature of 0 takes the largest logit.  Returns (tokens int32 [B], logprob fp32 [B]: the
     log probability under the filtered distribution); ``tokens``: an int32 [B] tensor to write into.  Asynchronous; may
     be captured into a CUDA graph."""
-    import torch
-    check_tensor("logits", logits, logits.device, (torch.float32, torch.bfloat16), (None, None))
-    if not logits.is_cuda:
+    index = logits.get_device()
+    if index < 0:
         raise ValueError("logits must be a CUDA tensor")
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits must be fp32 or bf16 [B, V], got {logits.dtype} {tuple(logits.shape)}")
     b, v = logits.shape
-    if b and logits.stride(1) != 1:
+    stride, inner = logits.stride()
+    if inner != 1 and v > 1:
         raise ValueError("logits must be contiguous along the vocabulary")
-    check_tensor("u", u, logits.device, (torch.float32,), (b,))
-    d = SampleDesc()
-    d.logits, d.row_stride, d.batch, d.vocab = logits.data_ptr(), max(logits.stride(0), v) if b < 2 else logits.stride(0), b, v
-    d.bf16 = int(logits.dtype == torch.bfloat16)
-    u = u.contiguous()
-    keep = (_row_setting(d, "temperature", temperature, b, logits.device, torch.float32, 1.0),
-            _row_setting(d, "top_k", top_k, b, logits.device, torch.int32, 0),
-            _row_setting(d, "top_p", top_p, b, logits.device, torch.float32, 1.0),
-            _row_setting(d, "min_p", min_p, b, logits.device, torch.float32, 0.0))
+    check_tensor("u", u, index, torch.float32, (b,))
+    values, rows, keep = [], [], [u.contiguous()]
+    for name, x, off, dtype in (("temperature", temperature, 1.0, torch.float32), ("top_k", top_k, 0, torch.int32),
+                                ("top_p", top_p, 1.0, torch.float32), ("min_p", min_p, 0.0, torch.float32)):
+        if isinstance(x, torch.Tensor):
+            check_tensor(name, x, index, dtype, (b,))
+            if not x.is_contiguous():
+                x = x.contiguous()
+            keep.append(x)  # alive until the launch is queued
+            rows.append(x.data_ptr())
+            values.append(off)
+        else:
+            rows.append(0)
+            values.append(off if x is None else x)
     if tokens is None:
         tokens = torch.empty((b,), dtype=torch.int32, device=logits.device)
+        keep.append(tokens)
     else:
-        check_tensor("tokens", tokens, logits.device, (torch.int32,), (b,))
+        check_tensor("tokens", tokens, index, torch.int32, (b,))
         if not tokens.is_contiguous():
             raise ValueError("tokens must be contiguous")
     logprob = torch.empty((b,), dtype=torch.float32, device=logits.device)
-    d.u, d.tokens, d.logprob = u.data_ptr(), tokens.data_ptr(), logprob.data_ptr()
-    dev, st = on_device(logits, stream)
-    with dev:
-        _check(load().mk_sample(C.byref(d), st))
+    d = SampleDesc(logits.data_ptr(), stride if b > 1 else v, b, v, logits.dtype is torch.bfloat16, keep[0].data_ptr(),
+                   tokens.data_ptr(), logprob.data_ptr(), *rows, *values)
+    launch(index, stream, load().mk_sample, C.byref(d))
     if stream is not None:
-        for t in (u, logprob, *keep):  # made on the current stream, used on `stream`
-            if t is not None:
-                t.record_stream(stream)
+        for t in (logprob, *keep):  # made on the current stream, used on `stream`
+            t.record_stream(stream)
     return tokens, logprob
 
 
@@ -389,7 +390,6 @@ class Session:
 
     def __init__(self, shape, weights: Dict[str, object], kcache, vcache, seq_len0: Sequence[int], max_steps: int,
                  capture_hidden: bool = False, stream=None, **target):
-        import torch
         self.torch = torch
         self.shape = shape
         self.B = len(seq_len0)
@@ -471,7 +471,7 @@ class Session:
         """Decode ``num_steps`` steps from ``tokens[first_step]`` on, each next token sampled with the settings of
         :func:`sample` and the uniforms ``u[i]`` (fp32 [num_steps, B]) instead of taken by argmax.  Returns the sampled
         tokens int32 [num_steps, B] (a view of ``tokens``) and their log probabilities; asynchronous."""
-        check_tensor("u", u, self.logits.device, (self.torch.float32,), (num_steps, self.B))
+        check_tensor("u", u, self.logits.get_device(), torch.float32, (num_steps, self.B))
         logs = []
         for i in range(num_steps):
             self.run(first_step + i, 1, host_tokens=True, timeout_ns=timeout_ns)
@@ -517,7 +517,6 @@ class GlmSession:
     OUTPUTS = ("res_out", "qa", "sa", "qkva", "ik", "qb", "sb", "gate", "q", "iq")
 
     def __init__(self, dims, inputs: Dict[str, object], max_steps: int = 1, stream=None, **target):
-        import torch
         self.dims = dims
         dev = inputs["x"].device
         self.plan = Plan.glm(dims, max_steps, **target)
@@ -574,7 +573,6 @@ class GraphSession:
     """Workspace for an explicit-graph plan (counter tasks only)."""
 
     def __init__(self, plan: Plan, device="cuda:0", stream=None):
-        import torch
         self.plan = plan
         info = plan.info()
         self.workspace = torch.zeros(info["workspace_bytes"] + 256, dtype=torch.uint8, device=device)

@@ -38,8 +38,8 @@ def rows(**kw):
 def attend(**kw):
     a = rt.AttendDesc()
     a.q = a.out = a.lse = a.table = a.lens = A
-    a.q_stride[0] = a.out_stride[0] = 1024
-    a.q_stride[1] = a.out_stride[1] = 128
+    a.q_token_stride = a.out_token_stride = 1024
+    a.q_head_stride = a.out_head_stride = 128
     a.batch, a.table_width, a.q_heads, a.tokens, a.max_tokens, a.scale, a.num_sms = 3, 8, 8, 3, 1, 0.1, 152
     for k, v in kw.items():
         setattr(a, k, v)
@@ -84,8 +84,8 @@ def test_store_and_load_refusals(kw, args):
 @pytest.mark.parametrize("bad", [
     dict(q=0), dict(out=A + 8), dict(lens=0), dict(batch=-1), dict(batch=1025), dict(q_heads=6), dict(q_heads=0),
     dict(tokens=4), dict(max_tokens=-1), dict(window=-1), dict(scale=-0.5), dict(scale=float("nan")),
-    dict(scale=float("inf")), dict(table_width=0), dict(lse=A + 1), dict(q_stride=(C.c_int64 * 2)(1024, 4)),
-    dict(out_stride=(C.c_int64 * 2)(1020, 128)), dict(table_width=1 << 26)])
+    dict(scale=float("inf")), dict(table_width=0), dict(lse=A + 1), dict(q_head_stride=4),
+    dict(out_token_stride=1020), dict(table_width=1 << 26)])
 def test_attend_refusals(bad):
     lib = rt.load()
     assert lib.mk_cache_attend(C.byref(desc()), 0, C.byref(attend(**bad)), A, 1 << 30, None) in (
@@ -114,7 +114,7 @@ def test_copy_refusals(src, dst):
 
 
 @pytest.mark.parametrize("bad", [dict(logits=0), dict(u=0), dict(tokens=0), dict(batch=-1), dict(vocab=0),
-                                 dict(vocab=700000, row_stride=700000), dict(row_stride=999), dict(logits=A + 2),
+                                 dict(vocab=622593, row_stride=622593), dict(row_stride=999), dict(logits=A + 2),
                                  dict(tokens=A + 1)])
 def test_sample_refusals(bad):
     d = rt.SampleDesc()
