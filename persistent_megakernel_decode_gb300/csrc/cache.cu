@@ -54,9 +54,10 @@ DEV bool page_span(const MoveParams &m, int b, int slot, int &first, int &lo, in
     const int s = m.start[b], n = m.count[b];
     const int r0 = m.r.row0 ? m.r.row0[b] : 0;
     if (n == 0) return false;
+    const bool reports = slot == 0 && threadIdx.x % 32 == 0;
     if (s < 0 || n < 0 || n > m.max_count || r0 < 0 || r0 > m.r.rows || n > m.r.rows - r0 ||
         (int64_t)s + n > (int64_t)m.width * P) {
-        if (threadIdx.x == 0) note_failure(m.c.status, MK_ERR_DEVICE_CHECK, b, s, -1);
+        if (reports) note_failure(m.c.status, MK_ERR_DEVICE_CHECK, b, s, -1);
         return false;
     }
     const int j = s / P + slot;
@@ -67,7 +68,7 @@ DEV bool page_span(const MoveParams &m, int b, int slot, int &first, int &lo, in
     src0 = r0 - s;
     page = m.table[(size_t)b * m.width + j];
     if ((unsigned)page >= (unsigned)m.c.pages) {
-        if (threadIdx.x == 0) note_failure(m.c.status, MK_ERR_DEVICE_CHECK, b, first, page);
+        if (threadIdx.x % 32 == 0) note_failure(m.c.status, MK_ERR_DEVICE_CHECK, b, first, page);
         return false;
     }
     return true;
@@ -120,11 +121,11 @@ DEV void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&o
 // Codes of a page, rounded to a scale 1 / ratio times as large (ratio a power
 // of two: the product is exact in f16 wherever it is not far below e4m3's
 // least step, so each code is rounded once).
-DEV void rescale_page(uint32_t *w, int words, float ratio) {
+DEV void rescale_page(uint32_t *w, int words, float ratio, int tid, int threads) {
     const float r = fmaxf(ratio, 0x1p-24f);  // below, every product rounds to 0 as with this
     uint32_t r2;
     asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(r2) : "f"(r));
-    for (int i = threadIdx.x; i < words; i += blockDim.x) {
+    for (int i = tid; i < words; i += threads) {
         const uint32_t x = w[i];
         w[i] = half2_to_e4m3x2(half2_mul(e4m3x2_to_half2(x), r2)) |
                (half2_to_e4m3x2(half2_mul(e4m3x2_to_half2(x >> 16), r2)) << 16);
@@ -191,8 +192,8 @@ __global__ void __launch_bounds__(MOVE_THREADS) cache_store_kernel(const MovePar
     }
     const float sk = fmaxf(page_scale(ka), old_k), sv = fmaxf(page_scale(va), old_v);
     if (held && (sk > old_k || sv > old_v)) {
-        if (sk > old_k) rescale_page(reinterpret_cast<uint32_t *>(kp), P * D / 4, old_k * page_inverse(sk));
-        if (sv > old_v) rescale_page(reinterpret_cast<uint32_t *>(vp), P * D / 4, old_v * page_inverse(sv));
+        if (sk > old_k) rescale_page(reinterpret_cast<uint32_t *>(kp), P * D / 4, old_k * page_inverse(sk), tid, MOVE_THREADS);
+        if (sv > old_v) rescale_page(reinterpret_cast<uint32_t *>(vp), P * D / 4, old_v * page_inverse(sv), tid, MOVE_THREADS);
         __syncthreads();
     }
     const float ik = page_inverse(sk), iv = page_inverse(sv);
@@ -228,6 +229,73 @@ __global__ void __launch_bounds__(MOVE_THREADS) cache_store_kernel(const MovePar
     if (tid == 0) {
         m.c.ks[at] = sk;
         m.c.vs[at] = sv;
+    }
+}
+
+// Appending a few tokens (a decode step: one): one warp per (kv head,
+// sequence, layer), the lower lanes on K's vectors of 8 dims, the upper on
+// V's.  The block form above takes a CTA for each, most of whose threads have
+// nothing to do: 36 us against 7.8 for one token of 16 sequences, 36
+// layers, 8 heads of 128 (bound by the latency of three dependent loads).
+constexpr int APPEND_TOKENS = 4;
+template <int D, int P>
+__global__ void __launch_bounds__(MOVE_THREADS) cache_append_kernel(const MoveParams m, int heads) {
+    constexpr int VEC = D / 8;
+    const int lane = threadIdx.x % 32;
+    const int64_t w = (int64_t)blockIdx.x * (MOVE_THREADS / 32) + threadIdx.x / 32;
+    if (w >= (int64_t)heads * m.c.layers) return;  // heads: batch x kv heads
+    const int l = (int)(w / heads), bh = (int)(w % heads), b = bh / m.c.hkv, h = bh % m.c.hkv;
+    const bool is_v = lane >= VEC, busy = lane < 2 * VEC;
+    const int c = lane % VEC;
+    const int64_t *st = is_v ? m.r.vs : m.r.ks;
+    const uint16_t *src = (is_v ? m.r.v : m.r.k) + l * st[0] + b * st[1] + h * st[3];
+    for (int slot = 0; slot < 2; ++slot) {  // at most 4 tokens lie on at most two pages
+        int first, lo, hi, page, src0;
+        if (!page_span<P>(m, b, slot, first, lo, hi, page, src0)) continue;
+        const size_t at = m.c.at(l, page, h);
+        uint8_t *dst = (is_v ? m.c.v : m.c.k) + at * (P * D);
+        float *scale = (is_v ? m.c.vs : m.c.ks) + at;
+        const bool held = first < lo;
+        const float old = held ? *scale : 0.f;
+        uint4 x[APPEND_TOKENS];
+        uint32_t a = 0;
+#pragma unroll
+        for (int j = 0; j < APPEND_TOKENS; ++j) {
+            x[j] = make_uint4(0, 0, 0, 0);
+            if (busy && lo + j < hi) x[j] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(src0 + lo + j) * st[2]) + c);
+            a = max(a, amax8(x[j]));
+        }
+#pragma unroll
+        for (int o = 1; o < VEC; o <<= 1) a = max(a, __shfl_xor_sync(FULL, a, o));
+        const float s = fmaxf(page_scale(a), old);
+        // the whole page, for either half, by all lanes
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float ns = __shfl_sync(FULL, s, half * VEC), os = __shfl_sync(FULL, old, half * VEC);
+            uint8_t *pg = (half ? m.c.v : m.c.k) + at * (P * D);
+            if (!held) {
+                for (int i = lane; i < P * D / 16; i += 32) reinterpret_cast<uint4 *>(pg)[i] = make_uint4(0, 0, 0, 0);
+            } else if (ns > os) {
+                rescale_page(reinterpret_cast<uint32_t *>(pg), P * D / 4, os * page_inverse(ns), lane, 32);
+            }
+        }
+        __syncwarp();
+        const float inv = page_inverse(s);
+        if (busy) {
+#pragma unroll
+            for (int j = 0; j < APPEND_TOKENS; ++j) {
+                if (lo + j >= hi) break;
+                const uint2 e = encode8(x[j], inv);
+                const int t = lo + j - first;
+                if (!is_v) {
+                    reinterpret_cast<uint2 *>(dst + t * D)[c] = e;
+                } else {
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) dst[(c * 8 + d) * P + t] = (uint8_t)((d < 4 ? e.x : e.y) >> (8 * (d % 4)));
+                }
+            }
+            if (c == 0) *scale = s;
+        }
     }
 }
 
@@ -389,6 +457,18 @@ int mk_cache_store(const mk_cache_desc *cache, const mk_cache_rows *rows, const 
     MoveParams m;
     if (int rc = move_params(cache, rows, table, table_width, start, count, batch, max_count, m)) return rc;
     const bool d64 = cache->head_dim == 64, p32 = cache->page_tokens == 32;
+    if (m.max_count <= APPEND_TOKENS) {
+        const int64_t heads = (int64_t)batch * cache->kv_heads, warps = heads * cache->layers;
+        if (warps == 0 || m.max_count == 0) return MK_OK;
+        if (heads > INT32_MAX || warps / (MOVE_THREADS / 32) >= INT32_MAX)
+            return set_error(MK_ERR_UNSUPPORTED, "too many sequences and heads in one call");
+        void (*g)(const MoveParams, int) = d64 ? (p32 ? cache_append_kernel<64, 32> : cache_append_kernel<64, 64>)
+                                               : (p32 ? cache_append_kernel<128, 32> : cache_append_kernel<128, 64>);
+        g<<<(unsigned)((warps + MOVE_THREADS / 32 - 1) / (MOVE_THREADS / 32)), MOVE_THREADS, 0,
+            static_cast<cudaStream_t>(stream)>>>(m, (int)heads);
+        cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? MK_OK : serve_cuda_fail(e, "cache append launch");
+    }
     MoveFn f = d64 ? (p32 ? cache_store_kernel<64, 32> : cache_store_kernel<64, 64>)
                    : (p32 ? cache_store_kernel<128, 32> : cache_store_kernel<128, 64>);
     return launch_move(f, m, cache, batch, stream);

@@ -6,8 +6,9 @@
 // cut.  A cut is found by counting: a histogram over bins that follow the
 // order, the bin in which the running count (or weight) reaches its target,
 // then the same inside that bin, until few enough candidates are left to rank
-// them by comparing each with all.  The first bins are 1/64 octave of weight
-// wide (linear in the logit), later ones split the bin's range of keys.
+// them by comparing each with all.  The first bins are linear in the logit,
+// from the largest to the least or 32 octaves of weight down; later ones split
+// the bin's range of keys.
 //
 // Weights 2^-d, d = (max - z) log2(e) / temperature, are 64-bit fixed point
 // (2^44 for d = 0), relative accuracy 2^-30: d is carried as a pair of fp32
@@ -37,7 +38,7 @@ namespace cg = cooperative_groups;
 namespace mk {
 
 constexpr int SMP_THREADS = 512, SMP_WARPS = SMP_THREADS / 32;
-constexpr int SMP_BINS = 2048, SMP_SUB = 64;     // first-level bins; bins per octave of weight
+constexpr int SMP_BINS = 2048;                   // first-level bins
 constexpr int SMP_COARSE = 64, SMP_FINE = SMP_BINS / SMP_COARSE;  // first-level bins are searched in two steps
 constexpr int SMP_CAP = 1024;                    // candidates ranked directly
 constexpr int SMP_MAXCTAS = 16;
@@ -61,6 +62,7 @@ struct SmpParams {
 struct alignas(16) SmpShared {  // the logits behind it are read 16 bytes at a time
     uint32_t table[32];                             // 2^31 2^(-i/32)
     unsigned long long best[SMP_MAXCTAS];           // every CTA's largest (ordered logit, index)
+    uint32_t least[SMP_MAXCTAS];                    // every CTA's least logit above -inf, ordered
     unsigned long long slice_w[SMP_MAXCTAS];        // every CTA's slice of the histogram
     uint32_t slice_n[SMP_MAXCTAS];
     unsigned long long lo[SMP_MAXCTAS], hi[SMP_MAXCTAS];  // every CTA's least and largest key in the bin
@@ -72,8 +74,8 @@ struct alignas(16) SmpShared {  // the logits behind it are read 16 bytes at a t
     uint32_t cands;
     unsigned long long red[SMP_WARPS];
     uint32_t red_n[SMP_WARPS];
-    unsigned long long coarse_w[SMP_MAXCTAS][SMP_COARSE], fine_w[SMP_MAXCTAS][SMP_FINE];  // every CTA's
-    uint32_t coarse_n[SMP_MAXCTAS][SMP_COARSE], fine_n[SMP_MAXCTAS][SMP_FINE];
+    alignas(16) unsigned long long coarse_w[SMP_MAXCTAS][SMP_COARSE], fine_w[SMP_MAXCTAS][SMP_FINE];  // every CTA's
+    alignas(16) uint32_t coarse_n[SMP_MAXCTAS][SMP_COARSE], fine_n[SMP_MAXCTAS][SMP_FINE];
     uint32_t hist[4][SMP_BINS];                     // count; weight in 16-bit pieces
     unsigned long long ckey[SMP_CAP], cw[SMP_CAP];  // candidates (in CTA 0)
 };
@@ -87,22 +89,46 @@ DEV unsigned long long sample_key(float x, int i) {
     return ((unsigned long long)(~ordered_bits(x)) << 32) | (uint32_t)i;
 }
 
+// 2^31 2^(-i/32)
+__constant__ uint32_t c_table[32] = {
+    2147483648u, 2101467502u, 2056437387u, 2012372174u, 1969251188u, 1927054196u, 1885761398u, 1845353420u,
+    1805811301u, 1767116489u, 1729250827u, 1692196547u, 1655936265u, 1620452965u, 1585730000u, 1551751076u,
+    1518500250u, 1485961921u, 1454120821u, 1422962010u, 1392470869u, 1362633090u, 1333434672u, 1304861917u,
+    1276901417u, 1249540052u, 1222764986u, 1196563654u, 1170923762u, 1145833280u, 1121280436u, 1097253708u};
+
+// floor (up: ceiling) of f x for 0 <= f < 1, exactly: f = mantissa 2^-s.  (FP64
+// arithmetic is to be kept out of this file: a few instructions of it in
+// every thread cost more than the pass over the logits.)
+DEV unsigned long long frac_of(float f, unsigned long long x, bool up) {
+    const uint32_t bits = __float_as_uint(f);
+    const int s = 150 - (int)(bits >> 23);
+    if (s >= 128) return up && bits ? 1 : 0;  // below 2^-102 (or 0)
+    const unsigned long long m = (bits & 0x7fffffu) | 0x800000u, hi = __umul64hi(m, x), lo = m * x;
+    unsigned long long q, rest;
+    if (s < 64) {
+        q = hi << (64 - s) | lo >> s;
+        rest = lo << (64 - s);
+    } else {
+        q = s == 64 ? hi : hi >> (s - 64);
+        rest = lo | (s == 64 ? 0 : hi << (128 - s));
+    }
+    return q + (up && rest ? 1 : 0);
+}
+
 struct Weigher {
     float top, ch, cl;  // the row's maximum; log2(e) / temperature as a pair of fp32
     const uint32_t *table;
     DEV float octaves(float x) const { return (top - x) * ch; }  // d in fp32: monotone in x
-    // 2^44 2^-d
+    // 2^44 2^-d, without branches, so that several weights overlap
     DEV unsigned long long operator()(float x) const {
-        if (x == top) return 1ull << 44;
         const float dh = top - x;
         const float bp = dh - top;
         const float dl = (top - (dh - bp)) + (-x - bp);  // dh + dl = top - x exactly
-        const float t = dh * ch;
-        if (!(t < 45.f)) return 0;  // less than half a unit (or not finite)
-        const float te = fmaf(dh, ch, -t) + fmaf(dh, cl, dl * ch);
-        const float n = floorf(t);
+        const float t = fminf(dh * ch, 47.f);            // (NaN too) from 46 on the weight is 0
+        const float te = t < 46.f ? fmaf(dh, ch, -t) + fmaf(dh, cl, dl * ch) : 0.f;
+        const int n = __float2int_rz(t);
         // d in 32.32 fixed point; t - n is exact, te below 2^-17
-        const long long d = max(0ll, ((long long)n << 32) + (long long)(uint32_t)((t - n) * 4294967296.f) +
+        const long long d = max(0ll, ((long long)n << 32) + (long long)__float2uint_rz((t - (float)n) * 4294967296.f) +
                                          (long long)__float2int_rn(te * 4294967296.f));
         const uint32_t f = (uint32_t)d;
         // 2^-f = table x exp(-a), a = (f mod 1/32) ln 2 < 0.0217: terms to a^4 / 24 leave 4e-11
@@ -112,13 +138,16 @@ struct Weigher {
         q = 0xffffffffu - __umulhi(a, q);                          // 1 - a q
         const uint32_t e = 0x80000000u - (__umulhi(a, q) >> 1);    // 1 - a q, in 1.31
         const unsigned long long prod = (unsigned long long)table[f >> 27] * e;  // 2.62
-        const int s = 18 + (int)(d >> 32);
-        return s < 64 ? prod >> s : 0;
+        const unsigned long long r = prod >> min(18 + (int)(d >> 32), 63);
+        return x == top ? 1ull << 44 : r;  // (the largest may be infinite)
     }
 };
 
-// log(w / total) through the rest: exact near 0, where the rest is small.
-DEV float log_share(unsigned long long w, unsigned long long total) { return (float)-log1p((double)(total - w) / (double)w); }
+// log(w / total) = -log1p(rest / w): fp32 throughout, a few last places of the
+// result also near 0 (the conversions and the quotient half a place each).
+DEV float log_share(unsigned long long w, unsigned long long total) {
+    return -log1pf(__fdiv_rn(__ull2float_rn(total - w), __ull2float_rn(w)));
+}
 DEV unsigned long long warp_sum64(unsigned long long v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
@@ -140,6 +169,7 @@ struct Sampler {
     cg::cluster_group cl;
     int rank, ctas, first, n;  // n: multiple of 128
     Weigher w;
+    float bins;  // bins per octave of weight
 
     DEV float4 four(int i) const { return *reinterpret_cast<const float4 *>(x + i); }
 
@@ -308,29 +338,32 @@ struct Sampler {
         }
         cl.sync();
         if (rank == 0) {
-            // rank every candidate by comparing it with all: count and weight of those up to it
-            const int count = (int)s.bin_n;
-            for (int i = tid; i < count; i += SMP_THREADS) {
-                const unsigned long long key = s.ckey[i];
-                unsigned long long before = w_before;
-                uint32_t rk = n_before;
-                for (int j = 0; j < count; ++j)
-                    if (s.ckey[j] < key) {
-                        before += s.cw[j];
-                        ++rk;
-                    }
-                const unsigned long long with = before + s.cw[i];
-                if (by_weight ? (before < need && with >= need) : rk + 1 == need)
-                    for (int r = 0; r < ctas; ++r) {
-                        SmpShared *o = cl.map_shared_rank(&s, r);
-                        o->cut = key;
-                        o->cut_w = with;
-                    }
-            }
+            const int count = (int)s.bin_n, size = list_size(count);
+            sort(count, size);
+            announce(by_weight, need, n_before, w_before, count, size);
         }
         cl.sync();
         upto = s.cut_w;
         return s.cut;
+    }
+
+    // CTA 0, after sort: the key at which the target is reached, to all CTAs.
+    DEV void announce(bool by_weight, unsigned long long need, uint32_t n_before, unsigned long long w_before, int count,
+                      int size) const {
+        unsigned long long before = w_before + list_before(size);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = 2 * (int)threadIdx.x + k;
+            if (i >= count) break;
+            const unsigned long long with = before + s.cw[i];
+            if (by_weight ? before < need && with >= need : n_before + i + 1 == need)
+                for (int r = 0; r < ctas; ++r) {
+                    SmpShared *o = cl.map_shared_rank(&s, r);
+                    o->cut = s.ckey[i];
+                    o->cut_w = with;
+                }
+            before = with;
+        }
     }
 
     // First-level histogram of every logit above -inf, joined over the cluster.
@@ -386,18 +419,21 @@ struct Sampler {
         if (warp == 0) {  // lane: coarse bins 2 lane, 2 lane + 1
             uint32_t cn[2] = {0, 0};
             unsigned long long cw[2] = {0, 0};
-            for (int r = 0; r < ctas; ++r)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    cn[k] += s.coarse_n[r][2 * lane + k];
-                    cw[k] += s.coarse_w[r][2 * lane + k];
+            for (int r = 0; r < SMP_MAXCTAS; ++r)
+                if (r < ctas) {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(&s.coarse_n[r][2 * lane]);
+                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&s.coarse_w[r][2 * lane]);
+                    cn[0] += a.x;
+                    cn[1] += a.y;
+                    cw[0] += b.x;
+                    cw[1] += b.y;
                 }
             uint32_t pn = cn[0] + cn[1];
             unsigned long long pw = cw[0] + cw[1];
             running(lane, pn, pw);
             const unsigned long long all = __shfl_sync(FULL, pw, 31);
-            const double want = ceil((double)fmaxf(share, 0.f) * (double)all);
-            const unsigned long long goal = by_weight ? min(max((unsigned long long)want, 1ull), all) : need_n;
+            const unsigned long long goal = by_weight ? max(frac_of(fmaxf(share, 0.f), all, true), 1ull) : need_n;
             if (lane == 0) {
                 s.bin = -1;
                 s.need = goal;
@@ -431,10 +467,12 @@ struct Sampler {
             if (warp == 0) {
                 uint32_t fn = 0;
                 unsigned long long fw = 0;
-                for (int r = 0; r < ctas; ++r) {
-                    fn += s.fine_n[r][lane];
-                    fw += s.fine_w[r][lane];
-                }
+#pragma unroll
+                for (int r = 0; r < SMP_MAXCTAS; ++r)
+                    if (r < ctas) {
+                        fn += s.fine_n[r][lane];
+                        fw += s.fine_w[r][lane];
+                    }
                 uint32_t pn = fn;
                 unsigned long long pw = fw;
                 running(lane, pn, pw);
@@ -487,82 +525,135 @@ struct Sampler {
         cl.sync();
     }
 
-    // Calls f(i, count, weight) for every candidate i: how many others `before(j,
-    // i)` holds for, and their weight.  512 threads share the n^2 comparisons.
-    template <class B, class F>
-    DEV void each_before(int count, B before, F f) const {
-        int per = SMP_THREADS;  // candidates a round: a power of two, 32 threads each at most
-        while (per > SMP_THREADS / 32 && per / 2 >= count) per /= 2;
-        const int g = SMP_THREADS / per;
-        for (int i0 = 0; i0 < count; i0 += per) {
-            const int i = i0 + (int)threadIdx.x / g;
-            uint32_t c = 0;
-            unsigned long long sum = 0;
-            if (i < count)
-                for (int j = threadIdx.x % g; j < count; j += g)
-                    if (before(j, i)) {
-                        ++c;
-                        sum += s.cw[j];
-                    }
-            for (int o = 1; o < g; o <<= 1) {
-                c += __shfl_xor_sync(FULL, c, o);
-                sum += __shfl_xor_sync(FULL, sum, o);
+    // Sorts the list's `count` candidates by key, all threads; the entries up
+    // to `size`, a power of two, are filled with KEY_NONE, weight 0.  Up to 256
+    // by counting, for each, the smaller ones (2.5 us for two sorts of 100, a
+    // step of the bitonic form costs 0.09 us); above, the comparisons'
+    // shared-memory reads would take longer than the bitonic steps.
+    DEV void sort(int count, int size) const {
+        const int tid = threadIdx.x;
+        if (size <= 256) {
+            const int lg = min(5, 32 - __clz(SMP_THREADS / size) - 1), g = 1 << lg, i = tid >> lg;
+            const unsigned long long key = i < count ? s.ckey[i] : KEY_NONE, w = i < count ? s.cw[i] : 0;
+            uint32_t place = 0;
+            if (i < count) {
+#pragma unroll 4
+                for (int j = tid & (g - 1); j < count; j += g) place += s.ckey[j] < key;
             }
-            if (i < count && threadIdx.x % g == 0) f(i, c, sum);
+            for (int o = 1; o < g; o <<= 1) place += __shfl_xor_sync(FULL, place, o);
+            __syncthreads();
+            if ((tid & (g - 1)) == 0 && i < size) {
+                s.ckey[i < count ? place : i] = key;
+                s.cw[i < count ? place : i] = w;
+            }
+            __syncthreads();
+            return;
+        }
+        for (int i = count + tid; i < size; i += SMP_THREADS) {
+            s.ckey[i] = KEY_NONE;
+            s.cw[i] = 0;
         }
         __syncthreads();
+        for (int run = 2; run <= size; run *= 2)
+            for (int step = run / 2; step > 0; step /= 2) {
+                if (tid < size / 2) {
+                    const int i = 2 * tid - (tid & (step - 1)), j = i + step;
+                    const unsigned long long a = s.ckey[i], b = s.ckey[j];
+                    if ((a > b) == ((i & run) == 0)) {
+                        const unsigned long long wa = s.cw[i], wb = s.cw[j];
+                        s.ckey[i] = b;
+                        s.ckey[j] = a;
+                        s.cw[i] = wb;
+                        s.cw[j] = wa;
+                    }
+                }
+                __syncthreads();
+            }
     }
+    // This thread's candidates are 2 tid and 2 tid + 1: the weight before them,
+    // in the list's order.
+    DEV unsigned long long list_before(int size) const {
+        const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+        const unsigned long long own = 2 * tid < size ? s.cw[2 * tid] + s.cw[2 * tid + 1] : 0;
+        uint32_t none = 0;
+        unsigned long long sum = own;
+        running(lane, none, sum);
+        __syncthreads();  // s.red was read
+        if (lane == 31) s.red[warp] = sum;
+        __syncthreads();
+        sum -= own;
+#pragma unroll
+        for (int i = 0; i < SMP_WARPS; ++i)
+            if (i < warp) sum += s.red[i];
+        return sum;
+    }
+    DEV static int list_size(int count) { return count <= 2 ? 2 : 1 << (32 - __clz(count - 1)); }
 
-    DEV int bin_of(float v) const { return (int)fminf((float)(SMP_BINS - 1), w.octaves(v) * (float)SMP_SUB); }
+    DEV int bin_of(float v) const { return (int)fminf((float)(SMP_BINS - 1), w.octaves(v) * bins); }
 };
 
 // The rest of a row among the candidates of CTA 0's list, which hold every
 // logit up to the cuts: top_k of them (or all), then top-p (`need` of the
 // weight if it is known, else top_p of the top_k's), then those >= least.
 static __device__ __noinline__ void finish_few(const Sampler &k, int count, int top_k, float top_p, unsigned long long need,
-                                               float least, float u, int *token, float *logprob) {
+                                               float least, unsigned long long least_w, float u, int *token, float *logprob) {
     SmpShared &s = k.s;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    // rank and weight before each candidate, over the histogram (done with)
-    unsigned long long *cb = reinterpret_cast<unsigned long long *>(s.hist[2]);
-    static_assert(SMP_CAP * 8 <= 2 * sizeof s.hist[0] && SMP_CAP <= SMP_BINS, "fits");
-    k.each_before(count, [&](int j, int i) { return s.ckey[j] < s.ckey[i]; },
-                  [&](int i, uint32_t c, unsigned long long sum) {
-                      cb[i] = sum;
-                      s.hist[0][i] = c;  // the rank
-                      if ((int)c == top_k - 1) s.cut_w = sum + s.cw[i];
-                  });
+    const int size = k.list_size(count);
+    k.sort(count, size);  // rank = place in the list
+    unsigned long long before = k.list_before(size);
+    const int i0 = 2 * tid;
+    if (i0 < count) {
+        const unsigned long long w0 = s.cw[i0];
+        if (i0 == top_k - 1) s.cut_w = before + w0;
+        if (i0 + 1 == top_k - 1) s.cut_w = before + w0 + s.cw[i0 + 1];
+    }
+    __syncthreads();
     if (need == 0) {
         need = s.cut_w;
-        if (top_p < 1.f)
-            need = min(max((unsigned long long)ceil((double)fmaxf(top_p, 0.f) * (double)s.cut_w), 1ull), s.cut_w);
+        if (top_p < 1.f) need = max(frac_of(fmaxf(top_p, 0.f), s.cut_w, true), 1ull);
     }
-    // what is kept, by weight: the others' becomes 0
+    // what is dropped goes to the end of the list, without weight; the rest in the vocabulary's order
     unsigned long long sum = 0;
-    for (int i = tid; i < count; i += SMP_THREADS) {
-        const uint32_t ob = ~(uint32_t)(s.ckey[i] >> 32);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = i0 + j;
+        if (i >= count) break;
+        const unsigned long long key = s.ckey[i], w = s.cw[i];
+        const uint32_t ob = ~(uint32_t)(key >> 32);
         const float z = __uint_as_float(ob & 0x80000000u ? ob & 0x7fffffffu : ~ob);
-        if ((int)s.hist[0][i] >= top_k || cb[i] >= need || z < least) s.cw[i] = 0;
-        sum += s.cw[i];
+        const bool keep = i < top_k && before < need && z >= least && w >= least_w;
+        before += w;
+        sum += keep ? w : 0;
+        s.ckey[i] = keep ? (unsigned long long)(uint32_t)key : KEY_NONE;
+        s.cw[i] = keep ? w : 0;
     }
+    const int kept = __syncthreads_count(i0 < count && s.ckey[i0] != KEY_NONE) + __syncthreads_count(i0 + 1 < count && s.ckey[i0 + 1] != KEY_NONE);
     sum = warp_sum64(sum);
-    __syncthreads();
     if (lane == 0) s.red[warp] = sum;
     __syncthreads();
     unsigned long long total = 0;
     for (int i = 0; i < SMP_WARPS; ++i) total += s.red[i];
-    const unsigned long long target = min((unsigned long long)((double)u * (double)total), total - 1);
-    k.each_before(count, [&](int j, int i) { return (uint32_t)s.ckey[j] < (uint32_t)s.ckey[i]; },  // by index
-                  [&](int i, uint32_t, unsigned long long before) {
-                      if (before <= target && target < before + s.cw[i]) {
-                          *token = (int)(uint32_t)s.ckey[i];
-                          if (logprob) *logprob = log_share(s.cw[i], total);
-                      }
-                  });
+    // a prefix of the list was kept: the rest holds no weight and need not be sorted
+    const int ksize = k.list_size(kept);
+    k.sort(kept, ksize);
+    const unsigned long long target = frac_of(u, total, false);
+    before = k.list_before(ksize);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = i0 + j;
+        if (i >= kept) break;
+        const unsigned long long w = s.cw[i];
+        if (before <= target && target < before + w) {
+            *token = (int)(uint32_t)s.ckey[i];
+            if (logprob) *logprob = log_share(w, total);
+        }
+        before += w;
+    }
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) {
+__global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const SmpParams p) {
     SmpShared &s = *reinterpret_cast<SmpShared *>(mk_smem);
     float *x = reinterpret_cast<float *>(mk_smem + sizeof(SmpShared));
     cg::cluster_group cl = cg::this_cluster();
@@ -572,11 +663,12 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
     unsigned long long *rows = reinterpret_cast<unsigned long long *>(x + p.chunk);
 
     // the row's share into shared memory, and its largest (logit, index)
-    float top = -INFINITY;
+    float top = -INFINITY, bottom = INFINITY;
     int at = 0;
     const auto put = [&](int i, float v) {
         v = v != v ? -INFINITY : v + 0.f;  // -0 counts as 0
         x[i] = v;
+        if (v > -INFINITY) bottom = fminf(bottom, v);
         if (v > top || (v == top && first + i < at)) {
             top = v;
             at = first + i;
@@ -609,16 +701,31 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
     // largest (ordered logit, ~index) of the block, then of the cluster
     unsigned long long best = ((unsigned long long)ordered_bits(top) << 32) | (uint32_t)~at;
     best = ~warp_min64(~best);
-    if (lane == 0) s.red[warp] = best;
-    if (tid < 32) s.table[tid] = (uint32_t)(exp2(-tid / 32.0) * 2147483648.0 + 0.5);
+    const uint32_t low = __reduce_min_sync(FULL, ordered_bits(bottom));
+    if (lane == 0) {
+        s.red[warp] = best;
+        s.red_n[warp] = low;
+    }
+    if (tid < 32) s.table[tid] = c_table[tid];
     __syncthreads();
     if (tid < ctas) {
-        for (int i = 0; i < SMP_WARPS; ++i) best = max(best, s.red[i]);
+        uint32_t lo = ~0u;
+        for (int i = 0; i < SMP_WARPS; ++i) {
+            best = max(best, s.red[i]);
+            lo = min(lo, s.red_n[i]);
+        }
         *cl.map_shared_rank(&s.best[rank], tid) = best;
+        *cl.map_shared_rank(&s.least[rank], tid) = lo;
     }
     cl.sync();
     best = 0;
-    for (int r = 0; r < ctas; ++r) best = max(best, s.best[r]);
+    uint32_t lob = ~0u;
+#pragma unroll
+    for (int r = 0; r < SMP_MAXCTAS; ++r)
+        if (r < ctas) {
+            best = max(best, s.best[r]);
+            lob = min(lob, s.least[r]);
+        }
     const int arg = (int)~(uint32_t)best;
     const uint32_t ob = (uint32_t)(best >> 32);
     top = __uint_as_float(ob & 0x80000000u ? ob & 0x7fffffffu : ~ob);
@@ -634,16 +741,18 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
         }
         return;
     }
-    const double c = 1.4426950408889634 / (double)temp;
-    const float ch = (float)c;
-    Sampler k{p, s, x, rows, cl, rank, ctas, first, n, {top, ch, ch < INFINITY ? (float)(c - (double)ch) : 0.f, s.table}};
+    // log2(e) / temperature as ch + cl: quotient, then the exact remainder's
+    const float log2e = 1.44269502f, log2e_lo = 1.92596303e-8f, ch = __fdiv_rn(log2e, temp);
+    const float cl_ = ch < INFINITY ? (fmaf(-ch, temp, log2e) + log2e_lo) / temp : 0.f;
+    Sampler k{p, s, x, rows, cl, rank, ctas, first, n, {top, ch, cl_, s.table}, 0.f};
+    // the logits' span in octaves, 32 at most; all in one bin if they are equal
+    const float span = fminf(k.w.octaves(__uint_as_float(lob & 0x80000000u ? lob & 0x7fffffffu : ~lob)), 32.f);
+    k.bins = span > 0.f ? (float)SMP_BINS / span : 0.f;
 
     const float u = fminf(fmaxf(p.u[row], 0.f), 0x1.fffffep-1f);
-    float least = -INFINITY;
-    if (min_p > 0.f) {
-        // w >= min_p  <=>  z >= max + temperature ln(min_p): the least fp32 number that is
-        least = min_p >= 1.f ? top : __double2float_ru((double)top + (double)temp * log((double)min_p));
-    }
+    // min_p as a least weight; from 1 on only the largest logit itself
+    const float least = min_p >= 1.f ? top : -INFINITY;
+    const unsigned long long least_w = min_p > 0.f && min_p < 1.f ? frac_of(min_p, 1ull << 44, true) : 0;
     unsigned long long cut = sample_key(-3.402823466e38f, 0x7fffffff), cut_w = 0;  // every finite logit
     bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.f;
     if (by_k || by_p) {
@@ -659,7 +768,7 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
         if ((by_k || by_p) && upto <= SMP_CAP) {
             k.gather(0, bin);
             if (rank != 0) return;
-            finish_few(k, upto, by_k ? top_k : (int)upto, by_p ? top_p : 1.f, by_p && !by_k ? need : 0, least, u,
+            finish_few(k, upto, by_k ? top_k : (int)upto, by_p ? top_p : 1.f, by_p && !by_k ? need : 0, least, least_w, u,
                        p.tokens + row, p.logprob ? p.logprob + row : nullptr);
             return;
         }
@@ -667,20 +776,18 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
             cl.sync();  // the bins were read
             cut = k.find(false, top_k, cut, cut_w);
             if (by_p) {
-                const double want = ceil((double)fmaxf(top_p, 0.f) * (double)cut_w);
-                need = min(max((unsigned long long)want, 1ull), cut_w);
+                need = max(frac_of(fmaxf(top_p, 0.f), cut_w, true), 1ull);
                 cut = k.find(true, need, cut, cut_w);
             }
         } else if (by_p && s.bin_n <= SMP_CAP) {
             const uint32_t count = s.bin_n;
             const unsigned long long before = s.before_w;
             k.gather(bin, bin);
-            if (rank == 0)
-                k.each_before((int)count, [&](int j, int i) { return s.ckey[j] < s.ckey[i]; },
-                              [&](int i, uint32_t, unsigned long long sum) {
-                                  if (before + sum < need && before + sum + s.cw[i] >= need)
-                                      for (int r = 0; r < ctas; ++r) cl.map_shared_rank(&s, r)->cut = s.ckey[i];
-                              });
+            if (rank == 0) {
+                const int size = k.list_size((int)count);
+                k.sort((int)count, size);
+                k.announce(true, need, 0, before, (int)count, size);
+            }
             cl.sync();
             cut = s.cut;
         } else if (by_p) {
@@ -689,16 +796,15 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
         }
     }
     // weight of what a pass keeps: per 128 logits (rows), per CTA, per cluster
-    const auto keeps = [&](float v, int i) { return v >= least && sample_key(v, first + i) <= cut; };
+    const auto kept = [&](float v, int i) -> unsigned long long {
+        const unsigned long long ww = k.w(v);
+        return v >= least && sample_key(v, first + i) <= cut && ww >= least_w ? ww : 0;
+    };
     const auto kept_weight = [&]() {
         for (int r = warp; r < n / SMP_ROW; r += SMP_WARPS) {
             const int i = r * SMP_ROW + lane * 4;
             const float4 v = k.four(i);
-            unsigned long long sum = 0;
-            if (keeps(v.x, i)) sum += k.w(v.x);
-            if (keeps(v.y, i + 1)) sum += k.w(v.y);
-            if (keeps(v.z, i + 2)) sum += k.w(v.z);
-            if (keeps(v.w, i + 3)) sum += k.w(v.w);
+            unsigned long long sum = kept(v.x, i) + kept(v.y, i + 1) + kept(v.z, i + 2) + kept(v.w, i + 3);
             sum = warp_sum64(sum);
             if (lane == 0) rows[r] = sum;
         }
@@ -719,7 +825,7 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
         return all;
     };
     const unsigned long long total = kept_weight();
-    const unsigned long long target = min((unsigned long long)((double)u * (double)total), total - 1);
+    const unsigned long long target = frac_of(u, total, false);
     unsigned long long before = 0;
     for (int r = 0; r < rank; ++r) before += s.kept[r];
     if (warp == 0 && before <= target && target < before + s.kept[rank]) {
@@ -747,7 +853,7 @@ __global__ void __launch_bounds__(SMP_THREADS) sample_kernel(const SmpParams p) 
         unsigned long long ww[4], sum = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            ww[j] = keeps(e[j], i + j) ? k.w(e[j]) : 0;
+            ww[j] = kept(e[j], i + j);
             sum += ww[j];
         }
         unsigned long long q = sum;
@@ -783,9 +889,12 @@ extern "C" int mk_sample(const mk_sample_desc *d, void *stream) {
     if (!d->logits || !d->u || !d->tokens) return set_error(MK_ERR_INVALID, "null argument");
     if (d->logits % (d->bf16 ? 2 : 4) || (d->u | d->tokens | d->logprob) % 4)
         return set_error(MK_ERR_INVALID, "a pointer is not aligned to its type");
-    // CTAs per row: as many SMs as a row can use while rows are few; at least
-    // what its share of shared memory asks for
-    int ctas = d->batch <= 8 ? 16 : d->batch <= 16 ? 8 : d->batch <= 40 ? 4 : 2;
+    // CTAs per row.  Few rows: as many SMs as a cluster may span (one row of
+    // 151,936: 14 us with 16, 16 with 8, 22 with 4; its top-p alone 24, 34, 56);
+    // many: fewer, longer shares, since clusters of 16 do not pack (32 rows: 23
+    // us with 4, 39 with 16 and with 8; 128 rows: 83, 122, 119).  At least what
+    // a share of shared memory asks for, at most one per 1024 logits.
+    int ctas = d->batch <= 16 ? 16 : 4;
     while (ctas < SMP_MAXCTAS && (d->vocab + ctas - 1) / ctas > SMP_CHUNK) ctas *= 2;
     while (ctas > 1 && d->vocab < ctas * 1024) ctas /= 2;
     if (d->batch > INT32_MAX / SMP_MAXCTAS) return set_error(MK_ERR_UNSUPPORTED, "too many rows");
