@@ -25,11 +25,12 @@
 // thread t of a quad holds the probabilities of the P/4 tokens from (P/4) t
 // on, and its V operand is one P/4-byte run of a transposed V row.
 //
-// Work split.  The pages of all (sequence, row tile, kv head) form one axis,
-// cut into equal ranges, one per CTA (one CTA per SM): ragged batches and
-// single long sequences balance alike.  A producer warp streams the pages
-// through a shared-memory ring with bulk copies; warps of a tile take every
-// (8 / tiles)-th page and merge in shared memory.  A unit that one CTA covers
+// Work split.  The pages of all units (sequence, row tile, kv head) form one
+// axis, each weighted with the warps its tile occupies side by side, cut into
+// equal ranges, one per CTA (one CTA per SM): ragged batches and single long
+// sequences balance alike.  A producer warp streams the pages through a
+// shared-memory ring with bulk copies; the consumer warps take them in turn
+// (as many side by side as the tile's rows need) and merge in shared memory.  A unit that one CTA covers
 // is written at once; ranges cut by a CTA boundary go to the workspace and a
 // second small launch (dependent launch, so that its start overlaps) merges
 // them in order: results do not depend on timing.
@@ -54,8 +55,7 @@ struct AttParams {
     const int *table, *lens, *q_start;
     int batch, width, group, tokens, max_tokens, window, ring, ctas;
     float scale_log2;
-    // workspace: prefix int64 [batch + 1]; partial (m, l) [ctas][2][RT][2]; partial O [ctas][2][RT][D]
-    long long *prefix;
+    // workspace: partial (m, l) [ctas][2][RT][2]; partial O [ctas][2][RT][D]
     float *part_ml, *part_o;
 };
 
@@ -90,13 +90,62 @@ DEV AttSeq att_seq(const AttParams &p, int b, bool report) {
     return s;
 }
 
-// CTAs that get work: every one of them at least a page.
-DEV int att_used(long long total, int ctas) { return (int)min((long long)ctas, total); }
+// Tiles of rt rows: 8 NT rows a warp, up to rt / (8 NT) warps side by side
+__host__ __device__ constexpr int att_nt(int rt) { return rt == 8 ? 1 : 2; }
+
+// Warps side by side on a tile of so many rows: 1, 2 or 4.
+template <int RT>
+DEV int att_side(int rows) {
+    const int need = (min(RT, rows) + 8 * att_nt(RT) - 1) / (8 * att_nt(RT));
+    return need <= 1 ? 1 : need == 2 ? 2 : 4;
+}
+// Work items of a sequence: its units' pages, each as many items as its tile
+// has warps side by side.  All tiles but the last are full.
+template <int RT>
+DEV long long att_items(const AttParams &p, int cnt, int np) {
+    const int rows = cnt * p.group, tiles = (rows + RT - 1) / RT;
+    if (tiles == 0) return 0;
+    return (long long)p.c.hkv * np * ((tiles - 1) * att_side<RT>(RT) + att_side<RT>(rows - (tiles - 1) * RT));
+}
+// prefix[1 .. n]: values -> running sums, by the whole block; prefix[0] = 0.
+DEV void att_running(long long *prefix, int n) {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        long long carry = 0;
+        if (lane == 0) prefix[0] = 0;
+        for (int b0 = 0; b0 < n; b0 += 32) {
+            const int b = b0 + lane;
+            long long v = b < n ? prefix[b + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(FULL, v, o);
+                if (lane >= o) v += u;
+            }
+            v += carry;
+            if (b < n) prefix[b + 1] = v;
+            carry = __shfl_sync(FULL, v, 31);
+        }
+    }
+    __syncthreads();
+}
+
+// A quotient that mostly fits 32 bits.
+DEV long long att_div(long long a, long long b) {
+    return (a | b) <= 0xffffffffll ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// CTAs that get work: every range is at least one page's items long, so that
+// a page begins in each.
+template <int RT>
+DEV int att_used(long long total, int ctas) {
+    return (int)max(1ll, min((long long)ctas, total / (RT / (8 * att_nt(RT)))));
+}
 // CTA of work item x when `total` items are cut into `ctas` <= total ranges [c total / ctas, (c + 1) total / ctas).
-DEV int att_owner(long long x, long long total, int ctas) { return (int)(((x + 1) * ctas - 1) / total); }
+DEV int att_owner(long long x, long long total, int ctas) { return (int)att_div((x + 1) * ctas - 1, total); }
 
 struct AttShared {
-    long long *prefix;  // [batch + 1]: pages of all units before each sequence
+    long long *prefix;  // [batch + 1]: work items before each sequence
     int4 *seq;          // [batch]: AttSeq without hi
     float2 *scale;      // [ring]: (K scale, V scale), K scale < 0: page not loaded
     uint64_t *full_k, *full_v, *empty_k, *empty_v;
@@ -106,9 +155,6 @@ struct AttShared {
     int *ctrl;          // [0] abort
     uint8_t *ring;      // [ring][K page, V page]
 };
-
-// Tiles of rt rows: 8 NT rows a warp, rt / (8 NT) warps side by side
-__host__ __device__ constexpr int att_nt(int rt) { return rt == 8 ? 1 : 2; }
 
 __host__ __device__ constexpr int att_fixed_bytes(int D, int nt) {
     return ATT_WARPS * 8 * nt * (D + 4) * 4 + ATT_WARPS * 8 * nt * 2 * 4 + ATT_MAXRING * (8 + 32 + 8) + 16;
@@ -142,7 +188,7 @@ DEV AttShared att_shared(const AttParams &p) {
     return s;
 }
 
-// Work item x (a page of a unit) belongs to the last sequence b with prefix[b] <= x that has any.
+// Work item x belongs to the last sequence b with prefix[b] <= x that has any.
 DEV int att_find(const long long *prefix, int batch, long long x) {
     int a = 0, z = batch;
     while (z - a > 1) {
@@ -152,9 +198,6 @@ DEV int att_find(const long long *prefix, int batch, long long x) {
     }
     return a;
 }
-// A quotient that mostly fits 32 bits.
-DEV long long att_div(long long a, int b) { return a <= 0xffffffffll ? (long long)((uint32_t)a / (uint32_t)b) : a / b; }
-
 // The pages of a sequence that the rows of one of its tiles see: [lo, hi).
 template <int P, int RT>
 DEV void att_tile_pages(const AttParams &p, const int4 &q, int tile, int &lo, int &hi) {
@@ -165,53 +208,65 @@ DEV void att_tile_pages(const AttParams &p, const int4 &q, int tile, int &lo, in
     lo = p.window > 0 ? max(0, bottom - p.window + 1) / P : 0;
 }
 
-// One range of pages of one unit, as the consumer warps walk them.
+// One range of pages of one unit, as every warp of the CTA walks them.  A page
+// belongs to the CTA in whose range its first item lies.
 struct AttSeg {
-    int tile, h, pg, n;       // pages [pg, pg + n) of the sequence
+    int b, tile, h, pg, n;    // pages [pg, pg + n) of the sequence
     int q0, cnt, len;
     bool whole;               // the unit's every page
-    bool first;               // the CTA's first range
+    bool head;                // the unit's first page among them
 };
 
-DEV void att_range(const AttParams &p, long long total, long long &x, long long &end) {
-    const int ctas = max(1, att_used(total, p.ctas));
-    x = end = 0;
-    if ((int)blockIdx.x < ctas) {
-        x = (long long)blockIdx.x * total / ctas;
-        end = (long long)(blockIdx.x + 1) * total / ctas;
-    }
-}
-
-template <int P>
+template <int P, int RT>
 struct AttWalk {
     const AttParams &p;
     const AttShared &s;
     long long x, end;
     int b;
-    bool first = true;
     DEV AttWalk(const AttParams &p_, const AttShared &s_) : p(p_), s(s_) {
-        att_range(p, s.prefix[p.batch], x, end);
+        const long long total = s.prefix[p.batch];
+        const int ctas = att_used<RT>(total, p.ctas);
+        x = end = 0;
+        if ((int)blockIdx.x < ctas) {
+            x = att_div((long long)blockIdx.x * total, ctas);
+            end = att_div((long long)(blockIdx.x + 1) * total, ctas);
+        }
         b = att_find(s.prefix, p.batch, x);
     }
     DEV bool next(AttSeg &g) {
-        if (x >= end) return false;
-        while (s.prefix[b + 1] <= x) ++b;
-        const int4 q = s.seq[b];
-        const int np = (q.z + P - 1) / P - q.w;
-        const long long r = x - s.prefix[b];
-        const int unit = (int)att_div(r, np), pg = (int)(r - (long long)unit * np);
-        g.n = (int)min((long long)(np - pg), end - x);
-        x += g.n;
-        g.tile = unit / p.c.hkv;
-        g.h = unit - g.tile * p.c.hkv;
-        g.pg = q.w + pg;
-        g.q0 = q.x;
-        g.cnt = q.y;
-        g.len = q.z;
-        g.whole = g.n == np;
-        g.first = first;
-        first = false;
-        return true;
+        while (x < end) {
+            while (s.prefix[b + 1] <= x) ++b;
+            const int4 q = s.seq[b];
+            const int np = (q.z + P - 1) / P - q.w, rows = q.y * p.group, tiles = (rows + RT - 1) / RT;
+            // the full tiles' units, then the last tile's
+            constexpr int FULL_SIDE = RT / (8 * att_nt(RT));
+            long long r = x - s.prefix[b];
+            const long long full = (long long)(tiles - 1) * p.c.hkv * np * FULL_SIDE;
+            const bool last = r >= full;
+            const int side = last ? att_side<RT>(rows - (tiles - 1) * RT) : FULL_SIDE;
+            if (last) r -= full;
+            const long long items = (long long)np * side;
+            int unit = (int)att_div(r, items);
+            const int within = (int)(r - unit * items);
+            if (last) unit += (tiles - 1) * p.c.hkv;
+            const int first = (within + side - 1) / side;  // the first page that begins at or after x
+            const long long left = items - within;         // items to the unit's end
+            const int until = left <= end - x ? np : (within + (int)(end - x) + side - 1) / side;
+            x += min(left, end - x);
+            if (first >= until) continue;
+            g.b = b;
+            g.tile = unit / p.c.hkv;
+            g.h = unit - g.tile * p.c.hkv;
+            g.pg = q.w + first;
+            g.n = until - first;
+            g.q0 = q.x;
+            g.cnt = q.y;
+            g.len = q.z;
+            g.whole = g.n == np;
+            g.head = first == 0;
+            return true;
+        }
+        return false;
     }
 };
 
@@ -245,41 +300,49 @@ template <int D, int P, int RT>
 DEV void att_produce(const AttParams &p, const AttShared &s) {
     constexpr int PAGE = P * D;
     const int lane = threadIdx.x % 32;
-    long long x, end;
-    att_range(p, s.prefix[p.batch], x, end);
-    const bool mine = lane < p.ring;
     uint8_t *dst = s.ring + (size_t)lane * 2 * PAGE;
-    // page number (-1: not loaded) and kv head of this lane's next page
-    const auto look = [&](long long i, int &id, int &h) {
+    AttWalk<P, RT> walk(p, s);
+    AttSeg g;
+    bool more = walk.next(g);
+    int before = 0;  // pages of the ranges done
+    // The CTA's page number base + lane: this lane's next (want), its number
+    // (-1: not loaded) and its kv head.
+    const auto look = [&](int base, bool &want, int &id, int &h) {
+        want = false;
         id = -1;
         h = 0;
-        if (!mine || i >= end) return;
-        int b = att_find(s.prefix, p.batch, i);
-        while (s.prefix[b + 1] <= i) ++b;
-        const int4 q = s.seq[b];
-        const int np = (q.z + P - 1) / P - q.w;
-        const long long r = i - s.prefix[b];
-        const int unit = (int)att_div(r, np), pg = q.w + (int)(r - (long long)unit * np);
-        const int tile = unit / p.c.hkv;
-        h = unit - tile * p.c.hkv;
-        int lo, hi;
-        att_tile_pages<P, RT>(p, q, tile, lo, hi);
-        if (pg < lo || pg >= hi) return;
-        id = p.table[(size_t)b * p.width + pg];
-        if ((unsigned)id >= (unsigned)p.c.pages) {
-            note_failure(p.c.status, MK_ERR_DEVICE_CHECK, b, pg * P, id);
-            id = -1;
+        int b = -1, pg = 0;
+        while (more) {
+            const int k = base + lane - before;
+            if (lane < p.ring && k >= 0 && k < g.n) {
+                want = true;
+                h = g.h;
+                pg = g.pg + k;
+                int lo, hi;
+                att_tile_pages<P, RT>(p, make_int4(g.q0, g.cnt, g.len, 0), g.tile, lo, hi);
+                if (pg >= lo && pg < hi) b = g.b;
+            }
+            if (before + g.n >= base + p.ring) break;
+            before += g.n;
+            more = walk.next(g);
+        }
+        if (b >= 0) {  // all lanes' table entries at once
+            id = p.table[(size_t)b * p.width + pg];
+            if ((unsigned)id >= (unsigned)p.c.pages) {
+                note_failure(p.c.status, MK_ERR_DEVICE_CHECK, b, pg * P, id);
+                id = -1;
+            }
         }
     };
+    bool want;
     int id, h;
-    look(x + lane, id, h);
+    look(0, want, id, h);
     uint32_t turn = 0, k_fills = 0, v_fills = 0;
     bool ok = true;
-    for (; x < end && ok; x += p.ring, ++turn) {
-        const bool want = mine && x + lane < end;
+    for (; ok && __any_sync(FULL, want); ++turn) {
         const size_t at = (size_t)(id < 0 ? 0 : id) * p.c.hkv + h;
         float2 sc = make_float2(-1.f, 0.f);
-        if (want && id >= 0) sc = make_float2(p.c.ks[at], p.c.vs[at]);
+        if (id >= 0) sc = make_float2(p.c.ks[at], p.c.vs[at]);
         const int now = id;
         bool k_todo = want, v_todo = want;
         const uint32_t ph = (turn & 1) ^ 1;
@@ -306,7 +369,7 @@ DEV void att_produce(const AttParams &p, const AttShared &s) {
             v_todo = v_todo && !v;
             k_fills += k;
             v_fills += v;
-            if (spin == 0) look(x + p.ring + lane, id, h);  // the next turn's pages, while this one's slots come free
+            if (spin == 0) look(((int)turn + 1) * p.ring, want, id, h);  // the next turn's, while this one's slots come free
             if (spin > 256) {
                 __nanosleep(spin > 4096 ? 1000 : 100);
                 const bool give_up = spin > 4000000 || *reinterpret_cast<volatile int *>(s.ctrl);  // a few seconds
@@ -392,33 +455,42 @@ DEV float att_load_q(const uint16_t *row, int t, uint32_t (&qb)[D / 64][8]) {
     return big >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(254 - up) << 23);
 }
 
+// n arrivals at once
+DEV void mbar_arrive_n(uint64_t *b, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(b)), "r"(n) : "memory");
+}
 DEV void att_consumer_bar() { asm volatile("bar.sync 1, %0;" ::"n"(ATT_WARPS * 32) : "memory"); }
 
 template <int D, int P, int RT>
 DEV void att_consume(const AttParams &p, const AttShared &s) {
-    constexpr int NT = att_nt(RT), WT = RT / (8 * NT), NG = ATT_WARPS / WT;  // row tiles a warp, warps a tile, page groups
+    constexpr int NT = att_nt(RT), WT = RT / (8 * NT);  // 8-row tiles a warp, warps for a full tile
     constexpr int PAGE = P * D, RUN = P / 4, NM = P / 16, ND = D / 16, LD = D + 4;
+    constexpr bool QS = NT > 1;  // the query operand in shared memory (registers would spill)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g8 = lane / 4, t = lane % 4;
-    const int wt = warp % WT, grp = warp / WT;
-    AttWalk<P> walk(p, s);
+    AttWalk<P, RT> walk(p, s);
     AttSeg g;
     bool ok = true;
-    // this warp's pages are those of the CTA's ranges with number grp, grp + NG, ...; `mine` is the next one's, in
-    // ring slot st at phase ph; `before` counts the pages of the ranges done
-    int mine = grp, before = 0, st = grp;
-    uint32_t ph = 0;
-    const auto settle = [&] {
-        while (st >= p.ring) {
-            st -= p.ring;
-            ph ^= 1;
-        }
-    };
-    settle();
+    int before = 0;  // pages of the CTA's ranges done
     while (walk.next(g)) {
-        const int rows = g.cnt * p.group, row0 = g.tile * RT + wt * 8 * NT, base = g.len - g.cnt;
+        const int rows = g.cnt * p.group, base = g.len - g.cnt;
+        // as many warps side by side as the tile's rows need (1, 2 or 4), the
+        // others on other pages: group grp takes every ng-th page of the range
+        const int side = att_side<RT>(rows - g.tile * RT);
+        const int wt = warp % side, grp = warp / side, ng = ATT_WARPS / side;
+        const int row0 = g.tile * RT + wt * 8 * NT;
+        int st = (before + grp) % p.ring;  // ring slot and phase of this warp's next page
+        uint32_t ph = ((before + grp) / p.ring) & 1;
+        const auto settle = [&] {
+            while (st >= p.ring) {
+                st -= p.ring;
+                ph ^= 1;
+            }
+        };
         const auto pos_of = [&](int r) { return r < rows ? base + r / p.group : -1; };  // a row sees [least, pos]
         const auto least_of = [&](int pos) { return p.window > 0 ? max(0, pos - p.window + 1) : 0; };
-        uint32_t qb[NT][D / 64][8];
+        uint32_t qb[QS ? 1 : NT][D / 64][8];
+        // fragment j of tile n: qs[((n * D / 64 + h2) * 2 + j) * 32 + lane]
+        uint4 *qs = reinterpret_cast<uint4 *>(s.merge) + wt * (NT * D / 32) * 32;
         float f[NT][2], m[NT][2], l[NT][2], o[NT][ND][4];
         int pos[NT][2];
         int all_hi = INT_MAX, all_lo = 0;  // pages within need no masks
@@ -432,7 +504,13 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                 all_hi = min(all_hi, base + tok);
                 all_lo = max(all_lo, least_of(base + tok));
             }
-            const float qf = att_load_q<D>(qrow, t, qb[n]) * p.scale_log2;
+            const float qf = att_load_q<D>(qrow, t, qb[QS ? 0 : n]) * p.scale_log2;
+            if constexpr (QS)
+                if (grp == 0)
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i)
+                        qs[(n * (D / 32) + i) * 32 + lane] = make_uint4(qb[0][i / 2][4 * (i % 2)], qb[0][i / 2][4 * (i % 2) + 1],
+                                                                        qb[0][i / 2][4 * (i % 2) + 2], qb[0][i / 2][4 * (i % 2) + 3]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {  // its columns of the products
                 f[n][e] = __shfl_sync(FULL, qf, 8 * t + 4 * e);
@@ -445,7 +523,8 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
         }
         all_hi = __reduce_min_sync(FULL, all_hi);
         all_lo = __reduce_max_sync(FULL, all_lo);
-        for (; mine < before + g.n; mine += NG, st += NG, settle()) {
+        if constexpr (QS) att_consumer_bar();
+        for (int mine = before + grp; mine < before + g.n; mine += ng, st += ng, settle()) {
             const int pg = g.pg + mine - before;
             if (ok) ok = att_wait(p, s, &s.has_k[st], mine, &s.full_k[st], ph);
             ok = __all_sync(FULL, ok);
@@ -472,6 +551,12 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                             x[i] = *reinterpret_cast<const uint2 *>(kr + 4 * i * D + h2 * 64 + 8 * jj);
                             y[i] = *reinterpret_cast<const uint2 *>(kr + (4 * i + 2) * D + h2 * 64 + 8 * jj);
                         }
+                        uint4 qj[NT];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            if constexpr (QS) qj[n] = qs[(n * (D / 32) + 2 * h2 + jj) * 32 + lane];
+                            else qj[n] = make_uint4(qb[n][h2][4 * jj], qb[n][h2][4 * jj + 1], qb[n][h2][4 * jj + 2], qb[n][h2][4 * jj + 3]);
+                        }
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -482,11 +567,11 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                                 e4m3x4_to_half2(yw, a1, a3);
 #pragma unroll
                                 for (int n = 0; n < NT; ++n)
-                                    att_mma(c[n][i], a0, a1, a2, a3, qb[n][h2][4 * jj + 2 * j], qb[n][h2][4 * jj + 2 * j + 1]);
+                                    att_mma(c[n][i], a0, a1, a2, a3, j ? qj[n].z : qj[n].x, j ? qj[n].w : qj[n].y);
                             }
                     }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.empty_k[st]);  // K is read: the next one loads during the rest
+                if (lane == 0) mbar_arrive_n(&s.empty_k[st], WT / side);  // K is read: the next one loads during the rest
                 const int first = pg * P + RUN * (g8 >> 1) + (g8 & 1);  // token of c[.][0][0]; [i][2u + e]: + 4 i + 2 u
                 float alpha[NT][2];
                 uint32_t pb[NT][NM][2];
@@ -605,12 +690,13 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
             }
             __syncwarp();
             if (lane == 0) {
-                if (!there) mbar_arrive(&s.empty_k[st]);
-                mbar_arrive(&s.empty_v[st]);
+                if (!there) mbar_arrive_n(&s.empty_k[st], WT / side);
+                mbar_arrive_n(&s.empty_v[st], WT / side);
             }
         }
         before += g.n;
-        // merge the NG warps of each tile
+        // merge the ng warps of each tile
+        if constexpr (QS) att_consumer_bar();  // the query operand lies where the sums go
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float *mo = s.merge + ((warp * NT + n) * 8 + 2 * t) * LD + g8;
@@ -631,16 +717,17 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
         att_consumer_bar();
         for (int i = threadIdx.x; i < RT * (D / 4); i += ATT_WARPS * 32) {
             const int row = i / (D / 4), d4 = i % (D / 4);
-            // row of the tile -> (warp side by side, row of the warp); group k is WT warps further
-            const auto at = [&](int k) { return (k * WT + row / (8 * NT)) * 8 * NT + row % (8 * NT); };
+            const int rr = g.tile * RT + row;
+            if (rr >= rows) continue;
+            // row of the tile -> (warp side by side, row of the warp); group k is `side` warps further
+            const auto at = [&](int k) { return (k * side + row / (8 * NT)) * 8 * NT + row % (8 * NT); };
             float big = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < NG; ++k) big = fmaxf(big, s.ml[at(k) * 2]);
+            for (int k = 0; k < ng; ++k) big = fmaxf(big, s.ml[at(k) * 2]);
             const float mu = big == -INFINITY ? 0.f : big;
             float sum = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < NG; ++k) {
+#pragma unroll 4
+            for (int k = 0; k < ng; ++k) {
                 const float a = exp2_fast(s.ml[at(k) * 2] - mu);
                 const float4 x = *reinterpret_cast<const float4 *>(s.merge + at(k) * LD + 4 * d4);
                 sum = fmaf(a, s.ml[at(k) * 2 + 1], sum);
@@ -649,8 +736,6 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                 acc.z = fmaf(a, x.z, acc.z);
                 acc.w = fmaf(a, x.w, acc.w);
             }
-            const int rr = g.tile * RT + row;
-            if (rr >= rows) continue;
             if (g.whole) {
                 const int64_t token = g.q0 + rr / p.group;
                 const int hd = g.h * p.group + rr % p.group;
@@ -660,7 +745,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                 if (p.lse && d4 == 0)
                     p.lse[token * (p.group * p.c.hkv) + hd] = att_lse(big, sum);
             } else {
-                const size_t slot = ((size_t)blockIdx.x * 2 + (g.first ? 0 : 1)) * RT + row;
+                const size_t slot = ((size_t)blockIdx.x * 2 + (g.head ? 1 : 0)) * RT + row;
                 *reinterpret_cast<float4 *>(p.part_o + slot * D + 4 * d4) = acc;
                 if (d4 == 0) *reinterpret_cast<float2 *>(p.part_ml + slot * 2) = make_float2(big, sum);
             }
@@ -676,7 +761,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) cache_attend_kernel(const AttP
     const int tid = threadIdx.x;
     for (int b = tid; b < p.batch; b += ATT_THREADS) {
         const AttSeq q = att_seq<P>(p, b, blockIdx.x == 0);
-        s.prefix[b + 1] = (long long)((q.cnt * p.group + RT - 1) / RT) * (q.hi - q.lo) * p.c.hkv;
+        s.prefix[b + 1] = att_items<RT>(p, q.cnt, q.hi - q.lo);
         s.seq[b] = make_int4(q.q0, q.cnt, q.len, q.lo);
     }
     if (tid >= ATT_THREADS - 32 && tid - (ATT_THREADS - 32) < p.ring) {
@@ -688,41 +773,27 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) cache_attend_kernel(const AttP
         mbar_init(&s.empty_v[i], RT / (8 * att_nt(RT)));
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (tid == 0) {
-        s.prefix[0] = 0;
-        s.ctrl[0] = 0;
-    }
-    __syncthreads();
-    if (tid < 32) {  // running sums, 32 sequences at a time
-        long long carry = 0;
-        for (int b0 = 0; b0 < p.batch; b0 += 32) {
-            const int b = b0 + tid;
-            long long v = b < p.batch ? s.prefix[b + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(FULL, v, o);
-                if (tid >= o) v += u;
-            }
-            v += carry;
-            if (b < p.batch) s.prefix[b + 1] = v;
-            carry = __shfl_sync(FULL, v, 31);
-        }
-    }
-    __syncthreads();
-    if (blockIdx.x == 0)
-        for (int b = tid; b <= p.batch; b += ATT_THREADS) p.prefix[b] = s.prefix[b];
+    if (tid == 0) s.ctrl[0] = 0;
+    att_running(s.prefix, p.batch);
     if (tid >= ATT_WARPS * 32) att_produce<D, P, RT>(p, s);
     else att_consume<D, P, RT>(p, s);
 }
 
 // One warp per query row: rows that see nothing get zeros, rows whose pages
 // two or more CTAs shared are merged, in the order of the CTAs; the others
-// are written already.
-template <int D, int P>
-__global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p, int rt) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x % 32, heads = p.group * p.c.hkv;
-    const int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+// are written already.  All that does not need the main kernel's results (the
+// sequences' running page counts again, the row's sequence) runs while that
+// one still does.
+template <int D, int P, int RT>
+__global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
+    long long *prefix = reinterpret_cast<long long *>(mk_smem);
+    const int tid = threadIdx.x, lane = tid % 32, heads = p.group * p.c.hkv;
+    for (int b = tid; b < p.batch; b += 256) {
+        const AttSeq q = att_seq<P>(p, b, false);
+        prefix[b + 1] = att_items<RT>(p, q.cnt, q.hi - q.lo);
+    }
+    att_running(prefix, p.batch);
+    const int64_t w = (int64_t)blockIdx.x * 8 + tid / 32;
     if (w >= (int64_t)p.tokens * heads) return;
     const int token = (int)(w / heads), head = (int)(w % heads);
     int b;
@@ -747,21 +818,33 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p, int
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     float big = -INFINITY, sum = 0.f;
     if (np > 0) {
-        const long long total = p.prefix[p.batch], x0 = p.prefix[b] + ((long long)(r / rt) * p.c.hkv + h) * np;
-        const int ctas = att_used(total, p.ctas);
-        const int c0 = att_owner(x0, total, ctas), c1 = att_owner(x0 + np - 1, total, ctas);
+        const int rows = s.cnt * p.group, tile = r / RT, side = att_side<RT>(rows - tile * RT);
+        const long long total = prefix[p.batch];
+        const long long x0 = prefix[b] + (long long)tile * p.c.hkv * np * att_side<RT>(RT) + (long long)h * np * side;
+        const int ctas = att_used<RT>(total, p.ctas);
+        const int c0 = att_owner(x0, total, ctas), c1 = att_owner(x0 + (long long)(np - 1) * side, total, ctas);
         if (c0 == c1) return;
-        for (int c = c0; c <= c1; ++c) {
-            // the unit is the CTA's first range unless it begins inside the CTA's
-            const int k = c == c0 && x0 > (long long)c * total / ctas ? 1 : 0;
-            const size_t slot = ((size_t)c * 2 + k) * rt + r % rt;
-            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + slot * 2);
-            const float top = fmaxf(big, ml.x), mu = top == -INFINITY ? 0.f : top;
+        const auto slot = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * RT + r % RT; };  // c0 has the unit's head
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        for (int c = c0; c <= c1; c += 32) {  // the maxima first, 32 CTAs at a time
+            const int mine = c + lane;
+            const float2 ml = mine <= c1 ? *reinterpret_cast<const float2 *>(p.part_ml + slot(mine) * 2)
+                                         : make_float2(-INFINITY, 0.f);
+            const float top = fmaxf(big, warp_max(ml.x)), mu = top == -INFINITY ? 0.f : top;
             const float a = exp2_fast(big - mu), e = exp2_fast(ml.x - mu);
             big = top;
-            sum = fmaf(sum, a, ml.y * e);
+            sum *= a;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(acc[i], a, p.part_o[slot * D + lane * V + i] * e);
+            for (int i = 0; i < V; ++i) acc[i] *= a;
+            const int n = min(32, c1 - c + 1);
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) {
+                const float ej = __shfl_sync(FULL, e, j), lj = __shfl_sync(FULL, ml.y, j);
+                const float *o = p.part_o + slot(c + j) * D + lane * V;
+                sum = fmaf(lj, ej, sum);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(o[i], ej, acc[i]);
+            }
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -773,7 +856,7 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p, int
 
 struct AttPlan {
     int rt, ctas;
-    uint64_t prefix_bytes, ml_bytes, o_bytes;
+    uint64_t ml_bytes, o_bytes;
 };
 
 static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, AttPlan &pl) {
@@ -798,7 +881,6 @@ static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, AttPlan &pl
     const int64_t rows = (int64_t)std::max(1, std::min(a->max_tokens, a->tokens)) * (a->q_heads / c->kv_heads);
     pl.rt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     pl.ctas = sms;
-    pl.prefix_bytes = ((uint64_t)(a->batch + 1) * 8 + 255) / 256 * 256;
     pl.ml_bytes = ((uint64_t)sms * 2 * pl.rt * 8 + 255) / 256 * 256;
     pl.o_bytes = (uint64_t)sms * 2 * pl.rt * c->head_dim * 4;
     return MK_OK;
@@ -809,6 +891,11 @@ template <int D, int P>
 static AttFn att_kernel(int rt) {
     return rt == 8 ? cache_attend_kernel<D, P, 8> : rt == 16 ? cache_attend_kernel<D, P, 16>
          : rt == 32 ? cache_attend_kernel<D, P, 32> : cache_attend_kernel<D, P, 64>;
+}
+template <int D, int P>
+static AttFn att_merge_kernel(int rt) {
+    return rt == 8 ? cache_attend_merge<D, P, 8> : rt == 16 ? cache_attend_merge<D, P, 16>
+         : rt == 32 ? cache_attend_merge<D, P, 32> : cache_attend_merge<D, P, 64>;
 }
 
 }  // namespace mk
@@ -821,7 +908,7 @@ int mk_cache_attend_workspace(const mk_cache_desc *cache, const mk_attend_desc *
     AttPlan pl;
     if (!bytes) return set_error(MK_ERR_INVALID, "bytes is null");
     if (int rc = att_plan(cache, attend, pl)) return rc;
-    *bytes = pl.prefix_bytes + pl.ml_bytes + pl.o_bytes;
+    *bytes = pl.ml_bytes + pl.o_bytes;
     return MK_OK;
 }
 
@@ -840,7 +927,7 @@ int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc 
     for (int i = 0; i < 2; ++i)
         if (a->q_stride[i] % 8 || a->out_stride[i] % 8)
             return set_error(MK_ERR_INVALID, "q and out strides must be multiples of 8 elements");
-    if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < pl.prefix_bytes + pl.ml_bytes + pl.o_bytes)
+    if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < pl.ml_bytes + pl.o_bytes)
         return set_error(MK_ERR_INVALID, "workspace missing, unaligned (16 bytes) or too small");
     const int D = cache->head_dim, P = cache->page_tokens;
     const size_t layer_rows = (size_t)layer * cache->pages * cache->kv_heads;
@@ -867,9 +954,8 @@ int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc 
     p.scale_log2 = a->scale * 1.4426950408889634f;
     p.ctas = pl.ctas;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    p.prefix = reinterpret_cast<long long *>(ws);
-    p.part_ml = reinterpret_cast<float *>(ws + pl.prefix_bytes);
-    p.part_o = reinterpret_cast<float *>(ws + pl.prefix_bytes + pl.ml_bytes);
+    p.part_ml = reinterpret_cast<float *>(ws);
+    p.part_o = reinterpret_cast<float *>(ws + pl.ml_bytes);
     const int fixed = att_fixed_bytes(D, att_nt(pl.rt)) + att_seq_bytes(p.batch) + 128;
     p.ring = std::min(ATT_MAXRING, (SERVE_SMEM - fixed) / (2 * P * D));
     const int smem = fixed + p.ring * 2 * P * D;
@@ -891,9 +977,10 @@ int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc 
     cfg.stream = st;
     cfg.attrs = &dep;
     cfg.numAttrs = 1;
-    void (*mf)(const AttParams, int) = D == 64 ? (P == 32 ? cache_attend_merge<64, 32> : cache_attend_merge<64, 64>)
-                                               : (P == 32 ? cache_attend_merge<128, 32> : cache_attend_merge<128, 64>);
-    e = cudaLaunchKernelEx(&cfg, mf, (const AttParams)p, pl.rt);
+    cfg.dynamicSmemBytes = (size_t)(p.batch + 1) * 8;
+    AttFn mf = D == 64 ? (P == 32 ? att_merge_kernel<64, 32>(pl.rt) : att_merge_kernel<64, 64>(pl.rt))
+                       : (P == 32 ? att_merge_kernel<128, 32>(pl.rt) : att_merge_kernel<128, 64>(pl.rt));
+    e = cudaLaunchKernelEx(&cfg, mf, (const AttParams)p);
     return e == cudaSuccess ? MK_OK : serve_cuda_fail(e, "attention merge launch");
 }
 
