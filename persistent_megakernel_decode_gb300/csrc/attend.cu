@@ -880,9 +880,12 @@ static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, AttPlan &pl
     // row tiles of 8, 16, 32 or 64 rows: the least that takes a sequence's rows of one kv head
     const int64_t rows = (int64_t)std::max(1, std::min(a->max_tokens, a->tokens)) * (a->q_heads / c->kv_heads);
     pl.rt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    pl.ctas = sms;
-    pl.ml_bytes = ((uint64_t)sms * 2 * pl.rt * 8 + 255) / 256 * 256;
-    pl.o_bytes = (uint64_t)sms * 2 * pl.rt * c->head_dim * 4;
+    // no more CTAs than pages there can be (all tiles' together, each as many items as it has warps side by side)
+    const int64_t side = pl.rt == 64 ? 4 : pl.rt == 32 ? 2 : 1;
+    const int64_t tiles = a->batch + (int64_t)a->tokens * (a->q_heads / c->kv_heads) / pl.rt;
+    pl.ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(1, std::min<int64_t>(tiles * c->kv_heads, INT32_MAX) * a->table_width * side));
+    pl.ml_bytes = ((uint64_t)pl.ctas * 2 * pl.rt * 8 + 255) / 256 * 256;
+    pl.o_bytes = (uint64_t)pl.ctas * 2 * pl.rt * c->head_dim * 4;
     return MK_OK;
 }
 

@@ -17,6 +17,7 @@ import torch
 from . import runtime as rt
 
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+_I32, _BF16 = torch.int32, torch.bfloat16
 
 
 class Kv8Cache:
@@ -47,7 +48,7 @@ class Kv8Cache:
                                   self.status.data_ptr(), L, N, H, P, D)
         self._ref = C.byref(self._desc)  # never changed after this
         self._lib = rt.load()
-        self._sizes = {}  # workspace bytes by (batch, q heads, tokens, most tokens of a sequence, num_sms)
+        self._sizes = {}  # workspace bytes by (batch, table width, q heads, tokens, most tokens of a sequence, num_sms)
 
     @classmethod
     def empty(cls, layers: int, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
@@ -58,20 +59,21 @@ class Kv8Cache:
         return cls(codes(page_tokens, head_dim).view(torch.float8_e4m3fn),
                    codes(head_dim, page_tokens).view(torch.float8_e4m3fn), scale(), scale())
 
-    def _ints(self, b, **tensors):
-        """int32 [b] device arrays, contiguous."""
-        for name, t in tensors.items():
-            if t is not None and (t.dtype is not torch.int32 or t.get_device() != self.index or t.shape != (b,)
-                                  or not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous int32 [{b}] tensor on cuda:{self.index}, got {t.dtype} "
-                                 f"{tuple(t.shape)} on {t.device}")
+    def _ints(self, b, name, t):
+        """An int32 [b] device array, contiguous: its address."""
+        if t.dtype is not _I32 or t.get_device() != self.index or t.shape != (b,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 [{b}] tensor on cuda:{self.index}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
 
     def _table(self, table, b):
-        if (table.dtype is not torch.int32 or table.get_device() != self.index or table.dim() != 2
-                or table.shape[0] != b or not table.is_contiguous()):
+        """Address and width of an int32 [b, width] device array, contiguous."""
+        shape = table.shape
+        if (table.dtype is not _I32 or table.get_device() != self.index or len(shape) != 2 or shape[0] != b
+                or not table.is_contiguous()):
             raise ValueError(f"table must be a contiguous int32 [{b}, width] tensor on cuda:{self.index}, got "
                              f"{table.dtype} {tuple(table.shape)} on {table.device}")
-        return table.shape[1]
+        return table.data_ptr(), shape[1]
 
     # ---- moving tokens ----
     def _move(self, call, k, v, table, start, count, row0, max_count, stream, writes):
@@ -79,21 +81,24 @@ class Kv8Cache:
         if len(shape) != 5 or shape[0] != self.layers or shape[3] != self.kv_heads or shape[4] != self.head_dim:
             raise ValueError(f"k has shape {tuple(shape)}, expected ({self.layers}, B, T, {self.kv_heads}, {self.head_dim})")
         ks, vs, kp, vp = k.stride(), v.stride(), k.data_ptr(), v.data_ptr()
-        for name, t in (("k", k), ("v", v)):
-            rt.check_tensor(name, t, self.index, torch.bfloat16, shape)
+        if (k.dtype is not _BF16 or v.dtype is not _BF16 or k.get_device() != self.index or v.get_device() != self.index
+                or v.shape != shape):
+            for name, t in (("k", k), ("v", v)):
+                rt.check_tensor(name, t, self.index, _BF16, shape)
         if (ks[4] != 1 or vs[4] != 1 or (kp | vp) % 16
                 or (ks[0] | ks[1] | ks[2] | ks[3] | vs[0] | vs[1] | vs[2] | vs[3]) % 8):
             raise ValueError("k and v: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8 elements")
         if writes and any(s[i] == 0 and shape[i] > 1 for s in (ks, vs) for i in ((0, 2, 3) if row0 is not None else (0, 1, 2, 3))):
             raise ValueError("rows that overlap cannot be written")
         b, rows = shape[1], shape[2]
-        width = self._table(table, b)
-        self._ints(b, start=start, count=count, row0=row0)
+        at, width = self._table(table, b)
+        first, n = self._ints(b, "start", start), self._ints(b, "count", count)
+        offset = 0 if row0 is None else self._ints(b, "row0", row0)
         if b == 0 or rows == 0:
             return
-        r = rt.CacheRows(kp, vp, ks[:4], vs[:4], rows, row0.data_ptr() if row0 is not None else 0)
-        rt.launch(self.index, stream, call, self._ref, C.byref(r), table.data_ptr(), width, start.data_ptr(),
-                  count.data_ptr(), b, rows if max_count is None else max_count)
+        r = rt.CacheRows(kp, vp, *ks[:4], *vs[:4], rows, offset)
+        rt.launch(self.index, stream, call, self._ref, C.byref(r), at, width, first, n, b,
+                  rows if max_count is None else max_count)
 
     def store(self, k, v, table, start, count, row0=None, max_count: Optional[int] = None, stream=None):
         """Quantise new tokens into the cache, all layers: row ``row0[b] + i`` (default 0 + i) of sequence b in ``k`` and
@@ -126,19 +131,19 @@ class Kv8Cache:
         hq = shape[-2]
         if packed:
             b = q_start.numel() - 1
-            self._ints(max(b, 0) + 1, q_start=q_start)
+            queries = self._ints(max(b, 0) + 1, "q_start", q_start)
             total, most = shape[0], shape[0] if max_tokens is None else max_tokens
         else:
-            b, most = shape[0], shape[1]
+            b, most, queries = shape[0], shape[1], 0
             total = b * most
             if max_tokens is not None and max_tokens != most:
                 raise ValueError("max_tokens is q's second axis without q_start")
-        width = self._table(table, b)
-        self._ints(b, lens=lens)
+        at, width = self._table(table, b)
+        held = self._ints(b, "lens", lens)
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            out = torch.empty(shape, dtype=_BF16, device=self.device)
         else:
-            rt.check_tensor("out", out, self.index, torch.bfloat16, shape)
+            rt.check_tensor("out", out, self.index, _BF16, shape)
         if lse is None:
             lse = torch.empty(shape[:-1], dtype=torch.float32, device=self.device)
         else:
@@ -150,40 +155,38 @@ class Kv8Cache:
                       or (not packed and b > 1 and (qs[0] != qs[1] * most or os[0] != os[1] * most))):
             raise ValueError("q and out: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8 "
                              "elements, and sequences evenly spaced rows")
-        a = rt.AttendDesc(qp, op, lse.data_ptr(), qs[-3], qs[-2], os[-3], os[-2], table.data_ptr(), lens.data_ptr(),
-                          q_start.data_ptr() if packed else 0, b, width, hq, total, most, window,
-                          D ** -0.5 if scale is None else scale, self.num_sms)
+        a = rt.AttendDesc(qp, op, lse.data_ptr(), qs[-3], qs[-2], os[-3], os[-2], at, held, queries, b, width, hq, total,
+                          most, window, D ** -0.5 if scale is None else scale, self.num_sms)
         own = workspace is None
         if own:
-            workspace = torch.empty(self._workspace(a), dtype=torch.uint8, device=self.device)
+            size = self._sizes.get((b, width, hq, total, most, self.num_sms)) or self._workspace(a)
+            workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
         else:
             rt.check_tensor("workspace", workspace, self.index, torch.uint8)
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
-        rt.launch(self.index, stream, self._lib.mk_cache_attend, self._ref, layer, C.byref(a), workspace.data_ptr(),
-                  workspace.numel())
+            size = workspace.numel()
+        rt.launch(self.index, stream, self._lib.mk_cache_attend, self._ref, layer, C.byref(a), workspace.data_ptr(), size)
         if stream is not None:
             for t in (out, lse) + ((workspace,) if own else ()):  # made on the current stream, used on `stream`
                 t.record_stream(stream)
         return out, lse
 
     def _workspace(self, a) -> int:
-        key = (a.batch, a.q_heads, a.tokens, a.max_tokens, a.num_sms)
-        size = self._sizes.get(key)
-        if size is None:
-            n = C.c_uint64()
-            with torch.cuda.device(self.index):
-                rt._check(self._lib.mk_cache_attend_workspace(self._ref, C.byref(a), C.byref(n)))
-            if len(self._sizes) >= 1024:
-                self._sizes.clear()
-            size = self._sizes[key] = n.value
-        return size
+        n = C.c_uint64()
+        with torch.cuda.device(self.index):
+            rt._check(self._lib.mk_cache_attend_workspace(self._ref, C.byref(a), C.byref(n)))
+        if len(self._sizes) >= 1024:
+            self._sizes.clear()
+        self._sizes[a.batch, a.table_width, a.q_heads, a.tokens, a.max_tokens, a.num_sms] = n.value
+        return n.value
 
-    def attend_workspace(self, batch: int, q_heads: int, max_tokens: int = 1) -> int:
-        """Bytes of workspace :meth:`attend` needs for up to ``batch`` sequences of up to ``max_tokens`` queries."""
+    def attend_workspace(self, batch: int, q_heads: int, max_tokens: int = 1, table_width: int = 1 << 20) -> int:
+        """Bytes of workspace :meth:`attend` needs for up to ``batch`` sequences of up to ``max_tokens`` queries (and
+        ``table_width`` pages)."""
         a = rt.AttendDesc()
-        a.batch, a.q_heads, a.tokens, a.max_tokens, a.table_width = batch, q_heads, batch * max_tokens, max_tokens, 1
-        a.num_sms = self.num_sms
+        a.batch, a.q_heads, a.tokens, a.max_tokens = batch, q_heads, batch * max_tokens, max_tokens
+        a.table_width, a.num_sms = table_width, self.num_sms
         return self._workspace(a)
 
     # ---- pages ----

@@ -119,8 +119,9 @@ class CacheDesc(C.Structure):
 
 
 class CacheRows(C.Structure):
-    _fields_ = [("k", C.c_uint64), ("v", C.c_uint64), ("k_stride", C.c_int64 * 4), ("v_stride", C.c_int64 * 4),
-                ("rows", C.c_int), ("row0", C.c_uint64)]
+    _fields_ = [("k", C.c_uint64), ("v", C.c_uint64)] + [
+        (f"{n}_stride_{x}", C.c_int64) for n in "kv" for x in ("layer", "seq", "token", "head")] + [
+        ("rows", C.c_int), ("row0", C.c_uint64)]
 
 
 class AttendDesc(C.Structure):
@@ -241,6 +242,9 @@ def launch(index: int, stream, call, *args):
         raise MkError(rc, load().mk_last_error().decode())
 
 
+_SETTINGS = ("temperature", "top_k", "top_p", "min_p")
+
+
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, stream=None):
     """Draw one token per row of ``logits`` [B, V] (fp32 or bf16 CUDA tensor, any row stride) with the uniforms ``u``
     [B] (fp32, [0, 1)): temperature, then top-k, top-p, min-p, in this order (``mk_sample`` in ``include/mk.h`` has the
@@ -258,28 +262,30 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     if inner != 1 and v > 1:
         raise ValueError("logits must be contiguous along the vocabulary")
     check_tensor("u", u, index, torch.float32, (b,))
-    values, rows, keep = [], [], [u.contiguous()]
-    for name, x, off, dtype in (("temperature", temperature, 1.0, torch.float32), ("top_k", top_k, 0, torch.int32),
-                                ("top_p", top_p, 1.0, torch.float32), ("min_p", min_p, 0.0, torch.float32)):
+    if not u.is_contiguous():
+        u = u.contiguous()
+    values, rows, keep = [1.0, 0, 1.0, 0.0], [0, 0, 0, 0], [u]
+    for i, x in enumerate((temperature, top_k, top_p, min_p)):
+        if x is None:
+            continue
         if isinstance(x, torch.Tensor):
-            check_tensor(name, x, index, dtype, (b,))
+            check_tensor(_SETTINGS[i], x, index, torch.int32 if i == 1 else torch.float32, (b,))
             if not x.is_contiguous():
                 x = x.contiguous()
             keep.append(x)  # alive until the launch is queued
-            rows.append(x.data_ptr())
-            values.append(off)
+            rows[i] = x.data_ptr()
         else:
-            rows.append(0)
-            values.append(off if x is None else x)
+            values[i] = x
+    device = logits.device
     if tokens is None:
-        tokens = torch.empty((b,), dtype=torch.int32, device=logits.device)
+        tokens = torch.empty((b,), dtype=torch.int32, device=device)
         keep.append(tokens)
     else:
         check_tensor("tokens", tokens, index, torch.int32, (b,))
         if not tokens.is_contiguous():
             raise ValueError("tokens must be contiguous")
-    logprob = torch.empty((b,), dtype=torch.float32, device=logits.device)
-    d = SampleDesc(logits.data_ptr(), stride if b > 1 else v, b, v, logits.dtype is torch.bfloat16, keep[0].data_ptr(),
+    logprob = torch.empty((b,), dtype=torch.float32, device=device)
+    d = SampleDesc(logits.data_ptr(), stride if b > 1 else v, b, v, logits.dtype is torch.bfloat16, u.data_ptr(),
                    tokens.data_ptr(), logprob.data_ptr(), *rows, *values)
     launch(index, stream, load().mk_sample, C.byref(d))
     if stream is not None:

@@ -29,7 +29,7 @@ def desc(**kw):
 
 
 def rows(**kw):
-    r = rt.CacheRows(A, A, (C.c_int64 * 4)(8, 8, 8, 8), (C.c_int64 * 4)(8, 8, 8, 8), 100, 0)
+    r = rt.CacheRows(A, A, *[8] * 8, 100, 0)
     for k, v in kw.items():
         setattr(r, k, v)
     return r
@@ -65,7 +65,7 @@ def test_cache_descriptor_refusals(bad, code):
 
 
 @pytest.mark.parametrize("kw, args", [
-    (dict(k=0), {}), (dict(v=A + 2), {}), (dict(k_stride=(C.c_int64 * 4)(8, 8, 4, 8)), {}), (dict(rows=-1), {}),
+    (dict(k=0), {}), (dict(v=A + 2), {}), (dict(k_stride_token=4), {}), (dict(rows=-1), {}),
     ({}, dict(batch=-1)), ({}, dict(width=0)), ({}, dict(count=-1)), ({}, dict(table=0)), ({}, dict(start=0)),
     ({}, dict(batch=70000))])
 def test_store_and_load_refusals(kw, args):
