@@ -580,19 +580,33 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float fk = f[n][e] * sc.x;
-                        float mx = -INFINITY;
 #pragma unroll
                         for (int i = 0; i < NM; ++i)
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                float z = c[n][i][2 * u + e] * fk;
-                                if (edge) {
+                            for (int u = 0; u < 2; ++u) c[n][i][2 * u + e] *= fk;
+                    }
+                if (__builtin_expect(edge, 0)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int least = least_of(pos[n][e]);
+#pragma unroll
+                            for (int i = 0; i < NM; ++i)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
                                     const int x = first + 4 * i + 2 * u;
-                                    if (x > pos[n][e] || x < least_of(pos[n][e])) z = -INFINITY;
+                                    if (x > pos[n][e] || x < least) c[n][i][2 * u + e] = -INFINITY;
                                 }
-                                c[n][i][2 * u + e] = z;
-                                mx = fmaxf(mx, z);
-                            }
+                        }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(c[n][0][e], c[n][0][2 + e]);
+#pragma unroll
+                        for (int i = 1; i < NM; ++i) mx = fmaxf(mx, fmaxf(c[n][i][e], c[n][i][2 + e]));
                         mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
@@ -618,6 +632,19 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                         for (int u = 0; u < 2; ++u) pb[n][i][u] = transpose8(half2_of(c[n][i][2 * u], c[n][i][2 * u + 1]));
                 ok = att_wait(p, s, &s.has_v[st], mine, &s.full_v[st], ph);
                 ok = __all_sync(FULL, ok);
+                // A masked token's weight is 0, but 0 x NaN is NaN: where masks
+                // apply, NaN codes are taken out, and a product of the mask with
+                // their places says which sums really contain one.
+                bool dirty = false;
+                if (__builtin_expect(edge, 0)) {
+                    uint32_t bad = 0;
+#pragma unroll 1
+                    for (int i = lane; i < PAGE / 16; i += 32) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(vp + 16 * i);
+                        bad |= nan_bytes(x.x) | nan_bytes(x.y) | nan_bytes(x.z) | nan_bytes(x.w);
+                    }
+                    dirty = __any_sync(FULL, bad != 0);
+                }
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
                     uint32_t w[2][RUN / 4];
@@ -632,43 +659,35 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                             w[u][0] = x.x, w[u][1] = x.y;
                         }
                     }
-                    if (edge) {
-                        // A masked token's weight is 0, but 0 x NaN is NaN: NaN
-                        // codes are taken out, and a product of the mask with
-                        // their places says which sums really contain one.
-                        uint32_t bad = 0;
+                    if (__builtin_expect(dirty, 0)) {
+                        uint32_t at[2][RUN / 4];
 #pragma unroll
-                        for (int i = 0; i < RUN / 4; ++i) bad |= nan_bytes(w[0][i]) | nan_bytes(w[1][i]);
-                        if (__any_sync(FULL, bad != 0)) {
-                            uint32_t at[2][RUN / 4];
+                        for (int i = 0; i < RUN / 4; ++i)
 #pragma unroll
-                            for (int i = 0; i < RUN / 4; ++i)
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const uint32_t nb = nan_bytes(w[u][i]);
-                                    w[u][i] &= ~nb;
-                                    at[u][i] = nb & 0x38383838u;  // 1.0
-                                }
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                const int ps = pos_of(row0 + 8 * n + g8), ls = least_of(ps);
-                                float z[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                                for (int i = 0; i < RUN / 4; ++i) {
-                                    uint32_t see[2];
-#pragma unroll
-                                    for (int k = 0; k < 2; ++k) {
-                                        const int x = pg * P + RUN * t + 4 * i + 2 * k;
-                                        see[k] = (x <= ps && x >= ls ? 0x3c00u : 0u) |
-                                                 (x + 1 <= ps && x + 1 >= ls ? 0x3c000000u : 0u);
-                                    }
-                                    att_mma(z, e4m3x2_to_half2(at[0][i]), e4m3x2_to_half2(at[1][i]),
-                                            e4m3x2_to_half2(at[0][i] >> 16), e4m3x2_to_half2(at[1][i] >> 16), see[0], see[1]);
-                                }
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    if (z[k] > 0.f) o[n][d][k] = __uint_as_float(0x7fc00000u);
+                            for (int u = 0; u < 2; ++u) {
+                                const uint32_t nb = nan_bytes(w[u][i]);
+                                w[u][i] &= ~nb;
+                                at[u][i] = nb & 0x38383838u;  // 1.0
                             }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const int ps = pos_of(row0 + 8 * n + g8), ls = least_of(ps);
+                            float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int i = 0; i < RUN / 4; ++i) {
+                                uint32_t see[2];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int x = pg * P + RUN * t + 4 * i + 2 * k;
+                                    see[k] = (x <= ps && x >= ls ? 0x3c00u : 0u) |
+                                             (x + 1 <= ps && x + 1 >= ls ? 0x3c000000u : 0u);
+                                }
+                                att_mma(z, e4m3x2_to_half2(at[0][i]), e4m3x2_to_half2(at[1][i]),
+                                        e4m3x2_to_half2(at[0][i] >> 16), e4m3x2_to_half2(at[1][i] >> 16), see[0], see[1]);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (z[k] > 0.f) o[n][d][k] = __uint_as_float(0x7fc00000u);
                         }
                     }
                     float a[NT][4];
