@@ -74,8 +74,11 @@ struct alignas(16) SmpShared {  // the logits behind it are read 16 bytes at a t
     uint32_t cands;
     unsigned long long red[SMP_WARPS];
     uint32_t red_n[SMP_WARPS];
-    alignas(16) unsigned long long coarse_w[SMP_MAXCTAS][SMP_COARSE], fine_w[SMP_MAXCTAS][SMP_FINE];  // every CTA's
-    alignas(16) uint32_t coarse_n[SMP_MAXCTAS][SMP_COARSE], fine_n[SMP_MAXCTAS][SMP_FINE];
+    // sums over all CTAs, added by them (one set for each of two searches), and
+    // over the found coarse bin's fine bins
+    alignas(16) unsigned long long coarse_w[2][SMP_COARSE];
+    unsigned long long fine_w[SMP_FINE];
+    uint32_t coarse_n[2][SMP_COARSE], fine_n[SMP_FINE];
     uint32_t hist[4][SMP_BINS];                     // count; weight in 16-bit pieces
     unsigned long long ckey[SMP_CAP], cw[SMP_CAP];  // candidates (in CTA 0)
 };
@@ -371,10 +374,11 @@ struct Sampler {
     // target: `need` of the count, or the fraction `share` of the weight.
     // s.bin (-1: there are fewer than `need`), s.before_n / before_w, s.bin_n,
     // and the total weight are the same in every CTA afterwards.
-    DEV void first_bin(bool by_weight, uint32_t need_n, float share, unsigned long long &need, unsigned long long &total) {
+    DEV void first_bin(int set, bool by_weight, uint32_t need_n, float share, unsigned long long &need, unsigned long long &total) {
         const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
         for (int i = tid; i < (by_weight ? 4 : 1) * SMP_BINS; i += SMP_THREADS) s.hist[0][i] = 0;
         if (tid == 0) s.cands = 0;  // before any CTA's gather: a cluster barrier comes first
+        if (tid < SMP_FINE) s.fine_n[tid] = 0, s.fine_w[tid] = 0;
         __syncthreads();
         for (int i = tid * 4; i < n; i += SMP_THREADS * 4) {
             const float4 v = four(i);
@@ -411,24 +415,14 @@ struct Sampler {
             }
             for (int r = tid % T; r < ctas; r += T) {
                 SmpShared *q = cl.map_shared_rank(&s, r);
-                q->coarse_n[rank][c] = cn;
-                q->coarse_w[rank][c] = cw;
+                atomicAdd(&q->coarse_n[set][c], cn);
+                if (by_weight) atomicAdd(&q->coarse_w[set][c], cw);
             }
         }
         cl.sync();
         if (warp == 0) {  // lane: coarse bins 2 lane, 2 lane + 1
-            uint32_t cn[2] = {0, 0};
-            unsigned long long cw[2] = {0, 0};
-#pragma unroll
-            for (int r = 0; r < SMP_MAXCTAS; ++r)
-                if (r < ctas) {
-                    const uint2 a = *reinterpret_cast<const uint2 *>(&s.coarse_n[r][2 * lane]);
-                    const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&s.coarse_w[r][2 * lane]);
-                    cn[0] += a.x;
-                    cn[1] += a.y;
-                    cw[0] += b.x;
-                    cw[1] += b.y;
-                }
+            const uint32_t cn[2] = {s.coarse_n[set][2 * lane], s.coarse_n[set][2 * lane + 1]};
+            const unsigned long long cw[2] = {s.coarse_w[set][2 * lane], s.coarse_w[set][2 * lane + 1]};
             uint32_t pn = cn[0] + cn[1];
             unsigned long long pw = cw[0] + cw[1];
             running(lane, pn, pw);
@@ -460,19 +454,13 @@ struct Sampler {
         if (c >= 0) {
             if (warp < ctas) {
                 const uint32_t *h = cl.map_shared_rank(&s.hist[0][c * SMP_FINE + lane], warp);
-                s.fine_n[warp][lane] = h[0];
-                s.fine_w[warp][lane] = by_weight ? hist_weight(h) : 0;
+                atomicAdd(&s.fine_n[lane], h[0]);
+                if (by_weight) atomicAdd(&s.fine_w[lane], hist_weight(h));
             }
             __syncthreads();
             if (warp == 0) {
-                uint32_t fn = 0;
-                unsigned long long fw = 0;
-#pragma unroll
-                for (int r = 0; r < SMP_MAXCTAS; ++r)
-                    if (r < ctas) {
-                        fn += s.fine_n[r][lane];
-                        fw += s.fine_w[r][lane];
-                    }
+                const uint32_t fn = s.fine_n[lane];
+                const unsigned long long fw = s.fine_w[lane];
                 uint32_t pn = fn;
                 unsigned long long pw = fw;
                 running(lane, pn, pw);
@@ -495,7 +483,7 @@ struct Sampler {
     }
     // inclusive sums over the warp
     DEV static void running(int lane, uint32_t &pn, unsigned long long &pw) {
-#pragma unroll
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t a = __shfl_up_sync(FULL, pn, o);
             const unsigned long long b = __shfl_up_sync(FULL, pw, o);
@@ -707,6 +695,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const SmpParams 
         s.red_n[warp] = low;
     }
     if (tid < 32) s.table[tid] = c_table[tid];
+    if (tid < 2 * SMP_COARSE) s.coarse_n[0][tid] = 0, s.coarse_w[0][tid] = 0;  // before the cluster barrier
     __syncthreads();
     if (tid < ctas) {
         uint32_t lo = ~0u;
@@ -757,11 +746,11 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const SmpParams 
     bool by_k = top_k > 0 && top_k < p.vocab, by_p = top_p < 1.f;
     if (by_k || by_p) {
         unsigned long long need, all;
-        k.first_bin(!by_k, top_k, top_p, need, all);
+        k.first_bin(0, !by_k, top_k, top_p, need, all);
         if (by_k && s.bin < 0) {  // fewer than top_k logits above -inf: no cut there
             by_k = false;
             cl.sync();  // the bins were read
-            if (by_p) k.first_bin(true, 0, top_p, need, all);
+            if (by_p) k.first_bin(1, true, 0, top_p, need, all);
         }
         const int bin = s.bin;
         const uint32_t upto = s.before_n + s.bin_n;
