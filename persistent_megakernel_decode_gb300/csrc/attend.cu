@@ -813,57 +813,58 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
     }
     att_running(prefix, p.batch);
     const int64_t w = (int64_t)blockIdx.x * 8 + tid / 32;
-    if (w >= (int64_t)p.tokens * heads) return;
-    const int token = (int)(w / heads), head = (int)(w % heads);
-    int b;
+    const int token = (int)min(w / heads, (int64_t)p.tokens - 1), head = (int)(w % heads);
+    int b = 0;
     if (p.q_start) {
-        int a = 0, z = p.batch;  // the last b with q_start[b] <= token
-        while (z - a > 1) {
-            const int mid = (a + z) / 2;
-            if (p.q_start[mid] <= token) a = mid;
+        int z = p.batch;  // the last b with q_start[b] <= token
+        while (z - b > 1) {
+            const int mid = (b + z) / 2;
+            if (p.q_start[mid] <= token) b = mid;
             else z = mid;
         }
-        b = a;
     } else {
-        b = token / p.max_tokens;
-        if (b >= p.batch) return;
+        b = min(token / p.max_tokens, p.batch - 1);
     }
     const AttSeq s = att_seq<P>(p, b, false);
-    if (token < s.q0 || token >= s.q0 + s.cnt) return;
     const int np = s.hi - s.lo, h = head / p.group, r = (token - s.q0) * p.group + head % p.group;
+    bool todo = w < (int64_t)p.tokens * heads && token >= s.q0 && token < s.q0 + s.cnt;
+    int c0 = 0, c1 = -1;
+    if (todo && np > 0) {
+        const int rows = s.cnt * p.group, tile = r / RT, side = att_side<RT>(rows - tile * RT);
+        const long long total = prefix[p.batch];
+        const long long x0 = prefix[b] + (long long)tile * p.c.hkv * np * att_side<RT>(RT) + (long long)h * np * side;
+        const int ctas = att_used<RT>(total, p.ctas);
+        c0 = att_owner(x0, total, ctas);
+        c1 = att_owner(x0 + (long long)(np - 1) * side, total, ctas);
+        todo = c0 != c1;
+    }
+    // every thread waits: this grid must not be done before the main kernel is
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!todo) return;
+    const auto slot = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * RT + r % RT; };  // c0 has the unit's head
     constexpr int V = D / 32;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     float big = -INFINITY, sum = 0.f;
-    if (np > 0) {
-        const int rows = s.cnt * p.group, tile = r / RT, side = att_side<RT>(rows - tile * RT);
-        const long long total = prefix[p.batch];
-        const long long x0 = prefix[b] + (long long)tile * p.c.hkv * np * att_side<RT>(RT) + (long long)h * np * side;
-        const int ctas = att_used<RT>(total, p.ctas);
-        const int c0 = att_owner(x0, total, ctas), c1 = att_owner(x0 + (long long)(np - 1) * side, total, ctas);
-        if (c0 == c1) return;
-        const auto slot = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * RT + r % RT; };  // c0 has the unit's head
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        for (int c = c0; c <= c1; c += 32) {  // the maxima first, 32 CTAs at a time
-            const int mine = c + lane;
-            const float2 ml = mine <= c1 ? *reinterpret_cast<const float2 *>(p.part_ml + slot(mine) * 2)
-                                         : make_float2(-INFINITY, 0.f);
-            const float top = fmaxf(big, warp_max(ml.x)), mu = top == -INFINITY ? 0.f : top;
-            const float a = exp2_fast(big - mu), e = exp2_fast(ml.x - mu);
-            big = top;
-            sum *= a;
+    for (int c = c0; c <= c1; c += 32) {  // the maxima first, 32 CTAs at a time
+        const int mine = c + lane;
+        const float2 ml = mine <= c1 ? *reinterpret_cast<const float2 *>(p.part_ml + slot(mine) * 2)
+                                     : make_float2(-INFINITY, 0.f);
+        const float top = fmaxf(big, warp_max(ml.x)), mu = top == -INFINITY ? 0.f : top;
+        const float a = exp2_fast(big - mu), e = exp2_fast(ml.x - mu);
+        big = top;
+        sum *= a;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] *= a;
-            const int n = min(32, c1 - c + 1);
+        for (int i = 0; i < V; ++i) acc[i] *= a;
+        const int n = min(32, c1 - c + 1);
 #pragma unroll 4
-            for (int j = 0; j < n; ++j) {
-                const float ej = __shfl_sync(FULL, e, j), lj = __shfl_sync(FULL, ml.y, j);
-                const float *o = p.part_o + slot(c + j) * D + lane * V;
-                sum = fmaf(lj, ej, sum);
+        for (int j = 0; j < n; ++j) {
+            const float ej = __shfl_sync(FULL, e, j), lj = __shfl_sync(FULL, ml.y, j);
+            const float *o = p.part_o + slot(c + j) * D + lane * V;
+            sum = fmaf(lj, ej, sum);
 #pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] = fmaf(o[i], ej, acc[i]);
-            }
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(o[i], ej, acc[i]);
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;

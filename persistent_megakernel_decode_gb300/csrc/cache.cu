@@ -48,7 +48,8 @@ struct MoveParams {
 };
 
 // The tokens [lo, hi) of sequence b on its slot-th touched page, and that
-// page; false if there are none or a check fails.
+// page's number as the table has it (page_ok checks it: what does not need the
+// page may load meanwhile); false if there are none or a check fails.
 template <int P>
 DEV bool page_span(const MoveParams &m, int b, int slot, int &first, int &lo, int &hi, int &page, int &src0) {
     const int s = m.start[b], n = m.count[b];
@@ -66,12 +67,13 @@ DEV bool page_span(const MoveParams &m, int b, int slot, int &first, int &lo, in
     lo = max(s, first);
     hi = first + min(s - first + n, P);
     src0 = r0 - s;
-    page = m.table[(size_t)b * m.width + j];
-    if ((unsigned)page >= (unsigned)m.c.pages) {
-        if (threadIdx.x % 32 == 0) note_failure(m.c.status, MK_ERR_DEVICE_CHECK, b, first, page);
-        return false;
-    }
+    page = __ldg(&m.table[(size_t)b * m.width + j]);
     return true;
+}
+DEV bool page_ok(const MoveParams &m, int b, int first, int page) {
+    if ((unsigned)page < (unsigned)m.c.pages) return true;
+    if (threadIdx.x % 32 == 0) note_failure(m.c.status, MK_ERR_DEVICE_CHECK, b, first, page);
+    return false;
 }
 
 // Largest finite magnitude of 8 bf16 values, as bf16 bits (they order like
@@ -147,10 +149,6 @@ __global__ void __launch_bounds__(MOVE_THREADS) cache_store_kernel(const MovePar
     const int h = blockIdx.x % m.c.hkv, slot = blockIdx.x / m.c.hkv, b = blockIdx.y, l = blockIdx.z, tid = threadIdx.x;
     int first, lo, hi, page, src0;
     if (!page_span<P>(m, b, slot, first, lo, hi, page, src0)) return;
-    const size_t at = m.c.at(l, page, h);
-    uint8_t *kp = m.c.k + at * (P * D), *vp = m.c.v + at * (P * D);
-    const bool held = first < lo;
-    const float old_k = held ? m.c.ks[at] : 0.f, old_v = held ? m.c.vs[at] : 0.f;
     const uint16_t *ksrc = m.r.k + l * m.r.ks[0] + b * m.r.ks[1] + h * m.r.ks[3];
     const uint16_t *vsrc = m.r.v + l * m.r.vs[0] + b * m.r.vs[1] + h * m.r.vs[3];
     uint4 kx[KN], vx[VN][4];
@@ -172,6 +170,11 @@ __global__ void __launch_bounds__(MOVE_THREADS) cache_store_kernel(const MovePar
                 vx[i][j] = __ldg(reinterpret_cast<const uint4 *>(vsrc + (int64_t)(src0 + t0 + j) * m.r.vs[2]) + c);
         }
     }
+    if (!page_ok(m, b, first, page)) return;
+    const size_t at = m.c.at(l, page, h);
+    uint8_t *kp = m.c.k + at * (P * D), *vp = m.c.v + at * (P * D);
+    const bool held = first < lo;
+    const float old_k = held ? m.c.ks[at] : 0.f, old_v = held ? m.c.vs[at] : 0.f;
 #pragma unroll
     for (int i = 0; i < KN; ++i) ka = max(ka, amax8(kx[i]));
 #pragma unroll
@@ -252,19 +255,21 @@ __global__ void __launch_bounds__(MOVE_THREADS) cache_append_kernel(const MovePa
     for (int slot = 0; slot < 2; ++slot) {  // at most 4 tokens lie on at most two pages
         int first, lo, hi, page, src0;
         if (!page_span<P>(m, b, slot, first, lo, hi, page, src0)) continue;
-        const size_t at = m.c.at(l, page, h);
-        uint8_t *dst = (is_v ? m.c.v : m.c.k) + at * (P * D);
-        float *scale = (is_v ? m.c.vs : m.c.ks) + at;
-        const bool held = first < lo;
-        const float old = held ? *scale : 0.f;
         uint4 x[APPEND_TOKENS];
         uint32_t a = 0;
 #pragma unroll
         for (int j = 0; j < APPEND_TOKENS; ++j) {
             x[j] = make_uint4(0, 0, 0, 0);
             if (busy && lo + j < hi) x[j] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(src0 + lo + j) * st[2]) + c);
-            a = max(a, amax8(x[j]));
         }
+        if (!page_ok(m, b, first, page)) continue;
+        const size_t at = m.c.at(l, page, h);
+        uint8_t *dst = (is_v ? m.c.v : m.c.k) + at * (P * D);
+        float *scale = (is_v ? m.c.vs : m.c.ks) + at;
+        const bool held = first < lo;
+        const float old = held ? *scale : 0.f;
+#pragma unroll
+        for (int j = 0; j < APPEND_TOKENS; ++j) a = max(a, amax8(x[j]));
 #pragma unroll
         for (int o = 1; o < VEC; o <<= 1) a = max(a, __shfl_xor_sync(FULL, a, o));
         const float s = fmaxf(page_scale(a), old);
@@ -318,7 +323,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) cache_load_kernel(const MovePara
     constexpr int VU = (P / 4) * (D / 8), VN = (VU + MOVE_THREADS - 1) / MOVE_THREADS;
     const int h = blockIdx.x % m.c.hkv, slot = blockIdx.x / m.c.hkv, b = blockIdx.y, l = blockIdx.z, tid = threadIdx.x;
     int first, lo, hi, page, src0;
-    if (!page_span<P>(m, b, slot, first, lo, hi, page, src0)) return;
+    if (!page_span<P>(m, b, slot, first, lo, hi, page, src0) || !page_ok(m, b, first, page)) return;
     const size_t at = m.c.at(l, page, h);
     const uint8_t *kp = m.c.k + at * (P * D), *vp = m.c.v + at * (P * D);
     const float sk = m.c.ks[at], sv = m.c.vs[at];

@@ -48,6 +48,7 @@ class Kv8Cache:
                                   self.status.data_ptr(), L, N, H, P, D)
         self._ref = C.byref(self._desc)  # never changed after this
         self._lib = rt.load()
+        self._kept = None  # the default stream's workspace
         self._sizes = {}  # workspace bytes by (batch, table width, q heads, tokens, most tokens of a sequence, num_sms)
 
     @classmethod
@@ -121,8 +122,8 @@ class Kv8Cache:
         [total, Hq, D], sequence b's queries being rows q_start[b] .. q_start[b + 1] - 1 (``max_tokens``: the most of
         one sequence, a hint).  ``window`` > 0: a query sees that many last tokens, itself among them.  Returns (out
         bf16 like q, lse fp32 without the last axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8
-        tensor of at least :meth:`attend_workspace` bytes, used by one call at a time; by default one is allocated per
-        call."""
+        tensor of at least :meth:`attend_workspace` bytes, used by one call at a time; by default calls on the default
+        stream share one that the cache keeps, others allocate their own."""
         D, packed, shape = self.head_dim, q_start is not None, q.shape
         if (q.dtype is not torch.bfloat16 or q.get_device() != self.index or len(shape) != (3 if packed else 4)
                 or shape[-1] != D):
@@ -160,7 +161,13 @@ class Kv8Cache:
         own = workspace is None
         if own:
             size = self._sizes.get((b, width, hq, total, most, self.num_sms)) or self._workspace(a)
-            workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+            if stream is None and torch._C._cuda_getCurrentRawStream(self.index) == 0:
+                # the default stream is one queue for good and cannot be captured: its calls share one workspace
+                workspace = self._kept
+                if workspace is None or workspace.numel() < size:
+                    workspace = self._kept = torch.empty(size, dtype=torch.uint8, device=self.device)
+            else:
+                workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
         else:
             rt.check_tensor("workspace", workspace, self.index, torch.uint8)
             if not workspace.is_contiguous():
