@@ -27,6 +27,8 @@
 // spread over 16 SMs), each CTA keeping its share of the row in shared
 // memory; histograms are joined through distributed shared memory.  What
 // bounds it is latency: the row is read once, then cluster barriers follow.
+// Measured (one GB300, device time): one row of 128,256 with all filters 12.7
+// us (its bytes take 0.08), 16 rows of 151,936 with mixed settings 28 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -615,3 +615,99 @@ def test_session_samples_parks_forks_and_restores():
     assert torch.equal(d.logits, e.logits)
     with pytest.raises(ValueError):
         a.sample(steps, u[0])
+
+
+# ---- arguments ----
+def test_load_into_packed_rows_and_parts_of_a_session():
+    """Packed ragged rows of load; a session's positions from the middle on, stored and brought back."""
+    H, D, P, cnt = 2, 64, 32, [5, 0, 33]
+    c, r = both(1, 8, H, P, D)
+    pages = [[3], [], [6, 0]]
+    fill(c, r, pages, cnt, 120, 1)
+    flat = [torch.full((sum(cnt) + 2, H, D), 7.0, dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+    e = lambda x: x[None, None].expand(1, 3, -1, -1, -1)  # noqa: E731
+    c.load(e(flat[0]), e(flat[1]), table_of(pages), i32([0, 0, 0]), i32(cnt), row0=i32([1, 6, 6]), max_count=33)
+    c.check()
+    for n, t in zip("kv", flat):
+        want = torch.full((sum(cnt) + 2, H, D), 7.0, dtype=torch.bfloat16)
+        for b, at in ((0, 1), (2, 6)):
+            for i in range(cnt[b]):
+                want[at + i] = r.token(n, 0, pages[b], i).to(torch.bfloat16)
+        assert torch.equal(t.cpu(), want)
+    with pytest.raises(ValueError, match="overlap"):
+        c.load(e(flat[0]), e(flat[1]), table_of(pages), i32([0, 0, 0]), i32(cnt))
+    shape = synth.TINY
+    w = synth.make_weights(shape, 41, device=DEV)
+    kc, vc = synth.make_cache(shape, 2, 90, 141, device=DEV)
+    s = rt.Session(shape, w, kc, vc, [80, 60], 1)
+    c = kvcache.Kv8Cache.empty(shape.L, 8, shape.Hkv, shape.D, P, DEV)
+    r = ref.RefCache(shape.L, 8, shape.Hkv, P, shape.D)
+    tab = i32([[0, 1, 2], [3, 4, -1]])
+    s.store_kv(c, tab, i32([40, 0]), i32([40, 60]))
+    k0 = kc.clone()
+    kc.zero_()
+    s.load_kv(c, tab, i32([50, 10]), i32([30, 20]), max_count=30)
+    s.sync()
+    c.check()
+    r.store("k", k0[:, 0, :, 40:80].transpose(1, 2).cpu(), [0, 1, 2], 40)
+    r.store("k", k0[:, 1, :, :60].transpose(1, 2).cpu(), [3, 4], 0)
+    for b, pages, lo, hi in ((0, [0, 1, 2], 50, 80), (1, [3, 4], 10, 30)):
+        for j in range(90):
+            want = torch.stack([r.token("k", l, pages, j) for l in range(shape.L)]) if lo <= j < hi else 0.0
+            assert (kc[:, b, :, j].double().cpu() == want).all()
+
+
+def test_attend_arguments():
+    c, r = both(1, 4, 1, 32, 64)
+    pages = [[2, 1]]
+    fill(c, r, pages, [50], 130, 1)
+    tab, n, q = table_of(pages), i32([50]), gen(1, 1, 2, 64, seed=131).to(DEV)
+    size = c.attend_workspace(1, 2)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device=DEV)
+    want = c.attend(q, tab, n)
+    got = c.attend(q, tab, n, workspace=ws, out=torch.empty_like(q))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # in the place of the queries
+    p = q.clone()
+    assert torch.equal(c.attend(p, tab, n, out=p)[0], want[0])
+    bad = [dict(q=q.float()), dict(q=q[0]), dict(q=q[..., :32]), dict(q=q.cpu()), dict(tab=tab.long()), dict(tab=tab[0]),
+           dict(tab=tab.cpu()), dict(n=n.long()), dict(n=i32([50, 50])), dict(max_tokens=2), dict(out=q.float()),
+           dict(lse=q), dict(workspace=q), dict(q_start=i32([0, 1]))]
+    for kw in bad:
+        a = dict(q=q, tab=tab, n=n)
+        a.update({k: kw[k] for k in a if k in kw})
+        with pytest.raises(ValueError):
+            c.attend(a["q"], a["tab"], a["n"], **{k: v for k, v in kw.items() if k not in a})
+    for kw in (dict(workspace=ws[:16]), dict(layer=1), dict(layer=-1), dict(window=-1), dict(scale=-1.0)):
+        with pytest.raises(rt.MkError):
+            c.attend(q, tab, n, **kw)
+    with pytest.raises(rt.MkError):  # 3 query heads over 2 kv heads
+        d, _ = both(1, 4, 2, 32, 64)
+        d.attend(gen(1, 1, 3, 64, seed=1).to(DEV), tab, n)
+    x = gen(1, 1, 5, 1, 64, seed=2).to(DEV)
+    for args in ((x.float(), x, tab, n, n), (x[:, :, :, :, :32], x, tab, n, n), (x, x[:, :, :4], tab, n, n),
+                 (x, x, tab, n.long(), n), (x, x, tab.cpu(), n, n), (x[..., ::2], x[..., ::2], tab, n, n)):
+        with pytest.raises(ValueError):
+            c.store(*args)
+    with pytest.raises(ValueError):
+        kvcache.Kv8Cache(c.k, c.k, c.k_scale, c.v_scale)
+    with pytest.raises(ValueError):
+        kvcache.Kv8Cache(c.k[:, ::2], c.v[:, ::2], c.k_scale[:, ::2], c.v_scale[:, ::2])
+    with pytest.raises(ValueError):
+        c.copy_pages([0, 1], [2])
+    c.check()
+
+
+def test_no_sequences_and_no_tokens():
+    c, _ = both(1, 4, 1, 32, 64)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    out, lse = c.attend(torch.zeros((0, 1, 2, 64), dtype=torch.bfloat16, device=DEV), none.view(0, 1), none)
+    assert out.shape == (0, 1, 2, 64) and lse.shape == (0, 1, 2)
+    out, lse = c.attend(torch.zeros((0, 2, 64), dtype=torch.bfloat16, device=DEV), i32([[0]]), i32([5]), q_start=i32([0, 0]))
+    assert out.shape == (0, 2, 64)
+    x = torch.zeros((1, 0, 3, 1, 64), dtype=torch.bfloat16, device=DEV)
+    c.store(x, x, none.view(0, 1), none, none)
+    c.load(x, x, none.view(0, 1), none, none)
+    t, lp = rt.sample(torch.zeros((0, 10), device=DEV), torch.zeros(0, device=DEV))
+    assert t.shape == (0,) and lp.shape == (0,)
+    c.check()
