@@ -28,8 +28,8 @@
 // on, and its V operand is one P/4-byte run of a transposed V row.
 //
 // Work split.  The pages of all units (sequence, row tile, kv head) form one
-// axis, each weighted with the warps its tile occupies side by side, cut into
-// equal ranges, one per CTA (one CTA per SM): ragged batches and single long
+// axis, each weighted with the warps its tile occupies side by side, and with
+// a constant for beginning and merging a unit, cut into equal ranges, one per CTA (one CTA per SM): ragged batches and single long
 // sequences balance alike.  A producer warp streams the pages through a
 // shared-memory ring with bulk copies; the consumer warps take them in turn
 // (as many side by side as the tile's rows need) and merge in shared memory.
@@ -108,13 +108,18 @@ DEV int att_side(int rows) {
     const int need = (min(RT, rows) + 8 * att_nt(RT) - 1) / (8 * att_nt(RT));
     return need <= 1 ? 1 : need == 2 ? 2 : 4;
 }
-// Work items of a sequence: its units' pages, each as many items as its tile
-// has warps side by side.  All tiles but the last are full.
+// What beginning and merging a unit costs a CTA, in items (measured: 4 to 5
+// thousand clocks, 375 to 700 an item, with one tile a warp; 10, 525 with two).
+__host__ __device__ constexpr int att_fixed_items(int rt) { return rt == 8 ? 8 : 16; }
+// Work items of a sequence: of each unit the fixed ones, then its pages', each
+// as many as its tile has warps side by side.  All tiles but the last are full.
 template <int RT>
 DEV long long att_items(const AttParams &p, int cnt, int np) {
     const int rows = cnt * p.group, tiles = (rows + RT - 1) / RT;
-    if (tiles == 0) return 0;
-    return (long long)p.c.hkv * np * ((tiles - 1) * att_side<RT>(RT) + att_side<RT>(rows - (tiles - 1) * RT));
+    if (tiles == 0 || np == 0) return 0;
+    constexpr int FIXED = att_fixed_items(RT);
+    return p.c.hkv * ((tiles - 1) * ((long long)np * att_side<RT>(RT) + FIXED) +
+                      (long long)np * att_side<RT>(rows - (tiles - 1) * RT) + FIXED);
 }
 // prefix[1 .. n]: values -> running sums, by the whole block; prefix[0] = 0.
 DEV void att_running(long long *prefix, int n) {
@@ -248,19 +253,20 @@ struct AttWalk {
             const int4 q = s.seq[b];
             const int np = (q.z + P - 1) / P - q.w, rows = q.y * p.group, tiles = (rows + RT - 1) / RT;
             // the full tiles' units, then the last tile's
-            constexpr int FULL_SIDE = RT / (8 * att_nt(RT));
+            constexpr int FULL_SIDE = RT / (8 * att_nt(RT)), FIXED = att_fixed_items(RT);
             long long r = x - s.prefix[b];
-            const long long full = (long long)(tiles - 1) * p.c.hkv * np * FULL_SIDE;
+            const long long full = (long long)(tiles - 1) * p.c.hkv * (np * FULL_SIDE + FIXED);
             const bool last = r >= full;
             const int side = last ? att_side<RT>(rows - (tiles - 1) * RT) : FULL_SIDE;
             if (last) r -= full;
-            const long long items = (long long)np * side;
+            const long long items = (long long)np * side + FIXED;
             int unit = (int)att_div(r, items);
             const int within = (int)(r - unit * items);
             if (last) unit += (tiles - 1) * p.c.hkv;
-            const int first = (within + side - 1) / side;  // the first page that begins at or after x
-            const long long left = items - within;         // items to the unit's end
-            const int until = left <= end - x ? np : (within + (int)(end - x) + side - 1) / side;
+            const long long left = items - within;  // items to the unit's end
+            // the first page that begins at or after x, and at or after the range's end
+            const int first = max(0, within - FIXED + side - 1) / side;
+            const int until = left <= end - x ? np : max(0, within + (int)(end - x) - FIXED + side - 1) / side;
             x += min(left, end - x);
             if (first >= until) continue;
             g.b = b;
@@ -841,7 +847,9 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
     if (todo && np > 0) {
         const int rows = s.cnt * p.group, tile = r / RT, side = att_side<RT>(rows - tile * RT);
         const long long total = prefix[p.batch];
-        const long long x0 = prefix[b] + (long long)tile * p.c.hkv * np * att_side<RT>(RT) + (long long)h * np * side;
+        constexpr int FIXED = att_fixed_items(RT);
+        const long long x0 = prefix[b] + (long long)tile * p.c.hkv * (np * att_side<RT>(RT) + FIXED) +
+                             h * ((long long)np * side + FIXED) + FIXED;  // the first page's item
         const int ctas = att_used<RT>(total, p.ctas);
         c0 = att_owner(x0, total, ctas);
         c1 = att_owner(x0 + (long long)(np - 1) * side, total, ctas);
@@ -912,7 +920,7 @@ static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, AttPlan &pl
     // no more CTAs than pages there can be (all tiles' together, each as many items as it has warps side by side)
     const int64_t side = pl.rt == 64 ? 4 : pl.rt == 32 ? 2 : 1;
     const int64_t tiles = a->batch + (int64_t)a->tokens * (a->q_heads / c->kv_heads) / pl.rt;
-    pl.ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(1, std::min<int64_t>(tiles * c->kv_heads, INT32_MAX) * a->table_width * side));
+    pl.ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(1, std::min<int64_t>(tiles * c->kv_heads, INT32_MAX) * (a->table_width * side + att_fixed_items(pl.rt))));
     pl.ml_bytes = ((uint64_t)pl.ctas * 2 * pl.rt * 8 + 255) / 256 * 256;
     pl.o_bytes = (uint64_t)pl.ctas * 2 * pl.rt * c->head_dim * 4;
     return MK_OK;
