@@ -38,8 +38,8 @@
 // start overlaps) merges them in order: results do not depend on timing.
 //
 // Measured (one GB300, device time): 16 sequences of 16-32K tokens, 32 q / 8
-// kv heads of 128: 129 us, 6.1 TB/s, 89 % of the bytes' time at the copy rate;
-// 8 sequences of 512-4096, heads of 64: 15.8 us, of which the bytes are 2.8
+// kv heads of 128: 127 us, 6.2 TB/s, 91 % of the copy rate; 8 sequences of
+// 512-4096, heads of 64: 13.3 us, of which the bytes are 2.8
 // (two launches, two dependent look-ups, the ramp of the loads and the merge
 // are the rest); 64 new tokens a sequence over 4000: 185 TFLOP/s, bound by the
 // instructions per product that a 16-row operand held in registers costs.
@@ -108,9 +108,12 @@ DEV int att_side(int rows) {
     const int need = (min(RT, rows) + 8 * att_nt(RT) - 1) / (8 * att_nt(RT));
     return need <= 1 ? 1 : need == 2 ? 2 : 4;
 }
-// What beginning and merging a unit costs a CTA, in items (measured: 4 to 5
-// thousand clocks, 375 to 700 an item, with one tile a warp; 10, 525 with two).
-__host__ __device__ constexpr int att_fixed_items(int rt) { return rt == 8 ? 8 : 16; }
+// What beginning and merging a unit costs a CTA, in items.  By the clock 4 to 5
+// thousand clocks, at 375 to 700 an item, with one tile a warp; 10 thousand, at
+// 525, with two.  Measured over six sets of lengths, 8 sequences of the 1B
+// shape / 13 with up to 9 drafted tokens: none 15.8 / 41 us, 4 and 8 items
+// 14.3 / 30, 12 and 24 13.3 / 26.6, 16 and 40 12.7 / 27.3.
+__host__ __device__ constexpr int att_fixed_items(int rt) { return rt == 8 ? 12 : 24; }
 // Work items of a sequence: of each unit the fixed ones, then its pages', each
 // as many as its tile has warps side by side.  All tiles but the last are full.
 template <int RT>
