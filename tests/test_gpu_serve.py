@@ -287,6 +287,22 @@ def test_attend_nan_only_where_it_is_seen():
             assert math.isnan(lse[i, h]) == bool(nan.all())
 
 
+@pytest.mark.parametrize("P, D, G, T", [(32, 64, 2, 1), (64, 128, 4, 12)])
+def test_attend_as_many_sequences_as_a_call_takes(P, D, G, T):
+    rng = random.Random(T)
+    lens = [rng.choice([0, T, T + 1, 45]) for _ in range(1024)]
+    c, r = both(1, 2100, 1, P, D)
+    pages = deal(lens, P, 2100, rng)
+    fill(c, r, pages, lens, 110, 1)
+    q = gen(1024, T, G, D, seed=111)
+    got = c.attend(q.to(DEV), table_of(pages), i32(lens))
+    c.check()
+    some = rng.sample(range(1024), 60) + [0, 1023]
+    check_attend(r, (got[0][some], got[1][some]), q[some], [pages[b] for b in some], [lens[b] for b in some], 0, 0)
+    with pytest.raises(rt.MkError):
+        c.attend(gen(1025, 1, G, D, seed=1).to(DEV), i32([[0]] * 1025), i32([1] * 1025))
+
+
 @pytest.mark.parametrize("P, D, G, T", [(64, 128, 4, 1), (32, 64, 2, 1), (32, 128, 4, 3), (64, 64, 8, 7)])
 @pytest.mark.parametrize("sms", [1, 2, 5])
 def test_attend_many_pages_per_cta(P, D, G, T, sms):
