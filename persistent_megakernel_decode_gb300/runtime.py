@@ -467,7 +467,8 @@ class Session:
 
     def sample(self, step: int, u, temperature=None, top_k=None, top_p=None, min_p=None):
         """Sample the tokens that follow ``step`` from its logits (see :func:`sample`; ``u`` [B]) into ``tokens[step +
-        1]``, where step ``step + 1`` run with ``host_tokens`` reads them.  Returns (tokens, logprob), both [B]."""
+        1]``, where step ``step + 1`` run with ``host_tokens`` reads them.  Runs on the session's stream: ``u`` and the
+        settings must be ready there.  Returns (tokens, logprob), both [B]."""
         if not 0 <= step < self.max_steps:
             raise ValueError(f"step {step} outside the planned {self.max_steps}")
         return sample(self.logits, u, temperature, top_k, top_p, min_p, tokens=self.tokens[step + 1], stream=self.stream)
