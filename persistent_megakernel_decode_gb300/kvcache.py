@@ -152,11 +152,13 @@ class Kv8Cache:
             if not lse.is_contiguous():
                 raise ValueError("lse must be contiguous")
         qs, os, qp, op = q.stride(), out.stride(), q.data_ptr(), out.data_ptr()
-        if total and (qs[-1] != 1 or os[-1] != 1 or (qp | op) % 16 or (qs[-2] | qs[-3] | os[-2] | os[-3]) % 8
-                      or (not packed and b > 1 and (qs[0] != qs[1] * most or os[0] != os[1] * most))):
+        # rows are tokens: one a sequence apart, or the sequences one after the other
+        qt, ot = (qs[0], os[0]) if packed or most == 1 else (qs[1], os[1])
+        if total and (qs[-1] != 1 or os[-1] != 1 or (qp | op) % 16 or (qs[-2] | qt | os[-2] | ot) % 8
+                      or (not packed and b > 1 and (qs[0] != qt * most or os[0] != ot * most))):
             raise ValueError("q and out: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8 "
                              "elements, and sequences evenly spaced rows")
-        a = rt.AttendDesc(qp, op, lse.data_ptr(), qs[-3], qs[-2], os[-3], os[-2], at, held, queries, b, width, hq, total,
+        a = rt.AttendDesc(qp, op, lse.data_ptr(), qt, qs[-2], ot, os[-2], at, held, queries, b, width, hq, total,
                           most, window, D ** -0.5 if scale is None else scale, self.num_sms)
         own = workspace is None
         if own:

@@ -633,6 +633,68 @@ def test_session_samples_parks_forks_and_restores():
         a.sample(steps, u[0])
 
 
+# ---- far and short ----
+def test_offsets_beyond_32_bits():
+    """Pages, token rows and logits whose byte (and element) offsets pass 2^31 and 2^32."""
+    P, D, H, N, n = 64, 128, 8, 70000, 70     # 4.6 GB of K codes
+    c = kvcache.Kv8Cache.empty(1, N, H, D, P, DEV)
+    ids = [N - 1, 40000]
+    r = ref.RefCache(1, 2, H, P, D)
+    far = 2 ** 31 + 4096                      # elements between the two token blocks of the buffer
+    buf = torch.zeros(far + n * H * D + 64, dtype=torch.bfloat16, device=DEV)
+    rows = {k: gen(1, n, H, D, seed=150 + i) for i, k in enumerate("kv")}
+    for i, k in enumerate("kv"):
+        buf.as_strided((1, 1, n, H, D), (0, 0, H * D, D, 1), far * i).copy_(rows[k][:, None])
+        r.store(k, rows[k], [0, 1], 0)
+    k, v = (buf.as_strided((1, 1, n, H, D), (8, 8, H * D, D, 1), far * i) for i in range(2))
+    tab = i32([ids])
+    c.store(k, v, tab, i32([0]), i32([n]))
+    for name in "kv":
+        for j, page in enumerate(ids):
+            x = ref.e4m3_values(getattr(c, name).view(torch.uint8)[0, page].cpu())
+            x = x.transpose(1, 2) if name == "v" else x
+            assert torch.equal(x, r.code[name][0, j])
+    q = gen(1, 1, 2 * H, D, seed=152)
+    check_attend(r, c.attend(q.to(DEV), tab, i32([n])), q, [[0, 1]], [n], 0, 0)
+    c.copy_pages(ids, [7, 60000], table=tab)
+    assert tab.tolist() == [[7, 60000]]
+    check_attend(r, c.attend(q.to(DEV), tab, i32([n])), q, [[0, 1]], [n], 0, 0)
+    back = buf.as_strided((2, 1, n, H, D), (far, 8, H * D, D, 1))  # both blocks as two rows far apart
+    buf.zero_()
+    c.load(back[:1], back[1:], tab, i32([0]), i32([n]))
+    for i, name in enumerate("kv"):
+        want = torch.stack([r.token(name, 0, [0, 1], j) for j in range(n)]).to(torch.bfloat16)
+        assert torch.equal(back[i, 0].cpu(), want)
+    c.check()
+    z = buf.as_strided((2, 1000), (far, 1))
+    x = torch.randn(2, 1000, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    z.copy_(x)
+    u = torch.tensor([0.3, 0.8])
+    check_sample(x, u, rt.sample(z, u.to(DEV), top_p=0.9), [dict(top_p=0.9)] * 2)
+
+
+def test_attend_more_queries_than_tokens_and_spread_rows():
+    """A sequence shorter than its new tokens: the first queries see nothing. One new token a sequence taken out of longer
+    rows, the output into such rows."""
+    P, D, H, G, T = 32, 64, 2, 2, 7
+    lens = [3, 40]
+    c, r = both(1, 4, H, P, D, poison=True)
+    pages = [[3], [0, 2]]
+    fill(c, r, pages, lens, 160, 1)
+    q = gen(2, T, H * G, D, seed=161)
+    for window in (0, 2):
+        got = c.attend(q.to(DEV), table_of(pages), i32(lens), window=window)
+        assert (got[0][0, :4] == 0).all() and (got[1][0, :4] == -math.inf).all()
+        check_attend(r, got, q, pages, lens, 0, window)
+    long, out = q.to(DEV), torch.full((2, 5, H * G, D), 9.0, dtype=torch.bfloat16, device=DEV)
+    got = c.attend(long[:, 6:], table_of(pages), i32(lens), out=out[:, 2:3])
+    check_attend(r, got, q[:, 6:], pages, lens, 0, 0)
+    assert (out[:, :2] == 9).all() and (out[:, 3:] == 9).all()
+    with pytest.raises(ValueError, match="evenly spaced"):
+        c.attend(long[:, 5:], table_of(pages), i32(lens))
+    c.check()
+
+
 # ---- arguments ----
 def test_load_into_packed_rows_and_parts_of_a_session():
     """Packed ragged rows of load; a session's positions from the middle on, stored and brought back."""
