@@ -242,8 +242,10 @@ __global__ void __launch_bounds__(MOVE_THREADS) cache_store_kernel(const MovePar
 // Appending a few tokens (a decode step: one): one warp per (kv head,
 // sequence, layer), the lower lanes on K's vectors of 8 dims, the upper on
 // V's.  The block form above takes a CTA for each, most of whose threads have
-// nothing to do: 36 us against 8.0 for one token of 16 sequences, 36
-// layers, 8 heads of 128 (bound by the latency of three dependent loads).
+// nothing to do.  16 sequences, 36 layers, 8 heads of 128, this form / the
+// block form: 1 token 8.0 / 32 us, 2 13.8 / 37, 4 27.6 / 41, 8 50 / 47, 16 89 /
+// 49 (8 sequences, 16 layers, heads of 64: 3.7 / 6.2, 4.1 / 7.0, 6.0 / 7.5, 10.6
+// / 8.3, 14.8 / 8.3).  A token's V is one byte in each of D sectors of its page.
 constexpr int APPEND_TOKENS = 4;
 template <int D, int P>
 __global__ void __launch_bounds__(MOVE_THREADS) cache_append_kernel(const MoveParams m, int heads) {
