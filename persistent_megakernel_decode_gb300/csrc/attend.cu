@@ -166,7 +166,7 @@ struct AttShared {
     int4 *seq;          // [batch]: AttSeq without hi
     float2 *scale;      // [ring]: (K scale, V scale), K scale < 0: page not loaded
     uint64_t *full_k, *full_v, *empty_k, *empty_v;
-    int *has_k, *has_v; // [ring]: number of the page that the slot was last asked to load
+    int *has_k, *has_v; // [ring]: number of the page whose turn the slot's K and V are at
     float *merge;       // [8 warps][8 NT rows][D + 4]
     float *ml;          // [8 warps][8 NT rows][2]
     int *ctrl;          // [0] abort
@@ -725,11 +725,16 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                         for (int k = 0; k < 4; ++k) o[n][d][k] = fmaf(a[n][k], sc.y, o[n][d][k] * alpha[n][k % 2]);
                 }
             }
-            __syncwarp();
-            if (lane == 0) {
-                if (!there) mbar_arrive_n(&s.empty_k[st], WT / side);
-                mbar_arrive_n(&s.empty_v[st], WT / side);
+            if (!there) {
+                // Not loaded, but its V has a turn too: warps of the page before it
+                // may still read the slot's V, and arriving now would be taken for them.
+                __syncwarp();
+                if (lane == 0) mbar_arrive_n(&s.empty_k[st], WT / side);
+                ok = att_wait(p, s, &s.has_v[st], mine, &s.full_v[st], ph);
+                ok = __all_sync(FULL, ok);
             }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive_n(&s.empty_v[st], WT / side);
         }
         before += g.n;
         // merge the ng warps of each tile
