@@ -8,6 +8,7 @@ masks, what a failed check does); this module checks arguments and marshals them
 from __future__ import annotations
 
 import ctypes as C
+import threading
 from array import array
 from typing import List, Optional, Sequence, Tuple
 
@@ -49,6 +50,7 @@ class Kv8Cache:
         self._ref = C.byref(self._desc)  # never changed after this
         self._lib = rt.load()
         self._kept = None  # the default stream's workspace
+        self._lock = threading.Lock()  # of _kept, from its choice to the last launch that uses it
         self._sizes = {}  # workspace bytes by (batch, table width, q heads, tokens, most tokens of a sequence, num_sms)
 
     @classmethod
@@ -163,19 +165,24 @@ class Kv8Cache:
         own = workspace is None
         if own:
             size = self._sizes.get((b, width, hq, total, most, self.num_sms)) or self._workspace(a)
-            if stream is None and torch._C._cuda_getCurrentRawStream(self.index) == 0:
-                # the default stream is one queue for good and cannot be captured: its calls share one workspace
-                workspace = self._kept
-                if workspace is None or workspace.numel() < size:
-                    workspace = self._kept = torch.empty(size, dtype=torch.uint8, device=self.device)
-            else:
-                workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
         else:
             rt.check_tensor("workspace", workspace, self.index, torch.uint8)
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
             size = workspace.numel()
-        rt.launch(self.index, stream, self._lib.mk_cache_attend, self._ref, layer, C.byref(a), workspace.data_ptr(), size)
+        if own and stream is None and torch._C._cuda_getCurrentRawStream(self.index) == 0:
+            # Calls on the default stream share a workspace.  One call is two launches, which another thread's must not
+            # come between; the stream orders the calls, and cannot be captured.
+            with self._lock:
+                if self._kept is None or self._kept.numel() < size:
+                    self._kept = torch.empty(size, dtype=torch.uint8, device=self.device)
+                rt.launch(self.index, stream, self._lib.mk_cache_attend, self._ref, layer, C.byref(a),
+                          self._kept.data_ptr(), size)
+        else:
+            if own:
+                workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
+            rt.launch(self.index, stream, self._lib.mk_cache_attend, self._ref, layer, C.byref(a), workspace.data_ptr(),
+                      size)
         if stream is not None:
             for t in (out, lse) + ((workspace,) if own else ()):  # made on the current stream, used on `stream`
                 t.record_stream(stream)

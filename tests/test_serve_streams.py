@@ -1,0 +1,100 @@
+"""Which stream and which workspace a call of the serving operators uses, on the CPU: the library's calls and torch's
+streams are replaced by records."""
+import contextlib
+import threading
+import time
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from persistent_megakernel_decode_gb300 import kvcache
+from persistent_megakernel_decode_gb300 import runtime as rt
+
+BF16, I32 = torch.bfloat16, torch.int32
+
+
+class Stream:
+    """A stand-in for a torch stream of device -1, where CPU tensors lie."""
+
+    def __init__(self, handle):
+        self.cuda_stream, self.device_index = handle, -1
+
+
+@pytest.fixture
+def machine(monkeypatch):
+    """Current streams per thread (default: handle 0), launches [(stream handle, arguments)] and what tensors went through."""
+    m = SimpleNamespace(local=threading.local(), launches=[], made=[], recorded=[], default=Stream(0), during=lambda *a: None)
+    m.current = lambda *a: getattr(m.local, "stream", m.default)
+
+    @contextlib.contextmanager
+    def under(stream):
+        before, m.local.stream = m.current(), stream
+        try:
+            yield
+        finally:
+            m.local.stream = before
+
+    def launch(index, stream, call, *args):
+        m.during(args)
+        m.launches.append(((stream or m.current()).cuda_stream, call, args))
+
+    empty, contiguous = torch.empty, torch.Tensor.contiguous
+
+    def made(t):
+        m.made.append((t, m.current().cuda_stream))
+        return t
+
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: m.current().cuda_stream, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", m.current)
+    monkeypatch.setattr(torch.cuda, "stream", under)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: m.recorded.append((t.data_ptr(), s.cuda_stream)))
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made(empty(*a, **k)))
+    monkeypatch.setattr(torch.Tensor, "contiguous", lambda t: made(contiguous(t)))
+    monkeypatch.setattr(rt, "launch", launch)
+    m.under = under
+    return m
+
+
+def cache(monkeypatch):
+    """A Kv8Cache of CPU tensors."""
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    k, v = (torch.zeros((1, 8, 1) + s, dtype=torch.uint8) for s in ((32, 64), (64, 32)))
+    c = kvcache.Kv8Cache(k, v, torch.zeros(1, 8, 1), torch.zeros(1, 8, 1))
+    monkeypatch.setattr(c, "_workspace", lambda a: 4096 * a.batch)
+    return c
+
+
+def ask(c, b, **kw):
+    return c.attend(torch.zeros((b, 1, 2, 64), dtype=BF16), torch.zeros((b, 3), dtype=I32), torch.ones(b, dtype=I32), **kw)
+
+
+def test_threads_do_not_share_a_workspace_in_use(machine, monkeypatch):
+    """A call of attention is two launches: another thread's must not come between them with the same workspace."""
+    c = cache(monkeypatch)
+    held, lock, clashes = {}, threading.Lock(), []
+
+    def during(args):
+        at, size = args[3], args[4]
+        with lock:
+            clashes.extend(x for x in held.items() if x[0] < at + size and at < x[0] + x[1])
+            held[at] = size
+        time.sleep(0.002)
+        with lock:
+            held.pop(at, None)
+    machine.during = during
+    threads = [threading.Thread(target=lambda n=n: [ask(c, n) for _ in range(10)]) for n in (1, 2, 3, 1)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert len(machine.launches) == 40 and not clashes
+
+
+def test_default_stream_keeps_one_workspace(machine, monkeypatch):
+    c = cache(monkeypatch)
+    ask(c, 2)
+    ask(c, 1)
+    ask(c, 2)
+    assert len({a[3] for _, _, a in machine.launches}) == 1
+    with machine.under(Stream(7)):  # another stream: a workspace of the call's own
+        ask(c, 2)
+    assert machine.launches[-1][0] == 7 and machine.launches[-1][2][3] != machine.launches[0][2][3]
