@@ -242,6 +242,30 @@ def launch(index: int, stream, call, *args):
         raise MkError(rc, load().mk_last_error().decode())
 
 
+def is_current(index: int, stream) -> bool:
+    """Is ``stream`` None or the current torch stream of CUDA device ``index``?"""
+    if stream is None:
+        return True
+    if stream.device_index != index:
+        raise ValueError(f"a stream of cuda:{stream.device_index} for tensors of cuda:{index}")
+    return stream.cuda_stream == torch._C._cuda_getCurrentRawStream(index)
+
+
+def beside(index: int, stream, call, *args):
+    """``call(*args)`` with ``stream``, another one than the current, as the current stream: what the call makes and
+    copies is in order with its launches.  The arguments' memory stays theirs until ``stream`` is past the call, the
+    results' until the caller's current stream is past what it had queued when they were dropped."""
+    here = torch.cuda.current_stream(index)
+    with torch.cuda.stream(stream):
+        got = call(*args)
+    for t in args:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    for t in got or ():
+        t.record_stream(here)
+    return got
+
+
 _SETTINGS = ("temperature", "top_k", "top_p", "min_p")
 
 
@@ -250,11 +274,13 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     [B] (fp32, [0, 1)): temperature, then top-k, top-p, min-p, in this order (``mk_sample`` in ``include/mk.h`` has the
     definitions).  Each setting is None (off; temperature 1), a number, or a CUDA tensor of one value per row (fp32;
     int32 for ``top_k``); a temperature of 0 takes the largest logit.  Returns (tokens int32 [B], logprob fp32 [B]: the
-    log probability under the filtered distribution); ``tokens``: an int32 [B] tensor to write into.  Asynchronous; may
-    be captured into a CUDA graph."""
+    log probability under the filtered distribution); ``tokens``: an int32 [B] tensor to write into.  Asynchronous on
+    ``stream`` (default: the current one), where the tensors must be ready; may be captured into a CUDA graph."""
     index = logits.get_device()
     if index < 0:
         raise ValueError("logits must be a CUDA tensor")
+    if not is_current(index, stream):
+        return beside(index, stream, sample, logits, u, temperature, top_k, top_p, min_p, tokens)
     if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"logits must be fp32 or bf16 [B, V], got {logits.dtype} {tuple(logits.shape)}")
     b, v = logits.shape
@@ -279,7 +305,6 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     device = logits.device
     if tokens is None:
         tokens = torch.empty((b,), dtype=torch.int32, device=device)
-        keep.append(tokens)
     else:
         check_tensor("tokens", tokens, index, torch.int32, (b,))
         if not tokens.is_contiguous():
@@ -287,10 +312,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     logprob = torch.empty((b,), dtype=torch.float32, device=device)
     d = SampleDesc(logits.data_ptr(), stride if b > 1 else v, b, v, logits.dtype is torch.bfloat16, u.data_ptr(),
                    tokens.data_ptr(), logprob.data_ptr(), *rows, *values)
-    launch(index, stream, load().mk_sample, C.byref(d))
-    if stream is not None:
-        for t in (logprob, *keep):  # made on the current stream, used on `stream`
-            t.record_stream(stream)
+    launch(index, None, load().mk_sample, C.byref(d))
     return tokens, logprob
 
 
@@ -485,6 +507,7 @@ class Session:
             logs.append(self.sample(first_step + i, u[i], temperature, top_k, top_p, min_p)[1])
         with self.torch.cuda.stream(self.stream):
             logprob = self.torch.stack(logs) if logs else u.new_empty((0, self.B))
+        logprob.record_stream(self.torch.cuda.current_stream(self.logits.device))  # where the caller reads it
         return self.tokens[first_step + 1: first_step + 1 + num_steps], logprob
 
     def store_kv(self, cache, table, start, count, max_count: Optional[int] = None):

@@ -5,7 +5,9 @@ import threading
 import pytest
 import torch
 
-from test_gpu_serve import DEV, both, deal, fill, gen, i32, table_of
+from persistent_megakernel_decode_gb300 import runtime as rt
+from persistent_megakernel_decode_gb300 import synth
+from test_gpu_serve import DEV, both, check_sample, deal, fill, gen, i32, table_of
 
 pytestmark = [pytest.mark.gpu, pytest.mark.timeout(300)]
 
@@ -15,6 +17,17 @@ def built():
     from persistent_megakernel_decode_gb300 import build
     build.build()
     assert torch.cuda.is_available()
+
+
+def hold(ms=60):
+    """Keep the current stream busy, so that what is queued behind this has not run when another stream's work has."""
+    torch.cuda._sleep(int(ms * 2e6))
+
+
+def recycled(shape, dtype, value):
+    """Free a block of memory to the current stream's pool while its filling is still queued there."""
+    hold()
+    torch.empty(shape, dtype=dtype, device=DEV).fill_(value)
 
 
 def test_threads_on_one_cache():
@@ -40,3 +53,41 @@ def test_threads_on_one_cache():
     [t.join() for t in threads]
     assert wrong == [0] * len(work)
     c.check()
+
+
+def test_sample_beside_a_busy_current_stream():
+    """Strided uniforms and settings, and results in recycled memory, while the current stream is behind."""
+    B, V = 6, 9000
+    z = torch.randn(B, V, generator=torch.Generator().manual_seed(1)) * 2
+    u = torch.rand(B, 3, generator=torch.Generator().manual_seed(2))
+    p = torch.rand(3, B, generator=torch.Generator().manual_seed(3)) * 0.5 + 0.5
+    k = torch.randint(5, 4000, (B, 2), generator=torch.Generator().manual_seed(4)).to(torch.int32)
+    zd, ud, pd, kd = z.to(DEV), u.to(DEV), p.to(DEV).t().contiguous().t(), k.to(DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(3):
+        recycled((B,), torch.int32, -5)
+        recycled((B,), torch.float32, 5.0)
+        got = rt.sample(zd, ud[:, i], top_k=kd[:, i % 2], top_p=pd[i], stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        check_sample(z, u[:, i], got, [dict(top_k=int(k[b, i % 2]), top_p=float(p[i, b])) for b in range(B)])
+
+
+def test_session_of_another_stream_samples_transposed_uniforms():
+    shape, steps, lens = synth.TINY, 3, [40, 21]
+    w = synth.make_weights(shape, 31, device=DEV)
+    u = torch.rand(2, steps, generator=torch.Generator().manual_seed(1)).to(DEV)  # [B, steps]
+    got = []
+    for stream in (None, torch.cuda.Stream()):
+        kc, vc = synth.make_cache(shape, 2, 80, 131, device=DEV)
+        s = rt.Session(shape, w, kc, vc, lens, steps, stream=stream)
+        s.tokens[0] = i32([5, 900])
+        torch.cuda.synchronize()
+        if stream is not None:
+            hold()
+        tokens, logprob = s.generate(0, steps, u.t(), temperature=0.875, top_k=200)
+        s.sync()
+        torch.cuda.synchronize()
+        got.append((tokens.clone(), logprob.clone()))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])

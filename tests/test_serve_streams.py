@@ -14,11 +14,17 @@ from persistent_megakernel_decode_gb300 import runtime as rt
 BF16, I32 = torch.bfloat16, torch.int32
 
 
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from persistent_megakernel_decode_gb300 import build
+    build.build()
+
+
 class Stream:
-    """A stand-in for a torch stream of device -1, where CPU tensors lie."""
+    """A stand-in for a torch stream."""
 
     def __init__(self, handle):
-        self.cuda_stream, self.device_index = handle, -1
+        self.cuda_stream, self.device_index = handle, 0
 
 
 @pytest.fixture
@@ -42,9 +48,11 @@ def machine(monkeypatch):
     empty, contiguous = torch.empty, torch.Tensor.contiguous
 
     def made(t):
-        m.made.append((t, m.current().cuda_stream))
+        m.made.append((t.data_ptr(), m.current().cuda_stream))
         return t
 
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: m.current().cuda_stream, raising=False)
     monkeypatch.setattr(torch.cuda, "current_stream", m.current)
     monkeypatch.setattr(torch.cuda, "stream", under)
@@ -58,7 +66,6 @@ def machine(monkeypatch):
 
 def cache(monkeypatch):
     """A Kv8Cache of CPU tensors."""
-    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
     k, v = (torch.zeros((1, 8, 1) + s, dtype=torch.uint8) for s in ((32, 64), (64, 32)))
     c = kvcache.Kv8Cache(k, v, torch.zeros(1, 8, 1), torch.zeros(1, 8, 1))
     monkeypatch.setattr(c, "_workspace", lambda a: 4096 * a.batch)
@@ -98,3 +105,23 @@ def test_default_stream_keeps_one_workspace(machine, monkeypatch):
     with machine.under(Stream(7)):  # another stream: a workspace of the call's own
         ask(c, 2)
     assert machine.launches[-1][0] == 7 and machine.launches[-1][2][3] != machine.launches[0][2][3]
+
+
+def test_sample_works_on_its_own_stream(machine):
+    """The copies of strided arguments and the results are made on the stream that the launch is on."""
+    z, s = torch.zeros(4, 100), Stream(9)
+    u, k = torch.zeros(4, 2)[:, 1], torch.zeros((4, 3), dtype=I32)[:, 1]
+    out = rt.sample(z, u, top_k=k, stream=s)
+    (handle, _, _), = machine.launches
+    assert handle == 9 and len(machine.made) == 4 and {h for _, h in machine.made} == {9}
+    for t in (z, u, k):  # may be dropped after the call
+        assert (t.data_ptr(), 9) in machine.recorded
+    for t in out:        # may be dropped while the caller's stream reads them
+        assert (t.data_ptr(), 0) in machine.recorded
+    machine.made.clear(), machine.recorded.clear()
+    rt.sample(z, u, top_k=k, stream=machine.default)
+    assert machine.launches[-1][0] == 0 and {h for _, h in machine.made} == {0} and not machine.recorded
+    other = Stream(9)
+    other.device_index = 1
+    with pytest.raises(ValueError, match="stream of cuda:1"):
+        rt.sample(z, u, stream=other)
