@@ -126,6 +126,9 @@ class Kv8Cache:
         bf16 like q, lse fp32 without the last axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8
         tensor of at least :meth:`attend_workspace` bytes, used by one call at a time; by default calls on the default
         stream share one that the cache keeps, others allocate their own."""
+        if not rt.is_current(self.index, stream):
+            return rt.beside(self.index, stream, self.attend, q, table, lens, layer, q_start, max_tokens, scale, window, out,
+                             lse, workspace)
         D, packed, shape = self.head_dim, q_start is not None, q.shape
         if (q.dtype is not torch.bfloat16 or q.get_device() != self.index or len(shape) != (3 if packed else 4)
                 or shape[-1] != D):
@@ -170,22 +173,18 @@ class Kv8Cache:
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
             size = workspace.numel()
-        if own and stream is None and torch._C._cuda_getCurrentRawStream(self.index) == 0:
+        if own and torch._C._cuda_getCurrentRawStream(self.index) == 0:
             # Calls on the default stream share a workspace.  One call is two launches, which another thread's must not
             # come between; the stream orders the calls, and cannot be captured.
             with self._lock:
                 if self._kept is None or self._kept.numel() < size:
                     self._kept = torch.empty(size, dtype=torch.uint8, device=self.device)
-                rt.launch(self.index, stream, self._lib.mk_cache_attend, self._ref, layer, C.byref(a),
+                rt.launch(self.index, None, self._lib.mk_cache_attend, self._ref, layer, C.byref(a),
                           self._kept.data_ptr(), size)
         else:
             if own:
                 workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
-            rt.launch(self.index, stream, self._lib.mk_cache_attend, self._ref, layer, C.byref(a), workspace.data_ptr(),
-                      size)
-        if stream is not None:
-            for t in (out, lse) + ((workspace,) if own else ()):  # made on the current stream, used on `stream`
-                t.record_stream(stream)
+            rt.launch(self.index, None, self._lib.mk_cache_attend, self._ref, layer, C.byref(a), workspace.data_ptr(), size)
         return out, lse
 
     def _workspace(self, a) -> int:

@@ -91,3 +91,24 @@ def test_session_of_another_stream_samples_transposed_uniforms():
         torch.cuda.synchronize()
         got.append((tokens.clone(), logprob.clone()))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_attend_beside_a_busy_current_stream():
+    """Results and workspace in recycled memory of which the current stream still has work queued."""
+    P, D, H, G, lens = 64, 128, 2, 4, [2500, 64, 1111]
+    c, r = both(1, 120, H, P, D)
+    pages = deal(lens, P, 120, random.Random(5))
+    fill(c, r, pages, lens, 210, 1)
+    a = (gen(3, 2, H * G, D, seed=9).to(DEV), table_of(pages), i32(lens))
+    want = c.attend(*a)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    size = c.attend_workspace(3, H * G, 2, a[1].shape[1])
+    for _ in range(3):
+        recycled(want[0].shape, torch.bfloat16, -5)
+        recycled(want[1].shape, torch.float32, 5.0)
+        recycled((size,), torch.uint8, 77)
+        got = c.attend(*a, stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))

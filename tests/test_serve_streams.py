@@ -125,3 +125,28 @@ def test_sample_works_on_its_own_stream(machine):
     other.device_index = 1
     with pytest.raises(ValueError, match="stream of cuda:1"):
         rt.sample(z, u, stream=other)
+
+
+def test_attend_works_on_its_own_stream(machine, monkeypatch):
+    """Results and workspace come from the memory of the stream that the launches are on."""
+    c, s = cache(monkeypatch), Stream(9)
+    machine.made.clear()
+    out = ask(c, 2, stream=s)
+    (handle, _, args), = machine.launches
+    assert handle == 9 and len(machine.made) == 3 and {h for _, h in machine.made} == {9}
+    assert args[3] in [at for at, _ in machine.made]
+    for t in out:
+        assert (t.data_ptr(), 0) in machine.recorded
+    machine.recorded.clear()
+    ask(c, 2, stream=machine.default)
+    assert machine.launches[-1][0] == 0 and not machine.recorded
+
+
+def test_attend_keeps_arguments_of_another_stream(machine, monkeypatch):
+    c, s = cache(monkeypatch), Stream(9)
+    a = [torch.zeros((2, 2, 64), dtype=BF16), torch.zeros((1, 3), dtype=I32), torch.ones(1, dtype=I32)]
+    kw = dict(q_start=torch.tensor([0, 2], dtype=I32), out=torch.zeros((2, 2, 64), dtype=BF16), lse=torch.zeros(2, 2),
+              workspace=torch.zeros(8192, dtype=torch.uint8))
+    c.attend(*a, stream=s, **kw)
+    for t in [*a, *kw.values()]:
+        assert (t.data_ptr(), 9) in machine.recorded
