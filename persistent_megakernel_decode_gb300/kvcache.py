@@ -78,8 +78,15 @@ class Kv8Cache:
                              f"{table.dtype} {tuple(table.shape)} on {table.device}")
         return table.data_ptr(), shape[1]
 
+    def _beside(self, stream, call, *args):
+        for t in (self.k, self.v, self.k_scale, self.v_scale, self.status):
+            t.record_stream(stream)
+        return rt.beside(self.index, stream, call, *args)
+
     # ---- moving tokens ----
     def _move(self, call, k, v, table, start, count, row0, max_count, stream, writes):
+        if not rt.is_current(self.index, stream):
+            return self._beside(stream, self._move, call, k, v, table, start, count, row0, max_count, None, writes)
         shape = k.shape
         if len(shape) != 5 or shape[0] != self.layers or shape[3] != self.kv_heads or shape[4] != self.head_dim:
             raise ValueError(f"k has shape {tuple(shape)}, expected ({self.layers}, B, T, {self.kv_heads}, {self.head_dim})")
@@ -100,7 +107,7 @@ class Kv8Cache:
         if b == 0 or rows == 0:
             return
         r = rt.CacheRows(kp, vp, *ks[:4], *vs[:4], rows, offset)
-        rt.launch(self.index, stream, call, self._ref, C.byref(r), at, width, first, n, b,
+        rt.launch(self.index, None, call, self._ref, C.byref(r), at, width, first, n, b,
                   rows if max_count is None else max_count)
 
     def store(self, k, v, table, start, count, row0=None, max_count: Optional[int] = None, stream=None):
@@ -127,8 +134,8 @@ class Kv8Cache:
         tensor of at least :meth:`attend_workspace` bytes, used by one call at a time; by default calls on the default
         stream share one that the cache keeps, others allocate their own."""
         if not rt.is_current(self.index, stream):
-            return rt.beside(self.index, stream, self.attend, q, table, lens, layer, q_start, max_tokens, scale, window, out,
-                             lse, workspace)
+            return self._beside(stream, self.attend, q, table, lens, layer, q_start, max_tokens, scale, window, out, lse,
+                                workspace)
         D, packed, shape = self.head_dim, q_start is not None, q.shape
         if (q.dtype is not torch.bfloat16 or q.get_device() != self.index or len(shape) != (3 if packed else 4)
                 or shape[-1] != D):
@@ -208,6 +215,8 @@ class Kv8Cache:
     def copy_pages(self, src: Sequence[int], dst: Sequence[int], table=None, stream=None):
         """Copy pages ``src[i]`` -> ``dst[i]`` in all layers (codes and scales); no dst may repeat or be a src.  With
         ``table`` (a contiguous int32 tensor) its entries that name a src are renamed to the dst."""
+        if not rt.is_current(self.index, stream):
+            return self._beside(stream, self.copy_pages, src, dst, table)
         s, d = array("i", src), array("i", dst)
         if len(s) != len(d):
             raise ValueError("src and dst must be lists of the same length")
@@ -215,7 +224,7 @@ class Kv8Cache:
             rt.check_tensor("table", table, self.index, torch.int32)
             if not table.is_contiguous():
                 raise ValueError("table must be contiguous")
-        rt.launch(self.index, stream, self._lib.mk_cache_copy, self._ref, s.buffer_info()[0], d.buffer_info()[0], len(s),
+        rt.launch(self.index, None, self._lib.mk_cache_copy, self._ref, s.buffer_info()[0], d.buffer_info()[0], len(s),
                   table.data_ptr() if table is not None else None, table.numel() if table is not None else 0)
 
     def check(self, stream=None):

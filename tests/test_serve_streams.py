@@ -150,3 +150,18 @@ def test_attend_keeps_arguments_of_another_stream(machine, monkeypatch):
     c.attend(*a, stream=s, **kw)
     for t in [*a, *kw.values()]:
         assert (t.data_ptr(), 9) in machine.recorded
+
+
+def test_moves_keep_arguments_of_another_stream(machine, monkeypatch):
+    c, s = cache(monkeypatch), Stream(9)
+    k, v = (torch.zeros((1, 2, 5, 1, 64), dtype=BF16) for _ in "kv")
+    tab, ints = torch.zeros((2, 3), dtype=I32), [torch.zeros(2, dtype=I32) for _ in range(3)]
+    for f in (c.store, c.load):
+        machine.recorded.clear()
+        f(k, v, tab, ints[0], ints[1], row0=ints[2], stream=s)
+        assert machine.launches[-1][0] == 9
+        for t in (k, v, tab, *ints, c.k, c.v, c.k_scale, c.v_scale, c.status):
+            assert (t.data_ptr(), 9) in machine.recorded
+    machine.recorded.clear()
+    c.copy_pages([0], [1], table=tab, stream=s)
+    assert machine.launches[-1][0] == 9 and (tab.data_ptr(), 9) in machine.recorded
