@@ -44,6 +44,8 @@ class Kv8Cache:
         self.layers, self.pages, self.kv_heads, self.page_tokens, self.head_dim = L, N, H, P, D
         self.device = k.device
         self.status = torch.zeros(4, dtype=torch.int32, device=k.device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.index).synchronize()  # the status words are zero for calls on any stream
         self.num_sms = 0  # SMs that attend plans for; 0: all of the device
         self._desc = rt.CacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   self.status.data_ptr(), L, N, H, P, D)

@@ -5,6 +5,7 @@ import threading
 import pytest
 import torch
 
+from persistent_megakernel_decode_gb300 import kvcache
 from persistent_megakernel_decode_gb300 import runtime as rt
 from persistent_megakernel_decode_gb300 import synth
 from test_gpu_serve import DEV, both, check_sample, deal, fill, gen, i32, table_of
@@ -112,3 +113,20 @@ def test_attend_beside_a_busy_current_stream():
         side.synchronize()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_a_new_cache_on_another_stream():
+    """The status words of a cache made behind queued work, in recycled memory."""
+    side = torch.cuda.Stream()
+    c = kvcache.Kv8Cache.empty(1, 4, 1, 64, 32, DEV)
+    q, n = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16, device=DEV), i32([3])
+    tabs = i32([[2]]), i32([[4]])
+    torch.cuda.synchronize()
+    recycled((4,), torch.int32, 7)
+    d = kvcache.Kv8Cache(c.k, c.v, c.k_scale, c.v_scale)
+    d.check(side)
+    d.attend(q, tabs[0], n, stream=side)
+    d.check(side)
+    d.attend(q, tabs[1], n, stream=side)
+    with pytest.raises(rt.MkError, match="page 4"):
+        d.check(side)

@@ -24,7 +24,10 @@ class Stream:
     """A stand-in for a torch stream."""
 
     def __init__(self, handle):
-        self.cuda_stream, self.device_index = handle, 0
+        self.cuda_stream, self.device_index, self.synced = handle, 0, 0
+
+    def synchronize(self):
+        self.synced += 1
 
 
 @pytest.fixture
@@ -56,6 +59,7 @@ def machine(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: m.current().cuda_stream, raising=False)
     monkeypatch.setattr(torch.cuda, "current_stream", m.current)
     monkeypatch.setattr(torch.cuda, "stream", under)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: m.recorded.append((t.data_ptr(), s.cuda_stream)))
     monkeypatch.setattr(torch, "empty", lambda *a, **k: made(empty(*a, **k)))
     monkeypatch.setattr(torch.Tensor, "contiguous", lambda t: made(contiguous(t)))
@@ -165,3 +169,9 @@ def test_moves_keep_arguments_of_another_stream(machine, monkeypatch):
     machine.recorded.clear()
     c.copy_pages([0], [1], table=tab, stream=s)
     assert machine.launches[-1][0] == 9 and (tab.data_ptr(), 9) in machine.recorded
+
+
+def test_a_new_cache_may_be_used_on_any_stream(machine, monkeypatch):
+    """Its status words are zero before the first call can run, whatever stream that is on."""
+    cache(monkeypatch)
+    assert machine.default.synced == 1
