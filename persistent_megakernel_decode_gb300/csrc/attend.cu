@@ -72,6 +72,8 @@ struct AttParams {
 DEV float att_lse(float big, float sum) {
     return sum == 0.f ? -INFINITY : (big - 14.f + log2f(sum)) * 0.6931471805599453f;
 }
+// 1 / the sum of exponentials, from their sum times 2^14.
+DEV float att_inverse(float sum) { return sum == 0.f ? 0.f : 16384.f / sum; }
 
 // What a sequence asks for: its query rows, its pages [lo, hi) that any row sees.
 struct AttSeq {
@@ -164,7 +166,8 @@ DEV int att_owner(long long x, long long total, int ctas) { return (int)att_div(
 struct AttShared {
     long long *prefix;  // [batch + 1]: work items before each sequence
     int4 *seq;          // [batch]: AttSeq without hi
-    float2 *scale;      // [ring]: (K scale, V scale), K scale < 0: page not loaded
+    float2 *scale;      // [ring]: (K scale, V scale without the probabilities' 2^14, so that the sums reach as far as
+                        // fp32 does), K scale < 0: page not loaded
     uint64_t *full_k, *full_v, *empty_k, *empty_v;
     int *has_k, *has_v; // [ring]: number of the page whose turn the slot's K and V are at
     float *merge;       // [8 warps][8 NT rows][D + 4]
@@ -360,7 +363,7 @@ DEV void att_produce(const AttParams &p, const AttShared &s) {
     for (; ok && __any_sync(FULL, want); ++turn) {
         const size_t at = (size_t)(id < 0 ? 0 : id) * p.c.hkv + h;
         float2 sc = make_float2(-1.f, 0.f);
-        if (id >= 0) sc = make_float2(p.c.ks[at], p.c.vs[at]);
+        if (id >= 0) sc = make_float2(p.c.ks[at], p.c.vs[at] * 0x1p-14f);
         const int now = id;
         bool k_todo = want, v_todo = want;
         const uint32_t ph = (turn & 1) ^ 1;
@@ -781,7 +784,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
             if (g.whole) {
                 const int64_t token = g.q0 + rr / p.group;
                 const int hd = g.h * p.group + rr % p.group;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const float inv = att_inverse(sum);
                 *reinterpret_cast<uint2 *>(p.out + token * p.os_t + (int64_t)hd * p.os_h + 4 * d4) =
                     make_uint2(bf16_pair(acc.x * inv, acc.y * inv), bf16_pair(acc.z * inv, acc.w * inv));
                 if (p.lse && d4 == 0)
@@ -892,7 +895,7 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
             for (int i = 0; i < V; ++i) acc[i] = fmaf(o[i], ej, acc[i]);
         }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = att_inverse(sum);
     uint16_t *dst = p.out + (int64_t)token * p.os_t + (int64_t)head * p.os_h + lane * V;
 #pragma unroll
     for (int i = 0; i < V; i += 2) *reinterpret_cast<uint32_t *>(dst + i) = bf16_pair(acc[i] * inv, acc[i + 1] * inv);
