@@ -75,6 +75,9 @@ DEV float att_lse(float big, float sum) {
 // 1 / the sum of exponentials, from their sum times 2^14.
 DEV float att_inverse(float sum) { return sum == 0.f ? 0.f : 16384.f / sum; }
 
+// The first position that a query at pos sees (pos < 0: sees none, any window's end fits 32 bits).
+DEV int att_least(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
+
 // What a sequence asks for: its query rows, its pages [lo, hi) that any row sees.
 struct AttSeq {
     int q0, cnt, len, lo, hi;
@@ -225,7 +228,7 @@ DEV void att_tile_pages(const AttParams &p, const int4 &q, int tile, int &lo, in
     const int i0 = tile * RT / p.group, i1 = (min((tile + 1) * RT, rows) - 1) / p.group;
     const int top = q.z - q.y + i1, bottom = q.z - q.y + i0;
     hi = top < 0 ? 0 : top / P + 1;
-    lo = p.window > 0 ? max(0, bottom - p.window + 1) / P : 0;
+    lo = att_least(bottom, p.window) / P;
 }
 
 // One range of pages of one unit, as every warp of the CTA walks them.  A page
@@ -508,7 +511,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
             }
         };
         const auto pos_of = [&](int r) { return r < rows ? base + r / p.group : -1; };  // a row sees [least, pos]
-        const auto least_of = [&](int pos) { return p.window > 0 ? max(0, pos - p.window + 1) : 0; };
+        const auto least_of = [&](int pos) { return att_least(pos, p.window); };
         uint32_t qb[QS ? 1 : NT][D / 64][8];
         // fragment j of tile n: qs[((n * D / 64 + h2) * 2 + j) * 32 + lane]
         uint4 *qs = reinterpret_cast<uint4 *>(s.merge) + wt * (NT * D / 32) * 32;

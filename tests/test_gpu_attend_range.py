@@ -1,7 +1,6 @@
 """Cache attention at the ends of its arguments' ranges: large values, windows beyond any length.  Tolerances as derived in
 ``test_gpu_serve``."""
 import random
-import sys
 
 import pytest
 import torch
@@ -34,3 +33,19 @@ def test_values_near_the_ends_of_bf16(P, D, T, power):
     got = c.attend(q.to(DEV), table_of(pages), i32(lens))
     c.check()
     check_attend(r, got, q, pages, lens, 0, 0)
+
+
+@pytest.mark.parametrize("P, D", [(32, 64), (64, 128)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3])
+def test_windows_beyond_any_length(P, D, window):
+    """They are no windows, also for sequences shorter than their new tokens."""
+    H, G, T, lens = 2, 2, 17, [3, 40, 16, 150]
+    c, r = both(1, 20, H, P, D, poison=True)
+    pages = deal(lens, P, 20, random.Random(7))
+    fill(c, r, pages, lens, 230, 1)
+    q = gen(4, T, H * G, D, seed=231)
+    got = c.attend(q.to(DEV), table_of(pages), i32(lens), window=window)
+    c.check()
+    check_attend(r, got, q, pages, lens, 0, 0)
+    for a, b in zip(got, c.attend(q.to(DEV), table_of(pages), i32(lens))):
+        assert torch.equal(a, b)
