@@ -110,7 +110,7 @@ class Kv8Cache:
             return
         r = rt.CacheRows(kp, vp, *ks[:4], *vs[:4], rows, offset)
         rt.launch(self.index, None, call, self._ref, C.byref(r), at, width, first, n, b,
-                  rows if max_count is None else max_count)
+                  rows if max_count is None else rt.c_int(max_count))
 
     def store(self, k, v, table, start, count, row0=None, max_count: Optional[int] = None, stream=None):
         """Quantise new tokens into the cache, all layers: row ``row0[b] + i`` (default 0 + i) of sequence b in ``k`` and
@@ -147,7 +147,7 @@ class Kv8Cache:
         if packed:
             b = q_start.numel() - 1
             queries = self._ints(max(b, 0) + 1, "q_start", q_start)
-            total, most = shape[0], shape[0] if max_tokens is None else max_tokens
+            total, most = shape[0], shape[0] if max_tokens is None else rt.c_int(max_tokens)
         else:
             b, most, queries = shape[0], shape[1], 0
             total = b * most
@@ -173,7 +173,7 @@ class Kv8Cache:
             raise ValueError("q and out: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8 "
                              "elements, and sequences evenly spaced rows")
         a = rt.AttendDesc(qp, op, lse.data_ptr(), qt, qs[-2], ot, os[-2], at, held, queries, b, width, hq, total,
-                          most, window, D ** -0.5 if scale is None else scale, self.num_sms)
+                          most, rt.c_int(window), D ** -0.5 if scale is None else scale, self.num_sms)
         own = workspace is None
         if own:
             size = self._sizes.get((b, width, hq, total, most, self.num_sms)) or self._workspace(a)
@@ -188,12 +188,12 @@ class Kv8Cache:
             with self._lock:
                 if self._kept is None or self._kept.numel() < size:
                     self._kept = torch.empty(size, dtype=torch.uint8, device=self.device)
-                rt.launch(self.index, None, self._lib.mk_cache_attend, self._ref, layer, C.byref(a),
+                rt.launch(self.index, None, self._lib.mk_cache_attend, self._ref, rt.c_int(layer), C.byref(a),
                           self._kept.data_ptr(), size)
         else:
             if own:
                 workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
-            rt.launch(self.index, None, self._lib.mk_cache_attend, self._ref, layer, C.byref(a), workspace.data_ptr(), size)
+            rt.launch(self.index, None, self._lib.mk_cache_attend, self._ref, rt.c_int(layer), C.byref(a), workspace.data_ptr(), size)
         return out, lse
 
     def _workspace(self, a) -> int:
@@ -209,8 +209,8 @@ class Kv8Cache:
         """Bytes of workspace :meth:`attend` needs for up to ``batch`` sequences of up to ``max_tokens`` queries (and
         ``table_width`` pages)."""
         a = rt.AttendDesc()
-        a.batch, a.q_heads, a.tokens, a.max_tokens = batch, q_heads, batch * max_tokens, max_tokens
-        a.table_width, a.num_sms = table_width, self.num_sms
+        a.batch, a.q_heads, a.tokens, a.max_tokens = map(rt.c_int, (batch, q_heads, batch * max_tokens, max_tokens))
+        a.table_width, a.num_sms = rt.c_int(table_width), self.num_sms
         return self._workspace(a)
 
     # ---- pages ----

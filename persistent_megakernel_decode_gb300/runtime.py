@@ -214,6 +214,11 @@ def launch_probe(num_workers: int, cooperative: bool, stream) -> None:
     _check(load().mk_launch_probe(int(num_workers), int(cooperative), C.c_void_p(stream.cuda_stream)))
 
 
+def c_int(x: int) -> int:
+    """``x`` held to the range of a C int (ctypes would pass its low 32 bits)."""
+    return x if -2 ** 31 <= x < 2 ** 31 else min(max(x, -2 ** 31), 2 ** 31 - 1)
+
+
 def check_tensor(name, t, index: int, dtype, shape=None):
     """``t`` must lie on CUDA device ``index`` and have the type and the shape."""
     if t.get_device() != index:
@@ -301,7 +306,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
             keep.append(x)  # alive until the launch is queued
             rows[i] = x.data_ptr()
         else:
-            values[i] = x
+            values[i] = c_int(x) if i == 1 else x
     device = logits.device
     if tokens is None:
         tokens = torch.empty((b,), dtype=torch.int32, device=device)

@@ -1,6 +1,7 @@
-"""Which stream and which workspace a call of the serving operators uses, on the CPU: the library's calls and torch's
+"""Which stream, workspace and numbers a call of the serving operators passes on, on the CPU: the library's calls and torch's
 streams are replaced by records."""
 import contextlib
+import sys
 import threading
 import time
 from types import SimpleNamespace
@@ -175,3 +176,25 @@ def test_a_new_cache_may_be_used_on_any_stream(machine, monkeypatch):
     """Its status words are zero before the first call can run, whatever stream that is on."""
     cache(monkeypatch)
     assert machine.default.synced == 1
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32 + 1, sys.maxsize])
+def test_numbers_beyond_32_bits_are_not_wrapped(machine, monkeypatch, big):
+    c, most = cache(monkeypatch), 2 ** 31 - 1
+    last = lambda: machine.launches[-1][2]  # noqa: E731
+    rt.sample(torch.zeros(2, 100), torch.zeros(2), top_k=big)
+    assert last()[0]._obj.top_k == most
+    ask(c, 1, window=big)
+    assert last()[2]._obj.window == most
+    ask(c, 1, layer=big)
+    assert last()[1] == most  # which the library refuses
+    c.attend(torch.zeros((2, 2, 64), dtype=BF16), torch.zeros((1, 3), dtype=I32), torch.ones(1, dtype=I32),
+             q_start=torch.tensor([0, 2], dtype=I32), max_tokens=big)
+    assert last()[2]._obj.max_tokens == most
+    x, n = torch.zeros((1, 1, 5, 1, 64), dtype=BF16), torch.zeros(1, dtype=I32)
+    c.store(x, x, torch.zeros((1, 3), dtype=I32), n, n, max_count=big)
+    assert last()[-1] == most
+    asked = []
+    monkeypatch.setattr(c, "_workspace", lambda a: asked.append((a.batch, a.tokens, a.max_tokens)))
+    c.attend_workspace(4, 2, max_tokens=big)
+    assert asked == [(4, most, most)]
