@@ -13,7 +13,6 @@ from dataclasses import dataclass
 from typing import Dict, List, Optional, Sequence
 
 import numpy as np
-import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmk.so")
@@ -232,6 +231,7 @@ def check_tensor(name, t, index: int, dtype, shape=None):
 def launch(index: int, stream, call, *args):
     """``call(*args, stream handle)`` with CUDA device ``index`` current, on ``stream`` (a torch stream of that device) or
     on the device's current torch stream; raises ``MkError`` on a status."""
+    import torch
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
     elif stream.device_index != index:
@@ -251,6 +251,7 @@ def is_current(index: int, stream) -> bool:
     """Is ``stream`` None or the current torch stream of CUDA device ``index``?"""
     if stream is None:
         return True
+    import torch
     if stream.device_index != index:
         raise ValueError(f"a stream of cuda:{stream.device_index} for tensors of cuda:{index}")
     return stream.cuda_stream == torch._C._cuda_getCurrentRawStream(index)
@@ -260,6 +261,7 @@ def beside(index: int, stream, call, *args):
     """``call(*args)`` with ``stream``, another one than the current, as the current stream: what the call makes and
     copies is in order with its launches.  The arguments' memory stays theirs until ``stream`` is past the call, the
     results' until the caller's current stream is past what it had queued when they were dropped."""
+    import torch
     here = torch.cuda.current_stream(index)
     with torch.cuda.stream(stream):
         got = call(*args)
@@ -281,6 +283,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     int32 for ``top_k``); a temperature of 0 takes the largest logit.  Returns (tokens int32 [B], logprob fp32 [B]: the
     log probability under the filtered distribution); ``tokens``: an int32 [B] tensor to write into.  Asynchronous on
     ``stream`` (default: the current one), where the tensors must be ready; may be captured into a CUDA graph."""
+    import torch
     index = logits.get_device()
     if index < 0:
         raise ValueError("logits must be a CUDA tensor")
@@ -423,6 +426,7 @@ class Session:
 
     def __init__(self, shape, weights: Dict[str, object], kcache, vcache, seq_len0: Sequence[int], max_steps: int,
                  capture_hidden: bool = False, stream=None, **target):
+        import torch
         self.torch = torch
         self.shape = shape
         self.B = len(seq_len0)
@@ -505,7 +509,7 @@ class Session:
         """Decode ``num_steps`` steps from ``tokens[first_step]`` on, each next token sampled with the settings of
         :func:`sample` and the uniforms ``u[i]`` (fp32 [num_steps, B]) instead of taken by argmax.  Returns the sampled
         tokens int32 [num_steps, B] (a view of ``tokens``) and their log probabilities; asynchronous."""
-        check_tensor("u", u, self.logits.get_device(), torch.float32, (num_steps, self.B))
+        check_tensor("u", u, self.logits.get_device(), self.torch.float32, (num_steps, self.B))
         logs = []
         for i in range(num_steps):
             self.run(first_step + i, 1, host_tokens=True, timeout_ns=timeout_ns)
@@ -552,6 +556,7 @@ class GlmSession:
     OUTPUTS = ("res_out", "qa", "sa", "qkva", "ik", "qb", "sb", "gate", "q", "iq")
 
     def __init__(self, dims, inputs: Dict[str, object], max_steps: int = 1, stream=None, **target):
+        import torch
         self.dims = dims
         dev = inputs["x"].device
         self.plan = Plan.glm(dims, max_steps, **target)
@@ -608,6 +613,7 @@ class GraphSession:
     """Workspace for an explicit-graph plan (counter tasks only)."""
 
     def __init__(self, plan: Plan, device="cuda:0", stream=None):
+        import torch
         self.plan = plan
         info = plan.info()
         self.workspace = torch.zeros(info["workspace_bytes"] + 256, dtype=torch.uint8, device=device)
