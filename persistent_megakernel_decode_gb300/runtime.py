@@ -509,6 +509,8 @@ class Session:
         """Decode ``num_steps`` steps from ``tokens[first_step]`` on, each next token sampled with the settings of
         :func:`sample` and the uniforms ``u[i]`` (fp32 [num_steps, B]) instead of taken by argmax.  Returns the sampled
         tokens int32 [num_steps, B] (a view of ``tokens``) and their log probabilities; asynchronous."""
+        if first_step < 0 or num_steps < 0 or first_step + num_steps > self.max_steps:
+            raise ValueError(f"steps {first_step} .. {first_step + num_steps - 1} outside the planned {self.max_steps}")
         check_tensor("u", u, self.logits.get_device(), self.torch.float32, (num_steps, self.B))
         logs = []
         for i in range(num_steps):

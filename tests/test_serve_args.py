@@ -232,3 +232,13 @@ def test_reference_sampling_by_hand():
     assert ref.sample_row(z, 0.99, top_p=0.0)[0] == 1
     assert ref.sample_row(z, 0.99, min_p=0.5)[0] == 2
     assert ref.sample_row(torch.full((4,), -float("inf")), 0.5) == (0, -float("inf"))
+
+
+def test_generate_refuses_steps_that_were_not_planned():
+    """Before any step runs: the cache and the tokens stay as they are."""
+    s = object.__new__(rt.Session)
+    s.max_steps, s.B, s.logits, s.torch = 4, 2, torch.zeros(2, 8), torch
+    s.run = lambda *a, **k: pytest.fail("a step ran")
+    for first, n in ((3, 2), (-1, 2), (0, 5), (5, 0), (1, -1)):
+        with pytest.raises(ValueError, match="outside the planned 4"):
+            s.generate(first, n, torch.zeros(max(n, 0), 2))
