@@ -45,14 +45,19 @@ def measured_peaks():
         return 6800.0, "fallback"
 
 
-def kernel_source_hash():
+def kernel_source_hash(root=ROOT):
+    """Hash of what the interpreter and its planner are compiled from: the sources without the serving operators' (which
+    they do not include), and mk.h without its section on those."""
     h = hashlib.sha256()
     from persistent_megakernel_decode_gb300 import build as _b
     for f in _b.SOURCES + _b.HEADERS:
-        with open(os.path.join(ROOT, "persistent_megakernel_decode_gb300", "csrc", f), "rb") as fh:
-            h.update(fh.read())
-    with open(os.path.join(ROOT, "include", "mk.h"), "rb") as fh:
-        h.update(fh.read())
+        if f not in _b.SERVING:
+            with open(os.path.join(root, "persistent_megakernel_decode_gb300", "csrc", f), "rb") as fh:
+                h.update(fh.read())
+    with open(os.path.join(root, "include", "mk.h"), "rb") as fh:
+        hdr = fh.read()
+    first = hdr.rindex(b"/*", 0, hdr.index(b" * Serving operators:"))
+    h.update(hdr[:first] + hdr[hdr.index(b"/* Thread-local description"):])
     return h.hexdigest()[:16]
 
 

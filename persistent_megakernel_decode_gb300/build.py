@@ -19,6 +19,8 @@ LIB = os.path.join(LIB_DIR, "libmk.so")
 SOURCES = ["interp.cu", "api.cpp", "planner.cpp", "cache.cu", "attend.cu", "sample.cu", "pages.cpp"]
 HEADERS = ["mk_internal.h", "planner.h", "dev_common.cuh", "dev_ops.cuh", "dev_glm.cuh", "dev_tc.cuh", "dev_glm_tc.cuh",
            "dev_serve.cuh"]
+# the operators beside the interpreter: no file of its kernel or planner includes them
+SERVING = ["cache.cu", "attend.cu", "sample.cu", "pages.cpp", "dev_serve.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
