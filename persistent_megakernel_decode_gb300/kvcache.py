@@ -159,6 +159,8 @@ class Kv8Cache:
             out = torch.empty(shape, dtype=_BF16, device=self.device)
         else:
             rt.check_tensor("out", out, self.index, _BF16, shape)
+            if any(n > 1 and x == 0 for n, x in zip(shape, out.stride())):
+                raise ValueError("rows that overlap cannot be written")
         if lse is None:
             lse = torch.empty(shape[:-1], dtype=torch.float32, device=self.device)
         else:

@@ -198,3 +198,12 @@ def test_numbers_beyond_32_bits_are_not_wrapped(machine, monkeypatch, big):
     monkeypatch.setattr(c, "_workspace", lambda a: asked.append((a.batch, a.tokens, a.max_tokens)))
     c.attend_workspace(4, 2, max_tokens=big)
     assert asked == [(4, most, most)]
+
+
+def test_attend_refuses_an_output_of_overlapping_rows(machine, monkeypatch):
+    c, q = cache(monkeypatch), torch.zeros((3, 1, 2, 64), dtype=BF16)
+    for out in (q[:1].expand(3, 1, 2, 64), q[:, :, :1].expand(3, 1, 2, 64)):
+        with pytest.raises(ValueError, match="overlap"):
+            ask(c, 3, out=out)
+    ask(c, 3, out=q)
+    assert len(machine.launches) == 1
