@@ -17,6 +17,7 @@ import torch
 
 from . import runtime as rt
 
+rt.need_torch()
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _I32, _BF16 = torch.int32, torch.bfloat16
 
@@ -87,7 +88,7 @@ class Kv8Cache:
 
     # ---- moving tokens ----
     def _move(self, call, k, v, table, start, count, row0, max_count, stream, writes):
-        if not rt.is_current(self.index, stream):
+        if stream is not None and not rt.is_current(self.index, stream):
             return self._beside(stream, self._move, call, k, v, table, start, count, row0, max_count, None, writes)
         shape = k.shape
         if len(shape) != 5 or shape[0] != self.layers or shape[3] != self.kv_heads or shape[4] != self.head_dim:
@@ -135,7 +136,7 @@ class Kv8Cache:
         bf16 like q, lse fp32 without the last axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8
         tensor of at least :meth:`attend_workspace` bytes, used by one call at a time; by default calls on the default
         stream share one that the cache keeps, others allocate their own."""
-        if not rt.is_current(self.index, stream):
+        if stream is not None and not rt.is_current(self.index, stream):
             return self._beside(stream, self.attend, q, table, lens, layer, q_start, max_tokens, scale, window, out, lse,
                                 workspace)
         D, packed, shape = self.head_dim, q_start is not None, q.shape
@@ -219,7 +220,7 @@ class Kv8Cache:
     def copy_pages(self, src: Sequence[int], dst: Sequence[int], table=None, stream=None):
         """Copy pages ``src[i]`` -> ``dst[i]`` in all layers (codes and scales); no dst may repeat or be a src.  With
         ``table`` (a contiguous int32 tensor) its entries that name a src are renamed to the dst."""
-        if not rt.is_current(self.index, stream):
+        if stream is not None and not rt.is_current(self.index, stream):
             return self._beside(stream, self.copy_pages, src, dst, table)
         s, d = array("i", src), array("i", dst)
         if len(s) != len(d):

@@ -14,6 +14,8 @@ from typing import Dict, List, Optional, Sequence
 
 import numpy as np
 
+torch = None  # what works on tensors imports it (need_torch): planning does without
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmk.so")
 
@@ -213,6 +215,11 @@ def launch_probe(num_workers: int, cooperative: bool, stream) -> None:
     _check(load().mk_launch_probe(int(num_workers), int(cooperative), C.c_void_p(stream.cuda_stream)))
 
 
+def need_torch():
+    global torch
+    import torch
+
+
 def c_int(x: int) -> int:
     """``x`` held to the range of a C int (ctypes would pass its low 32 bits)."""
     return x if -2 ** 31 <= x < 2 ** 31 else min(max(x, -2 ** 31), 2 ** 31 - 1)
@@ -231,7 +238,6 @@ def check_tensor(name, t, index: int, dtype, shape=None):
 def launch(index: int, stream, call, *args):
     """``call(*args, stream handle)`` with CUDA device ``index`` current, on ``stream`` (a torch stream of that device) or
     on the device's current torch stream; raises ``MkError`` on a status."""
-    import torch
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
     elif stream.device_index != index:
@@ -248,10 +254,7 @@ def launch(index: int, stream, call, *args):
 
 
 def is_current(index: int, stream) -> bool:
-    """Is ``stream`` None or the current torch stream of CUDA device ``index``?"""
-    if stream is None:
-        return True
-    import torch
+    """Is ``stream`` the current torch stream of CUDA device ``index``?"""
     if stream.device_index != index:
         raise ValueError(f"a stream of cuda:{stream.device_index} for tensors of cuda:{index}")
     return stream.cuda_stream == torch._C._cuda_getCurrentRawStream(index)
@@ -261,7 +264,6 @@ def beside(index: int, stream, call, *args):
     """``call(*args)`` with ``stream``, another one than the current, as the current stream: what the call makes and
     copies is in order with its launches.  The arguments' memory stays theirs until ``stream`` is past the call, the
     results' until the caller's current stream is past what it had queued when they were dropped."""
-    import torch
     here = torch.cuda.current_stream(index)
     with torch.cuda.stream(stream):
         got = call(*args)
@@ -283,11 +285,12 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     int32 for ``top_k``); a temperature of 0 takes the largest logit.  Returns (tokens int32 [B], logprob fp32 [B]: the
     log probability under the filtered distribution); ``tokens``: an int32 [B] tensor to write into.  Asynchronous on
     ``stream`` (default: the current one), where the tensors must be ready; may be captured into a CUDA graph."""
-    import torch
+    if torch is None:
+        need_torch()
     index = logits.get_device()
     if index < 0:
         raise ValueError("logits must be a CUDA tensor")
-    if not is_current(index, stream):
+    if stream is not None and not is_current(index, stream):
         return beside(index, stream, sample, logits, u, temperature, top_k, top_p, min_p, tokens)
     if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"logits must be fp32 or bf16 [B, V], got {logits.dtype} {tuple(logits.shape)}")
@@ -426,7 +429,7 @@ class Session:
 
     def __init__(self, shape, weights: Dict[str, object], kcache, vcache, seq_len0: Sequence[int], max_steps: int,
                  capture_hidden: bool = False, stream=None, **target):
-        import torch
+        need_torch()
         self.torch = torch
         self.shape = shape
         self.B = len(seq_len0)
@@ -558,7 +561,7 @@ class GlmSession:
     OUTPUTS = ("res_out", "qa", "sa", "qkva", "ik", "qb", "sb", "gate", "q", "iq")
 
     def __init__(self, dims, inputs: Dict[str, object], max_steps: int = 1, stream=None, **target):
-        import torch
+        need_torch()
         self.dims = dims
         dev = inputs["x"].device
         self.plan = Plan.glm(dims, max_steps, **target)
@@ -615,7 +618,7 @@ class GraphSession:
     """Workspace for an explicit-graph plan (counter tasks only)."""
 
     def __init__(self, plan: Plan, device="cuda:0", stream=None):
-        import torch
+        need_torch()
         self.plan = plan
         info = plan.info()
         self.workspace = torch.zeros(info["workspace_bytes"] + 256, dtype=torch.uint8, device=device)
