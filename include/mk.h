@@ -547,7 +547,12 @@ int mk_cache_load(const mk_cache_desc *cache, const mk_cache_rows *rows, const i
  * of a sequence whose length fails its check (offsets that fail: its rows are
  * left alone); a page number that fails is skipped, as if its tokens were
  * masked.  One that sees a NaN, or holds a value that is not finite, gets
- * NaN.  q head h uses kv head h / (q_heads / kv_heads). */
+ * NaN.  q head h uses kv head h / (q_heads / kv_heads).
+ * Precision: sums, maxima and lse are fp32.  q enters its product as f16
+ * times a power of two (exact but for elements below 2^-31 of their row's
+ * largest), the cache's codes as f16 (exact), a probability as f16 (2^-11 of
+ * it).  Scores, and the sum of |v_j| exp(s_j - max s), have to stay within
+ * fp32's range. */
 typedef struct {
     uint64_t q;                   /* device bf16 [tokens, q_heads, D], strides below, D contiguous */
     uint64_t out;                 /* device bf16, the same shape */
@@ -625,7 +630,10 @@ void mk_pages_free(mk_pages_t pages);
  * logprob 0.  top_k <= 0, top_p >= 1 (or NaN) and min_p <= 0 (or NaN) switch
  * a filter off.  NaN logits count as -inf; a row with no logit above -inf
  * gives token 0 and logprob -inf.  Each setting is one value for all rows,
- * or, where its pointer is not 0, one per row. */
+ * or, where its pointer is not 0, one per row.
+ * Precision: w_i are whole multiples of 2^-44 of the largest, and to 2^-30 of
+ * themselves from 2^-14 of the largest on; a smaller w_i than 2^-44 counts as
+ * 0 (such a token is not drawn, also not by u = 0).  Their sums are exact. */
 typedef struct {
     uint64_t logits;              /* device, [batch, vocab], row stride below */
     int64_t row_stride;           /* elements, >= vocab */

@@ -29,20 +29,24 @@
 //
 // Work split.  The pages of all units (sequence, row tile, kv head) form one
 // axis, each weighted with the warps its tile occupies side by side, and with
-// a constant for beginning and merging a unit, cut into equal ranges, one per CTA (one CTA per SM): ragged batches and single long
-// sequences balance alike.  A producer warp streams the pages through a
+// a constant for beginning and merging a unit, cut into equal ranges, one per
+// CTA (one CTA per SM): ragged batches and single long sequences balance alike.  A producer warp streams the pages through a
 // shared-memory ring with bulk copies; the consumer warps take them in turn
 // (as many side by side as the tile's rows need) and merge in shared memory.
+// A page that a tile does not see, or whose number is out of range, takes its
+// turn in the ring without being loaded.
 // A unit that one CTA covers is written at once; ranges cut by a CTA boundary
 // go to the workspace and a second small launch (dependent launch, so that its
 // start overlaps) merges them in order: results do not depend on timing.
 //
 // Measured (one GB300, device time): 16 sequences of 16-32K tokens, 32 q / 8
-// kv heads of 128: 127 us, 6.2 TB/s, 91 % of the copy rate; 8 sequences of
-// 512-4096, heads of 64: 13.3 us, of which the bytes are 2.8
+// kv heads of 128: 128 us, 6.1 TB/s, 90 % of the copy rate; 8 sequences of
+// 512-4096, heads of 64: 13.0 us, of which the bytes are 2.8
 // (two launches, two dependent look-ups, the ramp of the loads and the merge
-// are the rest); 64 new tokens a sequence over 4000: 185 TFLOP/s, bound by the
-// instructions per product that a 16-row operand held in registers costs.
+// are the rest); 64 new tokens a sequence over 4000: 190 TFLOP/s, bound by the
+// instructions per product that a 16-row operand held in registers costs; a
+// prompt of 2048 new tokens: 377 us, 91 TFLOP/s, half of its tiles' pages
+// passing through the ring unseen.
 #include <algorithm>
 #include <climits>
 

@@ -11,7 +11,8 @@
 // the bin's range of keys.
 //
 // Weights 2^-d, d = (max - z) log2(e) / temperature, are 64-bit fixed point
-// (2^44 for d = 0), relative accuracy 2^-30: d is carried as a pair of fp32
+// (2^44 for d = 0), accurate to 2^-30 of themselves or to 2^-44, whichever is
+// more (the relative figure holds from 2^-14 on): d is carried as a pair of fp32
 // numbers, 2^-d as integers (32-entry table times a polynomial of exp(-a), a <
 // ln 2 / 32).  Integer sums do not depend on their order, so neither does the
 // token, and the cumulative sums keep the accuracy that a 150,000-token
@@ -27,8 +28,8 @@
 // spread over 16 SMs), each CTA keeping its share of the row in shared
 // memory; histograms are joined through distributed shared memory.  What
 // bounds it is latency: the row is read once, then cluster barriers follow.
-// Measured (one GB300, device time): one row of 128,256 with all filters 12.7
-// us (its bytes take 0.08), 16 rows of 151,936 with mixed settings 28 us.
+// Measured (one GB300, device time): one row of 128,256 with all filters 12.8
+// us (its bytes take 0.08), 16 rows of 151,936 with mixed settings 28.3 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -2,8 +2,9 @@
 
 Binding of the ``mk_cache_*`` and ``mk_pages_*`` calls of ``include/mk.h``, which has the definitions (layout, scales,
 masks, what a failed check does); this module checks arguments and marshals them.  Every call is asynchronous on
-``stream`` (default: the current torch stream of the cache's device) and may be captured into a CUDA graph, except
-``Kv8Cache.check``, which synchronises.
+``stream`` (default: the current torch stream of the cache's device), where its tensors have to be ready, and may be
+captured into a CUDA graph, except ``Kv8Cache.check``, which synchronises.  Tensors may be dropped after the call.
+Threads may share a ``Kv8Cache`` (not a ``PagePool``).
 """
 from __future__ import annotations
 
@@ -132,10 +133,11 @@ class Kv8Cache:
         """Attention of new tokens over ``layer`` of the cache (their K/V stored before): ``lens[b]`` tokens are cached,
         the last T of them are the queries.  ``q`` is bf16 [B, T, Hq, D], or with ``q_start`` (int32 [B + 1]) packed
         [total, Hq, D], sequence b's queries being rows q_start[b] .. q_start[b + 1] - 1 (``max_tokens``: the most of
-        one sequence, a hint).  ``window`` > 0: a query sees that many last tokens, itself among them.  Returns (out
-        bf16 like q, lse fp32 without the last axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8
-        tensor of at least :meth:`attend_workspace` bytes, used by one call at a time; by default calls on the default
-        stream share one that the cache keeps, others allocate their own."""
+        one sequence, a hint for the height of the tiles and so for the workspace; default: all rows).  ``window`` > 0:
+        a query sees that many last tokens, itself among them.  Returns (out bf16 like q, lse fp32 without the last
+        axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8 tensor of at least
+        :meth:`attend_workspace` bytes, used by one call at a time; by default calls on the default stream share one
+        that the cache keeps, others allocate their own."""
         if stream is not None and not rt.is_current(self.index, stream):
             return self._beside(stream, self.attend, q, table, lens, layer, q_start, max_tokens, scale, window, out, lse,
                                 workspace)
@@ -196,7 +198,8 @@ class Kv8Cache:
         else:
             if own:
                 workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
-            rt.launch(self.index, None, self._lib.mk_cache_attend, self._ref, rt.c_int(layer), C.byref(a), workspace.data_ptr(), size)
+            rt.launch(self.index, None, self._lib.mk_cache_attend, self._ref, rt.c_int(layer), C.byref(a),
+                      workspace.data_ptr(), size)
         return out, lse
 
     def _workspace(self, a) -> int:
@@ -210,7 +213,7 @@ class Kv8Cache:
 
     def attend_workspace(self, batch: int, q_heads: int, max_tokens: int = 1, table_width: int = 1 << 20) -> int:
         """Bytes of workspace :meth:`attend` needs for up to ``batch`` sequences of up to ``max_tokens`` queries (and
-        ``table_width`` pages)."""
+        ``table_width`` pages; packed queries: with that ``max_tokens`` as its hint)."""
         a = rt.AttendDesc()
         a.batch, a.q_heads, a.tokens, a.max_tokens = map(rt.c_int, (batch, q_heads, batch * max_tokens, max_tokens))
         a.table_width, a.num_sms = rt.c_int(table_width), self.num_sms

@@ -279,7 +279,7 @@ _SETTINGS = ("temperature", "top_k", "top_p", "min_p")
 
 
 def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, stream=None):
-    """Draw one token per row of ``logits`` [B, V] (fp32 or bf16 CUDA tensor, any row stride) with the uniforms ``u``
+    """Draw one token per row of ``logits`` [B, V] (fp32 or bf16 CUDA tensor, rows V or more apart) with the uniforms ``u``
     [B] (fp32, [0, 1)): temperature, then top-k, top-p, min-p, in this order (``mk_sample`` in ``include/mk.h`` has the
     definitions).  Each setting is None (off; temperature 1), a number, or a CUDA tensor of one value per row (fp32;
     int32 for ``top_k``); a temperature of 0 takes the largest logit.  Returns (tokens int32 [B], logprob fp32 [B]: the
@@ -527,12 +527,12 @@ class Session:
     def store_kv(self, cache, table, start, count, max_count: Optional[int] = None):
         """Park K/V in an 8-bit paged cache (``kvcache.Kv8Cache`` with this model's layers, heads and head_dim):
         positions ``start[b]`` .. ``start[b] + count[b] - 1`` of every sequence, all layers, into the pages of ``table``
-        (int32 CUDA tensors [B, width], [B], [B])."""
+        (int32 CUDA tensors [B, width], [B], [B]).  Runs on the session's stream: these must be ready there."""
         cache.store(self.kcache.transpose(2, 3), self.vcache.transpose(2, 3), table, start, count, row0=start,
                     max_count=max_count, stream=self.stream)
 
     def load_kv(self, cache, table, start, count, max_count: Optional[int] = None):
-        """The inverse of :meth:`store_kv`: bring those positions back from the 8-bit cache."""
+        """The inverse of :meth:`store_kv`, on the same stream: bring those positions back from the 8-bit cache."""
         cache.load(self.kcache.transpose(2, 3), self.vcache.transpose(2, 3), table, start, count, row0=start,
                    max_count=max_count, stream=self.stream)
 
