@@ -408,13 +408,14 @@ DEV void att_produce(const AttParams &p, const AttShared &s) {
             }
         }
     }
-    if (!ok) {  // let the copies in flight land before the CTA ends
+    if (!ok) {
         if (lane == 0) note_failure(p.c.status, MK_ERR_TIMEOUT, -1, blockIdx.x, -1);
         *reinterpret_cast<volatile int *>(s.ctrl) = 1;
-        for (int i = 0; i < 200 && k_fills && !mbar_wait_hint(&s.full_k[lane], (k_fills - 1) & 1, 1000000); ++i) {
-        }
-        for (int i = 0; i < 200 && v_fills && !mbar_wait_hint(&s.full_v[lane], (v_fills - 1) & 1, 1000000); ++i) {
-        }
+    }
+    // the copies in flight land before the CTA ends, also where the warps that wanted them have given up
+    for (int i = 0; i < 200 && k_fills && !mbar_wait_hint(&s.full_k[lane], (k_fills - 1) & 1, 1000000); ++i) {
+    }
+    for (int i = 0; i < 200 && v_fills && !mbar_wait_hint(&s.full_v[lane], (v_fills - 1) & 1, 1000000); ++i) {
     }
 }
 

@@ -45,7 +45,10 @@ class Barrier:
 class Ring:
     """pages: for each range the CTA walks, (warps side by side, [is the page loaded?])."""
 
-    def __init__(self, ring, full_side, ranges, softmax, wait_for_v, rng):
+    def __init__(self, ring, full_side, ranges, softmax, wait_for_v, rng, give_up=None, land=True):
+        """give_up: the step at which a warp's time runs out; land: the producer waits for its last
+        copies always, not only where it has given up itself."""
+        self.give_up, self.land, self.steps, self.fills = give_up, land, 0, {}
         self.ring, self.wt, self.ranges, self.softmax, self.wait_for_v, self.rng = ring, full_side, ranges, softmax, wait_for_v, rng
         self.full_k = [Barrier(2) for _ in range(ring)]
         self.full_v = [Barrier(1) for _ in range(ring)]
@@ -56,8 +59,13 @@ class Ring:
         self.flying = []  # (barrier, array, slot, page)
         self.at_barrier = [0] * WARPS
 
+    def fly(self, bar, where, slot, page):
+        self.flying.append((bar, where, slot, page))
+        self.fills[id(bar)] = bar, page // self.ring + 1
+
     # every step yields whether it got on
     def produce(self):
+        k_todo, v_todo = set(), set()
         pages = [x for _, r in self.ranges for x in r]
         for base in range(0, len(pages), self.ring):
             lanes = range(min(self.ring, len(pages) - base))
@@ -71,14 +79,14 @@ class Ring:
                     k = i in k_todo and (turn == 0 or self.empty_k[i].done(ph))
                     if k and there:
                         self.full_k[i].arrive(1, 1)
-                        self.flying.append((self.full_k[i], self.k, i, n))
+                        self.fly(self.full_k[i], self.k, i, n)
                     v = i in v_todo and (turn == 0 or self.empty_v[i].done(ph))
                     if v:
                         self.has_v[i] = n
                         yield True
                         if there:
                             self.full_v[i].arrive(1, 1)
-                            self.flying.append((self.full_v[i], self.v, i, n))
+                            self.fly(self.full_v[i], self.v, i, n)
                     if k:
                         self.has_k[i] = n
                         yield True
@@ -92,12 +100,21 @@ class Ring:
                     if v:
                         v_todo.discard(i)
                     some |= k or v
+                if not some and self.gone():
+                    break
                 yield some
+            if k_todo or v_todo:
+                break
+        while (self.land or k_todo or v_todo) and any(bar.phase < n for bar, n in self.fills.values()):
+            yield False
+
+    def gone(self):
+        return self.give_up is not None and self.steps > self.give_up
 
     def _wait(self, has, full, st, n, ph):
-        while has[st] != n:
+        while has[st] != n and not self.gone():
             yield False
-        while not full[st].done(ph):
+        while not full[st].done(ph) and not self.gone():
             yield False
 
     def consume(self, warp):
@@ -106,7 +123,10 @@ class Ring:
             grp, ng = warp // side, WARPS // side
             for mine in range(before + grp, before + len(pages), ng):
                 st, ph = mine % self.ring, mine // self.ring & 1
-                yield from self._wait(self.has_k, self.full_k, st, mine, ph)
+                if not self.gone():
+                    yield from self._wait(self.has_k, self.full_k, st, mine, ph)
+                if self.gone():
+                    continue
                 there = pages[mine - before]
                 yield True
                 if there and self.k[st] != mine:
@@ -117,6 +137,8 @@ class Ring:
                     for _ in range(self.softmax if there else 0):
                         yield True
                     yield from self._wait(self.has_v, self.full_v, st, mine, ph)
+                    if self.gone():
+                        continue
                     if there and self.v[st] != mine:
                         raise Broken(f"V of page {self.v[st]} read for {mine}")
                 yield True
@@ -133,7 +155,10 @@ class Ring:
         """True if everybody came to the end; False if nobody can go on."""
         actors = [self.produce()] + [self.consume(w) for w in range(WARPS)]
         idle = set()  # actors that last found nothing to do
-        while actors or self.flying:
+        while actors:
+            self.steps += 1
+            if self.steps - 1 == self.give_up:
+                idle.clear()
             i = self.rng.randrange(len(actors) + (len(self.flying) > 0))
             if i == len(actors):
                 bar, where, slot, page = self.flying.pop(self.rng.randrange(len(self.flying)))
@@ -151,6 +176,8 @@ class Ring:
                 idle.clear()
             if actors and not self.flying and len(idle) == len(actors):
                 return False
+        if self.flying:
+            raise Broken("the block ended with copies in flight")
         return True
 
 
@@ -199,6 +226,27 @@ def test_ring_of_any_length(ring):
         for kind in ("loaded", "prompt", "window", "bad"):
             for softmax in (0, 6):
                 assert Ring(ring, full, ranges_of(kind, side, rng), softmax, True, rng).run(), (full, side, kind)
+
+
+@pytest.mark.parametrize("ring, side", [(9, 4), (12, 1), (32, 2)])
+def test_a_warp_that_gives_up_leaves_no_copy_behind(ring, side):
+    """Wherever time runs out, all come to the end and every copy has landed before the block does."""
+    for seed in range(120):
+        for kind in ("loaded", "prompt", "bad"):
+            rng = random.Random(seed)
+            a = ring, side, ranges_of(kind, side, rng), 3, True, rng
+            whole = Ring(*a)
+            assert whole.run()
+            assert Ring(*a, give_up=rng.randrange(whole.steps)).run()
+    left = 0  # a producer that is done before a warp gives up has to wait too
+    for seed in range(20):
+        a = ring, side, [(side, [True] * ring)], 3, True
+        assert Ring(*a, random.Random(seed), give_up=30).run()
+        try:
+            Ring(*a, random.Random(seed), give_up=30, land=False).run()
+        except Broken:
+            left += 1
+    assert left > 10
 
 
 def test_model_finds_a_slot_released_too_early():
