@@ -130,3 +130,52 @@ def test_a_new_cache_on_another_stream():
     d.attend(q, tabs[1], n, stream=side)
     with pytest.raises(rt.MkError, match="page 4"):
         d.check(side)
+
+
+def test_forked_streams_and_two_graphs_at_once():
+    """Two graphs, each with load, page copy, attention and sampling on a stream forked inside the capture, replayed at the
+    same time on two streams."""
+    P, D, H, G, lens = 32, 64, 2, 4, [700, 90]
+    c, r = both(1, 80, H, P, D)
+    pages = deal(lens, P, 60, random.Random(8))
+    fill(c, r, pages, lens, 240, 1)
+    free = sorted(set(range(80)) - {x for p in pages for x in p})
+    tab, n = table_of(pages), i32(lens)
+    z, u = torch.randn(2, 4000, generator=torch.Generator().manual_seed(5)).to(DEV), torch.rand(2, 3, device=DEV)
+    lo, count = i32([5, 6]), i32([40, 33])
+    graphs, kept = [], []
+    for i in range(2):
+        q = gen(2, 3 + i, H * G, D, seed=241 + i).to(DEV)
+        rows = [torch.zeros((1, 2, 40, H, D), dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+        kept.append(q)  # the graphs read it
+        src, dst = [pages[0][i]], [free[i]]
+
+        def step(stream=None):
+            c.load(rows[0], rows[1], tab, lo, count, stream=stream)
+            c.copy_pages(src, dst, stream=stream)
+            return c.attend(q, tab, n, stream=stream) + rt.sample(z, u[:, i], top_p=0.9, stream=stream)
+        want = [t.clone() for t in step()]
+        loaded = [t.clone() for t in rows]
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            side.wait_stream(torch.cuda.current_stream())
+            out = step(side)
+            torch.cuda.current_stream().wait_stream(side)
+        graphs.append((graph, out, want, rows, loaded, src, dst))
+    on = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for _, out, _, rows, _, _, dst in graphs:
+            for t in rows:
+                t.zero_()
+            c.k.view(torch.uint8)[:, dst] = 0
+        torch.cuda.synchronize()
+        for s, (graph, *_) in zip(on, graphs):
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for _, out, want, rows, loaded, src, dst in graphs:
+            assert all(torch.equal(a, b) for a, b in zip([*out, *rows], want + loaded))
+            assert torch.equal(c.k.view(torch.uint8)[:, dst], c.k.view(torch.uint8)[:, src])
+    c.check()
