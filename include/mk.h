@@ -541,7 +541,8 @@ int mk_cache_load(const mk_cache_desc *cache, const mk_cache_rows *rows, const i
 
 /* Attention of new tokens over one layer of the cache.  Sequence b has T_b
  * query tokens, at positions len[b] - T_b + i (their K/V already stored):
- *   s_j = scale q . k_j,  max(0, pos - window + 1) <= j <= pos (window 0: from 0)
+ *   s_j = scale q . k_j,  max(0, pos - window + 1) <= j <= pos (window 0: from 0),
+ *         and with a window j < sinks, j <= pos
  *   out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
  * A query that sees no token gets out = 0, lse = -inf, and so do all queries
  * of a sequence whose length fails its check (offsets that fail: its rows are
@@ -568,6 +569,7 @@ typedef struct {
     int window;
     float scale;                  /* >= 0; usually 1 / sqrt(D) */
     int num_sms;                  /* SMs to plan for; 0 = all of the current device */
+    int sinks;                    /* with a window: the first tokens of a sequence that all its queries see as well */
 } mk_attend_desc;
 
 /* Device bytes of workspace mk_cache_attend needs (contents need no
@@ -581,6 +583,30 @@ int mk_cache_attend_workspace(const mk_cache_desc *cache, const mk_attend_desc *
 int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc *attend, void *workspace,
                     uint64_t workspace_bytes, void *stream);
 
+/* Sequences whose first tokens lie in the same pages: group g is the
+ * sequences first[g] .. first[g + 1] - 1, and the first shared[g] tokens of
+ * each are those that the table row of the group's first sequence with queries
+ * names (the rows of the others are not read there).  What counts of it is
+ * rounded down to whole pages, and to those that every query of the group
+ * sees; sequences in no group, and groups of one, share nothing. */
+typedef struct {
+    uint64_t first;               /* device int32 [groups + 1], not falling, within 0 .. batch */
+    uint64_t shared;              /* device int32 [groups] */
+    int groups;                   /* at most batch, and 1024 less it */
+} mk_shared_desc;
+
+/* mk_cache_attend (the same results but for rounding: same masks, checks and
+ * precision; window and sinks must be 0), with the pages that a group shares
+ * read once for all of its rows (no counterpart on the pages).  A group list
+ * that falls or leaves 0 .. batch, or a negative shared length, is a failed
+ * check: nothing is shared then (in that group).  Workspace like
+ * mk_cache_attend's, of its own size. */
+int mk_cache_attend_shared_workspace(const mk_cache_desc *cache, const mk_attend_desc *attend,
+                                     const mk_shared_desc *shared, uint64_t *bytes);
+/* See mk_shared_desc (no counterpart on the pages). */
+int mk_cache_attend_shared(const mk_cache_desc *cache, int layer, const mk_attend_desc *attend,
+                           const mk_shared_desc *shared, void *workspace, uint64_t workspace_bytes, void *stream);
+
 /* Copy pages src[i] -> dst[i], all layers, codes and scales (no counterpart
  * on the pages).  src and dst are host arrays of n page numbers, read before
  * the call returns; no dst may repeat or be a src (MK_ERR_INVALID).  With a
@@ -588,6 +614,27 @@ int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc 
  * renamed to its dst (to the first one listed, if a src repeats). */
 int mk_cache_copy(const mk_cache_desc *cache, const int32_t *src, const int32_t *dst, int n, int32_t *table,
                   int64_t table_entries, void *stream);
+
+/* Reorder beams (no counterpart on the pages): row r = b beams + w of the new
+ * table continues row b beams + parents[r] of the old one, for all layers.
+ * parents int32 [batch x beams] counts within the prompt; -1: itself.  lens
+ * int32 [batch x beams] are the tokens that the rows hold, the same for all
+ * beams of a prompt.  With t = len / P:
+ *   columns < t are the parent's: full pages, which rows share from then on;
+ *   column t, where len % P > 0, is the page being filled, which must be its
+ *     row's own.  The parent's goes to the parent itself if it is among its
+ *     children, else to the first of them.  The other children of all parents,
+ *     in order, take those of the rows without children, in order, into which
+ *     the parent's len % P tokens are copied (other slots of that page stay);
+ *   all further columns (and column t of a full len) stay the row's own: pages
+ *     that it may fill later.
+ * So a beam needs pages for all it may ever write, and no page is taken or
+ * given back here.  table_out must not overlap table.  A prompt whose lens
+ * differ or leave the table, or with a parent outside [-1, beams), is a failed
+ * check: its rows stay as they are.  A copy between pages out of range is one
+ * too, and not made.  At most 64 beams. */
+int mk_cache_reorder(const mk_cache_desc *cache, const int32_t *table, const int32_t *lens, const int32_t *parents,
+                     int32_t *table_out, int batch, int beams, int table_width, void *stream);
 
 /* Synchronise `stream`, read the cache's status words into status[4] (may be
  * NULL) and return status[0]: MK_OK, MK_ERR_DEVICE_CHECK or MK_ERR_TIMEOUT;
@@ -652,6 +699,37 @@ typedef struct {
  * counterpart there).  tokens may be a row of MK_BIND_TOKENS, which the next
  * MK_RUN_HOST_TOKENS step reads. */
 int mk_sample(const mk_sample_desc *sample, void *stream);
+
+/* Beam search's selection (no counterpart on the pages).  Beam w of prompt b
+ * has the score s and, in row b beams + w, the logits z of its next token; its
+ * candidates are s + z_v - log sum exp z for every token v with z_v > -inf.
+ *   A beam whose score is not finite has none.
+ *   A finished one (its byte is not 0) has one: its score, with token `end`.
+ * The num largest of the prompt's candidates, ties to the lower beam, then the
+ * lower token: their totals, beams and tokens, largest first; -inf, -1 and -1
+ * behind the last where there are fewer.  NaN logits count as -inf; where the
+ * largest logit is +inf, those that are share the probability.
+ * Precision: totals are compared in 64 bits, with the sum of exponentials good
+ * to about 2^-28 of itself; scores are rounded to fp32 at the end. */
+typedef struct {
+    uint64_t logits;              /* device, [batch x beams, vocab], row stride below */
+    int64_t row_stride;           /* elements, >= vocab */
+    int batch, beams, vocab;      /* at most 64 beams and a vocab of 622592 */
+    int bf16;                     /* 1: bf16 logits, 0: fp32 */
+    int num;                      /* continuations wanted, at most 128 */
+    int end;                      /* the token of finished beams */
+    uint64_t scores;              /* device fp32 [batch, beams] */
+    uint64_t finished;            /* device bytes [batch, beams], or 0: none has finished */
+    uint64_t out_scores, parents, tokens;  /* device fp32, int32, int32 [batch, num]: out */
+} mk_beam_desc;
+
+/* Device bytes of workspace mk_beam_select needs (contents need no
+ * initialising; calls that may overlap in time need workspaces of their own;
+ * no counterpart on the pages). */
+int mk_beam_select_workspace(const mk_beam_desc *beam, uint64_t *bytes);
+/* See mk_beam_desc (no counterpart on the pages).  The outputs must not
+ * overlap the inputs. */
+int mk_beam_select(const mk_beam_desc *beam, void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* Thread-local description of the last non-zero status (no counterpart on
  * the pages: the error string of this C ABI). */

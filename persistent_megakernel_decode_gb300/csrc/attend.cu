@@ -66,10 +66,16 @@ struct AttParams {
     float *lse;
     int64_t qs_t, qs_h, os_t, os_h;
     const int *table, *lens, *q_start;
-    int batch, width, group, tokens, max_tokens, window, ring, ctas;
+    int batch, width, group, tokens, max_tokens, window, sinks, sink_pages, ring, ctas;
     float scale_log2;
     // workspace: partial (m, l) [ctas][2][RT][2]; partial O [ctas][2][RT][D]
     float *part_ml, *part_o;
+    // shared prefixes: groups of consecutive sequences; what a row's own tokens
+    // and its group's give, where one CTA had all of it: (m, l) [2][tokens][q
+    // heads][2], O [2][tokens][q heads][D]
+    const int *groups, *shared;
+    int ngroups;
+    float *row_ml, *row_o;
 };
 
 // ln of the sum of exponentials: maximum in log2 units, sum times 2^14.
@@ -82,20 +88,26 @@ DEV float att_inverse(float sum) { return sum == 0.f ? 0.f : 16384.f / sum; }
 // The first position that a query at pos sees (pos < 0: sees none, any window's end fits 32 bits).
 DEV int att_least(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
 
-// What a sequence asks for: its query rows, its pages [lo, hi) that any row sees.
+// What a sequence asks for: its query rows, and the pages that any row sees:
+// [0, hi) without the `gap` pages behind those of the sinks.
 struct AttSeq {
-    int q0, cnt, len, lo, hi;
+    int q0, cnt, len, gap, hi;
+    bool bad;  // its rows are not known
 };
+// The page of a sequence's i-th seen one.
+DEV int att_page(const AttParams &p, int i, int gap) { return i < p.sink_pages ? i : i + gap; }
 
 template <int P>
 DEV AttSeq att_seq(const AttParams &p, int b, bool report) {
     AttSeq s;
+    s.bad = false;
     s.len = p.lens[b];
     s.q0 = p.q_start ? p.q_start[b] : b * p.max_tokens;
     s.cnt = (p.q_start ? p.q_start[b + 1] : s.q0 + p.max_tokens) - s.q0;
     if (s.q0 < 0 || s.cnt < 0 || s.q0 > p.tokens || s.cnt > p.tokens - s.q0) {  // its rows are not known: none
         if (report) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, b, s.q0, -1);
-        s.q0 = s.cnt = s.len = s.lo = s.hi = 0;
+        s.q0 = s.cnt = s.len = s.gap = s.hi = 0;
+        s.bad = true;
         return s;
     }
     if (s.len < 0 || (int64_t)s.len > (int64_t)p.width * P) {
@@ -104,7 +116,8 @@ DEV AttSeq att_seq(const AttParams &p, int b, bool report) {
     }
     s.hi = (s.len + P - 1) / P;
     const int64_t first = (int64_t)s.len - s.cnt - p.window + 1;
-    s.lo = p.window > 0 && first > 0 ? min((int)(first / P), s.hi) : 0;
+    const int lo = p.window > 0 && first > 0 ? min((int)(first / P), s.hi) : 0;
+    s.gap = max(0, lo - p.sink_pages);
     return s;
 }
 
@@ -170,9 +183,85 @@ DEV int att_used(long long total, int ctas) {
 // CTA of work item x when `total` items are cut into `ctas` <= total ranges [c total / ctas, (c + 1) total / ctas).
 DEV int att_owner(long long x, long long total, int ctas) { return (int)att_div((x + 1) * ctas - 1, total); }
 
+// Shared prefixes.  lim[g]: the pages that all rows of group g see and take
+// together; lead[g]: the sequence whose table row names them.
+struct AttGroups {
+    int *lead, *lim, *grp;  // [ngroups], [ngroups], [ngroups + 1]: the groups' first sequences
+};
+__host__ __device__ constexpr int att_group_bytes(int n) { return n ? (3 * n + 1) * 4 : 0; }
+DEV AttGroups att_groups_at(void *at, int n) {
+    int *x = static_cast<int *>(at);
+    return {x, x + n, x + 2 * n};
+}
+// The group of a sequence, or -1.
+DEV int att_group_of(const AttParams &p, const AttGroups &s, int b) {
+    int a = 0, z = p.ngroups;  // the last group that begins at or before b
+    while (z - a > 1) {
+        const int mid = (a + z) / 2;
+        if (s.grp[mid] <= b) a = mid;
+        else z = mid;
+    }
+    return b >= s.grp[a] && b < s.grp[a + 1] ? a : -1;
+}
+// By the whole block.  What `shared` says is a bound: only full pages, and of
+// them those that every query of the group sees whole.
+template <int P>
+DEV void att_groups(const AttParams &p, const AttGroups &s, bool report) {
+    const int n = p.ngroups, tid = threadIdx.x, threads = blockDim.x;
+    bool bad = false;
+    for (int g = tid; g <= n; g += threads) {
+        const int x = p.groups[g];
+        s.grp[g] = x;
+        bad |= x < 0 || x > p.batch || (g < n && p.groups[g + 1] < x);
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && report && tid == 0) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, -1, -1, -1);
+    for (int g = tid; g < n; g += threads) {
+        const int x = p.shared[g];
+        if (x < 0 && report) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, s.grp[g], x, -1);
+        s.lead[g] = INT_MAX;
+        s.lim[g] = bad || s.grp[g + 1] - s.grp[g] < 2 ? 0 : max(x, 0) / P;
+    }
+    __syncthreads();
+    for (int b = tid; b < p.batch && !bad; b += threads) {
+        const int g = att_group_of(p, s, b);
+        if (g < 0) continue;
+        const AttSeq q = att_seq<P>(p, b, false);
+        if (q.bad) atomicMin(&s.lim[g], 0);  // where its rows begin is not known either
+        if (q.cnt == 0) continue;
+        atomicMin(&s.lead[g], b);
+        atomicMin(&s.lim[g], max(0, q.len - q.cnt + 1) / P);
+    }
+    __syncthreads();
+}
+DEV int att_units(const AttParams &p, bool sh) { return sh ? p.ngroups + p.batch : p.batch; }
+// Unit v: a sequence, or with shared prefixes a group's rows over its pages
+// (every row sees all of them), or a sequence's rows over the pages behind.
+template <int P, bool SH>
+DEV AttSeq att_unit(const AttParams &p, const AttGroups &s, int v, bool report) {
+    if constexpr (!SH) return att_seq<P>(p, v, report);
+    if (v >= p.ngroups) {
+        const int b = v - p.ngroups;
+        AttSeq q = att_seq<P>(p, b, report);
+        const int g = att_group_of(p, s, b);
+        q.gap = g < 0 ? 0 : min(s.lim[g], q.hi);
+        return q;
+    }
+    AttSeq q{0, 0, 0, 0, 0, false};
+    if (s.lim[v] > 0 && s.lead[v] < p.batch) {
+        q.q0 = p.q_start ? p.q_start[s.grp[v]] : s.grp[v] * p.max_tokens;
+        q.cnt = (p.q_start ? p.q_start[s.grp[v + 1]] : s.grp[v + 1] * p.max_tokens) - q.q0;
+        q.hi = s.lim[v];
+        q.len = q.hi * P;
+    }
+    return q;
+}
+
 struct AttShared {
-    long long *prefix;  // [batch + 1]: work items before each sequence
-    int4 *seq;          // [batch]: AttSeq without hi
+    // A unit is what a sequence's own pages are (shared prefixes: the groups' first, then the sequences')
+    long long *prefix;  // [units + 1]: work items before each
+    int4 *seq;          // [units]: AttSeq without hi
+    AttGroups groups;
     float2 *scale;      // [ring]: (K scale, V scale without the probabilities' 2^14, so that the sums reach as far as
                         // fp32 does), K scale < 0: page not loaded
     uint64_t *full_k, *full_v, *empty_k, *empty_v;
@@ -186,7 +275,9 @@ struct AttShared {
 __host__ __device__ constexpr int att_fixed_bytes(int D, int nt) {
     return ATT_WARPS * 8 * nt * (D + 4) * 4 + ATT_WARPS * 8 * nt * 2 * 4 + ATT_MAXRING * (8 + 32 + 8) + 16;
 }
-__host__ __device__ constexpr int att_seq_bytes(int batch) { return batch * 16 + (batch + 1) * 8; }
+__host__ __device__ constexpr int att_seq_bytes(int batch, int ngroups) {
+    return (ngroups + batch) * 16 + (ngroups + batch + 1) * 8 + att_group_bytes(ngroups);
+}
 
 template <int D, int NT>
 DEV AttShared att_shared(const AttParams &p) {
@@ -209,8 +300,9 @@ DEV AttShared att_shared(const AttParams &p) {
     s.merge = reinterpret_cast<float *>(at);
     at += ATT_WARPS * 8 * NT * (D + 4) * 4;
     s.seq = reinterpret_cast<int4 *>(at);
-    s.prefix = reinterpret_cast<long long *>(s.seq + p.batch);
-    const uint32_t used = (uint32_t)(at - mk_smem) + att_seq_bytes(p.batch);
+    s.prefix = reinterpret_cast<long long *>(s.seq + p.ngroups + p.batch);
+    s.groups = att_groups_at(s.prefix + p.ngroups + p.batch + 1, p.ngroups);
+    const uint32_t used = (uint32_t)(at - mk_smem) + att_seq_bytes(p.batch, p.ngroups);
     s.ring = mk_smem + ((used + 127) & ~127u);
     return s;
 }
@@ -225,12 +317,12 @@ DEV int att_find(const long long *prefix, int batch, long long x) {
     }
     return a;
 }
-// The pages of a sequence that the rows of one of its tiles see: [lo, hi).
+// The pages of a sequence that the rows of one of its tiles see: [lo, hi), and below hi those of the sinks.
 template <int P, int RT>
-DEV void att_tile_pages(const AttParams &p, const int4 &q, int tile, int &lo, int &hi) {
-    const int rows = q.y * p.group;
+DEV void att_tile_pages(const AttParams &p, int cnt, int len, int tile, int &lo, int &hi) {
+    const int rows = cnt * p.group;
     const int i0 = tile * RT / p.group, i1 = (min((tile + 1) * RT, rows) - 1) / p.group;
-    const int top = q.z - q.y + i1, bottom = q.z - q.y + i0;
+    const int top = len - cnt + i1, bottom = len - cnt + i0;
     hi = top < 0 ? 0 : top / P + 1;
     lo = att_least(bottom, p.window) / P;
 }
@@ -238,27 +330,28 @@ DEV void att_tile_pages(const AttParams &p, const int4 &q, int tile, int &lo, in
 // One range of pages of one unit, as every warp of the CTA walks them.  A page
 // belongs to the CTA in whose range its first item lies.
 struct AttSeg {
-    int b, tile, h, pg, n;    // pages [pg, pg + n) of the sequence
-    int q0, cnt, len;
+    int b, tile, h, pg, n;    // the pg-th page that the unit's rows see, and the n - 1 next
+    int q0, cnt, len, gap;
     bool whole;               // the unit's every page
     bool head;                // the unit's first page among them
 };
 
-template <int P, int RT>
+template <int P, int RT, bool SH>
 struct AttWalk {
     const AttParams &p;
     const AttShared &s;
     long long x, end;
     int b;
     DEV AttWalk(const AttParams &p_, const AttShared &s_) : p(p_), s(s_) {
-        const long long total = s.prefix[p.batch];
+        const int units = att_units(p, SH);
+        const long long total = s.prefix[units];
         const int ctas = att_used<RT>(total, p.ctas);
         x = end = 0;
         if ((int)blockIdx.x < ctas) {
             x = att_div((long long)blockIdx.x * total, ctas);
             end = att_div((long long)(blockIdx.x + 1) * total, ctas);
         }
-        b = att_find(s.prefix, p.batch, x);
+        b = att_find(s.prefix, units, x);
     }
     DEV bool next(AttSeg &g) {
         while (x < end) {
@@ -285,7 +378,8 @@ struct AttWalk {
             g.b = b;
             g.tile = unit / p.c.hkv;
             g.h = unit - g.tile * p.c.hkv;
-            g.pg = q.w + first;
+            g.pg = first;
+            g.gap = q.w;
             g.n = until - first;
             g.q0 = q.x;
             g.cnt = q.y;
@@ -324,12 +418,12 @@ DEV bool att_wait(const AttParams &p, const AttShared &s, int *has, int number, 
 // i-th: a loop over pages in one thread took 850 clocks a page, all of them
 // instruction latency.  All lanes poll their slots at once; those that are
 // free are filled.
-template <int D, int P, int RT>
+template <int D, int P, int RT, bool SH>
 DEV void att_produce(const AttParams &p, const AttShared &s) {
     constexpr int PAGE = P * D;
     const int lane = threadIdx.x % 32;
     uint8_t *dst = s.ring + (size_t)lane * 2 * PAGE;
-    AttWalk<P, RT> walk(p, s);
+    AttWalk<P, RT, SH> walk(p, s);
     AttSeg g;
     bool more = walk.next(g);
     int before = 0;  // pages of the ranges done
@@ -345,10 +439,14 @@ DEV void att_produce(const AttParams &p, const AttShared &s) {
             if (lane < p.ring && k >= 0 && k < g.n) {
                 want = true;
                 h = g.h;
-                pg = g.pg + k;
-                int lo, hi;
-                att_tile_pages<P, RT>(p, make_int4(g.q0, g.cnt, g.len, 0), g.tile, lo, hi);
-                if (pg >= lo && pg < hi) b = g.b;
+                pg = att_page(p, g.pg + k, g.gap);
+                if (SH && g.b < p.ngroups) {
+                    b = s.groups.lead[g.b];
+                } else {
+                    int lo, hi;
+                    att_tile_pages<P, RT>(p, g.cnt, g.len, g.tile, lo, hi);
+                    if ((pg >= lo || pg < p.sink_pages) && pg < hi) b = SH ? g.b - p.ngroups : g.b;
+                }
             }
             if (before + g.n >= base + p.ring) break;
             before += g.n;
@@ -490,18 +588,19 @@ DEV void mbar_arrive_n(uint64_t *b, uint32_t n) {
 }
 DEV void att_consumer_bar() { asm volatile("bar.sync 1, %0;" ::"n"(ATT_WARPS * 32) : "memory"); }
 
-template <int D, int P, int RT>
+template <int D, int P, int RT, bool SH>
 DEV void att_consume(const AttParams &p, const AttShared &s) {
     constexpr int NT = att_nt(RT), WT = RT / (8 * NT);  // 8-row tiles a warp, warps for a full tile
     constexpr int PAGE = P * D, RUN = P / 4, NM = P / 16, ND = D / 16, LD = D + 4;
     constexpr bool QS = NT > 1;  // the query operand in shared memory (registers would spill)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g8 = lane / 4, t = lane % 4;
-    AttWalk<P, RT> walk(p, s);
+    AttWalk<P, RT, SH> walk(p, s);
     AttSeg g;
     bool ok = true;
     int before = 0;  // pages of the CTA's ranges done
     while (walk.next(g)) {
-        const int rows = g.cnt * p.group, base = g.len - g.cnt;
+        const bool all = SH && g.b < p.ngroups;  // every row sees every token
+        const int rows = g.cnt * p.group, base = all ? g.len - 1 : g.len - g.cnt;
         // as many warps side by side as the tile's rows need (1, 2 or 4), the
         // others on other pages: group grp takes every ng-th page of the range
         const int side = att_side<RT>(rows - g.tile * RT);
@@ -515,7 +614,9 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                 ph ^= 1;
             }
         };
-        const auto pos_of = [&](int r) { return r < rows ? base + r / p.group : -1; };  // a row sees [least, pos]
+        const auto pos_of = [&](int r) {  // a row sees [least, pos], and below it the sinks
+            return r < rows ? base + (all ? 0 : r / p.group) : -1;
+        };
         const auto least_of = [&](int pos) { return att_least(pos, p.window); };
         uint32_t qb[QS ? 1 : NT][D / 64][8];
         // fragment j of tile n: qs[((n * D / 64 + h2) * 2 + j) * 32 + lane]
@@ -530,8 +631,8 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
             if (r < rows) {
                 const int tok = r / p.group;
                 qrow = p.q + (int64_t)(g.q0 + tok) * p.qs_t + (int64_t)(g.h * p.group + r - tok * p.group) * p.qs_h;
-                all_hi = min(all_hi, base + tok);
-                all_lo = max(all_lo, least_of(base + tok));
+                all_hi = min(all_hi, pos_of(r));
+                all_lo = max(all_lo, least_of(pos_of(r)));
             }
             const float qf = att_load_q<D>(qrow, t, qb[QS ? 0 : n]) * p.scale_log2;
             if constexpr (QS)
@@ -554,7 +655,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
         all_lo = __reduce_max_sync(FULL, all_lo);
         if constexpr (QS) att_consumer_bar();
         for (int mine = before + grp; mine < before + g.n; mine += ng, st += ng, settle()) {
-            const int pg = g.pg + mine - before;
+            const int pg = att_page(p, g.pg + mine - before, g.gap);
             if (ok) ok = att_wait(p, s, &s.has_k[st], mine, &s.full_k[st], ph);
             ok = __all_sync(FULL, ok);
             if (!ok) continue;
@@ -562,7 +663,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
             const bool there = sc.x >= 0.f || sc.x != sc.x;
             const uint8_t *kp = s.ring + (size_t)st * 2 * PAGE, *vp = kp + PAGE;
             if (there) {
-                const bool edge = pg * P < all_lo || pg * P + P - 1 > all_hi;
+                const bool edge = (pg * P < all_lo && pg * P + P - 1 >= p.sinks) || pg * P + P - 1 > all_hi;
                 float c[NT][NM][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -625,7 +726,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
 #pragma unroll
                                 for (int u = 0; u < 2; ++u) {
                                     const int x = first + 4 * i + 2 * u;
-                                    if (x > pos[n][e] || x < least) c[n][i][2 * u + e] = -INFINITY;
+                                    if (x > pos[n][e] || (x < least && x >= p.sinks)) c[n][i][2 * u + e] = -INFINITY;
                                 }
                         }
                 }
@@ -708,8 +809,8 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     const int x = pg * P + RUN * t + 4 * i + 2 * k;
-                                    see[k] = (x <= ps && x >= ls ? 0x3c00u : 0u) |
-                                             (x + 1 <= ps && x + 1 >= ls ? 0x3c000000u : 0u);
+                                    see[k] = (x <= ps && (x >= ls || x < p.sinks) ? 0x3c00u : 0u) |
+                                             (x + 1 <= ps && (x + 1 >= ls || x + 1 < p.sinks) ? 0x3c000000u : 0u);
                                 }
                                 att_mma(z, e4m3x2_to_half2(at[0][i]), e4m3x2_to_half2(at[1][i]),
                                         e4m3x2_to_half2(at[0][i] >> 16), e4m3x2_to_half2(at[1][i] >> 16), see[0], see[1]);
@@ -789,7 +890,11 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                 acc.z = fmaf(a, x.z, acc.z);
                 acc.w = fmaf(a, x.w, acc.w);
             }
-            if (g.whole) {
+            if (SH && g.whole) {
+                const size_t at_row = (((size_t)all * p.tokens + g.q0 + rr / p.group) * p.c.hkv + g.h) * p.group + rr % p.group;
+                *reinterpret_cast<float4 *>(p.row_o + at_row * D + 4 * d4) = acc;
+                if (d4 == 0) *reinterpret_cast<float2 *>(p.row_ml + at_row * 2) = make_float2(big, sum);
+            } else if (g.whole) {
                 const int64_t token = g.q0 + rr / p.group;
                 const int hd = g.h * p.group + rr % p.group;
                 const float inv = att_inverse(sum);
@@ -807,15 +912,16 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
     }
 }
 
-template <int D, int P, int RT>
+template <int D, int P, int RT, bool SH>
 __global__ void __launch_bounds__(ATT_THREADS, 1) cache_attend_kernel(const AttParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
     const AttShared s = att_shared<D, att_nt(RT)>(p);
-    const int tid = threadIdx.x;
-    for (int b = tid; b < p.batch; b += ATT_THREADS) {
-        const AttSeq q = att_seq<P>(p, b, blockIdx.x == 0);
-        s.prefix[b + 1] = att_items<RT>(p, q.cnt, q.hi - q.lo);
-        s.seq[b] = make_int4(q.q0, q.cnt, q.len, q.lo);
+    const int tid = threadIdx.x, units = att_units(p, SH);
+    if constexpr (SH) att_groups<P>(p, s.groups, blockIdx.x == 0);
+    for (int b = tid; b < units; b += ATT_THREADS) {
+        const AttSeq q = att_unit<P, SH>(p, s.groups, b, blockIdx.x == 0);
+        s.prefix[b + 1] = att_items<RT>(p, q.cnt, q.hi - q.gap);
+        s.seq[b] = make_int4(q.q0, q.cnt, q.len, q.gap);
     }
     if (tid >= ATT_THREADS - 32 && tid - (ATT_THREADS - 32) < p.ring) {
         const int i = tid - (ATT_THREADS - 32);
@@ -827,25 +933,28 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) cache_attend_kernel(const AttP
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (tid == 0) s.ctrl[0] = 0;
-    att_running(s.prefix, p.batch);
-    if (tid >= ATT_WARPS * 32) att_produce<D, P, RT>(p, s);
-    else att_consume<D, P, RT>(p, s);
+    att_running(s.prefix, units);
+    if (tid >= ATT_WARPS * 32) att_produce<D, P, RT, SH>(p, s);
+    else att_consume<D, P, RT, SH>(p, s);
 }
 
 // One warp per query row: rows that see nothing get zeros, rows whose pages
 // two or more CTAs shared are merged, in the order of the CTAs; the others
-// are written already.  All that does not need the main kernel's results (the
+// are written already.  With shared prefixes all rows are merged, the own
+// tokens' part first.  All that does not need the main kernel's results (the
 // sequences' running page counts again, the row's sequence) runs while that
 // one still does.
-template <int D, int P, int RT>
+template <int D, int P, int RT, bool SH>
 __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
     long long *prefix = reinterpret_cast<long long *>(mk_smem);
-    const int tid = threadIdx.x, lane = tid % 32, heads = p.group * p.c.hkv;
-    for (int b = tid; b < p.batch; b += 256) {
-        const AttSeq q = att_seq<P>(p, b, false);
-        prefix[b + 1] = att_items<RT>(p, q.cnt, q.hi - q.lo);
+    const int tid = threadIdx.x, lane = tid % 32, heads = p.group * p.c.hkv, units = att_units(p, SH);
+    const AttGroups groups = att_groups_at(prefix + units + 1, p.ngroups);
+    if constexpr (SH) att_groups<P>(p, groups, false);
+    for (int b = tid; b < units; b += 256) {
+        const AttSeq q = att_unit<P, SH>(p, groups, b, false);
+        prefix[b + 1] = att_items<RT>(p, q.cnt, q.hi - q.gap);
     }
-    att_running(prefix, p.batch);
+    att_running(prefix, units);
     const int64_t w = (int64_t)blockIdx.x * 8 + tid / 32;
     const int token = (int)min(w / heads, (int64_t)p.tokens - 1), head = (int)(w % heads);
     int b = 0;
@@ -859,50 +968,88 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
     } else {
         b = min(token / p.max_tokens, p.batch - 1);
     }
-    const AttSeq s = att_seq<P>(p, b, false);
-    const int np = s.hi - s.lo, h = head / p.group, r = (token - s.q0) * p.group + head % p.group;
-    bool todo = w < (int64_t)p.tokens * heads && token >= s.q0 && token < s.q0 + s.cnt;
-    int c0 = 0, c1 = -1;
-    if (todo && np > 0) {
+    // the CTAs that have parts of the row in one unit (n pages; c0 > c1: one
+    // CTA had it all), and the row's place in its tile
+    struct Part {
+        int n, c0, c1, row;
+    };
+    const long long total = prefix[units];
+    const int ctas = att_used<RT>(total, p.ctas);
+    const auto part_of = [&](int v, const AttSeq &s) {
+        Part x{s.hi - s.gap, 0, -1, 0};
+        if (x.n <= 0 || s.cnt <= 0) {
+            x.n = 0;
+            return x;
+        }
+        const int h = head / p.group, r = (token - s.q0) * p.group + head % p.group;
         const int rows = s.cnt * p.group, tile = r / RT, side = att_side<RT>(rows - tile * RT);
-        const long long total = prefix[p.batch];
         constexpr int FIXED = att_fixed_items(RT);
-        const long long x0 = prefix[b] + (long long)tile * p.c.hkv * (np * att_side<RT>(RT) + FIXED) +
-                             h * ((long long)np * side + FIXED) + FIXED;  // the first page's item
-        const int ctas = att_used<RT>(total, p.ctas);
-        c0 = att_owner(x0, total, ctas);
-        c1 = att_owner(x0 + (long long)(np - 1) * side, total, ctas);
-        todo = c0 != c1;
+        const long long x0 = prefix[v] + (long long)tile * p.c.hkv * (x.n * att_side<RT>(RT) + FIXED) +
+                             h * ((long long)x.n * side + FIXED) + FIXED;  // the first page's item
+        const int c0 = att_owner(x0, total, ctas), c1 = att_owner(x0 + (long long)(x.n - 1) * side, total, ctas);
+        if (c0 != c1) {
+            x.c0 = c0;
+            x.c1 = c1;
+        }
+        x.row = r % RT;
+        return x;
+    };
+    const AttSeq s = att_unit<P, SH>(p, groups, SH ? p.ngroups + b : b, false);
+    bool todo = w < (int64_t)p.tokens * heads && token >= s.q0 && token < s.q0 + s.cnt;
+    Part own{0, 0, -1, 0}, pre{0, 0, -1, 0};
+    if (todo) {
+        own = part_of(SH ? p.ngroups + b : b, s);
+        if constexpr (SH) {
+            const int g = att_group_of(p, groups, b);
+            if (g >= 0) pre = part_of(g, att_unit<P, SH>(p, groups, g, false));
+        } else {
+            todo = own.n == 0 || own.c0 <= own.c1;
+        }
     }
     // every thread waits: this grid must not be done before the main kernel is
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!todo) return;
-    const auto slot = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * RT + r % RT; };  // c0 has the unit's head
     constexpr int V = D / 32;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
     float big = -INFINITY, sum = 0.f;
-    for (int c = c0; c <= c1; c += 32) {  // the maxima first, 32 CTAs at a time
-        const int mine = c + lane;
-        const float2 ml = mine <= c1 ? *reinterpret_cast<const float2 *>(p.part_ml + slot(mine) * 2)
-                                     : make_float2(-INFINITY, 0.f);
-        const float top = fmaxf(big, warp_max(ml.x)), mu = top == -INFINITY ? 0.f : top;
-        const float a = exp2_fast(big - mu), e = exp2_fast(ml.x - mu);
-        big = top;
-        sum *= a;
+    const auto add = [&](const Part &x, int which) {
+        if (SH && x.n && x.c0 > x.c1) {  // one CTA had it all
+            const size_t at = ((size_t)which * p.tokens + token) * heads + head;
+            const float2 ml = *reinterpret_cast<const float2 *>(p.row_ml + at * 2);
+            const float *o = p.row_o + at * D + lane * V;
+            const float top = fmaxf(big, ml.x), mu = top == -INFINITY ? 0.f : top;
+            const float a = exp2_fast(big - mu), e = exp2_fast(ml.x - mu);
+            big = top;
+            sum = fmaf(ml.y, e, sum * a);
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] *= a;
-        const int n = min(32, c1 - c + 1);
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) {
-            const float ej = __shfl_sync(FULL, e, j), lj = __shfl_sync(FULL, ml.y, j);
-            const float *o = p.part_o + slot(c + j) * D + lane * V;
-            sum = fmaf(lj, ej, sum);
-#pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = fmaf(o[i], ej, acc[i]);
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(o[i], e, acc[i] * a);
         }
-    }
+        const auto slot = [&](int c) { return ((size_t)c * 2 + (c == x.c0 ? 1 : 0)) * RT + x.row; };  // c0 has the unit's head
+        for (int c = x.c0; c <= x.c1; c += 32) {  // the maxima first, 32 CTAs at a time
+            const int mine = c + lane;
+            const float2 ml = mine <= x.c1 ? *reinterpret_cast<const float2 *>(p.part_ml + slot(mine) * 2)
+                                           : make_float2(-INFINITY, 0.f);
+            const float top = fmaxf(big, warp_max(ml.x)), mu = top == -INFINITY ? 0.f : top;
+            const float a = exp2_fast(big - mu), e = exp2_fast(ml.x - mu);
+            big = top;
+            sum *= a;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] *= a;
+            const int n = min(32, x.c1 - c + 1);
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) {
+                const float ej = __shfl_sync(FULL, e, j), lj = __shfl_sync(FULL, ml.y, j);
+                const float *o = p.part_o + slot(c + j) * D + lane * V;
+                sum = fmaf(lj, ej, sum);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(o[i], ej, acc[i]);
+            }
+        }
+    };
+    add(own, 0);
+    if constexpr (SH) add(pre, 1);
     const float inv = att_inverse(sum);
     uint16_t *dst = p.out + (int64_t)token * p.os_t + (int64_t)head * p.os_h + lane * V;
 #pragma unroll
@@ -912,10 +1059,12 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
 
 struct AttPlan {
     int rt, ctas;
-    uint64_t ml_bytes, o_bytes;
+    uint64_t ml_bytes, o_bytes, row_ml_bytes, row_o_bytes;
+    uint64_t bytes() const { return ml_bytes + o_bytes + row_ml_bytes + row_o_bytes; }
 };
 
-static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, AttPlan &pl) {
+// ngroups: 0 without shared prefixes
+static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, int ngroups, AttPlan &pl) {
     if (!c || !a) return set_error(MK_ERR_INVALID, "null descriptor");
     if (a->batch < 0 || a->tokens < 0 || a->max_tokens < 0 || a->table_width <= 0)
         return set_error(MK_ERR_INVALID, "negative batch, tokens or max_tokens, or an empty table");
@@ -933,60 +1082,58 @@ static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, AttPlan &pl
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return serve_cuda_fail(e, "device query");
     }
-    // row tiles of 8, 16, 32 or 64 rows: the least that takes a sequence's rows of one kv head
-    const int64_t rows = (int64_t)std::max(1, std::min(a->max_tokens, a->tokens)) * (a->q_heads / c->kv_heads);
+    // row tiles of 8, 16, 32 or 64 rows: the least that takes a sequence's (or an average group's) rows of one kv head
+    const int group = a->q_heads / c->kv_heads;
+    int64_t rows = (int64_t)std::max(1, std::min(a->max_tokens, a->tokens)) * group;
+    if (ngroups) rows = std::max(rows, ((int64_t)a->tokens + ngroups - 1) / ngroups * group);
     pl.rt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     // no more CTAs than pages there can be (all tiles' together, each as many items as it has warps side by side)
     const int64_t side = pl.rt == 64 ? 4 : pl.rt == 32 ? 2 : 1;
-    const int64_t tiles = a->batch + (int64_t)a->tokens * (a->q_heads / c->kv_heads) / pl.rt;
+    const int64_t tiles = (a->batch + (int64_t)a->tokens * group / pl.rt) * (ngroups ? 2 : 1);
     pl.ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(1, std::min<int64_t>(tiles * c->kv_heads, INT32_MAX) * (a->table_width * side + att_fixed_items(pl.rt))));
     pl.ml_bytes = ((uint64_t)pl.ctas * 2 * pl.rt * 8 + 255) / 256 * 256;
     pl.o_bytes = (uint64_t)pl.ctas * 2 * pl.rt * c->head_dim * 4;
+    const uint64_t row_parts = ngroups ? 2ull * a->tokens * a->q_heads : 0;
+    pl.row_ml_bytes = (row_parts * 8 + 255) / 256 * 256;
+    pl.row_o_bytes = row_parts * c->head_dim * 4;
     return MK_OK;
 }
 
 using AttFn = void (*)(const AttParams);
-template <int D, int P>
+template <int D, int P, bool SH>
 static AttFn att_kernel(int rt) {
-    return rt == 8 ? cache_attend_kernel<D, P, 8> : rt == 16 ? cache_attend_kernel<D, P, 16>
-         : rt == 32 ? cache_attend_kernel<D, P, 32> : cache_attend_kernel<D, P, 64>;
+    return rt == 8 ? cache_attend_kernel<D, P, 8, SH> : rt == 16 ? cache_attend_kernel<D, P, 16, SH>
+         : rt == 32 ? cache_attend_kernel<D, P, 32, SH> : cache_attend_kernel<D, P, 64, SH>;
+}
+template <int D, int P, bool SH>
+static AttFn att_merge_kernel(int rt) {
+    return rt == 8 ? cache_attend_merge<D, P, 8, SH> : rt == 16 ? cache_attend_merge<D, P, 16, SH>
+         : rt == 32 ? cache_attend_merge<D, P, 32, SH> : cache_attend_merge<D, P, 64, SH>;
 }
 template <int D, int P>
-static AttFn att_merge_kernel(int rt) {
-    return rt == 8 ? cache_attend_merge<D, P, 8> : rt == 16 ? cache_attend_merge<D, P, 16>
-         : rt == 32 ? cache_attend_merge<D, P, 32> : cache_attend_merge<D, P, 64>;
+static void att_kernels(int rt, bool sh, AttFn &f, AttFn &merge) {
+    f = sh ? att_kernel<D, P, true>(rt) : att_kernel<D, P, false>(rt);
+    merge = sh ? att_merge_kernel<D, P, true>(rt) : att_merge_kernel<D, P, false>(rt);
 }
 
-}  // namespace mk
-
-using namespace mk;
-
-extern "C" {
-
-int mk_cache_attend_workspace(const mk_cache_desc *cache, const mk_attend_desc *attend, uint64_t *bytes) {
-    AttPlan pl;
-    if (!bytes) return set_error(MK_ERR_INVALID, "bytes is null");
-    if (int rc = att_plan(cache, attend, pl)) return rc;
-    *bytes = pl.ml_bytes + pl.o_bytes;
-    return MK_OK;
-}
-
-int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc *a, void *workspace,
-                    uint64_t workspace_bytes, void *stream) {
+// share: null without shared prefixes
+static int att_launch(const mk_cache_desc *cache, int layer, const mk_attend_desc *a, const mk_shared_desc *share,
+                      void *workspace, uint64_t workspace_bytes, void *stream) {
     AttParams p{};
     AttPlan pl;
     if (int rc = cache_check(cache, p.c)) return rc;
-    if (int rc = att_plan(cache, a, pl)) return rc;
+    const int ngroups = share ? share->groups : 0;
+    if (int rc = att_plan(cache, a, ngroups, pl)) return rc;
     if (layer < 0 || layer >= cache->layers) return set_error(MK_ERR_INVALID, "layer out of range");
-    if (a->window < 0 || !(a->scale >= 0.f) || a->scale > 3e38f)
-        return set_error(MK_ERR_INVALID, "window must not be negative, scale finite and not negative");
+    if (a->window < 0 || a->sinks < 0 || !(a->scale >= 0.f) || a->scale > 3e38f)
+        return set_error(MK_ERR_INVALID, "window and sinks must not be negative, scale finite and not negative");
     if (a->batch == 0 || a->tokens == 0) return MK_OK;
     if (!a->q || !a->out || !a->table || !a->lens) return set_error(MK_ERR_INVALID, "null argument");
     if (a->q % 16 || a->out % 16 || a->lse % 4) return set_error(MK_ERR_INVALID, "q and out must be 16-byte aligned");
     for (int i = 0; i < 2; ++i)
         if (a->q_stride[i] % 8 || a->out_stride[i] % 8)
             return set_error(MK_ERR_INVALID, "q and out strides must be multiples of 8 elements");
-    if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < pl.ml_bytes + pl.o_bytes)
+    if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < pl.bytes())
         return set_error(MK_ERR_INVALID, "workspace missing, unaligned (16 bytes) or too small");
     const int D = cache->head_dim, P = cache->page_tokens;
     const size_t layer_rows = (size_t)layer * cache->pages * cache->kv_heads;
@@ -1010,18 +1157,28 @@ int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc 
     p.tokens = a->tokens;
     p.max_tokens = a->max_tokens;
     p.window = a->window;
+    p.sinks = a->window ? std::min(a->sinks, a->table_width * P) : 0;
+    p.sink_pages = p.sinks ? (p.sinks - 1) / P + 1 : 0;
     p.scale_log2 = a->scale * 1.4426950408889634f;
     p.ctas = pl.ctas;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.part_ml = reinterpret_cast<float *>(ws);
     p.part_o = reinterpret_cast<float *>(ws + pl.ml_bytes);
-    const int fixed = att_fixed_bytes(D, att_nt(pl.rt)) + att_seq_bytes(p.batch) + 128;
+    if (ngroups) {
+        p.groups = reinterpret_cast<const int *>(share->first);
+        p.shared = reinterpret_cast<const int *>(share->shared);
+        p.ngroups = ngroups;
+        p.row_ml = reinterpret_cast<float *>(ws + pl.ml_bytes + pl.o_bytes);
+        p.row_o = reinterpret_cast<float *>(ws + pl.ml_bytes + pl.o_bytes + pl.row_ml_bytes);
+    }
+    const int fixed = att_fixed_bytes(D, att_nt(pl.rt)) + att_seq_bytes(p.batch, ngroups) + 128;
     p.ring = std::min(ATT_MAXRING, (SERVE_SMEM - fixed) / (2 * P * D));
     const int smem = fixed + p.ring * 2 * P * D;
-    AttFn f = D == 64 ? (P == 32 ? att_kernel<64, 32>(pl.rt) : att_kernel<64, 64>(pl.rt))
-                      : (P == 32 ? att_kernel<128, 32>(pl.rt) : att_kernel<128, 64>(pl.rt));
+    AttFn f, merge;
+    if (D == 64) P == 32 ? att_kernels<64, 32>(pl.rt, ngroups, f, merge) : att_kernels<64, 64>(pl.rt, ngroups, f, merge);
+    else P == 32 ? att_kernels<128, 32>(pl.rt, ngroups, f, merge) : att_kernels<128, 64>(pl.rt, ngroups, f, merge);
     static std::atomic<uint32_t> ready[SERVE_MAX_DEVICES];
-    const int variant = (D == 128 ? 8 : 0) + (P == 64 ? 4 : 0) + (pl.rt == 8 ? 0 : pl.rt == 16 ? 1 : pl.rt == 32 ? 2 : 3);
+    const int variant = (ngroups ? 16 : 0) + (D == 128 ? 8 : 0) + (P == 64 ? 4 : 0) + (pl.rt == 8 ? 0 : pl.rt == 16 ? 1 : pl.rt == 32 ? 2 : 3);
     if (int rc = serve_prepare(reinterpret_cast<const void *>(f), ready, variant, false)) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     f<<<pl.ctas, ATT_THREADS, smem, st>>>(p);
@@ -1036,11 +1193,55 @@ int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc 
     cfg.stream = st;
     cfg.attrs = &dep;
     cfg.numAttrs = 1;
-    cfg.dynamicSmemBytes = (size_t)(p.batch + 1) * 8;
-    AttFn mf = D == 64 ? (P == 32 ? att_merge_kernel<64, 32>(pl.rt) : att_merge_kernel<64, 64>(pl.rt))
-                       : (P == 32 ? att_merge_kernel<128, 32>(pl.rt) : att_merge_kernel<128, 64>(pl.rt));
-    e = cudaLaunchKernelEx(&cfg, mf, (const AttParams)p);
+    cfg.dynamicSmemBytes = (size_t)(ngroups + p.batch + 1) * 8 + att_group_bytes(ngroups);
+    e = cudaLaunchKernelEx(&cfg, merge, (const AttParams)p);
     return e == cudaSuccess ? MK_OK : serve_cuda_fail(e, "attention merge launch");
+}
+
+static int shared_check(const mk_attend_desc *a, const mk_shared_desc *s) {
+    if (!a || !s) return set_error(MK_ERR_INVALID, "null descriptor");
+    if (s->groups < 0) return set_error(MK_ERR_INVALID, "negative number of groups");
+    if (s->groups > a->batch || (int64_t)s->groups + a->batch > ATT_MAXB)
+        return set_error(MK_ERR_UNSUPPORTED, "more groups than sequences, or more than 1024 of both in one call");
+    if (a->window || a->sinks) return set_error(MK_ERR_UNSUPPORTED, "shared prefixes with a window");
+    return MK_OK;
+}
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" {
+
+int mk_cache_attend_workspace(const mk_cache_desc *cache, const mk_attend_desc *attend, uint64_t *bytes) {
+    AttPlan pl;
+    if (!bytes) return set_error(MK_ERR_INVALID, "bytes is null");
+    if (int rc = att_plan(cache, attend, 0, pl)) return rc;
+    *bytes = pl.bytes();
+    return MK_OK;
+}
+
+int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc *a, void *workspace,
+                    uint64_t workspace_bytes, void *stream) {
+    return att_launch(cache, layer, a, nullptr, workspace, workspace_bytes, stream);
+}
+
+int mk_cache_attend_shared_workspace(const mk_cache_desc *cache, const mk_attend_desc *attend,
+                                     const mk_shared_desc *shared, uint64_t *bytes) {
+    AttPlan pl;
+    if (!bytes) return set_error(MK_ERR_INVALID, "bytes is null");
+    if (int rc = shared_check(attend, shared)) return rc;
+    if (int rc = att_plan(cache, attend, shared->groups, pl)) return rc;
+    *bytes = pl.bytes();
+    return MK_OK;
+}
+
+int mk_cache_attend_shared(const mk_cache_desc *cache, int layer, const mk_attend_desc *a, const mk_shared_desc *shared,
+                           void *workspace, uint64_t workspace_bytes, void *stream) {
+    if (int rc = shared_check(a, shared)) return rc;
+    if (shared->groups && (!shared->first || !shared->shared || (shared->first | shared->shared) % 4))
+        return set_error(MK_ERR_INVALID, "groups and shared must be aligned device arrays");
+    return att_launch(cache, layer, a, shared, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

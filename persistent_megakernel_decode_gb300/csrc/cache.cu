@@ -419,6 +419,121 @@ __global__ void __launch_bounds__(COPY_THREADS) cache_copy_kernel(const __grid_c
     for (int h = tid; h < p.c.hkv; h += COPY_THREADS) scales[d * p.c.hkv + h] = scales[s * p.c.hkv + h];
 }
 
+// Reordering of beams.  A beam's state is its table row; full pages are named
+// by any number of rows, but the page being filled must be its row's own.  Of a
+// parent's children one keeps that page (the parent itself, else the first) and
+// each other one takes the page of a beam without children, of which there are
+// exactly as many, and a copy of the tokens in it: nothing is allocated, and no
+// page is both read and written.  Bound by the copies' bytes.
+constexpr int REORDER_BEAMS = 64, REORDER_THREADS = 256;
+
+struct ReorderParams {
+    CacheView c;
+    const int *table, *lens, *parents;
+    int *out;
+    int beams, width;
+};
+
+// CTA (row, 2 l + half): half 0 / 1 = K / V of layer l of the row's copy, if it
+// needs one; the last y row writes the table row.
+template <int D, int P>
+__global__ void __launch_bounds__(REORDER_THREADS) cache_reorder_kernel(const ReorderParams p) {
+    __shared__ int s_parent[REORDER_BEAMS], s_extra[REORDER_BEAMS], s_free[REORDER_BEAMS];
+    __shared__ int s_bad;
+    const int tid = threadIdx.x, W = p.beams, row = blockIdx.x % W, l = blockIdx.y / 2;
+    const int64_t row0 = blockIdx.x - row;
+    const bool names = l == p.c.layers, reports = names && row == 0;
+    const int n = p.lens[row0];
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    if (tid < W) {
+        int x = p.parents[row0 + tid];
+        const bool wrong = x < -1 || x >= W || p.lens[row0 + tid] != n || n < 0 || (int64_t)n > (int64_t)p.width * P;
+        if (wrong) {
+            s_bad = 1;
+            if (reports) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, (int)(row0 + tid), p.lens[row0 + tid], -1);
+        }
+        s_parent[tid] = x == -1 ? tid : x;
+    }
+    __syncthreads();
+    const bool bad = s_bad;
+    const int t = bad ? 0 : n / P, part = bad ? 0 : n % P;
+    bool extra = false, dead = true;
+    if (!bad && tid < W) {
+        const int mine = s_parent[tid];
+        bool older = false;  // the parent goes on itself, or has a child before this one
+        for (int i = 0; i < W; ++i) {
+            const int x = s_parent[i];
+            dead = dead && x != tid;
+            older = older || (x == mine && (i < tid || i == mine));
+        }
+        extra = mine != tid && older;
+        s_extra[tid] = extra;
+    }
+    __syncthreads();
+    if (!bad && tid < W && dead) {
+        int k = 0;
+        for (int i = 0; i < tid; ++i) {  // dead rows before this one
+            bool none = true;
+            for (int j = 0; j < W; ++j) none = none && s_parent[j] != i;
+            k += none;
+        }
+        s_free[k] = tid;
+    }
+    __syncthreads();
+    const int parent = bad ? row : s_parent[row];
+    int tail = parent;  // the row whose page being filled this one goes on with
+    bool copies = false;
+    if (part && s_extra[row]) {
+        int k = 0;
+        for (int i = 0; i < row; ++i) k += s_extra[i];
+        tail = s_free[k];
+        copies = true;
+    }
+    const int *from = p.table + (row0 + parent) * p.width;
+    if (names) {
+        const int *self = p.table + (row0 + row) * p.width;
+        for (int c = tid; c < p.width; c += REORDER_THREADS)
+            p.out[(row0 + row) * p.width + c] =
+                c < t ? from[c] : c == t && part ? p.table[(row0 + tail) * p.width + t] : self[c];
+    }
+    if (!copies) return;
+    const int src = from[t], dst = p.table[(row0 + tail) * p.width + t];
+    if ((unsigned)src >= (unsigned)p.c.pages || (unsigned)dst >= (unsigned)p.c.pages) {
+        if (names && tid == 0)
+            note_failure(p.c.status, MK_ERR_DEVICE_CHECK, (int)(row0 + row), t * P, (unsigned)src >= (unsigned)p.c.pages ? src : dst);
+        return;
+    }
+    if (names || src == dst) return;
+    const size_t a = p.c.at(l, src, 0), z = p.c.at(l, dst, 0);
+    if (blockIdx.y % 2 == 0) {
+        const int per = part * (D / 16);  // 16-byte pieces of a head
+        for (int i = tid; i < per * p.c.hkv; i += REORDER_THREADS) {
+            const int h = i / per, x = i - h * per;
+            reinterpret_cast<uint4 *>(p.c.k + (z + h) * P * D)[x] = reinterpret_cast<const uint4 *>(p.c.k + (a + h) * P * D)[x];
+        }
+        for (int h = tid; h < p.c.hkv; h += REORDER_THREADS) p.c.ks[z + h] = p.c.ks[a + h];
+        return;
+    }
+    const int per = (part + 15) / 16, rest = part % 16;  // pieces of a dim's tokens, and what the last has of 16
+    for (int i = tid; i < per * D * p.c.hkv; i += REORDER_THREADS) {
+        const int rw = i / per, x = i - rw * per;
+        uint4 *to = reinterpret_cast<uint4 *>(p.c.v + z * P * D + (size_t)rw * P) + x;
+        uint4 y = reinterpret_cast<const uint4 *>(p.c.v + a * P * D + (size_t)rw * P)[x];
+        if (rest && x == per - 1) {
+            const uint4 old = *to;
+            const auto mix = [&](uint32_t nw, uint32_t od, int w) {
+                const int bytes = min(max(rest - 4 * w, 0), 4);
+                const uint32_t m = bytes == 4 ? ~0u : (1u << (8 * bytes)) - 1;
+                return (nw & m) | (od & ~m);
+            };
+            y = make_uint4(mix(y.x, old.x, 0), mix(y.y, old.y, 1), mix(y.z, old.z, 2), mix(y.w, old.w, 3));
+        }
+        *to = y;
+    }
+    for (int h = tid; h < p.c.hkv; h += REORDER_THREADS) p.c.vs[z + h] = p.c.vs[a + h];
+}
+
 static int move_params(const mk_cache_desc *cache, const mk_cache_rows *rows, const int32_t *table, int width,
                        const int32_t *start, const int32_t *count, int batch, int max_count, MoveParams &m) {
     if (int rc = cache_check(cache, m.c)) return rc;
@@ -539,6 +654,32 @@ int mk_cache_copy(const mk_cache_desc *cache, const int32_t *src, const int32_t 
         if (e != cudaSuccess) return serve_cuda_fail(e, "page copy launch");
     }
     return MK_OK;
+}
+
+int mk_cache_reorder(const mk_cache_desc *cache, const int32_t *table, const int32_t *lens, const int32_t *parents,
+                     int32_t *table_out, int batch, int beams, int table_width, void *stream) {
+    ReorderParams p;
+    if (int rc = cache_check(cache, p.c)) return rc;
+    if (batch < 0 || beams <= 0 || table_width <= 0) return set_error(MK_ERR_INVALID, "negative batch, no beams or an empty table");
+    if (beams > REORDER_BEAMS) return set_error(MK_ERR_UNSUPPORTED, "more than 64 beams");
+    const int64_t rows = (int64_t)batch * beams;
+    if (rows > INT32_MAX || 2 * cache->layers + 1 > 65535) return set_error(MK_ERR_UNSUPPORTED, "too many rows or layers");
+    if (rows == 0) return MK_OK;
+    if (!table || !lens || !parents || !table_out) return set_error(MK_ERR_INVALID, "null argument");
+    if (table < table_out + rows * table_width && table_out < table + rows * table_width)
+        return set_error(MK_ERR_INVALID, "the new table overlaps the old one");
+    p.table = table;
+    p.lens = lens;
+    p.parents = parents;
+    p.out = table_out;
+    p.beams = beams;
+    p.width = table_width;
+    const bool p32 = cache->page_tokens == 32;
+    void (*f)(const ReorderParams) = cache->head_dim == 64 ? (p32 ? cache_reorder_kernel<64, 32> : cache_reorder_kernel<64, 64>)
+                                                           : (p32 ? cache_reorder_kernel<128, 32> : cache_reorder_kernel<128, 64>);
+    f<<<dim3((unsigned)rows, 2 * cache->layers + 1), REORDER_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? MK_OK : serve_cuda_fail(e, "reorder launch");
 }
 
 int mk_cache_status(const mk_cache_desc *cache, int clear, int32_t *status, void *stream) {

@@ -129,18 +129,39 @@ class Kv8Cache:
     # ---- attention ----
     def attend(self, q, table, lens, layer: int = 0, q_start=None, max_tokens: Optional[int] = None,
                scale: Optional[float] = None, window: int = 0, out=None, lse=None, workspace=None,
-               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+               stream=None, sinks: int = 0) -> Tuple[torch.Tensor, torch.Tensor]:
         """Attention of new tokens over ``layer`` of the cache (their K/V stored before): ``lens[b]`` tokens are cached,
         the last T of them are the queries.  ``q`` is bf16 [B, T, Hq, D], or with ``q_start`` (int32 [B + 1]) packed
         [total, Hq, D], sequence b's queries being rows q_start[b] .. q_start[b + 1] - 1 (``max_tokens``: the most of
         one sequence, a hint for the height of the tiles and so for the workspace; default: all rows).  ``window`` > 0:
-        a query sees that many last tokens, itself among them.  Returns (out bf16 like q, lse fp32 without the last
+        a query sees that many last tokens, itself among them, and the sequence's first ``sinks`` ones.  Returns (out bf16 like q, lse fp32 without the last
         axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8 tensor of at least
         :meth:`attend_workspace` bytes, used by one call at a time; by default calls on the default stream share one
         that the cache keeps, others allocate their own."""
         if stream is not None and not rt.is_current(self.index, stream):
             return self._beside(stream, self.attend, q, table, lens, layer, q_start, max_tokens, scale, window, out, lse,
-                                workspace)
+                                workspace, None, sinks)
+        return self._attend(q, table, lens, layer, q_start, max_tokens, scale, window, sinks, out, lse, workspace, None)
+
+    def attend_shared(self, q, table, lens, groups, shared, layer: int = 0, q_start=None, max_tokens: Optional[int] = None,
+                      scale: Optional[float] = None, out=None, lse=None, workspace=None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """:meth:`attend` (without a window) of sequences that share their first pages, as beams or samples of one prompt and
+        conversations behind one instruction do; the shared pages are read once for all rows of a group.  Group g is the
+        sequences groups[g] .. groups[g + 1] - 1 (``groups``: int32 [G + 1]), whose first ``shared[g]`` (int32 [G]) tokens lie
+        in the same pages; what is not a whole page of that counts as the sequences' own.  The table rows still name every
+        page.  ``workspace``: at least :meth:`attend_shared_workspace` bytes."""
+        if stream is not None and not rt.is_current(self.index, stream):
+            return self._beside(stream, self.attend_shared, q, table, lens, groups, shared, layer, q_start, max_tokens, scale,
+                                out, lse, workspace)
+        n = groups.numel() - 1
+        if n < 0:
+            raise ValueError("groups must be an int32 [G + 1] tensor")
+        first, length = self._ints(n + 1, "groups", groups), self._ints(n, "shared", shared)
+        return self._attend(q, table, lens, layer, q_start, max_tokens, scale, 0, 0, out, lse, workspace,
+                            rt.SharedDesc(first, length, n))
+
+    def _attend(self, q, table, lens, layer, q_start, max_tokens, scale, window, sinks, out, lse, workspace, share):
         D, packed, shape = self.head_dim, q_start is not None, q.shape
         if (q.dtype is not torch.bfloat16 or q.get_device() != self.index or len(shape) != (3 if packed else 4)
                 or shape[-1] != D):
@@ -178,10 +199,16 @@ class Kv8Cache:
             raise ValueError("q and out: head_dim must be contiguous, the base 16-byte aligned, strides multiples of 8 "
                              "elements, and sequences evenly spaced rows")
         a = rt.AttendDesc(qp, op, lse.data_ptr(), qt, qs[-2], ot, os[-2], at, held, queries, b, width, hq, total,
-                          most, rt.c_int(window), D ** -0.5 if scale is None else scale, self.num_sms)
+                          most, rt.c_int(window), D ** -0.5 if scale is None else scale, self.num_sms, rt.c_int(sinks))
         own = workspace is None
+        if share is None:
+            call, args = self._lib.mk_cache_attend, (self._ref, rt.c_int(layer), C.byref(a))
+        else:
+            call, args = self._lib.mk_cache_attend_shared, (self._ref, rt.c_int(layer), C.byref(a), C.byref(share))
         if own:
-            size = self._sizes.get((b, width, hq, total, most, self.num_sms)) or self._workspace(a)
+            size = self._sizes.get((b, width, hq, total, most, self.num_sms, share.groups if share else None))
+            if not size:
+                size = self._workspace(a, share) if share else self._workspace(a)
         else:
             rt.check_tensor("workspace", workspace, self.index, torch.uint8)
             if not workspace.is_contiguous():
@@ -193,31 +220,41 @@ class Kv8Cache:
             with self._lock:
                 if self._kept is None or self._kept.numel() < size:
                     self._kept = torch.empty(size, dtype=torch.uint8, device=self.device)
-                rt.launch(self.index, None, self._lib.mk_cache_attend, self._ref, rt.c_int(layer), C.byref(a),
-                          self._kept.data_ptr(), size)
+                rt.launch(self.index, None, call, *args, self._kept.data_ptr(), size)
         else:
             if own:
                 workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
-            rt.launch(self.index, None, self._lib.mk_cache_attend, self._ref, rt.c_int(layer), C.byref(a),
-                      workspace.data_ptr(), size)
+            rt.launch(self.index, None, call, *args, workspace.data_ptr(), size)
         return out, lse
 
-    def _workspace(self, a) -> int:
+    def _workspace(self, a, share=None) -> int:
         n = C.c_uint64()
         with torch.cuda.device(self.index):
-            rt._check(self._lib.mk_cache_attend_workspace(self._ref, C.byref(a), C.byref(n)))
+            if share is None:
+                rt._check(self._lib.mk_cache_attend_workspace(self._ref, C.byref(a), C.byref(n)))
+            else:
+                rt._check(self._lib.mk_cache_attend_shared_workspace(self._ref, C.byref(a), C.byref(share), C.byref(n)))
         if len(self._sizes) >= 1024:
             self._sizes.clear()
-        self._sizes[a.batch, a.table_width, a.q_heads, a.tokens, a.max_tokens, a.num_sms] = n.value
+        self._sizes[a.batch, a.table_width, a.q_heads, a.tokens, a.max_tokens, a.num_sms, share.groups if share else None] = n.value
         return n.value
 
     def attend_workspace(self, batch: int, q_heads: int, max_tokens: int = 1, table_width: int = 1 << 20) -> int:
         """Bytes of workspace :meth:`attend` needs for up to ``batch`` sequences of up to ``max_tokens`` queries (and
         ``table_width`` pages; packed queries: with that ``max_tokens`` as its hint)."""
+        return self._workspace(self._sized(batch, q_heads, max_tokens, table_width))
+
+    def attend_shared_workspace(self, batch: int, q_heads: int, groups: int, max_tokens: int = 1,
+                                table_width: int = 1 << 20) -> int:
+        """Bytes of workspace :meth:`attend_shared` needs for up to ``batch`` sequences of up to ``max_tokens`` queries in
+        ``groups`` groups."""
+        return self._workspace(self._sized(batch, q_heads, max_tokens, table_width), rt.SharedDesc(0, 0, rt.c_int(groups)))
+
+    def _sized(self, batch, q_heads, max_tokens, table_width):
         a = rt.AttendDesc()
         a.batch, a.q_heads, a.tokens, a.max_tokens = map(rt.c_int, (batch, q_heads, batch * max_tokens, max_tokens))
         a.table_width, a.num_sms = rt.c_int(table_width), self.num_sms
-        return self._workspace(a)
+        return a
 
     # ---- pages ----
     def copy_pages(self, src: Sequence[int], dst: Sequence[int], table=None, stream=None):
@@ -234,6 +271,35 @@ class Kv8Cache:
                 raise ValueError("table must be contiguous")
         rt.launch(self.index, None, self._lib.mk_cache_copy, self._ref, s.buffer_info()[0], d.buffer_info()[0], len(s),
                   table.data_ptr() if table is not None else None, table.numel() if table is not None else 0)
+
+    def reorder(self, table, lens, parent, out=None, stream=None) -> torch.Tensor:
+        """The beams' states after a selection: returns the table (int32 like ``table``; ``out``: write it there) whose row
+        b W + w continues row b W + ``parent[b, w]`` (int32 [B, W], -1: itself) of ``table`` (int32 [B W, width]).
+        ``lens`` (int32 [B W]): the tokens that the rows hold, the same for all beams of a prompt.  Full pages are shared
+        from then on; the page being filled, which must be its row's own, is kept by one child and copied for the others
+        into the pages of beams without children, so the rows need pages for all that they may write from the beginning, and
+        the pages of a prompt's beams together stay the same ones (``mk_cache_reorder`` in ``include/mk.h``)."""
+        if stream is not None and not rt.is_current(self.index, stream):
+            return self._beside(stream, self._reorder, table, lens, parent, out)[0]
+        return self._reorder(table, lens, parent, out)[0]
+
+    def _reorder(self, table, lens, parent, out):
+        if parent.dim() != 2:
+            raise ValueError(f"parent must be int32 [B, W], got {parent.dtype} {tuple(parent.shape)}")
+        b, w = parent.shape
+        at, width = self._table(table, b * w)
+        held = self._ints(b * w, "lens", lens)
+        rt.check_tensor("parent", parent, self.index, _I32)
+        parent = parent.contiguous()
+        if out is None:
+            out = torch.empty_like(table)
+        else:
+            rt.check_tensor("out", out, self.index, _I32, table.shape)
+            if not out.is_contiguous():
+                raise ValueError("out must be contiguous")
+        rt.launch(self.index, None, self._lib.mk_cache_reorder, self._ref, at, held, parent.data_ptr(), out.data_ptr(), b, w,
+                  width)
+        return (out,)
 
     def check(self, stream=None):
         """Wait for ``stream`` and raise ``MkError`` if a device-side check has failed since the last call."""

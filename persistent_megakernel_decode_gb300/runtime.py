@@ -47,7 +47,9 @@ EXPORTED = ["mk_plan", "mk_plan_graph", "mk_plan_info_get", "mk_plan_export", "m
             "mk_run_static", "mk_plan_glm", "mk_launch_probe", "mk_plan_export_attn_table",
             "mk_cache_store", "mk_cache_load", "mk_cache_attend", "mk_cache_attend_workspace", "mk_cache_copy",
             "mk_cache_status", "mk_pages_create", "mk_pages_alloc", "mk_pages_share", "mk_pages_release",
-            "mk_pages_compact", "mk_pages_info", "mk_pages_free", "mk_sample"]
+            "mk_pages_compact", "mk_pages_info", "mk_pages_free", "mk_sample",
+            "mk_cache_attend_shared", "mk_cache_attend_shared_workspace", "mk_cache_reorder", "mk_beam_select",
+            "mk_beam_select_workspace"]
 STATIC_WORKSPACE_BYTES = 64 << 20
 
 
@@ -130,7 +132,11 @@ class AttendDesc(C.Structure):
         (n, C.c_int64) for n in ("q_token_stride", "q_head_stride", "out_token_stride", "out_head_stride")] + [
         (n, C.c_uint64) for n in ("table", "lens", "q_start")] + [
         (n, C.c_int) for n in ("batch", "table_width", "q_heads", "tokens", "max_tokens", "window")] + [
-        ("scale", C.c_float), ("num_sms", C.c_int)]
+        ("scale", C.c_float), ("num_sms", C.c_int), ("sinks", C.c_int)]
+
+
+class SharedDesc(C.Structure):
+    _fields_ = [("first", C.c_uint64), ("shared", C.c_uint64), ("groups", C.c_int)]
 
 
 class SampleDesc(C.Structure):
@@ -138,6 +144,12 @@ class SampleDesc(C.Structure):
                 ("bf16", C.c_int)] + [(n, C.c_uint64) for n in (
                     "u", "tokens", "logprob", "temperature_rows", "top_k_rows", "top_p_rows", "min_p_rows")] + [
         ("temperature", C.c_float), ("top_k", C.c_int), ("top_p", C.c_float), ("min_p", C.c_float)]
+
+
+class BeamDesc(C.Structure):
+    _fields_ = [("logits", C.c_uint64), ("row_stride", C.c_int64)] + [
+        (n, C.c_int) for n in ("batch", "beams", "vocab", "bf16", "num", "end")] + [
+        (n, C.c_uint64) for n in ("scores", "finished", "out_scores", "parents", "tokens")]
 
 
 _lib = None
@@ -170,6 +182,10 @@ def load():
                                                                 P, P, C.c_int, C.c_int, P]
     lib.mk_cache_attend.argtypes = [C.POINTER(CacheDesc), C.c_int, C.POINTER(AttendDesc), P, C.c_uint64, P]
     lib.mk_cache_attend_workspace.argtypes = [C.POINTER(CacheDesc), C.POINTER(AttendDesc), C.POINTER(C.c_uint64)]
+    lib.mk_cache_attend_shared.argtypes = [C.POINTER(CacheDesc), C.c_int, C.POINTER(AttendDesc), C.POINTER(SharedDesc), P,
+                                           C.c_uint64, P]
+    lib.mk_cache_attend_shared_workspace.argtypes = [C.POINTER(CacheDesc), C.POINTER(AttendDesc), C.POINTER(SharedDesc),
+                                                     C.POINTER(C.c_uint64)]
     lib.mk_cache_copy.argtypes = [C.POINTER(CacheDesc), P, P, C.c_int, P, C.c_int64, P]
     lib.mk_cache_status.argtypes = [C.POINTER(CacheDesc), C.c_int, P, P]
     lib.mk_pages_create.argtypes = [C.c_int, C.POINTER(P)]
@@ -180,6 +196,9 @@ def load():
     lib.mk_pages_free.argtypes = [P]
     lib.mk_pages_free.restype = None
     lib.mk_sample.argtypes = [C.POINTER(SampleDesc), P]
+    lib.mk_cache_reorder.argtypes = [C.POINTER(CacheDesc), P, P, P, P, C.c_int, C.c_int, C.c_int, P]
+    lib.mk_beam_select.argtypes = [C.POINTER(BeamDesc), P, C.c_uint64, P]
+    lib.mk_beam_select_workspace.argtypes = [C.POINTER(BeamDesc), C.POINTER(C.c_uint64)]
     lib.mk_free.argtypes = [P]
     lib.mk_free.restype = None
     lib.mk_last_error.restype = C.c_char_p
@@ -325,6 +344,52 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
                    tokens.data_ptr(), logprob.data_ptr(), *rows, *values)
     launch(index, None, load().mk_sample, C.byref(d))
     return tokens, logprob
+
+
+def beam_select(logits, scores, num: Optional[int] = None, finished=None, end: int = 0, stream=None):
+    """Beam search's selection: of all tokens after all beams of a prompt the ``num`` (default: as many as beams) with the
+    largest score + log softmax(logits), ties to the lower beam, then the lower token (``mk_beam_desc`` in ``include/mk.h``
+    has the definitions).  ``logits`` [B W, V] (fp32 or bf16 CUDA tensor, rows V or more apart), ``scores`` fp32 [B, W]: a
+    beam whose score is not finite offers nothing, as all but one do before the first step.  ``finished`` (bool [B, W]): such
+    a beam goes on as it is, with token ``end``.  Returns (scores fp32, parents int32, tokens int32), all [B, num], the
+    largest first: beam ``parents[b, i]`` of prompt b goes on with ``tokens[b, i]``; -inf, -1 and -1 where there are fewer.
+    Asynchronous on ``stream`` (default: the current one), where the tensors must be ready; may be captured into a CUDA
+    graph."""
+    if torch is None:
+        need_torch()
+    index = logits.get_device()
+    if index < 0:
+        raise ValueError("logits must be a CUDA tensor")
+    if stream is not None and not is_current(index, stream):
+        return beside(index, stream, beam_select, logits, scores, num, finished, end)
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits must be fp32 or bf16 [B W, V], got {logits.dtype} {tuple(logits.shape)}")
+    if scores.dim() != 2:
+        raise ValueError(f"scores must be fp32 [B, W], got {scores.dtype} {tuple(scores.shape)}")
+    rows, v = logits.shape
+    b, w = scores.shape
+    check_tensor("scores", scores, index, torch.float32)
+    if b * w != rows:
+        raise ValueError(f"logits have {rows} rows for {b} x {w} scores")
+    stride, inner = logits.stride()
+    if inner != 1 and v > 1:
+        raise ValueError("logits must be contiguous along the vocabulary")
+    scores = scores.contiguous()
+    if finished is not None:
+        check_tensor("finished", finished, index, torch.bool, (b, w))
+        finished = finished.contiguous()
+    num = w if num is None else c_int(num)
+    shape, device = (b, max(num, 0)), logits.device
+    out = torch.empty(shape, dtype=torch.float32, device=device)
+    parents, tokens = (torch.empty(shape, dtype=torch.int32, device=device) for _ in range(2))
+    d = BeamDesc(logits.data_ptr(), stride if rows > 1 else v, b, w, v, logits.dtype is torch.bfloat16, num, c_int(end),
+                 scores.data_ptr(), 0 if finished is None else finished.data_ptr(), out.data_ptr(), parents.data_ptr(),
+                 tokens.data_ptr())
+    size = C.c_uint64()
+    _check(load().mk_beam_select_workspace(C.byref(d), C.byref(size)))
+    workspace = torch.empty(size.value, dtype=torch.uint8, device=device)
+    launch(index, None, load().mk_beam_select, C.byref(d), workspace.data_ptr(), size.value)
+    return out, parents, tokens
 
 
 class Plan:
