@@ -3,69 +3,67 @@
 // Mathematics.  A candidate (beam w, token v) has the total s_w + z_wv -
 // log sum_v exp z_wv; the `num` largest of a prompt's beams are wanted, ties to
 // the lowest w V + v.  Within a beam the order is that of the logits, so each
-// beam's row gives its `num` largest logits and the sum of its exponentials,
-// and the beams' short sorted lists are merged by their totals.
+// part of a beam's row gives its `num` largest logits and a sum of exponentials;
+// the parts' short lists are then ordered by their totals.
 //
 // The order between beams hangs on the sums: two totals closer than their
 // errors would change places.  Totals are therefore formed in 64 bits, and the
-// sum is kept to a few 2^-30 of itself: the row's largest logits (where single
+// sum is kept to a few 2^-28 of itself: a part's largest logits (where single
 // rounding errors weigh) by the fixed-point weights of dev_weigh.cuh, the rest
 // as fp32 2^f after a two-part reduction of the argument, whose errors (2^-23
-// of a term, either way) average out; all partial sums are joined as integers,
-// so no order of arrival changes anything.
+// of a term, either way) average out; partial sums are joined as integers, so
+// no order of arrival changes anything.
 //
-// The largest of a row without sorting it: a bound that at least `num` threads'
-// largest values reach is found by bisection, one barrier and vote a step; the
-// few logits that reach it (at most as many per thread as it holds) are ranked
-// by comparing each with all.  Ties at the bound go on by bisection over the
-// index.
+// The largest without sorting: a bound that at least `num` threads' largest
+// values reach is found by bisection, one barrier and vote a step; the few
+// logits that reach it (at most as many per thread as it holds) are listed.
+// Later pieces of the part list what is above the bound; now and then the bound
+// rises to what the listed allow, and the list shrinks to it.  At the end the
+// list is ranked by comparing each with all.
 //
-// Work split.  One cluster of CTAs per row, the row's logits in registers; the
-// clusters' lists meet in their first CTA.  A second, dependent launch merges
-// the beams of a prompt.  Bytes bound it: each logit is read once.
-#include <cooperative_groups.h>
-
+// Work split.  A CTA streams a part of a row, 4096 logits at a time in
+// registers, the next piece's loads in flight.  A second, dependent launch orders
+// a prompt's candidates, one CTA each.  Bytes bound it: each logit is read once.
 #include <algorithm>
 #include <climits>
 
 #include "dev_weigh.cuh"
 
-namespace cg = cooperative_groups;
-
 namespace mk {
 
-constexpr int BM_THREADS = 512, BM_WARPS = BM_THREADS / 32;
-constexpr int BM_MAXCTAS = 16, BM_MAXPER = 80;  // CTAs per row, logits per thread
+constexpr int BM_THREADS = 256, BM_WARPS = BM_THREADS / 32;
+constexpr int BM_PER = 16, BM_PIECE = BM_THREADS * BM_PER;  // logits per thread and CTA at a time
 constexpr int BM_MAXVOCAB = 622592;
 constexpr int BM_MAXBEAMS = 64, BM_MAXNUM = 128;
+constexpr int BM_CANDIDATES = 8192;                          // of a prompt at most: beams x parts x num
+constexpr int BM_MERGE_THREADS = 512;
 
-// What the second launch needs of a row beside its list.
-struct BeamRow {
+// What the second launch needs of a part beside its list.
+struct BeamPart {
     float top;              // the largest logit
     int ref;                // `rest` is in units of 2^(ref - 44)
-    unsigned long long list, rest;  // sums: of the weights relative to the largest, in 2^-44; of the others
+    unsigned long long list, rest;  // sums: of the listed weights relative to the largest, in 2^-44; of the others
 };
 
 struct BeamParams {
     const void *logits;
     int64_t row_stride;
-    int vocab, beams, num, chunk, ctas, cap;
+    int vocab, beams, num, chunk, parts, limit, cap;
     const float *scores;
     const uint8_t *finished;
     int end;
-    BeamRow *rows;              // workspace: [batch x beams]
-    unsigned long long *keys;   // workspace: [batch x beams][num], ascending, then KEY_NONE
+    BeamPart *rows;             // workspace: [batch x beams][parts]
+    unsigned long long *keys;   // workspace: [batch x beams][parts][num], ascending, then KEY_NONE
     float *out;
     int *parents, *tokens;
 };
 
 struct alignas(16) BeamShared {  // the lists lie behind it
     uint32_t table[32];
-    uint32_t tops[BM_MAXCTAS];                       // every CTA's largest logit, ordered
-    unsigned long long list[BM_MAXCTAS], rest[BM_MAXCTAS];  // every CTA's sums
     unsigned long long red[2][BM_WARPS];
-    uint32_t red_u[BM_WARPS];
-    int count;
+    uint32_t red_u[2 * BM_WARPS];
+    unsigned long long first;
+    int count, shrunk;
 };
 
 // A beam that is extended: its score is finite and it has not finished.
@@ -74,16 +72,11 @@ DEV bool beam_live(const BeamParams &p, int64_t row) {
     return fabsf(s) < INFINITY && !(p.finished && p.finished[row]);
 }
 
-// One logit: NaN counts as -inf, -0 as +0 (they are equal: the index decides).
+// A logit as it is ordered: NaN counts as -inf, -0 as +0 (they are equal: the index decides).
 DEV float beam_logit(float x) { return fmaxf(x, -INFINITY) + 0.f; }
 
-DEV float key_value(unsigned long long key) {
-    const uint32_t o = ~(uint32_t)(key >> 32);
-    return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
-}
-
-DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+DEV float ordered_value(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o); }
+DEV float key_value(unsigned long long key) { return ordered_value(~(uint32_t)(key >> 32)); }
 
 DEV float exp2_approx(float x) {
     float y;
@@ -103,178 +96,291 @@ DEV uint32_t block_sum(uint32_t v, uint32_t *red) {
     return sum;
 }
 
-// Ranks of `n` lists' entries among all of them: lists[l][0 .. len(l)) ascend
-// by `better`, and each entry's rank is its place plus, for every other list,
-// how many of that come before it.  rank[l * stride + i] must be zeroed.
-template <typename Len, typename Before>
-DEV void merge_ranks(int n, int stride, const Len &len, const Before &before, int *rank) {
-    const int pairs = n * n * stride;
-    for (int x = threadIdx.x; x < pairs; x += BM_THREADS) {
-        const int other = x % n, e = x / n, l = e / stride, i = e % stride;
-        if (i >= len(l)) continue;
-        int a = 0, z = len(other);
-        if (other == l) {
-            a = i;
-        } else {  // the first of `other` that does not come before
-            while (a < z) {
-                const int mid = (a + z) / 2;
-                if (before(other, mid, l, i)) a = mid + 1;
-                else z = mid;
-            }
-        }
-        if (a) atomicAdd(&rank[e], a);
+// A bound from lo up that at least `num` and at most `limit` threads' values
+// (ordered) reach, given that more than `limit` reach lo; false: more than
+// `limit` reach the bound, fewer than `num` exceed it.  The middle is first
+// that of the values between the threads' least and largest, where logits lie
+// evenly enough to be done in some five steps; then that of the 32-bit integers.
+template <int WARPS>
+DEV bool bisect(uint32_t mine, uint32_t &lo, int num, int limit, uint32_t *red) {
+    const int lane = threadIdx.x % 32;
+    uint32_t hi = __reduce_max_sync(FULL, mine), least = __reduce_min_sync(FULL, mine >= lo ? mine : ~0u);
+    __syncthreads();
+    if (lane == 0) {
+        red[threadIdx.x / 32] = hi;
+        red[WARPS + threadIdx.x / 32] = least;
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+        hi = max(hi, red[i]);
+        least = min(least, red[WARPS + i]);
+    }
+    lo = least;  // as many reach it
+    for (int step = 0; lo < hi; ++step) {
+        uint32_t mid = lo + (hi - lo + 1) / 2;
+        if (step < 10) mid = min(max(ordered_bits(0.5f * ordered_value(lo) + 0.5f * ordered_value(hi)), lo + 1), hi);
+        const int n = __syncthreads_count(mine >= mid);
+        if (n > limit) {
+            lo = mid;
+        } else if (n >= num) {
+            lo = mid;
+            return true;
+        } else {
+            hi = mid - 1;
+        }
+    }
+    return false;
 }
 
-template <int E, bool BF16>
-__global__ void __launch_bounds__(BM_THREADS) beam_row_kernel(const BeamParams p) {
+constexpr uint32_t LEAST = 0x00800000u;  // the least value above -inf, ordered
+
+template <bool BF16>
+__global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int VEC = BF16 ? 8 : 4;
+    constexpr int E = BM_PER, VEC = BF16 ? 8 : 4, SIZE = BF16 ? 2 : 4;
     BeamShared &s = *reinterpret_cast<BeamShared *>(mk_smem);
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int rank = (int)(blockIdx.x % p.ctas);
-    const int64_t row = blockIdx.x / p.ctas;
-    if (!beam_live(p, row)) return;  // the whole cluster
-    cluster_arrive();
-    cg::cluster_group cl = cg::this_cluster();
-    // behind s: candidates [cap], all CTAs' lists [ctas][num], ranks of either
+    // behind s: the listed keys [cap], their ranks [cap]
     unsigned long long *cand = reinterpret_cast<unsigned long long *>(mk_smem + sizeof(BeamShared));
-    unsigned long long *lists = cand + p.cap;
-    int *ranks = reinterpret_cast<int *>(lists + p.ctas * p.num);
+    int *ranks = reinterpret_cast<int *>(cand + p.cap);
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int part = (int)(blockIdx.x % p.parts);
+    const int64_t row = blockIdx.x / p.parts;
+    if (!beam_live(p, row)) return;
 
     // the CTA's logits [first, last), VEC of a thread together, from the 16-byte boundary at or before the first
-    const int first = min(rank * p.chunk, p.vocab), last = min(first + p.chunk, p.vocab);
-    constexpr int SIZE = BF16 ? 2 : 4;
+    const int first = part * p.chunk, last = min(first + p.chunk, p.vocab);
     const char *base = static_cast<const char *>(p.logits) + row * p.row_stride * SIZE;
-    const int shift = (int)(((uintptr_t)base + (size_t)first * SIZE) % 16 / SIZE);
-    const auto at = [&](int i) { return first - shift + (i / VEC * BM_THREADS + tid) * VEC + i % VEC; };
-    float v[E];
+    const int begin = first - (int)(((uintptr_t)base + (size_t)first * SIZE) % 16 / SIZE);
+    const int pieces = (last - begin + BM_PIECE - 1) / BM_PIECE;
+    uint4 raw[E / VEC];
+    const auto load = [&](int piece) {
 #pragma unroll
-    for (int i = 0; i < E; i += VEC) {
-        const int x = at(i);
-        if (x >= first && x + VEC <= last) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(base + (size_t)x * SIZE));
+        for (int i = 0; i < E / VEC; ++i) {
+            const int x = begin + piece * BM_PIECE + (i * BM_THREADS + tid) * VEC;
+            if (x >= first && x + VEC <= last) {
+                raw[i] = __ldcs(reinterpret_cast<const uint4 *>(base + (size_t)x * SIZE));
+            } else {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (BF16) {
+                        const uint16_t *z = reinterpret_cast<const uint16_t *>(base);
+                        const int a = x + 2 * j;
+                        const uint32_t lo = a >= first && a < last ? z[a] : 0xff80u, hi = a + 1 >= first && a + 1 < last ? z[a + 1] : 0xff80u;
+                        w[j] = lo | hi << 16;
+                    } else {
+                        w[j] = x + j >= first && x + j < last ? reinterpret_cast<const uint32_t *>(base)[x + j] : 0xff800000u;
+                    }
+                }
+                raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    };
+    load(0);
+    if (tid < 32) s.table[tid] = c_table[tid];
+    if (tid == 0) s.count = 0;
+    constexpr float CH = 1.44269502162933349609375f, CL = 1.92596303350011e-08f;  // log2(e)
+    // All of these are the same in every thread but `rest`.
+    float bound = ordered_value(LEAST);
+    bool strict = false;             // num logits of lower indices that reach the bound are listed: only what exceeds it is wanted
+    bool slow = false;               // logits too large for the products below
+    int ref = 0, room = p.cap;       // room: entries that the list has at least
+    unsigned long long rest = 0;
+    // 2^(x log2(e) - ref): x log2(e) = n + f, f good to 2^-26; e^-80 below the bound is nothing (-inf and NaN too)
+    const auto term = [&](float z) {
+        constexpr float ROUND = 12582912.f;  // its bits shifted left by 23 are 0
+        const float x = fmaxf(z, bound - 80.f);
+        const float t = fmaf(x, CH, ROUND), k = t - ROUND;
+        const float f = fmaf(x, CL, fmaf(x, CH, -k));
+        return __int_as_float(__float_as_int(exp2_approx(f)) + (__float_as_int(t) << 23) - (ref << 23));
+    };
+    const auto raise_to = [&](uint32_t o) {
+        bound = ordered_value(o);
+        strict = true;
+        slow = slow || !(fabsf(bound) <= 1e5f);
+        if (!slow) {
+            const int r = (int)ceilf(bound * CH);
+            rest = r - ref < 64 ? rest >> max(r - ref, 0) : 0;  // (a first bound below 0: nothing is summed yet)
+            ref = r;
+        }
+    };
+    // A listed logit's key; the list holds the index alone until it is first looked through.
+    const auto key_at = [&](int i) {
+        const unsigned long long key = cand[i];
+        if (key >> 32) return key;
+        const int x = (int)key;
+        if constexpr (BF16) return sample_key(beam_logit(bf16_at(reinterpret_cast<const uint16_t *>(base), x)), x);
+        else return sample_key(beam_logit(reinterpret_cast<const float *>(base)[x]), x);
+    };
+    // ranks of the listed among each other; the threads of a column share one
+    const auto rank_all = [&](int n) {
+        for (int i = tid; i < n; i += BM_THREADS) ranks[i] = 0;
+        __syncthreads();
+        int wide = 32;
+        while (wide < n && wide < BM_THREADS) wide *= 2;
+        for (int i = tid % wide; i < n; i += wide) {
+            const unsigned long long key = cand[i];
+            int before = 0;
+            for (int j = tid / wide; j < n; j += BM_THREADS / wide) before += cand[j] < key;
+            if (before) atomicAdd(&ranks[i], before);
+        }
+        __syncthreads();
+    };
+    // The bound up to what the threads' largest of the listed allow, the list
+    // down to it; `hard`: down to the num first, where few threads list them.
+    const auto shrink = [&](bool hard) {
+        const int n = s.count;
+        unsigned long long first_key = KEY_NONE;
+        for (int i = tid; i < n; i += BM_THREADS) {
+            const unsigned long long key = key_at(i);
+            cand[i] = key;
+            first_key = min(first_key, key);
+        }
+        if (tid == 0) s.shrunk = 0;
+        hard = hard && n > p.num;
+        const uint32_t floor = ordered_bits(bound);
+        if (hard) {
+            __syncthreads();
+            rank_all(n);
+            for (int i = tid; i < n; i += BM_THREADS)
+                if (ranks[i] == p.num - 1) s.red_u[0] = ~(uint32_t)(cand[i] >> 32);
+            __syncthreads();
+            raise_to(s.red_u[0]);
+        } else {
+            const uint32_t mine = first_key == KEY_NONE ? 0 : ~(uint32_t)(first_key >> 32);
+            if (__syncthreads_count(mine >= floor) > p.num) {
+                uint32_t lo = floor;
+                bisect<BM_WARPS>(mine, lo, p.num, p.num + p.num / 2 + 4, s.red_u);
+                if (lo > floor) raise_to(lo);
+            }
+        }
+        float a = 0.f;
+        for (int i0 = 0; i0 < n; i0 += BM_THREADS) {
+            const bool there = i0 + tid < n;
+            const unsigned long long key = there ? cand[i0 + tid] : KEY_NONE;
+            const bool out = hard && there && ranks[i0 + tid] >= p.num;
+            __syncthreads();
+            if (there) {
+                const float z = key_value(key);
+                if (z >= bound && !out) cand[atomicAdd(&s.shrunk, 1)] = key;
+                else if (!slow) a += term(z);
+            }
+        }
+        rest += __float2ull_rn(a * 0x1p44f);
+        __syncthreads();
+        if (tid == 0) s.count = s.shrunk;
+        __syncthreads();
+    };
+    for (int piece = 0; piece < pieces; ++piece) {
+        float v[E];
+#pragma unroll
+        for (int i = 0; i < E / VEC; ++i) {
+            const uint4 w = raw[i];
             if constexpr (BF16) {
                 float f[8];
                 bf16x8(w, f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i + j] = f[j];
+                for (int j = 0; j < 8; ++j) v[i * VEC + j] = f[j];
             } else {
-                v[i] = __uint_as_float(w.x), v[i + 1] = __uint_as_float(w.y);
-                v[i + 2] = __uint_as_float(w.z), v[i + 3] = __uint_as_float(w.w);
+                v[4 * i] = __uint_as_float(w.x), v[4 * i + 1] = __uint_as_float(w.y);
+                v[4 * i + 2] = __uint_as_float(w.z), v[4 * i + 3] = __uint_as_float(w.w);
             }
-        } else {
+        }
+        if (piece + 1 < pieces) load(piece + 1);
+        const auto at = [&](int i) { return begin + piece * BM_PIECE + (i / VEC * BM_THREADS + tid) * VEC + i % VEC; };
+        uint32_t want = 0;  // bit i: logit i is listed
+        float a[2] = {0.f, 0.f};
+        int threads = BM_THREADS;
+        if (strict) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                v[i + j] = -INFINITY;
-                if (x + j >= first && x + j < last) {
-                    if constexpr (BF16) v[i + j] = bf16_at(reinterpret_cast<const uint16_t *>(base), x + j);
-                    else v[i + j] = reinterpret_cast<const float *>(base)[x + j];
+            for (int i = 0; i < E; ++i) {
+                const float e = term(v[i]);
+                if (v[i] > bound) want |= 1u << i;
+                else a[i % 2] += e;
+            }
+            threads = __syncthreads_count(want != 0);
+        }
+        if (threads > p.limit || !strict) {  // the first piece, or one with many large logits: the bound from its own
+            float most = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < E; ++i) most = fmaxf(most, v[i]);
+            const uint32_t mine = ordered_bits(beam_logit(most));
+            uint32_t lo = ordered_bits(bound) + (strict ? 1 : 0);
+            int upto = INT_MAX;  // of the logits at the bound, those up to this index
+            threads = __syncthreads_count(mine >= lo);
+            if (threads > p.limit) {
+                const bool found = bisect<BM_WARPS>(mine, lo, p.num, p.num + p.num / 2 + 4, s.red_u);
+                raise_to(lo);
+                threads = p.limit;
+                if (!found) {  // many threads have the same largest logit
+                    uint32_t more = 0;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) more += v[i] > bound;
+                    const int need = p.num - (int)block_sum(more, s.red_u);
+                    int x = max(first, begin + piece * BM_PIECE) - 1, z = min(last, begin + (piece + 1) * BM_PIECE) - 1;
+                    if (need <= 0) z = x;
+                    while (z - x > 1) {  // the least index up to which `need` logits are at the bound
+                        const int mid = x + (z - x) / 2;
+                        uint32_t n = 0;
+#pragma unroll
+                        for (int i = 0; i < E; ++i) n += v[i] == bound && at(i) <= mid;
+                        if ((int)block_sum(n, s.red_u) >= need) z = mid;
+                        else x = mid;
+                    }
+                    upto = z;
+                }
+            }
+            want = 0;
+            a[0] = a[1] = 0.f;
+            const float from = ordered_value(lo);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const bool in = v[i] > from || (v[i] == from && at(i) <= upto);
+                want |= (uint32_t)in << i;
+                if (!in && strict) a[i % 2] += term(v[i]);  // (no bound yet: all that are finite are listed)
+            }
+        }
+        if (want) {
+            int to = atomicAdd(&s.count, __popc(want));
+            for (; want; want &= want - 1) cand[to++] = (uint32_t)at(__ffs(want) - 1);
+        }
+        if (!slow && strict) rest += __float2ull_rn((a[0] + a[1]) * 0x1p44f);
+        room -= threads * E;
+        if (room < p.limit * E || (piece >= 3 && (piece & (piece + 1)) == 0)) {
+            __syncthreads();
+            if (room < p.limit * E || piece + 1 < pieces) {
+                shrink(false);
+                room = p.cap - s.count;
+                if (room < p.limit * E) {
+                    __syncthreads();  // the count is read
+                    shrink(true);
+                    room = p.cap - s.count;
                 }
             }
         }
     }
-    if (tid < 32) s.table[tid] = c_table[tid];
-    if (tid == 0) s.count = 0;
-    for (int i = tid; i < p.cap; i += BM_THREADS) ranks[i] = 0;
-    float most = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        v[i] = beam_logit(v[i]);
-        most = fmaxf(most, v[i]);
-    }
-    const uint32_t mine = ordered_bits(most);
-    uint32_t top_bits = __reduce_max_sync(FULL, mine);
-    if (lane == 0) s.red_u[warp] = top_bits;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < BM_WARPS; ++i) top_bits = max(top_bits, s.red_u[i]);
-    cluster_wait();  // every CTA runs: its shared memory may be written
-    if (tid < p.ctas) *cl.map_shared_rank(&s.tops[rank], tid) = top_bits;
-    cluster_arrive();
-
-    // a bound that num threads' largest reach, and so many at most that their logits fit the list
-    const int limit = p.cap / E;
-    uint32_t lo = 0x00800000u, hi = top_bits;  // from the least value above -inf
-    int upto = INT_MAX;                        // of the logits at the bound, those up to this index
-    if (__syncthreads_count(mine >= lo) > limit) {
-        bool found = false;
-        while (lo < hi) {
-            const uint32_t mid = lo + (hi - lo + 1) / 2;
-            const int n = __syncthreads_count(mine >= mid);
-            if (n > limit) {
-                lo = mid;
-            } else if (n >= p.num) {
-                lo = mid;
-                found = true;
-                break;
-            } else {
-                hi = mid - 1;
-            }
-        }
-        if (!found) {  // many threads have the same largest logit
-            const float bound = key_value((unsigned long long)~lo << 32);
-            uint32_t more = 0;
-#pragma unroll
-            for (int i = 0; i < E; ++i) more += v[i] > bound;
-            const int need = p.num - (int)block_sum(more, s.red_u);
-            int a = first - 1, z = last - 1;  // the least index up to which `need` logits are at the bound
-            if (need <= 0) z = a;
-            while (z - a > 1) {
-                const int mid = a + (z - a) / 2;
-                uint32_t n = 0;
-#pragma unroll
-                for (int i = 0; i < E; ++i) n += v[i] == bound && at(i) <= mid;
-                if ((int)block_sum(n, s.red_u) >= need) z = mid;
-                else a = mid;
-            }
-            upto = z;
-        }
-    }
-    const float bound = key_value((unsigned long long)~lo << 32);
-    const auto listed = [&](float x, int i) { return x > bound || (x == bound && i <= upto); };
-    if (mine >= lo) {
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (listed(v[i], at(i))) cand[atomicAdd(&s.count, 1)] = sample_key(v[i], at(i));
-    }
-    __syncthreads();
+    shrink(false);
     const int n = s.count, kept = min(n, p.num);
-    // ranks: the threads of a column share a candidate
-    int wide = 32;
-    while (wide < n && wide < BM_THREADS) wide *= 2;
-    for (int i = tid % wide; i < n; i += wide) {
-        const unsigned long long key = cand[i];
-        int before = 0;
-        for (int j = tid / wide; j < n; j += BM_THREADS / wide) before += cand[j] < key;
-        if (before) atomicAdd(&ranks[i], before);
-    }
-    cluster_wait();  // the largest logits of all CTAs
-    uint32_t row_top = 0;
-    for (int i = 0; i < p.ctas; ++i) row_top = max(row_top, s.tops[i]);
-    const float top = key_value((unsigned long long)~row_top << 32);
-    const Weigher weigh{top, 1.44269502162933349609375f, 1.92596303350011e-08f, s.table};
-    unsigned long long list = 0, rest = 0;
-    int ref = 0;
-    if (top > -INFINITY) {
-        if (fabsf(top) <= 1e5f) {
-            // 2^(x log2(e) - ref): x log2(e) = n + f, f good to 2^-26 (the largest sum per thread is E)
-            constexpr float ROUND = 12582912.f;
-            const float least = top - 80.f;  // e^-80: nothing beside 2^-44
-            ref = (int)ceilf(top * weigh.ch);
-            float a[2] = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float x = fmaxf(v[i], least);
-                const float t = fmaf(x, weigh.ch, ROUND), k = t - ROUND;
-                const float f = fmaf(x, weigh.cl, fmaf(x, weigh.ch, -k));
-                const float e = __int_as_float(__float_as_int(exp2_approx(f)) + ((__float_as_int(t) - __float_as_int(ROUND) - ref) << 23));
-                a[i % 2] += listed(v[i], at(i)) || v[i] == -INFINITY ? 0.f : e;
-            }
-            rest = __float2ull_rn((a[0] + a[1]) * 0x1p44f);
-            for (int i = tid; i < n; i += BM_THREADS) list += weigh(key_value(cand[i]));
-        } else {
-            for (int i = 0; i < E; ++i) list += v[i] == -INFINITY ? 0 : weigh(v[i]);
+    rank_all(n);
+    for (int i = tid; i < n; i += BM_THREADS)
+        if (ranks[i] == 0) s.first = cand[i];
+    __syncthreads();
+    const float top = n ? key_value(s.first) : -INFINITY;
+    const Weigher weigh{top, CH, CL, s.table};
+    unsigned long long list = 0;
+    if (!slow) {
+        for (int i = tid; i < n; i += BM_THREADS) list += weigh(key_value(cand[i]));
+    } else {  // products with log2(e) would lose the fraction: all by the difference from the largest
+        rest = 0;
+#pragma unroll 1
+        for (int x = first + tid; x < last; x += BM_THREADS) {
+            float z;
+            if constexpr (BF16) z = bf16_at(reinterpret_cast<const uint16_t *>(base), x);
+            else z = reinterpret_cast<const float *>(base)[x];
+            z = beam_logit(z);
+            list += z == -INFINITY ? 0 : weigh(z);
         }
     }
     list = warp_sum64(list);
@@ -283,38 +389,18 @@ __global__ void __launch_bounds__(BM_THREADS) beam_row_kernel(const BeamParams p
         s.red[0][warp] = list;
         s.red[1][warp] = rest;
     }
-    __syncthreads();  // the ranks too
-    unsigned long long *to = cl.map_shared_rank(lists, 0) + rank * p.num;
+    __syncthreads();
+    unsigned long long *to = p.keys + (int64_t)blockIdx.x * p.num;
     for (int i = tid; i < n; i += BM_THREADS)
         if (ranks[i] < p.num) to[ranks[i]] = cand[i];
     for (int i = kept + tid; i < p.num; i += BM_THREADS) to[i] = KEY_NONE;
-    if (tid < 2) {
-        unsigned long long sum = 0;
-        for (int i = 0; i < BM_WARPS; ++i) sum += s.red[tid][i];
-        *cl.map_shared_rank(tid ? &s.rest[rank] : &s.list[rank], 0) = sum;
-    }
-    cluster_arrive();
-    cluster_wait();
-    if (rank != 0) return;
-
-    // the CTAs' lists into one
-    for (int i = tid; i < p.ctas * p.num; i += BM_THREADS) ranks[i] = 0;
-    __syncthreads();
-    const auto len = [&](int) { return p.num; };
-    merge_ranks(p.ctas, p.num, len, [&](int l, int i, int m, int j) {  // KEY_NONE: among themselves in the lists' order
-        const unsigned long long x = lists[l * p.num + i], y = lists[m * p.num + j];
-        return x < y || (x == y && l < m);
-    }, ranks);
-    __syncthreads();
-    for (int i = tid; i < p.ctas * p.num; i += BM_THREADS)
-        if (ranks[i] < p.num) p.keys[row * p.num + ranks[i]] = lists[i];
     if (tid == 0) {
-        BeamRow r{top, ref, 0, 0};
-        for (int i = 0; i < p.ctas; ++i) {
-            r.list += s.list[i];
-            r.rest += s.rest[i];
+        BeamPart r{top, ref, 0, 0};
+        for (int i = 0; i < BM_WARPS; ++i) {
+            r.list += s.red[0][i];
+            r.rest += s.red[1][i];
         }
-        p.rows[row] = r;
+        p.rows[blockIdx.x] = r;
     }
 }
 
@@ -324,87 +410,149 @@ DEV unsigned long long ordered64(double x) {
     return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
 }
 
-// One CTA per prompt: the beams' lists into one, by their totals.
-__global__ void __launch_bounds__(BM_THREADS) beam_merge_kernel(const BeamParams p) {
-    double *s_log = reinterpret_cast<double *>(mk_smem);  // [64]: of the sum of exp(z - top)
-    int *s_len = reinterpret_cast<int *>(s_log + BM_MAXBEAMS);  // [64]
-    const int tid = threadIdx.x, W = p.beams, K = p.num;
-    unsigned long long *total = reinterpret_cast<unsigned long long *>(s_len + BM_MAXBEAMS);  // [W][K]
-    int *token = reinterpret_cast<int *>(total + W * K), *ranks = token + W * K;
+DEV double unordered64(unsigned long long t) {
+    return __longlong_as_double(t >> 63 ? t & 0x7fffffffffffffffull : ~t);
+}
+
+// ln(sum 2^-44) for a sum of 1 and more of them: fp32's logarithm of the
+// fraction, corrected by how far its exponential is from it, so that no FP64
+// function is called (one warp's takes microseconds on this GPU).
+DEV double log_sum(unsigned long long sum, const uint32_t *table) {
+    const int lead = 63 - __clzll(sum);
+    const unsigned long long m = lead > 44 ? sum >> (lead - 44) : sum << (44 - lead);  // [1, 2) in 2^-44
+    const float y = logf((float)m * 0x1p-44f);
+    const Weigher weigh{0.f, 1.44269502162933349609375f, 1.92596303350011e-08f, table};
+    const unsigned long long w = y > 0.f ? weigh(-y) : 1ull << 44;  // exp(-y)
+    const unsigned long long prod = __umul64hi(m << 10, w << 10);   // 2^44 m exp(-y): 2^(54 + 54 - 64)
+    const float r = (float)((long long)prod - (1ll << 44)) * 0x1p-44f;
+    return ((double)(lead - 44) * 0.6931471805599453 + (double)y) + (double)r;
+}
+
+// One CTA per prompt: of all parts' candidates those with the largest totals.
+__global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const BeamParams p) {
+    const int tid = threadIdx.x, lane = tid % 32, W = p.beams, K = p.num, S = p.parts, per = S * K, all = W * per;
+    double *s_add = reinterpret_cast<double *>(mk_smem);            // [64]: a beam's score less its log sum of exp(z - top)
+    float *s_top = reinterpret_cast<float *>(s_add + BM_MAXBEAMS);  // [64]
+    int *s_state = reinterpret_cast<int *>(s_top + BM_MAXBEAMS);    // [64]: 2 extended, 1 finished, 0 neither
+    uint32_t *s_table = reinterpret_cast<uint32_t *>(s_state + BM_MAXBEAMS);  // [32]
+    uint32_t *s_red = s_table + 32;                                 // [32]
+    unsigned long long *total = reinterpret_cast<unsigned long long *>(s_red + 32);  // [all]: ordered
+    int *list = reinterpret_cast<int *>(total + all);               // [all]: those that reach the bound
+    int &s_count = list[all];
     const int64_t row0 = (int64_t)blockIdx.x * W;
-    for (int i = tid; i < W * K; i += BM_THREADS) ranks[i] = 0;
-    if (tid < W) s_len[tid] = 0;
+    if (tid == 0) s_count = 0;
+    if (tid < 32) s_table[tid] = c_table[tid];
+    if (tid < W) s_state[tid] = beam_live(p, row0 + tid) ? 2 : fabsf(p.scores[row0 + tid]) < INFINITY ? 1 : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tid < W && beam_live(p, row0 + tid)) {
-        const BeamRow r = p.rows[row0 + tid];
-        double sum = (double)r.list;
-        if (r.rest) sum += (double)r.rest * exp2((double)r.ref - (double)r.top * 1.4426950408889634);
-        s_log[tid] = log(sum * 0x1p-44);
-    }
     __syncthreads();
-    for (int i = tid; i < W * K; i += BM_THREADS) {
-        const int w = i / K, j = i % K;
+    const unsigned long long none = ordered64(-INFINITY);
+    const auto key_of = [&](int i) {
+        const int w = i / per;
+        return s_state[w] == 2 ? p.keys[(row0 + w) * per + (i - w * per)]
+             : s_state[w] == 1 && i == w * per ? (unsigned long long)(unsigned)p.end : KEY_NONE;  // finished: goes on as it is
+    };
+    const unsigned long long ahead = tid < all ? key_of(tid) : KEY_NONE;  // while the sums are formed
+    // a warp per beam: its largest logit and the sum (integers: in any order)
+    for (int w = tid / 32; w < W; w += BM_MERGE_THREADS / 32) {
         const float score = p.scores[row0 + w];
-        double t = -INFINITY;
-        int v = -1;
-        if (beam_live(p, row0 + w)) {
-            const unsigned long long key = p.keys[(row0 + w) * K + j];
-            if (key != KEY_NONE) {
-                const float z = key_value(key), top = p.rows[row0 + w].top;
-                t = (double)score + ((z == top ? 0.0 : (double)z - (double)top) - s_log[w]);
-                v = (int)(uint32_t)key;
-            }
-        } else if (j == 0 && fabsf(score) < INFINITY) {  // finished: goes on as it is
-            t = score;
-            v = p.end;
+        if (s_state[w] != 2) {
+            if (lane == 0) s_add[w] = score;
+            continue;
         }
-        total[i] = ordered64(t);
-        token[i] = v;
-        if (t > -INFINITY) atomicAdd(&s_len[w], 1);  // they come first
+        const BeamPart *r = p.rows + (row0 + w) * S;
+        float top = -INFINITY;
+        for (int i = lane; i < S; i += 32) top = fmaxf(top, r[i].top);
+        top = warp_max(top);
+        const Weigher weigh{top, 1.44269502162933349609375f, 1.92596303350011e-08f, s_table};
+        const float oh = fminf(top * weigh.ch, 0x1p20f), ol = oh < 0x1p20f ? fmaf(top, weigh.ch, -oh) + top * weigh.cl : 0.f;
+        const long long octaves = __float2ll_rn(oh * 0x1p32f) + __float2ll_rn(ol * 0x1p32f);  // top log2(e)
+        unsigned long long sum = 0;
+        for (int i = lane; i < S && top > -INFINITY; i += 32) {
+            const BeamPart x = r[i];
+            const unsigned long long a = x.top > -INFINITY ? weigh(x.top) : 0;
+            sum += __umul64hi(x.list, a) << 20 | x.list * a >> 44;
+            if (x.rest) {  // 2^(ref - top log2(e)): the exponent is below 2
+                const unsigned long long b = octave_weight(max(0ll, octaves - ((long long)x.ref - 2) * (1ll << 32)), s_table);
+                sum += __umul64hi(x.rest, b) << 22 | x.rest * b >> 42;
+            }
+        }
+        sum = warp_sum64(sum);
+        if (lane == 0) {
+            s_add[w] = sum ? (double)score - log_sum(sum, s_table) : 0.0;
+            s_top[w] = top;
+        }
     }
     __syncthreads();
-    // Of equal totals the lower beam comes first; a beam's own have their order.
-    merge_ranks(W, K, [&](int l) { return s_len[l]; }, [&](int l, int i, int m, int j) {
-        const unsigned long long x = total[l * K + i], y = total[m * K + j];
-        return x > y || (x == y && l < m);
-    }, ranks);
+    uint32_t most = 0;  // the thread's largest total, to fp32, ordered
+    for (int i = tid; i < all; i += BM_MERGE_THREADS) {
+        const int w = i / per;
+        const unsigned long long k = i == tid ? ahead : key_of(i);
+        unsigned long long t = none;
+        if (k != KEY_NONE) {
+            const float z = key_value(k), top = s_top[w];
+            const double d = s_state[w] == 1 || z == top ? 0.0 : (double)z - (double)top;
+            const double sum = d + s_add[w];
+            t = ordered64(sum);
+            if (t > none) most = max(most, ordered_bits((float)sum));
+        }
+        total[i] = t;
+    }
+    // a bound that num threads' largest reach: what reaches it is listed
+    uint32_t lo = 1;
+    if (__syncthreads_count(most > 0) > K + K / 2 + 4) bisect<BM_MERGE_THREADS / 32>(most, lo, K, K + K / 2 + 4, s_red);
+    if (most >= lo)
+        for (int i = tid; i < all; i += BM_MERGE_THREADS)
+            if (total[i] > none && ordered_bits((float)unordered64(total[i])) >= lo) list[atomicAdd(&s_count, 1)] = i;
     __syncthreads();
-    int all = 0;
-    for (int w = 0; w < W; ++w) all += s_len[w];
-    for (int i = tid; i < W * K; i += BM_THREADS) {
-        const int w = i / K;
-        if (i % K >= s_len[w] || ranks[i] >= K) continue;
-        const int64_t to = (int64_t)blockIdx.x * K + ranks[i];
-        const unsigned long long o = total[i];
-        p.out[to] = (float)__longlong_as_double(o >> 63 ? o & 0x7fffffffffffffffull : ~o);
+    const int n = s_count;
+    // Of equal totals the lower beam comes first, and within a beam the key.
+    for (int x = tid; x < n; x += BM_MERGE_THREADS) {
+        const int i = list[x], w = i / per;
+        const unsigned long long t = total[i], k = key_of(i);
+        int rank = 0;
+        for (int y = 0; y < n; ++y) {
+            const int j = list[y];
+            const unsigned long long u = total[j];
+            rank += u > t;
+            if (u == t && i != j) rank += j / per < w || (j / per == w && key_of(j) < k);
+        }
+        if (rank >= K) continue;
+        const int64_t to = (int64_t)blockIdx.x * K + rank;
+        p.out[to] = (float)unordered64(t);
         p.parents[to] = w;
-        p.tokens[to] = token[i];
+        p.tokens[to] = (int)(uint32_t)k;
     }
-    for (int i = all + tid; i < K; i += BM_THREADS) {
+    for (int i = n + tid; i < K; i += BM_MERGE_THREADS) {
         const int64_t to = (int64_t)blockIdx.x * K + i;
         p.out[to] = -INFINITY;
         p.parents[to] = p.tokens[to] = -1;
     }
 }
 
-using BeamFn = void (*)(const BeamParams);
-static constexpr int BM_PER[] = {8, 16, 24, 32, 48, BM_MAXPER};
-template <bool BF16>
-static BeamFn beam_kernel(int i) {
-    return i == 0 ? beam_row_kernel<8, BF16> : i == 1 ? beam_row_kernel<16, BF16> : i == 2 ? beam_row_kernel<24, BF16>
-         : i == 3 ? beam_row_kernel<32, BF16> : i == 4 ? beam_row_kernel<48, BF16> : beam_row_kernel<BM_MAXPER, BF16>;
+// Parts of a row.  As many CTAs as the GPU holds at once (3 an SM; 128 rows of
+// 151,936 fp32 logits: 33.9 us, with twice as many 40.1, three times 44.2), no
+// shorter parts than a piece, and no more candidates than the second launch
+// holds.
+static void beam_parts(const mk_beam_desc *d, int &parts, int &chunk) {
+    const int64_t rows = std::max<int64_t>(1, (int64_t)d->batch * d->beams);
+    int64_t n = std::max<int64_t>(1, 3 * 152 / rows);
+    n = std::min<int64_t>(n, (d->vocab + BM_PIECE - 1) / BM_PIECE);
+    n = std::min<int64_t>(n, BM_CANDIDATES / (d->beams * d->num));
+    chunk = (int)(((d->vocab + n - 1) / n + 7) / 8 * 8);
+    parts = (d->vocab + chunk - 1) / chunk;
 }
 
-static int beam_sizes(const mk_beam_desc *d) {
+static int beam_sizes(const mk_beam_desc *d, int &parts, int &chunk) {
     if (!d) return set_error(MK_ERR_INVALID, "null descriptor");
     if (d->batch < 0 || d->beams <= 0 || d->num <= 0 || d->vocab <= 0)
         return set_error(MK_ERR_INVALID, "batch negative, or beams, num or vocab not positive");
     if (d->beams > BM_MAXBEAMS || d->num > BM_MAXNUM) return set_error(MK_ERR_UNSUPPORTED, "more than 64 beams or 128 continuations");
     if (d->vocab > BM_MAXVOCAB) return set_error(MK_ERR_UNSUPPORTED, "vocab above 622592");
-    if ((int64_t)d->batch * d->beams > INT32_MAX / BM_MAXCTAS) return set_error(MK_ERR_UNSUPPORTED, "too many rows");
+    beam_parts(d, parts, chunk);
+    if ((int64_t)d->batch * d->beams * parts > INT32_MAX) return set_error(MK_ERR_UNSUPPORTED, "too many rows");
     return MK_OK;
 }
-static uint64_t beam_row_bytes(const mk_beam_desc *d) { return (uint64_t)d->batch * d->beams * sizeof(BeamRow); }
+static uint64_t beam_part_bytes(const mk_beam_desc *d, int parts) { return (uint64_t)d->batch * d->beams * parts * sizeof(BeamPart); }
 
 }  // namespace mk
 
@@ -414,8 +562,9 @@ extern "C" {
 
 int mk_beam_select_workspace(const mk_beam_desc *d, uint64_t *bytes) {
     if (!bytes) return set_error(MK_ERR_INVALID, "bytes is null");
-    if (int rc = beam_sizes(d)) return rc;
-    *bytes = beam_row_bytes(d) + (uint64_t)d->batch * d->beams * d->num * 8;
+    int parts, chunk;
+    if (int rc = beam_sizes(d, parts, chunk)) return rc;
+    *bytes = beam_part_bytes(d, parts) + (uint64_t)d->batch * d->beams * parts * d->num * 8;
     return MK_OK;
 }
 
@@ -440,43 +589,33 @@ int mk_beam_select(const mk_beam_desc *d, void *workspace, uint64_t workspace_by
     p.scores = reinterpret_cast<const float *>(d->scores);
     p.finished = reinterpret_cast<const uint8_t *>(d->finished);
     p.end = d->end;
-    p.rows = static_cast<BeamRow *>(workspace);
-    p.keys = reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(workspace) + beam_row_bytes(d));
+    beam_parts(d, p.parts, p.chunk);
+    p.rows = static_cast<BeamPart *>(workspace);
+    p.keys = reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(workspace) + beam_part_bytes(d, p.parts));
     p.out = reinterpret_cast<float *>(d->out_scores);
     p.parents = reinterpret_cast<int *>(d->parents);
     p.tokens = reinterpret_cast<int *>(d->tokens);
-    p.ctas = rows <= 64 ? 16 : 8;
-    while (p.ctas > 1 && d->vocab < p.ctas * 1024) p.ctas /= 2;
-    const int vec = d->bf16 ? 8 : 4;
-    const auto chunk_of = [&](int ctas) { return ((d->vocab + ctas - 1) / ctas + vec - 1) / vec * vec; };
-    while (p.ctas < BM_MAXCTAS && chunk_of(p.ctas) + vec > BM_MAXPER * BM_THREADS) p.ctas *= 2;
-    p.chunk = chunk_of(p.ctas);
-    int per = 0;
-    while (p.chunk + vec > BM_PER[per] * BM_THREADS) ++per;
-    // the list holds all logits of as many threads as may reach the bound
-    p.cap = std::max(64, 2 * p.num) * BM_PER[per];
+    // a piece lists all logits of as many threads as may reach its bound; the list takes two such pieces and more
+    p.limit = std::min(BM_THREADS, std::max(64, 2 * d->num));
+    p.cap = p.limit * BM_PER * 3;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    BeamFn f = d->bf16 ? beam_kernel<true>(per) : beam_kernel<false>(per);
+    void (*f)(const BeamParams) = d->bf16 ? beam_part_kernel<true> : beam_part_kernel<false>;
     static std::atomic<uint32_t> ready[SERVE_MAX_DEVICES];
-    if (int rc = serve_prepare(reinterpret_cast<const void *>(f), ready, 2 * per + (d->bf16 ? 1 : 0), true)) return rc;
-    if (int rc = serve_prepare(reinterpret_cast<const void *>(beam_merge_kernel), ready, 31, false)) return rc;
+    if (int rc = serve_prepare(reinterpret_cast<const void *>(f), ready, d->bf16 ? 1 : 0, false)) return rc;
+    if (int rc = serve_prepare(reinterpret_cast<const void *>(beam_merge_kernel), ready, 2, false)) return rc;
+    f<<<(unsigned)(rows * p.parts), BM_THREADS, sizeof(BeamShared) + p.cap * 12, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return serve_cuda_fail(e, "beam selection launch");
     cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = p.ctas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(rows * p.ctas));
-    cfg.blockDim = dim3(BM_THREADS);
-    cfg.dynamicSmemBytes = sizeof(BeamShared) + p.cap * 8 + p.ctas * p.num * 8 + std::max(p.cap, p.ctas * p.num) * 4;
+    cfg.gridDim = dim3((unsigned)d->batch);
+    cfg.blockDim = dim3(BM_MERGE_THREADS);
+    cfg.dynamicSmemBytes = BM_MAXBEAMS * 16 + 64 * 4 + p.beams * p.parts * p.num * 12 + 4;
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, f, (const BeamParams)p);
-    if (e != cudaSuccess) return serve_cuda_fail(e, "beam selection launch");
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)d->batch);
-    cfg.dynamicSmemBytes = BM_MAXBEAMS * 12 + p.beams * p.num * 16;
     e = cudaLaunchKernelEx(&cfg, beam_merge_kernel, (const BeamParams)p);
     return e == cudaSuccess ? MK_OK : serve_cuda_fail(e, "beam merge launch");
 }

@@ -23,6 +23,19 @@ static __constant__ uint32_t c_table[32] = {
     1518500250u, 1485961921u, 1454120821u, 1422962010u, 1392470869u, 1362633090u, 1333434672u, 1304861917u,
     1276901417u, 1249540052u, 1222764986u, 1196563654u, 1170923762u, 1145833280u, 1121280436u, 1097253708u};
 
+// 2^44 2^-d for d >= 0 in 32.32 fixed point, below 2^31.
+DEV unsigned long long octave_weight(long long d, const uint32_t *table) {
+    const uint32_t f = (uint32_t)d;
+    // 2^-f = table x exp(-a), a = (f mod 1/32) ln 2 < 0.0217: terms to a^4 / 24 leave 4e-11
+    const uint32_t a = __umulhi(f & 0x07ffffffu, 2977044472u);  // ln 2 in 0.32
+    uint32_t q = 715827883u - __umulhi(a, 178956971u);         // 1/6 - a/24
+    q = 0x80000000u - __umulhi(a, q);                          // 1/2 - a q
+    q = 0xffffffffu - __umulhi(a, q);                          // 1 - a q
+    const uint32_t e = 0x80000000u - (__umulhi(a, q) >> 1);    // 1 - a q, in 1.31
+    const unsigned long long prod = (unsigned long long)table[f >> 27] * e;  // 2.62
+    return prod >> min(18 + (int)(d >> 32), 63);
+}
+
 // 2^44 2^-d in 64-bit fixed point, accurate to 2^-30 of itself or to 2^-44.
 struct Weigher {
     float top, ch, cl;  // the row's maximum; log2(e) / temperature as a pair of fp32
@@ -39,15 +52,7 @@ struct Weigher {
         // d in 32.32 fixed point; t - n is exact, te below 2^-17
         const long long d = max(0ll, ((long long)n << 32) + (long long)__float2uint_rz((t - (float)n) * 4294967296.f) +
                                          (long long)__float2int_rn(te * 4294967296.f));
-        const uint32_t f = (uint32_t)d;
-        // 2^-f = table x exp(-a), a = (f mod 1/32) ln 2 < 0.0217: terms to a^4 / 24 leave 4e-11
-        const uint32_t a = __umulhi(f & 0x07ffffffu, 2977044472u);  // ln 2 in 0.32
-        uint32_t q = 715827883u - __umulhi(a, 178956971u);         // 1/6 - a/24
-        q = 0x80000000u - __umulhi(a, q);                          // 1/2 - a q
-        q = 0xffffffffu - __umulhi(a, q);                          // 1 - a q
-        const uint32_t e = 0x80000000u - (__umulhi(a, q) >> 1);    // 1 - a q, in 1.31
-        const unsigned long long prod = (unsigned long long)table[f >> 27] * e;  // 2.62
-        const unsigned long long r = prod >> min(18 + (int)(d >> 32), 63);
+        const unsigned long long r = octave_weight(d, table);
         return x == top ? 1ull << 44 : r;  // (the largest may be infinite)
     }
 };

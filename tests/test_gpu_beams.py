@@ -108,6 +108,19 @@ def test_select_all_large_values_in_one_threads_places():
         check_select(z, scores_of(1, 2, seed=8), 64)
 
 
+@pytest.mark.parametrize("num", [4, 128])
+def test_select_rising_logits_and_few_places(num):
+    """Each piece of a row above the one before; all large logits in a few threads' places, piece after piece."""
+    v = 70001
+    z = logits_of(4, v, seed=21, spread=0.3)
+    z[0] += torch.arange(v) * 1e-3
+    z[1] -= torch.arange(v) * 1e-3
+    z[2] += torch.floor(torch.arange(v) / 4096) * 3
+    z[3] += 30 * ((torch.arange(v) // 4 % 256) < 9)
+    check_select(z, scores_of(1, 4, seed=1), num)
+    check_select(z.to(torch.bfloat16), scores_of(2, 2, seed=2), num)
+
+
 def test_select_values_that_are_not_finite():
     z = logits_of(8, 1111, seed=9)
     z[0, ::3] = math.nan
