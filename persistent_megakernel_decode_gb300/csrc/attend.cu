@@ -47,79 +47,13 @@
 // instructions per product that a 16-row operand held in registers costs; a
 // prompt of 2048 new tokens: 377 us, 91 TFLOP/s, half of its tiles' pages
 // passing through the ring unseen.
-#include <algorithm>
-#include <climits>
-
-#include "dev_serve.cuh"
+#include "dev_attend.cuh"
 
 namespace mk {
 
 constexpr int ATT_WARPS = 8;                        // consumer warps
 constexpr int ATT_THREADS = (ATT_WARPS + 1) * 32;   // + the producer
-constexpr int ATT_MAXB = 1024;                      // sequences per call
 constexpr int ATT_MAXRING = 32;                     // pages in the ring (one producer lane each)
-
-struct AttParams {
-    CacheView c;  // of the layer: k, v, ks, vs point at it
-    const uint16_t *q;
-    uint16_t *out;
-    float *lse;
-    int64_t qs_t, qs_h, os_t, os_h;
-    const int *table, *lens, *q_start;
-    int batch, width, group, tokens, max_tokens, window, sinks, sink_pages, ring, ctas;
-    float scale_log2;
-    // workspace: partial (m, l) [ctas][2][RT][2]; partial O [ctas][2][RT][D]
-    float *part_ml, *part_o;
-    // shared prefixes: groups of consecutive sequences; what a row's own tokens
-    // and its group's give, where one CTA had all of it: (m, l) [2][tokens][q
-    // heads][2], O [2][tokens][q heads][D]
-    const int *groups, *shared;
-    int ngroups;
-    float *row_ml, *row_o;
-};
-
-// ln of the sum of exponentials: maximum in log2 units, sum times 2^14.
-DEV float att_lse(float big, float sum) {
-    return sum == 0.f ? -INFINITY : (big - 14.f + log2f(sum)) * 0.6931471805599453f;
-}
-// 1 / the sum of exponentials, from their sum times 2^14.
-DEV float att_inverse(float sum) { return sum == 0.f ? 0.f : 16384.f / sum; }
-
-// The first position that a query at pos sees (pos < 0: sees none, any window's end fits 32 bits).
-DEV int att_least(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
-
-// What a sequence asks for: its query rows, and the pages that any row sees:
-// [0, hi) without the `gap` pages behind those of the sinks.
-struct AttSeq {
-    int q0, cnt, len, gap, hi;
-    bool bad;  // its rows are not known
-};
-// The page of a sequence's i-th seen one.
-DEV int att_page(const AttParams &p, int i, int gap) { return i < p.sink_pages ? i : i + gap; }
-
-template <int P>
-DEV AttSeq att_seq(const AttParams &p, int b, bool report) {
-    AttSeq s;
-    s.bad = false;
-    s.len = p.lens[b];
-    s.q0 = p.q_start ? p.q_start[b] : b * p.max_tokens;
-    s.cnt = (p.q_start ? p.q_start[b + 1] : s.q0 + p.max_tokens) - s.q0;
-    if (s.q0 < 0 || s.cnt < 0 || s.q0 > p.tokens || s.cnt > p.tokens - s.q0) {  // its rows are not known: none
-        if (report) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, b, s.q0, -1);
-        s.q0 = s.cnt = s.len = s.gap = s.hi = 0;
-        s.bad = true;
-        return s;
-    }
-    if (s.len < 0 || (int64_t)s.len > (int64_t)p.width * P) {
-        if (report) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, b, s.len, -1);
-        s.len = 0;
-    }
-    s.hi = (s.len + P - 1) / P;
-    const int64_t first = (int64_t)s.len - s.cnt - p.window + 1;
-    const int lo = p.window > 0 && first > 0 ? min((int)(first / P), s.hi) : 0;
-    s.gap = max(0, lo - p.sink_pages);
-    return s;
-}
 
 // Tiles of rt rows: 8 NT rows a warp, up to rt / (8 NT) warps side by side
 __host__ __device__ constexpr int att_nt(int rt) { return rt == 8 ? 1 : 2; }
@@ -146,32 +80,11 @@ DEV long long att_items(const AttParams &p, int cnt, int np) {
     return p.c.hkv * ((tiles - 1) * ((long long)np * att_side<RT>(RT) + FIXED) +
                       (long long)np * att_side<RT>(rows - (tiles - 1) * RT) + FIXED);
 }
-// prefix[1 .. n]: values -> running sums, by the whole block; prefix[0] = 0.
-DEV void att_running(long long *prefix, int n) {
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        long long carry = 0;
-        if (lane == 0) prefix[0] = 0;
-        for (int b0 = 0; b0 < n; b0 += 32) {
-            const int b = b0 + lane;
-            long long v = b < n ? prefix[b + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(FULL, v, o);
-                if (lane >= o) v += u;
-            }
-            v += carry;
-            if (b < n) prefix[b + 1] = v;
-            carry = __shfl_sync(FULL, v, 31);
-        }
-    }
-    __syncthreads();
-}
-
-// A quotient that mostly fits 32 bits.
-DEV long long att_div(long long a, long long b) {
-    return (a | b) <= 0xffffffffll ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+// Of a unit of the main launch: with shared prefixes the groups' may be another's.
+template <int RT, bool SH>
+DEV long long att_unit_items(const AttParams &p, int v, const AttSeq &q) {
+    if (SH && p.pre_ctas && v < p.ngroups) return 0;
+    return att_items<RT>(p, q.cnt, q.hi - q.gap);
 }
 
 // CTAs that get work: every range is at least one page's items long, so that
@@ -180,83 +93,6 @@ template <int RT>
 DEV int att_used(long long total, int ctas) {
     return (int)max(1ll, min((long long)ctas, total / (RT / (8 * att_nt(RT)))));
 }
-// CTA of work item x when `total` items are cut into `ctas` <= total ranges [c total / ctas, (c + 1) total / ctas).
-DEV int att_owner(long long x, long long total, int ctas) { return (int)att_div((x + 1) * ctas - 1, total); }
-
-// Shared prefixes.  lim[g]: the pages that all rows of group g see and take
-// together; lead[g]: the sequence whose table row names them.
-struct AttGroups {
-    int *lead, *lim, *grp;  // [ngroups], [ngroups], [ngroups + 1]: the groups' first sequences
-};
-__host__ __device__ constexpr int att_group_bytes(int n) { return n ? (3 * n + 1) * 4 : 0; }
-DEV AttGroups att_groups_at(void *at, int n) {
-    int *x = static_cast<int *>(at);
-    return {x, x + n, x + 2 * n};
-}
-// The group of a sequence, or -1.
-DEV int att_group_of(const AttParams &p, const AttGroups &s, int b) {
-    int a = 0, z = p.ngroups;  // the last group that begins at or before b
-    while (z - a > 1) {
-        const int mid = (a + z) / 2;
-        if (s.grp[mid] <= b) a = mid;
-        else z = mid;
-    }
-    return b >= s.grp[a] && b < s.grp[a + 1] ? a : -1;
-}
-// By the whole block.  What `shared` says is a bound: only full pages, and of
-// them those that every query of the group sees whole.
-template <int P>
-DEV void att_groups(const AttParams &p, const AttGroups &s, bool report) {
-    const int n = p.ngroups, tid = threadIdx.x, threads = blockDim.x;
-    bool bad = false;
-    for (int g = tid; g <= n; g += threads) {
-        const int x = p.groups[g];
-        s.grp[g] = x;
-        bad |= x < 0 || x > p.batch || (g < n && p.groups[g + 1] < x);
-    }
-    bad = __syncthreads_or(bad);
-    if (bad && report && tid == 0) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, -1, -1, -1);
-    for (int g = tid; g < n; g += threads) {
-        const int x = p.shared[g];
-        if (x < 0 && report) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, s.grp[g], x, -1);
-        s.lead[g] = INT_MAX;
-        s.lim[g] = bad || s.grp[g + 1] - s.grp[g] < 2 ? 0 : max(x, 0) / P;
-    }
-    __syncthreads();
-    for (int b = tid; b < p.batch && !bad; b += threads) {
-        const int g = att_group_of(p, s, b);
-        if (g < 0) continue;
-        const AttSeq q = att_seq<P>(p, b, false);
-        if (q.bad) atomicMin(&s.lim[g], 0);  // where its rows begin is not known either
-        if (q.cnt == 0) continue;
-        atomicMin(&s.lead[g], b);
-        atomicMin(&s.lim[g], max(0, q.len - q.cnt + 1) / P);
-    }
-    __syncthreads();
-}
-DEV int att_units(const AttParams &p, bool sh) { return sh ? p.ngroups + p.batch : p.batch; }
-// Unit v: a sequence, or with shared prefixes a group's rows over its pages
-// (every row sees all of them), or a sequence's rows over the pages behind.
-template <int P, bool SH>
-DEV AttSeq att_unit(const AttParams &p, const AttGroups &s, int v, bool report) {
-    if constexpr (!SH) return att_seq<P>(p, v, report);
-    if (v >= p.ngroups) {
-        const int b = v - p.ngroups;
-        AttSeq q = att_seq<P>(p, b, report);
-        const int g = att_group_of(p, s, b);
-        q.gap = g < 0 ? 0 : min(s.lim[g], q.hi);
-        return q;
-    }
-    AttSeq q{0, 0, 0, 0, 0, false};
-    if (s.lim[v] > 0 && s.lead[v] < p.batch) {
-        q.q0 = p.q_start ? p.q_start[s.grp[v]] : s.grp[v] * p.max_tokens;
-        q.cnt = (p.q_start ? p.q_start[s.grp[v + 1]] : s.grp[v + 1] * p.max_tokens) - q.q0;
-        q.hi = s.lim[v];
-        q.len = q.hi * P;
-    }
-    return q;
-}
-
 struct AttShared {
     // A unit is what a sequence's own pages are (shared prefixes: the groups' first, then the sequences')
     long long *prefix;  // [units + 1]: work items before each
@@ -307,16 +143,6 @@ DEV AttShared att_shared(const AttParams &p) {
     return s;
 }
 
-// Work item x belongs to the last sequence b with prefix[b] <= x that has any.
-DEV int att_find(const long long *prefix, int batch, long long x) {
-    int a = 0, z = batch;
-    while (z - a > 1) {
-        const int mid = (a + z) / 2;
-        if (prefix[mid] <= x) a = mid;
-        else z = mid;
-    }
-    return a;
-}
 // The pages of a sequence that the rows of one of its tiles see: [lo, hi), and below hi those of the sinks.
 template <int P, int RT>
 DEV void att_tile_pages(const AttParams &p, int cnt, int len, int tile, int &lo, int &hi) {
@@ -529,16 +355,6 @@ DEV uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-DEV float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-DEV uint32_t half2_of(float lo, float hi) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
-    return h;
 }
 // Bytes of w that are e4m3's NaN codes (0x7f, 0xff), as a byte mask.
 DEV uint32_t nan_bytes(uint32_t w) {
@@ -920,7 +736,7 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) cache_attend_kernel(const AttP
     if constexpr (SH) att_groups<P>(p, s.groups, blockIdx.x == 0);
     for (int b = tid; b < units; b += ATT_THREADS) {
         const AttSeq q = att_unit<P, SH>(p, s.groups, b, blockIdx.x == 0);
-        s.prefix[b + 1] = att_items<RT>(p, q.cnt, q.hi - q.gap);
+        s.prefix[b + 1] = att_unit_items<RT, SH>(p, b, q);
         s.seq[b] = make_int4(q.q0, q.cnt, q.len, q.gap);
     }
     if (tid >= ATT_THREADS - 32 && tid - (ATT_THREADS - 32) < p.ring) {
@@ -936,6 +752,8 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) cache_attend_kernel(const AttP
     att_running(s.prefix, units);
     if (tid >= ATT_WARPS * 32) att_produce<D, P, RT, SH>(p, s);
     else att_consume<D, P, RT, SH>(p, s);
+    // the launch of the shared pages, beside which this one ran, is done before this one is
+    if constexpr (SH) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // One warp per query row: rows that see nothing get zeros, rows whose pages
@@ -952,9 +770,18 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
     if constexpr (SH) att_groups<P>(p, groups, false);
     for (int b = tid; b < units; b += 256) {
         const AttSeq q = att_unit<P, SH>(p, groups, b, false);
-        prefix[b + 1] = att_items<RT>(p, q.cnt, q.hi - q.gap);
+        prefix[b + 1] = att_unit_items<RT, SH>(p, b, q);
     }
     att_running(prefix, units);
+    // items of the shared pages' launch
+    long long *before = reinterpret_cast<long long *>(mk_smem + (units + 1) * 8 + (att_group_bytes(p.ngroups) + 7) / 8 * 8);
+    if (SH && p.pre_ctas) {
+        for (int g = tid; g < p.ngroups; g += 256) {
+            const AttSeq q = att_unit<P, SH>(p, groups, g, false);
+            before[g + 1] = pre_items(p, q.cnt, q.hi);
+        }
+        att_running(before, p.ngroups);
+    }
     const int64_t w = (int64_t)blockIdx.x * 8 + tid / 32;
     const int token = (int)min(w / heads, (int64_t)p.tokens - 1), head = (int)(w % heads);
     int b = 0;
@@ -1001,7 +828,18 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
         own = part_of(SH ? p.ngroups + b : b, s);
         if constexpr (SH) {
             const int g = att_group_of(p, groups, b);
-            if (g >= 0) pre = part_of(g, att_unit<P, SH>(p, groups, g, false));
+            if (g >= 0) {
+                const AttSeq u = att_unit<P, SH>(p, groups, g, false);
+                if (!p.pre_ctas) {
+                    pre = part_of(g, u);
+                } else if (u.cnt > 0 && u.hi > 0) {
+                    const int r = (token - u.q0) * p.group + head % p.group;
+                    const long long all = before[p.ngroups];
+                    const long long x0 = before[g] + ((long long)(r / PRE_ROWS) * p.c.hkv + head / p.group) * (u.hi + PRE_FIXED) + PRE_FIXED;
+                    const int n = pre_used(all, p.pre_ctas), c0 = att_owner(x0, all, n), c1 = att_owner(x0 + u.hi - 1, all, n);
+                    pre = c0 == c1 ? Part{u.hi, 0, -1, 0} : Part{u.hi, c0, c1, r % PRE_ROWS};
+                }
+            }
         } else {
             todo = own.n == 0 || own.c0 <= own.c1;
         }
@@ -1026,10 +864,13 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] = fmaf(o[i], e, acc[i] * a);
         }
-        const auto slot = [&](int c) { return ((size_t)c * 2 + (c == x.c0 ? 1 : 0)) * RT + x.row; };  // c0 has the unit's head
+        const bool pages = SH && which && p.pre_ctas;  // of the shared pages' launch
+        const int rt = pages ? PRE_ROWS : RT;
+        const float *part_ml = pages ? p.pre_ml : p.part_ml, *part_o = pages ? p.pre_o : p.part_o;
+        const auto slot = [&](int c) { return ((size_t)c * 2 + (c == x.c0 ? 1 : 0)) * rt + x.row; };  // c0 has the unit's head
         for (int c = x.c0; c <= x.c1; c += 32) {  // the maxima first, 32 CTAs at a time
             const int mine = c + lane;
-            const float2 ml = mine <= x.c1 ? *reinterpret_cast<const float2 *>(p.part_ml + slot(mine) * 2)
+            const float2 ml = mine <= x.c1 ? *reinterpret_cast<const float2 *>(part_ml + slot(mine) * 2)
                                            : make_float2(-INFINITY, 0.f);
             const float top = fmaxf(big, warp_max(ml.x)), mu = top == -INFINITY ? 0.f : top;
             const float a = exp2_fast(big - mu), e = exp2_fast(ml.x - mu);
@@ -1041,7 +882,7 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
 #pragma unroll 4
             for (int j = 0; j < n; ++j) {
                 const float ej = __shfl_sync(FULL, e, j), lj = __shfl_sync(FULL, ml.y, j);
-                const float *o = p.part_o + slot(c + j) * D + lane * V;
+                const float *o = part_o + slot(c + j) * D + lane * V;
                 sum = fmaf(lj, ej, sum);
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] = fmaf(o[i], ej, acc[i]);
@@ -1059,9 +900,15 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
 
 struct AttPlan {
     int rt, ctas;
-    uint64_t ml_bytes, o_bytes, row_ml_bytes, row_o_bytes;
-    uint64_t bytes() const { return ml_bytes + o_bytes + row_ml_bytes + row_o_bytes; }
+    int pre_ctas;
+    uint64_t ml_bytes, o_bytes, row_ml_bytes, row_o_bytes, pre_ml_bytes, pre_o_bytes;
+    uint64_t bytes() const { return ml_bytes + o_bytes + row_ml_bytes + row_o_bytes + pre_ml_bytes + pre_o_bytes; }
 };
+
+// Rows of an average group and kv head from which its shared pages get a launch of their own.
+#ifndef PRE_LEAST
+#define PRE_LEAST 16
+#endif
 
 // ngroups: 0 without shared prefixes
 static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, int ngroups, AttPlan &pl) {
@@ -1085,7 +932,9 @@ static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, int ngroups
     // row tiles of 8, 16, 32 or 64 rows: the least that takes a sequence's (or an average group's) rows of one kv head
     const int group = a->q_heads / c->kv_heads;
     int64_t rows = (int64_t)std::max(1, std::min(a->max_tokens, a->tokens)) * group;
-    if (ngroups) rows = std::max(rows, ((int64_t)a->tokens + ngroups - 1) / ngroups * group);
+    const int64_t group_rows = ngroups ? ((int64_t)a->tokens + ngroups - 1) / ngroups * group : 0;
+    pl.pre_ctas = group_rows >= PRE_LEAST ? sms : 0;
+    if (!pl.pre_ctas) rows = std::max(rows, group_rows);
     pl.rt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     // no more CTAs than pages there can be (all tiles' together, each as many items as it has warps side by side)
     const int64_t side = pl.rt == 64 ? 4 : pl.rt == 32 ? 2 : 1;
@@ -1096,6 +945,8 @@ static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, int ngroups
     const uint64_t row_parts = ngroups ? 2ull * a->tokens * a->q_heads : 0;
     pl.row_ml_bytes = (row_parts * 8 + 255) / 256 * 256;
     pl.row_o_bytes = row_parts * c->head_dim * 4;
+    pl.pre_ml_bytes = (uint64_t)pl.pre_ctas * 2 * PRE_ROWS * 8;
+    pl.pre_o_bytes = (uint64_t)pl.pre_ctas * 2 * PRE_ROWS * c->head_dim * 4;
     return MK_OK;
 }
 
@@ -1169,7 +1020,12 @@ static int att_launch(const mk_cache_desc *cache, int layer, const mk_attend_des
         p.shared = reinterpret_cast<const int *>(share->shared);
         p.ngroups = ngroups;
         p.row_ml = reinterpret_cast<float *>(ws + pl.ml_bytes + pl.o_bytes);
-        p.row_o = reinterpret_cast<float *>(ws + pl.ml_bytes + pl.o_bytes + pl.row_ml_bytes);
+        uint8_t *at = ws + pl.ml_bytes + pl.o_bytes + pl.row_ml_bytes;
+        p.row_o = reinterpret_cast<float *>(at);
+        at += pl.row_o_bytes;
+        p.pre_ctas = pl.pre_ctas;
+        p.pre_ml = reinterpret_cast<float *>(at);
+        p.pre_o = reinterpret_cast<float *>(at + pl.pre_ml_bytes);
     }
     const int fixed = att_fixed_bytes(D, att_nt(pl.rt)) + att_seq_bytes(p.batch, ngroups) + 128;
     p.ring = std::min(ATT_MAXRING, (SERVE_SMEM - fixed) / (2 * P * D));
@@ -1181,19 +1037,25 @@ static int att_launch(const mk_cache_desc *cache, int layer, const mk_attend_des
     const int variant = (ngroups ? 16 : 0) + (D == 128 ? 8 : 0) + (P == 64 ? 4 : 0) + (pl.rt == 8 ? 0 : pl.rt == 16 ? 1 : pl.rt == 32 ? 2 : 3);
     if (int rc = serve_prepare(reinterpret_cast<const void *>(f), ready, variant, false)) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    f<<<pl.ctas, ATT_THREADS, smem, st>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return serve_cuda_fail(e, "attention launch");
     cudaLaunchAttribute dep{};
     dep.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     dep.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(((int64_t)p.tokens * a->q_heads + 7) / 8));
-    cfg.blockDim = dim3(256);
     cfg.stream = st;
     cfg.attrs = &dep;
+    if (p.pre_ctas) {
+        if (int rc = prefix_launch(cache, p, st)) return rc;
+        cfg.numAttrs = 1;  // the main launch starts where the first one leaves SMs
+    }
+    cfg.gridDim = dim3((unsigned)pl.ctas);
+    cfg.blockDim = dim3(ATT_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, f, (const AttParams)p);
+    if (e != cudaSuccess) return serve_cuda_fail(e, "attention launch");
+    cfg.gridDim = dim3((unsigned)(((int64_t)p.tokens * a->q_heads + 7) / 8));
+    cfg.blockDim = dim3(256);
     cfg.numAttrs = 1;
-    cfg.dynamicSmemBytes = (size_t)(ngroups + p.batch + 1) * 8 + att_group_bytes(ngroups);
+    cfg.dynamicSmemBytes = (size_t)(ngroups + p.batch + 1) * 8 + (att_group_bytes(ngroups) + 7) / 8 * 8 + (ngroups ? (ngroups + 1) * 8 : 0);
     e = cudaLaunchKernelEx(&cfg, merge, (const AttParams)p);
     return e == cudaSuccess ? MK_OK : serve_cuda_fail(e, "attention merge launch");
 }

@@ -1,0 +1,216 @@
+// Shared by the cache attention's kernels (attend.cu, prefix.cu): parameters,
+// what a sequence or a group of sequences asks for, work items cut into ranges.
+#pragma once
+#include <algorithm>
+#include <climits>
+
+#include "dev_serve.cuh"
+
+namespace mk {
+
+constexpr int ATT_MAXB = 1024;  // sequences per call
+
+struct AttParams {
+    CacheView c;  // of the layer: k, v, ks, vs point at it
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    int64_t qs_t, qs_h, os_t, os_h;
+    const int *table, *lens, *q_start;
+    int batch, width, group, tokens, max_tokens, window, sinks, sink_pages, ring, ctas;
+    float scale_log2;
+    // workspace: partial (m, l) [ctas][2][RT][2]; partial O [ctas][2][RT][D]
+    float *part_ml, *part_o;
+    // shared prefixes: groups of consecutive sequences; what a row's own tokens
+    // and its group's give, where one CTA had all of it: (m, l) [2][tokens][q
+    // heads][2], O [2][tokens][q heads][D]
+    const int *groups, *shared;
+    int ngroups;
+    float *row_ml, *row_o;
+    // the groups' parts by tiles of 128 rows in a launch of their own (0 CTAs:
+    // none): its ring, and what its CTAs cut, like part_ml and part_o
+    int pre_ctas, pre_ring;
+    float *pre_ml, *pre_o;
+};
+
+// ln of the sum of exponentials: maximum in log2 units, sum times 2^14.
+DEV float att_lse(float big, float sum) {
+    return sum == 0.f ? -INFINITY : (big - 14.f + log2f(sum)) * 0.6931471805599453f;
+}
+// 1 / the sum of exponentials, from their sum times 2^14.
+DEV float att_inverse(float sum) { return sum == 0.f ? 0.f : 16384.f / sum; }
+
+// The first position that a query at pos sees (pos < 0: sees none, any window's end fits 32 bits).
+DEV int att_least(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
+
+// What a sequence asks for: its query rows, and the pages that any row sees:
+// [0, hi) without the `gap` pages behind those of the sinks.
+struct AttSeq {
+    int q0, cnt, len, gap, hi;
+    bool bad;  // its rows are not known
+};
+// The page of a sequence's i-th seen one.
+DEV int att_page(const AttParams &p, int i, int gap) { return i < p.sink_pages ? i : i + gap; }
+
+template <int P>
+DEV AttSeq att_seq(const AttParams &p, int b, bool report) {
+    AttSeq s;
+    s.bad = false;
+    s.len = p.lens[b];
+    s.q0 = p.q_start ? p.q_start[b] : b * p.max_tokens;
+    s.cnt = (p.q_start ? p.q_start[b + 1] : s.q0 + p.max_tokens) - s.q0;
+    if (s.q0 < 0 || s.cnt < 0 || s.q0 > p.tokens || s.cnt > p.tokens - s.q0) {  // its rows are not known: none
+        if (report) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, b, s.q0, -1);
+        s.q0 = s.cnt = s.len = s.gap = s.hi = 0;
+        s.bad = true;
+        return s;
+    }
+    if (s.len < 0 || (int64_t)s.len > (int64_t)p.width * P) {
+        if (report) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, b, s.len, -1);
+        s.len = 0;
+    }
+    s.hi = (s.len + P - 1) / P;
+    const int64_t first = (int64_t)s.len - s.cnt - p.window + 1;
+    const int lo = p.window > 0 && first > 0 ? min((int)(first / P), s.hi) : 0;
+    s.gap = max(0, lo - p.sink_pages);
+    return s;
+}
+
+// prefix[1 .. n]: values -> running sums, by the whole block; prefix[0] = 0.
+DEV void att_running(long long *prefix, int n) {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        long long carry = 0;
+        if (lane == 0) prefix[0] = 0;
+        for (int b0 = 0; b0 < n; b0 += 32) {
+            const int b = b0 + lane;
+            long long v = b < n ? prefix[b + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(FULL, v, o);
+                if (lane >= o) v += u;
+            }
+            v += carry;
+            if (b < n) prefix[b + 1] = v;
+            carry = __shfl_sync(FULL, v, 31);
+        }
+    }
+    __syncthreads();
+}
+
+// A quotient that mostly fits 32 bits.
+DEV long long att_div(long long a, long long b) {
+    return (a | b) <= 0xffffffffll ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// CTA of work item x when `total` items are cut into `ctas` <= total ranges [c total / ctas, (c + 1) total / ctas).
+DEV int att_owner(long long x, long long total, int ctas) { return (int)att_div((x + 1) * ctas - 1, total); }
+
+// Shared prefixes.  lim[g]: the pages that all rows of group g see and take
+// together; lead[g]: the sequence whose table row names them.
+struct AttGroups {
+    int *lead, *lim, *grp;  // [ngroups], [ngroups], [ngroups + 1]: the groups' first sequences
+};
+__host__ __device__ constexpr int att_group_bytes(int n) { return n ? (3 * n + 1) * 4 : 0; }
+DEV AttGroups att_groups_at(void *at, int n) {
+    int *x = static_cast<int *>(at);
+    return {x, x + n, x + 2 * n};
+}
+// The group of a sequence, or -1.
+DEV int att_group_of(const AttParams &p, const AttGroups &s, int b) {
+    int a = 0, z = p.ngroups;  // the last group that begins at or before b
+    while (z - a > 1) {
+        const int mid = (a + z) / 2;
+        if (s.grp[mid] <= b) a = mid;
+        else z = mid;
+    }
+    return b >= s.grp[a] && b < s.grp[a + 1] ? a : -1;
+}
+// By the whole block.  What `shared` says is a bound: only full pages, and of
+// them those that every query of the group sees whole.
+template <int P>
+DEV void att_groups(const AttParams &p, const AttGroups &s, bool report) {
+    const int n = p.ngroups, tid = threadIdx.x, threads = blockDim.x;
+    bool bad = false;
+    for (int g = tid; g <= n; g += threads) {
+        const int x = p.groups[g];
+        s.grp[g] = x;
+        bad |= x < 0 || x > p.batch || (g < n && p.groups[g + 1] < x);
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && report && tid == 0) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, -1, -1, -1);
+    for (int g = tid; g < n; g += threads) {
+        const int x = p.shared[g];
+        if (x < 0 && report) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, s.grp[g], x, -1);
+        s.lead[g] = INT_MAX;
+        s.lim[g] = bad || s.grp[g + 1] - s.grp[g] < 2 ? 0 : max(x, 0) / P;
+    }
+    __syncthreads();
+    for (int b = tid; b < p.batch && !bad; b += threads) {
+        const int g = att_group_of(p, s, b);
+        if (g < 0) continue;
+        const AttSeq q = att_seq<P>(p, b, false);
+        if (q.bad) atomicMin(&s.lim[g], 0);  // where its rows begin is not known either
+        if (q.cnt == 0) continue;
+        atomicMin(&s.lead[g], b);
+        atomicMin(&s.lim[g], max(0, q.len - q.cnt + 1) / P);
+    }
+    __syncthreads();
+}
+DEV int att_units(const AttParams &p, bool sh) { return sh ? p.ngroups + p.batch : p.batch; }
+// Unit v: a sequence, or with shared prefixes a group's rows over its pages
+// (every row sees all of them), or a sequence's rows over the pages behind.
+template <int P, bool SH>
+DEV AttSeq att_unit(const AttParams &p, const AttGroups &s, int v, bool report) {
+    if constexpr (!SH) return att_seq<P>(p, v, report);
+    if (v >= p.ngroups) {
+        const int b = v - p.ngroups;
+        AttSeq q = att_seq<P>(p, b, report);
+        const int g = att_group_of(p, s, b);
+        q.gap = g < 0 ? 0 : min(s.lim[g], q.hi);
+        return q;
+    }
+    AttSeq q{0, 0, 0, 0, 0, false};
+    if (s.lim[v] > 0 && s.lead[v] < p.batch) {
+        q.q0 = p.q_start ? p.q_start[s.grp[v]] : s.grp[v] * p.max_tokens;
+        q.cnt = (p.q_start ? p.q_start[s.grp[v + 1]] : s.grp[v + 1] * p.max_tokens) - q.q0;
+        q.hi = s.lim[v];
+        q.len = q.hi * P;
+    }
+    return q;
+}
+
+// Shared pages in a launch of their own (prefix.cu): tiles of 128 rows, and what
+// a unit (group, tile, kv head) costs beside its pages, in pages.
+constexpr int PRE_ROWS = 128, PRE_FIXED = 8;
+DEV long long pre_items(const AttParams &p, int cnt, int np) {
+    return np && cnt ? (long long)((cnt * p.group + PRE_ROWS - 1) / PRE_ROWS) * p.c.hkv * (np + PRE_FIXED) : 0;
+}
+DEV int pre_used(long long total, int ctas) { return (int)max(1ll, min((long long)ctas, total)); }
+
+
+// Work item x belongs to the last sequence b with prefix[b] <= x that has any.
+DEV int att_find(const long long *prefix, int batch, long long x) {
+    int a = 0, z = batch;
+    while (z - a > 1) {
+        const int mid = (a + z) / 2;
+        if (prefix[mid] <= x) a = mid;
+        else z = mid;
+    }
+    return a;
+}
+DEV float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+DEV uint32_t half2_of(float lo, float hi) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+
+int prefix_launch(const mk_cache_desc *cache, AttParams &p, cudaStream_t stream);  // prefix.cu
+
+}  // namespace mk

@@ -1,0 +1,682 @@
+// Attention of a group's rows over the pages that its sequences share: the
+// first of cache attention's launches where groups are large (attend.cu then
+// does the sequences' own pages and joins both).
+//
+// Mathematics.  As in attend.cu: one pass over the pages with the running
+// maximum m and sum l of the softmax in log2 units, sums in fp32, scores K q,
+// outputs P V.  Every row sees every token, so there are no masks.
+//
+// Matrix products.  tcgen05.mma kind::f16 on tiles of 128 rows (the group's
+// tokens x q heads of one kv head): S = Q K^T with Q in tensor memory and a
+// page's K in shared memory, then O = P V with P in tensor memory.  A page's
+// output starts from zero and is added in registers with the page's scale and
+// the softmax's correction, so that neither has to be folded into f16 values,
+// and no correction ever rewrites tensor memory.  Codes are expanded to f16
+// (exact) by four warps on their way from the ring the pages land in to the
+// swizzled tiles the products read; a row of Q is scaled by a power of two into
+// f16's range, probabilities are f16 times 2^14.
+//
+// Fewer rows.  The tile's 128 lanes hold two copies of up to 64 rows, or four of
+// up to 32: each copy takes the softmax of its share of a page's tokens, the
+// others' columns of its P staying zero, and the copies are joined at the end.
+// The products cost the same, and the softmax, one lane a row, a half or quarter.
+//
+// Roles.  Two streams of four softmax warps take pages in turn, so that one's
+// products run during the other's softmax; four converting warps; one producer
+// (bulk copies); one thread that issues the products.
+//
+// Work split.  As in attend.cu: the pages of all (group, tile, kv head) are one
+// axis cut into equal ranges, one per CTA; what a CTA boundary cuts is merged
+// by the call's last launch, in the order of the CTAs.
+#include "dev_attend.cuh"
+
+namespace mk {
+
+constexpr int PRE_THREADS = 512;
+constexpr int PRE_MAXRING = 32;
+
+// Tensor memory columns, P tokens a page: O of both streams, S, P, then Q.
+constexpr int PRE_O = 0, PRE_S = 256, PRE_P = 384, PRE_Q = 448;
+
+struct PreShared {
+    long long *prefix;  // [ngroups + 1]: work items before each group
+    int4 *unit;         // [ngroups]: first query row, query tokens, pages, leading sequence
+    AttGroups groups;
+    float2 *in_scale;   // [ring]: K scale (below 0: page not loaded), V scale without the probabilities' 2^14
+    float2 *scale;      // [4]: of the page on its way through the products, by page number % 4
+    float *qf;          // [128]: a row's factor
+    float *ml;          // [256][2]
+    float *merge;       // [256][33]
+    uint64_t *full, *empty;                                     // [ring]
+    uint64_t *k_full, *k_empty, *v_full, *v_empty;              // [2], by stream, as all further ones
+    uint64_t *s_full, *s_empty, *p_full, *o_full, *o_empty;
+    uint64_t *q_full, *q_empty, *drain;
+    int *ctrl;          // [0] abort, [1] tensor memory address
+    uint8_t *tiles;     // [2][K f16, V f16]
+    uint8_t *ring;      // [ring][K page, V page]
+};
+
+__host__ __device__ constexpr int pre_fixed_bytes(int ngroups) {
+    return (ngroups + 1) * 8 + ngroups * 16 + att_group_bytes(ngroups) + PRE_MAXRING * 8 + 4 * 8 + 128 * 4 + 256 * 8 +
+           256 * 33 * 4 + (2 * PRE_MAXRING + 9 * 2 + 3) * 8 + 8 + 64;
+}
+
+template <int D, int P>
+DEV PreShared pre_shared(const AttParams &p) {
+    PreShared s;
+    uint8_t *at = mk_smem;
+    const auto take = [&](size_t bytes) {
+        uint8_t *x = at;
+        at += bytes;
+        return x;
+    };
+    s.tiles = take(4 * P * D * 2);  // at 1024-byte boundaries: the dynamic shared memory starts at one (checked)
+    s.ring = take((size_t)p.pre_ring * 2 * P * D);
+    s.merge = reinterpret_cast<float *>(take(256 * 33 * 4));
+    s.ml = reinterpret_cast<float *>(take(256 * 8));
+    s.qf = reinterpret_cast<float *>(take(128 * 4));
+    s.unit = reinterpret_cast<int4 *>(take(p.ngroups * 16));
+    s.in_scale = reinterpret_cast<float2 *>(take(PRE_MAXRING * 8));
+    s.scale = reinterpret_cast<float2 *>(take(4 * 8));
+    s.full = reinterpret_cast<uint64_t *>(take((2 * PRE_MAXRING + 9 * 2 + 3) * 8));
+    s.empty = s.full + PRE_MAXRING;
+    s.k_full = s.empty + PRE_MAXRING;
+    s.k_empty = s.k_full + 2;
+    s.v_full = s.k_empty + 2;
+    s.v_empty = s.v_full + 2;
+    s.s_full = s.v_empty + 2;
+    s.s_empty = s.s_full + 2;
+    s.p_full = s.s_empty + 2;
+    s.o_full = s.p_full + 2;
+    s.o_empty = s.o_full + 2;
+    s.q_full = s.o_empty + 2;
+    s.q_empty = s.q_full + 1;
+    s.drain = s.q_empty + 1;
+    s.prefix = reinterpret_cast<long long *>(take((p.ngroups + 1) * 8));
+    s.ctrl = reinterpret_cast<int *>(take(8));
+    s.groups = att_groups_at(at, p.ngroups);
+    return s;
+}
+
+// ---- tensor memory and products
+DEV void pre_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+DEV void pre_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
+}
+DEV void pre_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+DEV void pre_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+DEV void pre_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+DEV void pre_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// f16 A and B (both K-major), fp32 D, 128 x n
+__host__ __device__ constexpr uint32_t pre_idesc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(PRE_ROWS >> 4) << 24); }
+// K-major operand of rows of 128 (64) bytes, swizzled by as much: 8-row groups 1024 (512) bytes apart.
+template <bool WIDE>
+DEV uint64_t pre_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)((WIDE ? 1024 : 512) >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)(WIDE ? 2 : 4) << 61;
+}
+// A warp's 32 lanes x N columns.
+template <int N>
+DEV void pre_ld(uint32_t addr, uint32_t (&r)[N]) {
+    static_assert(N == 8 || N == 16 || N == 32, "");
+    if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(addr));
+    else if constexpr (N == 16)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(addr));
+    else
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+              "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+              "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+            : "r"(addr));
+}
+template <int N>
+DEV void pre_st(uint32_t addr, const uint32_t (&r)[N]) {
+    static_assert(N == 4 || N == 8 || N == 16, "");
+    if constexpr (N == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+    else if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    else
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+            "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+            : "memory");
+}
+
+// ---- waits
+// Bounded (about two seconds); false: it ran out here or elsewhere in the CTA.
+DEV bool pre_wait(const AttParams &p, const PreShared &s, uint64_t *bar, uint32_t parity) {
+    if (mbar_test(bar, parity)) return true;
+    for (int i = 0; i < 20000; ++i) {
+        if (mbar_wait_hint(bar, parity, 100000)) return true;
+        if (*reinterpret_cast<volatile int *>(s.ctrl)) return false;
+    }
+    note_failure(p.c.status, MK_ERR_TIMEOUT, -1, blockIdx.x, -1);
+    *reinterpret_cast<volatile int *>(s.ctrl) = 1;
+    return false;
+}
+// By a whole warp: the same answer in all lanes.
+DEV bool pre_wait_warp(const AttParams &p, const PreShared &s, uint64_t *bar, uint32_t parity) {
+    return __all_sync(FULL, pre_wait(p, s, bar, parity));
+}
+
+// ---- the CTA's range, as every role walks it
+struct PreSeg {
+    int g, tile, h, pg, n;  // pages [pg, pg + n) of a unit
+    int q0, rows, lead;     // the group's first query token, its rows of one kv head, whose table row
+    bool whole, head;       // all of the unit's pages; its first among them
+    DEV int tile_rows() const { return min(PRE_ROWS, rows - tile * PRE_ROWS); }
+    DEV int copies() const { const int n = tile_rows(); return n <= 32 ? 4 : n <= 64 ? 2 : 1; }
+};
+struct PreWalk {
+    const AttParams &p;
+    const PreShared &s;
+    long long x = 0, end = 0;
+    int g;
+    DEV PreWalk(const AttParams &p_, const PreShared &s_) : p(p_), s(s_) {
+        const long long total = s.prefix[p.ngroups];
+        const int ctas = pre_used(total, p.pre_ctas);
+        if ((int)blockIdx.x < ctas) {
+            x = att_div((long long)blockIdx.x * total, ctas);
+            end = att_div((long long)(blockIdx.x + 1) * total, ctas);
+        }
+        g = att_find(s.prefix, p.ngroups, x);
+    }
+    DEV bool next(PreSeg &o) {
+        while (x < end) {
+            while (s.prefix[g + 1] <= x) ++g;
+            const int4 u = s.unit[g];
+            const int np = u.z, items = np + PRE_FIXED;
+            const long long r = x - s.prefix[g];
+            const int unit = (int)att_div(r, items), within = (int)(r - (long long)unit * items);
+            const long long left = items - within;  // items to the unit's end
+            const int first = max(0, within - PRE_FIXED);
+            const int until = left <= end - x ? np : max(0, within + (int)(end - x) - PRE_FIXED);
+            x += min(left, end - x);
+            if (first >= until) continue;
+            o.g = g;
+            o.tile = unit / p.c.hkv;
+            o.h = unit - o.tile * p.c.hkv;
+            o.pg = first;
+            o.n = until - first;
+            o.q0 = u.x;
+            o.rows = u.y * p.group;
+            o.lead = u.w;
+            o.whole = o.n == np;
+            o.head = first == 0;
+            return true;
+        }
+        return false;
+    }
+};
+
+// ---- producer warp: lane i looks up the i-th of 32 pages, then each issues its own in turn
+template <int D, int P>
+DEV void pre_produce(const AttParams &p, const PreShared &s) {
+    constexpr int PAGE = P * D;
+    const int lane = threadIdx.x % 32;
+    PreWalk walk(p, s);
+    PreSeg g;
+    bool more = walk.next(g), ok = true;
+    int before = 0, slot = 0;
+    uint32_t round = 0;
+    for (int base = 0; more && ok; base += 32) {
+        int id = -1, h = 0;
+        bool want = false;
+        while (more) {
+            const int k = base + lane - before;
+            if (k >= 0 && k < g.n) {
+                want = true;
+                h = g.h;
+                id = p.table[(size_t)g.lead * p.width + g.pg + k];
+                if ((unsigned)id >= (unsigned)p.c.pages) {
+                    note_failure(p.c.status, MK_ERR_DEVICE_CHECK, g.lead, (g.pg + k) * P, id);
+                    id = -1;
+                }
+            }
+            if (before + g.n > base + 32) break;
+            before += g.n;
+            more = walk.next(g);
+        }
+        const size_t at = (size_t)(id < 0 ? 0 : id) * p.c.hkv + h;
+        float2 sc = make_float2(-1.f, 0.f);
+        if (id >= 0) sc = make_float2(p.c.ks[at], p.c.vs[at] * 0x1p-14f);
+        const int n = __popc(__ballot_sync(FULL, want));
+        for (int i = 0; i < n && ok; ++i) {
+            if (lane == i) {
+                ok = round == 0 || pre_wait(p, s, &s.empty[slot], (round & 1) ^ 1);
+                if (ok) {
+                    s.in_scale[slot] = sc;
+                    uint8_t *dst = s.ring + (size_t)slot * 2 * PAGE;
+                    if (id >= 0) {
+                        mbar_expect_tx(&s.full[slot], 2 * PAGE);
+                        bulk_g2s_plain(dst, p.c.k + at * PAGE, PAGE, &s.full[slot]);
+                        bulk_g2s_plain(dst + PAGE, p.c.v + at * PAGE, PAGE, &s.full[slot]);
+                    } else {
+                        mbar_arrive(&s.full[slot]);
+                    }
+                }
+            }
+            ok = __shfl_sync(FULL, ok, i);
+            if (ok && ++slot == p.pre_ring) {
+                slot = 0;
+                ++round;
+            }
+        }
+    }
+    // the copies in flight land before the CTA ends, also where the warps that wanted them have given up
+    if (lane < p.pre_ring) {
+        const uint32_t fills = round + (lane < slot ? 1 : 0);
+        for (int i = 0; i < 200 && fills && !mbar_wait_hint(&s.full[lane], (fills - 1) & 1, 1000000); ++i) {
+        }
+    }
+}
+
+// ---- converting warps: a landed page's codes as f16 into the products' tiles
+// 16 codes as two 16-byte pieces
+DEV void pre_expand(uint4 x, uint4 &lo, uint4 &hi) {
+    e4m3x4_to_half2(x.x, lo.x, lo.y);
+    e4m3x4_to_half2(x.y, lo.z, lo.w);
+    e4m3x4_to_half2(x.z, hi.x, hi.y);
+    e4m3x4_to_half2(x.w, hi.z, hi.w);
+}
+template <int D, int P>
+DEV void pre_convert(const AttParams &p, const PreShared &s) {
+    constexpr int PAGE = P * D, N = PAGE / 16 / 128;  // 16-byte pieces of codes per thread
+    const int tid = threadIdx.x % 128, lane = tid % 32;
+    PreWalk walk(p, s);
+    PreSeg g;
+    int total = 0;
+    while (walk.next(g)) total += g.n;
+    int slot = 0;
+    uint32_t round = 0;
+    for (int n = 0; n < total; ++n) {
+        const int x = n & 1;
+        const uint32_t ph = (n >> 1) & 1;
+        if (!pre_wait_warp(p, s, &s.full[slot], round & 1)) return;
+        const float2 sc = s.in_scale[slot];
+        const bool there = sc.x >= 0.f || sc.x != sc.x;
+        const uint8_t *raw = s.ring + (size_t)slot * 2 * PAGE;
+        uint8_t *kt = s.tiles + (size_t)x * 2 * PAGE * 2, *vt = kt + PAGE * 2;
+        uint4 in[N];
+        const auto read = [&](const uint8_t *from) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                in[i] = there ? *reinterpret_cast<const uint4 *>(from + (i * 128 + tid) * 16) : make_uint4(0, 0, 0, 0);
+        };
+        read(raw);
+        if (!pre_wait_warp(p, s, &s.k_empty[x], ph ^ 1)) return;
+        if (tid == 0) s.scale[n & 3] = sc;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {  // token t, dims 16 j ..: block j / 4, pieces 2 (j % 4) and the next of its 128-byte row
+            const int at = i * 128 + tid, t = at / (D / 16), j = at % (D / 16), c = 2 * (j & 3);
+            uint4 lo, hi;
+            pre_expand(in[i], lo, hi);
+            uint8_t *row = kt + (j >> 2) * (P * 128) + t * 128;
+            // blocks lie a multiple of 1024 bytes apart: the second one's lanes store their second piece first
+            const bool swap = j >> 2;
+            *reinterpret_cast<uint4 *>(row + (((c + (swap ? 1 : 0)) ^ (t & 7)) << 4)) = swap ? hi : lo;
+            *reinterpret_cast<uint4 *>(row + (((c + (swap ? 0 : 1)) ^ (t & 7)) << 4)) = swap ? lo : hi;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.k_full[x]);
+        read(raw + PAGE);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.empty[slot]);
+        if (!pre_wait_warp(p, s, &s.v_empty[x], ph ^ 1)) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {  // dim d, tokens 16 j ..
+            const int at = i * 128 + tid, d = at / (P / 16), j = at % (P / 16);
+            uint4 lo, hi;
+            pre_expand(in[i], lo, hi);
+            uint8_t *row = vt + d * (P * 2);
+            const int sw = P == 64 ? d & 7 : (d >> 1) & 3;
+            *reinterpret_cast<uint4 *>(row + (((2 * j) ^ sw) << 4)) = lo;
+            *reinterpret_cast<uint4 *>(row + (((2 * j + 1) ^ sw) << 4)) = hi;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.v_full[x]);
+        if (++slot == p.pre_ring) {
+            slot = 0;
+            ++round;
+        }
+    }
+}
+
+// ---- the thread that issues the products
+template <int D, int P>
+DEV void pre_products(const AttParams &p, const PreShared &s, uint32_t tmem) {
+    constexpr int PAGE = P * D;
+    const uint32_t tiles = saddr(s.tiles);
+    PreWalk walk(p, s);
+    PreSeg g;
+    int n = 0;  // pages done
+    uint32_t seg = 0;
+    bool ok = true;
+    const auto scores = [&](int k) {
+        const int x = k & 1;
+        const uint32_t ph = (k >> 1) & 1;
+        ok = ok && pre_wait(p, s, &s.k_full[x], ph) && pre_wait(p, s, &s.s_empty[x], ph ^ 1);
+        if (!ok) return;
+        pre_fence_after();
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            pre_mma(tmem + PRE_S + x * 64, tmem + PRE_Q + i * 8,
+                    pre_desc<true>(tiles + x * 4 * PAGE + (i / 4) * (P * 128) + (i % 4) * 32), pre_idesc(P), i > 0);
+        pre_commit(&s.s_full[x]);
+        pre_commit(&s.k_empty[x]);
+    };
+    const auto outputs = [&](int k) {
+        const int x = k & 1;
+        const uint32_t ph = (k >> 1) & 1;
+        ok = ok && pre_wait(p, s, &s.p_full[x], ph) && pre_wait(p, s, &s.v_full[x], ph) && pre_wait(p, s, &s.o_empty[x], ph ^ 1);
+        if (!ok) return;
+        pre_fence_after();
+#pragma unroll
+        for (int i = 0; i < P / 16; ++i)
+            pre_mma(tmem + PRE_O + x * 128, tmem + PRE_P + x * 32 + i * 8,
+                    pre_desc<P == 64>(tiles + x * 4 * PAGE + 2 * PAGE + i * 32), pre_idesc(D), i > 0);
+        pre_commit(&s.o_full[x]);
+        pre_commit(&s.v_empty[x]);
+    };
+    for (; ok && walk.next(g); ++seg) {
+        ok = pre_wait(p, s, s.q_full, seg & 1);
+        if (!ok) break;
+        scores(n);
+        if (g.n == 1 && ok) pre_commit(s.q_empty);
+        for (int i = 0; i < g.n && ok; ++i) {
+            if (i + 1 < g.n) {
+                scores(n + i + 1);
+                if (i + 2 == g.n && ok) pre_commit(s.q_empty);
+            }
+            outputs(n + i);
+        }
+        n += g.n;
+    }
+    // what was issued ends before tensor memory is freed
+    pre_commit(s.drain);
+    for (int i = 0; i < 200 && !mbar_wait_hint(s.drain, 0, 1000000); ++i) {
+    }
+}
+
+// ---- softmax warps
+// One page's scores to probabilities: this thread's row, CN tokens from column c0 on.
+template <int CN>
+DEV void pre_softmax(uint32_t s_addr, uint32_t p_addr, float fk, float &m, float &l, float &alpha) {
+    constexpr int W = CN < 16 ? CN : 16;
+    uint32_t r[W];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < CN; c += W) {
+        pre_ld(s_addr + c, r);
+        pre_wait_ld();
+#pragma unroll
+        for (int i = 0; i < W; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
+    }
+    const float mn = fmaxf(m, mx * fk), mu = mn == -INFINITY ? 0.f : mn, off = 14.f - mu;
+    alpha = exp2_fast(m - mu);
+    m = mn;
+    float sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < CN; c += W) {
+        if (CN > W) {
+            pre_ld(s_addr + c, r);
+            pre_wait_ld();
+        }
+        uint32_t h[W / 2];
+#pragma unroll
+        for (int i = 0; i < W; i += 2) {
+            const float a = exp2_fast(fmaf(__uint_as_float(r[i]), fk, off)), b = exp2_fast(fmaf(__uint_as_float(r[i + 1]), fk, off));
+            sum += a + b;
+            h[i / 2] = half2_of(a, b);
+        }
+        pre_st(p_addr + c / 2, h);
+    }
+    l = fmaf(l, alpha, sum);
+}
+
+DEV void pre_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int D, int P>
+DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
+    const int x = threadIdx.x / 128, tid = threadIdx.x % 128, lane = tid % 32, warp = tid / 32;
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t s_addr = lanes + PRE_S + x * 64, p_addr = lanes + PRE_P + x * 32, o_addr = lanes + PRE_O + x * 128;
+    PreWalk walk(p, s);
+    PreSeg g;
+    int n = 0;  // pages before the segment
+    uint32_t seg = 0;
+    bool ok = true;  // a warp that gives up still takes its place at the barriers
+    for (; walk.next(g); ++seg, n += g.n) {
+        const int copies = g.copies(), each = PRE_ROWS / copies, copy = tid / each, rows = g.tile_rows();
+        if (x == 0) {  // the segment's queries
+            const int r = g.tile * PRE_ROWS + tid % each;
+            uint4 q[D / 8];
+            uint32_t big = 0;
+            const uint16_t *row = nullptr;
+            if (tid % each < rows) {
+                const int tok = r / p.group;
+                row = p.q + (int64_t)(g.q0 + tok) * p.qs_t + (int64_t)(g.h * p.group + r - tok * p.group) * p.qs_h;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) q[i] = row ? __ldg(reinterpret_cast<const uint4 *>(row) + i) : make_uint4(0, 0, 0, 0);
+            const auto word = [&](int i) { return i % 4 == 0 ? q[i / 4].x : i % 4 == 1 ? q[i / 4].y : i % 4 == 2 ? q[i / 4].z : q[i / 4].w; };
+#pragma unroll
+            for (int i = 0; i < D / 2; ++i) big = max(big, max((word(i) << 16) & 0x7fffffffu, word(i) & 0x7fff0000u));
+            // times 2^(14 - exponent): the row's largest value lands in [2^14, 2^15)
+            const int up = min(max(268 - (int)(big >> 23), 1), 253);
+            const float sc = __uint_as_float((uint32_t)up << 23);
+            if (seg > 0 && ok) ok = pre_wait_warp(p, s, s.q_empty, (seg - 1) & 1);
+            pre_fence_after();
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 16) {
+                uint32_t h[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    h[i] = half2_of(__uint_as_float(word(c + i) << 16) * sc, __uint_as_float(word(c + i) & 0xffff0000u) * sc);
+                pre_st(lanes + PRE_Q + c, h);
+            }
+            s.qf[tid] = big >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(254 - up) << 23);
+            pre_wait_st();
+            pre_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s.q_full);
+        }
+        if (copies > 1) {  // the other copies' columns stay zero
+            const uint32_t zero[16] = {};
+#pragma unroll
+            for (int c = 0; c < P / 2; c += 16) pre_st(p_addr + c, zero);
+            pre_wait_st();
+        }
+        if (ok) ok = pre_wait_warp(p, s, s.q_full, seg & 1);
+        const float qf = s.qf[tid] * p.scale_log2;
+        float m = -INFINITY, l = 0.f, o[D], later_alpha = 1.f, later_scale = 0.f;
+#pragma unroll
+        for (int i = 0; i < D; ++i) o[i] = 0.f;
+        // a page's output: added while the next one's is on its way
+        const auto add = [&](int k) {
+            ok = pre_wait_warp(p, s, &s.o_full[x], (k >> 1) & 1);
+            if (!ok) return;
+            pre_fence_after();
+            if (!__all_sync(FULL, later_alpha == 1.f)) {
+#pragma unroll
+                for (int i = 0; i < D; ++i) o[i] *= later_alpha;
+            }
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+                uint32_t r[16];
+                pre_ld(o_addr + c, r);
+                pre_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[c + i] = fmaf(__uint_as_float(r[i]), later_scale, o[c + i]);
+            }
+            pre_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.o_empty[x]);
+        };
+        int last = -1;
+        for (int k = n + ((n ^ x) & 1); k < n + g.n && ok; k += 2) {
+            ok = pre_wait_warp(p, s, &s.s_full[x], (k >> 1) & 1);
+            if (!ok) break;
+            pre_fence_after();
+            const float2 sc = s.scale[k & 3];
+            float alpha = 1.f;
+            if (sc.x >= 0.f || sc.x != sc.x) {
+                const float fk = qf * sc.x;
+                if (copies == 1) pre_softmax<P>(s_addr, p_addr, fk, m, l, alpha);
+                else if (copies == 2) pre_softmax<P / 2>(s_addr + copy * (P / 2), p_addr + copy * (P / 4), fk, m, l, alpha);
+                else pre_softmax<P / 4>(s_addr + copy * (P / 4), p_addr + copy * (P / 8), fk, m, l, alpha);
+            } else {  // a page that is not loaded: as if its tokens were masked
+                const uint32_t zero[16] = {};
+#pragma unroll
+                for (int c = 0; c < P / 2; c += 16) pre_st(p_addr + c, zero);
+            }
+            pre_wait_st();
+            pre_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&s.s_empty[x]);
+                mbar_arrive(&s.p_full[x]);
+            }
+            if (last >= 0) add(last);
+            last = k;
+            later_alpha = alpha;
+            later_scale = sc.y;
+        }
+        if (last >= 0 && ok) add(last);
+
+        // join the copies of both streams, 32 dims at a time
+        *reinterpret_cast<float2 *>(s.ml + threadIdx.x * 2) = make_float2(m, l);
+        pre_bar();
+        const int parts = 2 * copies;  // row r of the tile: threads r + i * each
+        float big = -INFINITY;
+        for (int i = 0; i < parts; ++i) big = fmaxf(big, s.ml[(tid % each + i * each) * 2]);
+        const float a = exp2_fast(m - (big == -INFINITY ? 0.f : big));
+        const size_t slot = ((size_t)blockIdx.x * 2 + (g.head ? 1 : 0)) * PRE_ROWS;
+        const auto at_row = [&](int r) {
+            const int rr = g.tile * PRE_ROWS + r;
+            return (((size_t)p.tokens + g.q0 + rr / p.group) * p.c.hkv + g.h) * p.group + rr % p.group;
+        };
+        if (threadIdx.x < rows) {  // (rows <= each: this thread's row is threadIdx.x)
+            float sum = 0.f;
+            for (int i = 0; i < parts; ++i) {
+                const float2 y = *reinterpret_cast<const float2 *>(s.ml + (threadIdx.x + i * each) * 2);
+                sum = fmaf(y.y, exp2_fast(y.x - (big == -INFINITY ? 0.f : big)), sum);
+            }
+            float *to = g.whole ? p.row_ml + at_row(threadIdx.x) * 2 : p.pre_ml + (slot + threadIdx.x) * 2;
+            *reinterpret_cast<float2 *>(to) = make_float2(big, sum);
+        }
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s.merge[threadIdx.x * 33 + i] = o[c + i] * a;
+            pre_bar();
+            for (int e = threadIdx.x; e < rows * 32; e += 256) {
+                const int r = e / 32, d = e % 32;
+                float sum = 0.f;
+                for (int i = 0; i < parts; ++i) sum += s.merge[(r + i * each) * 33 + d];
+                (g.whole ? p.row_o + at_row(r) * D : p.pre_o + (slot + r) * D)[c + d] = sum;
+            }
+            pre_bar();
+        }
+    }
+}
+
+template <int D, int P>
+__global__ void __launch_bounds__(PRE_THREADS, 1) cache_prefix_kernel(const AttParams p) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    const PreShared s = pre_shared<D, P>(p);
+    const int tid = threadIdx.x, warp = tid / 32;
+    att_groups<P>(p, s.groups, blockIdx.x == 0);
+    for (int g = tid; g < p.ngroups; g += PRE_THREADS) {
+        const AttSeq q = att_unit<P, true>(p, s.groups, g, false);
+        s.unit[g] = make_int4(q.q0, q.cnt, q.hi, s.groups.lead[g]);
+        s.prefix[g + 1] = pre_items(p, q.cnt, q.hi);
+    }
+    if (tid < p.pre_ring) {
+        mbar_init(&s.full[tid], 1);
+        mbar_init(&s.empty[tid], 4);
+    }
+    if (tid == 64) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&s.k_full[x], 4);
+            mbar_init(&s.v_full[x], 4);
+            mbar_init(&s.k_empty[x], 1);
+            mbar_init(&s.v_empty[x], 1);
+            mbar_init(&s.s_full[x], 1);
+            mbar_init(&s.s_empty[x], 4);
+            mbar_init(&s.p_full[x], 4);
+            mbar_init(&s.o_full[x], 1);
+            mbar_init(&s.o_empty[x], 4);
+        }
+        mbar_init(s.q_full, 4);
+        mbar_init(s.q_empty, 1);
+        mbar_init(s.drain, 1);
+        s.ctrl[0] = 0;
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (warp == 13) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&s.ctrl[1])) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        pre_fence_before();
+    }
+    att_running(s.prefix, p.ngroups);
+    pre_fence_after();
+    const uint32_t tmem = (uint32_t)s.ctrl[1];
+    // registers: 4 x 128 threads were launched with 128 each; 2 x 184 + 2 x 72
+    if (tid < 256) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        if ((saddr(s.tiles) & 1023) == 0) pre_rows<D, P>(p, s, tmem);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if ((saddr(s.tiles) & 1023) != 0) {
+            if (tid == 256) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, -1, -2, -1);
+        } else if (tid < 384) {
+            pre_convert<D, P>(p, s);
+        } else if (warp == 12) {
+            pre_produce<D, P>(p, s);
+        } else if (tid == 13 * 32) {
+            pre_products<D, P>(p, s, tmem);
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+int prefix_launch(const mk_cache_desc *cache, AttParams &p, cudaStream_t stream) {
+    const int D = cache->head_dim, P = cache->page_tokens;
+    const int fixed = pre_fixed_bytes(p.ngroups) + 4 * P * D * 2;
+    p.pre_ring = std::min(PRE_MAXRING, (SERVE_SMEM - fixed) / (2 * P * D));
+    const int smem = fixed + p.pre_ring * 2 * P * D;
+    void (*f)(const AttParams) = D == 64 ? (P == 32 ? cache_prefix_kernel<64, 32> : cache_prefix_kernel<64, 64>)
+                                         : (P == 32 ? cache_prefix_kernel<128, 32> : cache_prefix_kernel<128, 64>);
+    static std::atomic<uint32_t> ready[SERVE_MAX_DEVICES];
+    if (int rc = serve_prepare(reinterpret_cast<const void *>(f), ready, (D == 128 ? 2 : 0) + (P == 64 ? 1 : 0), false)) return rc;
+    f<<<p.pre_ctas, PRE_THREADS, smem, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? MK_OK : serve_cuda_fail(e, "prefix attention launch");
+}
+
+}  // namespace mk
