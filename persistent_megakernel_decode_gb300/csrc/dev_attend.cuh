@@ -132,6 +132,9 @@ DEV int att_group_of(const AttParams &p, const AttGroups &s, int b) {
 template <int P>
 DEV void att_groups(const AttParams &p, const AttGroups &s, bool report) {
     const int n = p.ngroups, tid = threadIdx.x, threads = blockDim.x;
+    // the first of everything at once: one round trip
+    const AttSeq mine = tid < p.batch ? att_seq<P>(p, tid, false) : AttSeq{0, 0, 0, 0, 0, false};
+    const int share = tid < n ? p.shared[tid] : 0;
     bool bad = false;
     for (int g = tid; g <= n; g += threads) {
         const int x = p.groups[g];
@@ -141,7 +144,7 @@ DEV void att_groups(const AttParams &p, const AttGroups &s, bool report) {
     bad = __syncthreads_or(bad);
     if (bad && report && tid == 0) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, -1, -1, -1);
     for (int g = tid; g < n; g += threads) {
-        const int x = p.shared[g];
+        const int x = g == tid ? share : p.shared[g];
         if (x < 0 && report) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, s.grp[g], x, -1);
         s.lead[g] = INT_MAX;
         s.lim[g] = bad || s.grp[g + 1] - s.grp[g] < 2 ? 0 : max(x, 0) / P;
@@ -150,7 +153,7 @@ DEV void att_groups(const AttParams &p, const AttGroups &s, bool report) {
     for (int b = tid; b < p.batch && !bad; b += threads) {
         const int g = att_group_of(p, s, b);
         if (g < 0) continue;
-        const AttSeq q = att_seq<P>(p, b, false);
+        const AttSeq q = b == tid ? mine : att_seq<P>(p, b, false);
         if (q.bad) atomicMin(&s.lim[g], 0);  // where its rows begin is not known either
         if (q.cnt == 0) continue;
         atomicMin(&s.lead[g], b);

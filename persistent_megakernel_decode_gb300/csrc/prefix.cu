@@ -8,13 +8,18 @@
 //
 // Matrix products.  tcgen05.mma kind::f16 on tiles of 128 rows (the group's
 // tokens x q heads of one kv head): S = Q K^T with Q in tensor memory and a
-// page's K in shared memory, then O = P V with P in tensor memory.  A page's
-// output starts from zero and is added in registers with the page's scale and
-// the softmax's correction, so that neither has to be folded into f16 values,
-// and no correction ever rewrites tensor memory.  Codes are expanded to f16
-// (exact) by four warps on their way from the ring the pages land in to the
-// swizzled tiles the products read; a row of Q is scaled by a power of two into
-// f16's range, probabilities are f16 times 2^14.
+// page's K in shared memory, then O += P V with P in tensor memory.  Codes are
+// expanded to f16 (exact) by eight warps on their way from the ring the pages
+// land in to the swizzled tiles the products read; a row of Q is scaled by a
+// power of two into f16's range.
+//
+// One reference.  P and the sum are relative to a row's reference r, which is
+// the first page's largest s + log2(the page's V scale) and follows a larger
+// one only when that is 2^8 above it: then O is rescaled in tensor memory, and
+// else nothing is.  P = 2^(s + log2 vs - r + 7) holds the V scale, so that pages
+// of different scales add up in one accumulator; it stays below 2^15, and what
+// it rounds away is 2^-11 of itself or 2^-32 of the reference.  The sum takes the
+// page's P as they are in fp32, times a power of two that removes the scale.
 //
 // Fewer rows.  The tile's 128 lanes hold two copies of up to 64 rows, or four of
 // up to 32: each copy takes the softmax of its share of a page's tokens, the
@@ -22,8 +27,8 @@
 // The products cost the same, and the softmax, one lane a row, a half or quarter.
 //
 // Roles.  Two streams of four softmax warps take pages in turn, so that one's
-// products run during the other's softmax; four converting warps; one producer
-// (bulk copies); one thread that issues the products.
+// products run during the other's softmax; four warps each expand K and V; one
+// producer (bulk copies); one warp issues the products.
 //
 // Work split.  As in attend.cu: the pages of all (group, tile, kv head) are one
 // axis cut into equal ranges, one per CTA; what a CTA boundary cuts is merged
@@ -32,7 +37,8 @@
 
 namespace mk {
 
-constexpr int PRE_THREADS = 512;
+constexpr int PRE_THREADS = 640;
+constexpr int PRE_ISSUER = 17;  // warp
 constexpr int PRE_MAXRING = 32;
 
 // Tensor memory columns, P tokens a page: O of both streams, S, P, then Q.
@@ -42,14 +48,17 @@ struct PreShared {
     long long *prefix;  // [ngroups + 1]: work items before each group
     int4 *unit;         // [ngroups]: first query row, query tokens, pages, leading sequence
     AttGroups groups;
-    float2 *in_scale;   // [ring]: K scale (below 0: page not loaded), V scale without the probabilities' 2^14
+    float2 *in_scale;   // [ring]: K scale (below 0: page not loaded), log2 of the V scale
     float2 *scale;      // [4]: of the page on its way through the products, by page number % 4
     float *qf;          // [128]: a row's factor
     float *ml;          // [256][2]
-    float *merge;       // [256][33]
+    float *merge;       // [256][36]; before that, the queries' rows
+    float **to;         // [128]: where a row's outputs go
     uint64_t *full, *empty;                                     // [ring]
-    uint64_t *k_full, *k_empty, *v_full, *v_empty;              // [2], by stream, as all further ones
-    uint64_t *s_full, *s_empty, *p_full, *o_full, *o_empty;
+    // [2], by stream: K's tile is written and the scores before are read; S is
+    // there; V's tile and P are written; O is there.  A tile is free again when
+    // its product is.
+    uint64_t *s_ready, *s_done, *o_ready, *o_done;
     uint64_t *q_full, *q_empty, *drain;
     int *ctrl;          // [0] abort, [1] tensor memory address
     uint8_t *tiles;     // [2][K f16, V f16]
@@ -57,8 +66,8 @@ struct PreShared {
 };
 
 __host__ __device__ constexpr int pre_fixed_bytes(int ngroups) {
-    return (ngroups + 1) * 8 + ngroups * 16 + att_group_bytes(ngroups) + PRE_MAXRING * 8 + 4 * 8 + 128 * 4 + 256 * 8 +
-           256 * 33 * 4 + (2 * PRE_MAXRING + 9 * 2 + 3) * 8 + 8 + 64;
+    return (ngroups + 1) * 8 + ngroups * 16 + att_group_bytes(ngroups) + PRE_MAXRING * 8 + 4 * 8 + 128 * 4 + 128 * 8 + 256 * 8 +
+           256 * 36 * 4 + (2 * PRE_MAXRING + 4 * 2 + 3) * 8 + 8 + 64;
 }
 
 template <int D, int P>
@@ -72,24 +81,20 @@ DEV PreShared pre_shared(const AttParams &p) {
     };
     s.tiles = take(4 * P * D * 2);  // at 1024-byte boundaries: the dynamic shared memory starts at one (checked)
     s.ring = take((size_t)p.pre_ring * 2 * P * D);
-    s.merge = reinterpret_cast<float *>(take(256 * 33 * 4));
+    s.merge = reinterpret_cast<float *>(take(256 * 36 * 4));
     s.ml = reinterpret_cast<float *>(take(256 * 8));
     s.qf = reinterpret_cast<float *>(take(128 * 4));
+    s.to = reinterpret_cast<float **>(take(128 * 8));
     s.unit = reinterpret_cast<int4 *>(take(p.ngroups * 16));
     s.in_scale = reinterpret_cast<float2 *>(take(PRE_MAXRING * 8));
     s.scale = reinterpret_cast<float2 *>(take(4 * 8));
-    s.full = reinterpret_cast<uint64_t *>(take((2 * PRE_MAXRING + 9 * 2 + 3) * 8));
+    s.full = reinterpret_cast<uint64_t *>(take((2 * PRE_MAXRING + 4 * 2 + 3) * 8));
     s.empty = s.full + PRE_MAXRING;
-    s.k_full = s.empty + PRE_MAXRING;
-    s.k_empty = s.k_full + 2;
-    s.v_full = s.k_empty + 2;
-    s.v_empty = s.v_full + 2;
-    s.s_full = s.v_empty + 2;
-    s.s_empty = s.s_full + 2;
-    s.p_full = s.s_empty + 2;
-    s.o_full = s.p_full + 2;
-    s.o_empty = s.o_full + 2;
-    s.q_full = s.o_empty + 2;
+    s.s_ready = s.empty + PRE_MAXRING;
+    s.s_done = s.s_ready + 2;
+    s.o_ready = s.s_done + 2;
+    s.o_done = s.o_ready + 2;
+    s.q_full = s.o_done + 2;
     s.q_empty = s.q_full + 1;
     s.drain = s.q_empty + 1;
     s.prefix = reinterpret_cast<long long *>(take((p.ngroups + 1) * 8));
@@ -99,6 +104,12 @@ DEV PreShared pre_shared(const AttParams &p) {
 }
 
 // ---- tensor memory and products
+// True in one thread of a whole warp, always the same.
+DEV bool pre_elect() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(e));
+    return e != 0;
+}
 DEV void pre_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -259,7 +270,11 @@ DEV void pre_produce(const AttParams &p, const PreShared &s) {
         }
         const size_t at = (size_t)(id < 0 ? 0 : id) * p.c.hkv + h;
         float2 sc = make_float2(-1.f, 0.f);
-        if (id >= 0) sc = make_float2(p.c.ks[at], p.c.vs[at] * 0x1p-14f);
+        if (id >= 0) {
+            // a power of two, or 0 for a page of zeros (any scale does then), or NaN
+            const float v = p.c.vs[at];
+            sc = make_float2(p.c.ks[at], v == 0.f ? -120.f : v != v ? v : (float)((int)(__float_as_uint(v) >> 23 & 255) - 127));
+        }
         const int n = __popc(__ballot_sync(FULL, want));
         for (int i = 0; i < n && ok; ++i) {
             if (lane == i) {
@@ -299,7 +314,7 @@ DEV void pre_expand(uint4 x, uint4 &lo, uint4 &hi) {
     e4m3x4_to_half2(x.z, hi.x, hi.y);
     e4m3x4_to_half2(x.w, hi.z, hi.w);
 }
-template <int D, int P>
+template <int D, int P, bool VALUES>
 DEV void pre_convert(const AttParams &p, const PreShared &s) {
     constexpr int PAGE = P * D, N = PAGE / 16 / 128;  // 16-byte pieces of codes per thread
     const int tid = threadIdx.x % 128, lane = tid % 32;
@@ -307,56 +322,47 @@ DEV void pre_convert(const AttParams &p, const PreShared &s) {
     PreSeg g;
     int total = 0;
     while (walk.next(g)) total += g.n;
+    uint64_t *ready = VALUES ? s.o_ready : s.s_ready, *done = VALUES ? s.o_done : s.s_done;
     int slot = 0;
     uint32_t round = 0;
     for (int n = 0; n < total; ++n) {
         const int x = n & 1;
-        const uint32_t ph = (n >> 1) & 1;
         if (!pre_wait_warp(p, s, &s.full[slot], round & 1)) return;
         const float2 sc = s.in_scale[slot];
         const bool there = sc.x >= 0.f || sc.x != sc.x;
-        const uint8_t *raw = s.ring + (size_t)slot * 2 * PAGE;
-        uint8_t *kt = s.tiles + (size_t)x * 2 * PAGE * 2, *vt = kt + PAGE * 2;
+        const uint8_t *raw = s.ring + (size_t)slot * 2 * PAGE + (VALUES ? PAGE : 0);
+        uint8_t *tile = s.tiles + (size_t)x * 4 * PAGE + (VALUES ? 2 * PAGE : 0);
         uint4 in[N];
-        const auto read = [&](const uint8_t *from) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                in[i] = there ? *reinterpret_cast<const uint4 *>(from + (i * 128 + tid) * 16) : make_uint4(0, 0, 0, 0);
-        };
-        read(raw);
-        if (!pre_wait_warp(p, s, &s.k_empty[x], ph ^ 1)) return;
-        if (tid == 0) s.scale[n & 3] = sc;
+        for (int i = 0; i < N; ++i)
+            in[i] = there ? *reinterpret_cast<const uint4 *>(raw + (i * 128 + tid) * 16) : make_uint4(0, 0, 0, 0);
+        if (n > 1 && !pre_wait_warp(p, s, &done[x], ((n >> 1) & 1) ^ 1)) return;  // the tile's last product
+        if (!VALUES && tid == 0) s.scale[n & 3] = sc;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {  // token t, dims 16 j ..: block j / 4, pieces 2 (j % 4) and the next of its 128-byte row
-            const int at = i * 128 + tid, t = at / (D / 16), j = at % (D / 16), c = 2 * (j & 3);
+        for (int i = 0; i < N; ++i) {
+            const int at = i * 128 + tid;
             uint4 lo, hi;
             pre_expand(in[i], lo, hi);
-            uint8_t *row = kt + (j >> 2) * (P * 128) + t * 128;
-            // blocks lie a multiple of 1024 bytes apart: the second one's lanes store their second piece first
-            const bool swap = j >> 2;
-            *reinterpret_cast<uint4 *>(row + (((c + (swap ? 1 : 0)) ^ (t & 7)) << 4)) = swap ? hi : lo;
-            *reinterpret_cast<uint4 *>(row + (((c + (swap ? 0 : 1)) ^ (t & 7)) << 4)) = swap ? lo : hi;
+            if constexpr (VALUES) {  // dim d, tokens 16 j ..
+                const int d = at / (P / 16), j = at % (P / 16), sw = P == 64 ? d & 7 : (d >> 1) & 3;
+                uint8_t *row = tile + d * (P * 2);
+                *reinterpret_cast<uint4 *>(row + (((2 * j) ^ sw) << 4)) = lo;
+                *reinterpret_cast<uint4 *>(row + (((2 * j + 1) ^ sw) << 4)) = hi;
+            } else {  // token t, dims 16 j ..: block j / 4, pieces 2 (j % 4) and the next of its 128-byte row
+                const int t = at / (D / 16), j = at % (D / 16), c = 2 * (j & 3);
+                uint8_t *row = tile + (j >> 2) * (P * 128) + t * 128;
+                // blocks lie a multiple of 1024 bytes apart: the second one's lanes store their second piece first
+                const int other = j >> 2;
+                *reinterpret_cast<uint4 *>(row + (((c + other) ^ (t & 7)) << 4)) = other ? hi : lo;
+                *reinterpret_cast<uint4 *>(row + (((c + 1 - other) ^ (t & 7)) << 4)) = other ? lo : hi;
+            }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s.k_full[x]);
-        read(raw + PAGE);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.empty[slot]);
-        if (!pre_wait_warp(p, s, &s.v_empty[x], ph ^ 1)) return;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {  // dim d, tokens 16 j ..
-            const int at = i * 128 + tid, d = at / (P / 16), j = at % (P / 16);
-            uint4 lo, hi;
-            pre_expand(in[i], lo, hi);
-            uint8_t *row = vt + d * (P * 2);
-            const int sw = P == 64 ? d & 7 : (d >> 1) & 3;
-            *reinterpret_cast<uint4 *>(row + (((2 * j) ^ sw) << 4)) = lo;
-            *reinterpret_cast<uint4 *>(row + (((2 * j + 1) ^ sw) << 4)) = hi;
+        if (lane == 0) {
+            mbar_arrive(&ready[x]);
+            mbar_arrive(&s.empty[slot]);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.v_full[x]);
         if (++slot == p.pre_ring) {
             slot = 0;
             ++round;
@@ -364,11 +370,12 @@ DEV void pre_convert(const AttParams &p, const PreShared &s) {
     }
 }
 
-// ---- the thread that issues the products
+// ---- the products, issued by one elected thread of a warp
 template <int D, int P>
 DEV void pre_products(const AttParams &p, const PreShared &s, uint32_t tmem) {
     constexpr int PAGE = P * D;
-    const uint32_t tiles = saddr(s.tiles);
+    if (!pre_elect()) return;
+    const uint64_t k_tile = pre_desc<true>(saddr(s.tiles)), v_tile = pre_desc<P == 64>(saddr(s.tiles) + 2 * PAGE);
     PreWalk walk(p, s);
     PreSeg g;
     int n = 0;  // pages done
@@ -376,41 +383,33 @@ DEV void pre_products(const AttParams &p, const PreShared &s, uint32_t tmem) {
     bool ok = true;
     const auto scores = [&](int k) {
         const int x = k & 1;
-        const uint32_t ph = (k >> 1) & 1;
-        ok = ok && pre_wait(p, s, &s.k_full[x], ph) && pre_wait(p, s, &s.s_empty[x], ph ^ 1);
+        ok = ok && pre_wait(p, s, &s.s_ready[x], (k >> 1) & 1);
         if (!ok) return;
         pre_fence_after();
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-            pre_mma(tmem + PRE_S + x * 64, tmem + PRE_Q + i * 8,
-                    pre_desc<true>(tiles + x * 4 * PAGE + (i / 4) * (P * 128) + (i % 4) * 32), pre_idesc(P), i > 0);
-        pre_commit(&s.s_full[x]);
-        pre_commit(&s.k_empty[x]);
+        for (int i = 0; i < D / 16; ++i)  // (descriptors count 16 bytes)
+            pre_mma(tmem + PRE_S + x * 64, tmem + PRE_Q + i * 8, k_tile + (x * 4 * PAGE + (i / 4) * (P * 128) + (i % 4) * 32) / 16,
+                    pre_idesc(P), i > 0);
+        pre_commit(&s.s_done[x]);
     };
-    const auto outputs = [&](int k) {
+    const auto outputs = [&](int k, bool first) {
         const int x = k & 1;
-        const uint32_t ph = (k >> 1) & 1;
-        ok = ok && pre_wait(p, s, &s.p_full[x], ph) && pre_wait(p, s, &s.v_full[x], ph) && pre_wait(p, s, &s.o_empty[x], ph ^ 1);
+        ok = ok && pre_wait(p, s, &s.o_ready[x], (k >> 1) & 1);
         if (!ok) return;
         pre_fence_after();
 #pragma unroll
         for (int i = 0; i < P / 16; ++i)
-            pre_mma(tmem + PRE_O + x * 128, tmem + PRE_P + x * 32 + i * 8,
-                    pre_desc<P == 64>(tiles + x * 4 * PAGE + 2 * PAGE + i * 32), pre_idesc(D), i > 0);
-        pre_commit(&s.o_full[x]);
-        pre_commit(&s.v_empty[x]);
+            pre_mma(tmem + PRE_O + x * 128, tmem + PRE_P + x * 32 + i * 8, v_tile + (x * 4 * PAGE + i * 32) / 16, pre_idesc(D),
+                    i > 0 || !first);
+        pre_commit(&s.o_done[x]);
     };
     for (; ok && walk.next(g); ++seg) {
         ok = pre_wait(p, s, s.q_full, seg & 1);
-        if (!ok) break;
-        scores(n);
-        if (g.n == 1 && ok) pre_commit(s.q_empty);
-        for (int i = 0; i < g.n && ok; ++i) {
-            if (i + 1 < g.n) {
-                scores(n + i + 1);
-                if (i + 2 == g.n && ok) pre_commit(s.q_empty);
-            }
-            outputs(n + i);
+        // scores two pages ahead: a stream's next ones are there when its softmax is done
+        for (int i = 0; i < g.n + 2 && ok; ++i) {
+            if (i < g.n) scores(n + i);
+            if (i + 1 == g.n && ok) pre_commit(s.q_empty);
+            if (i > 1) outputs(n + i - 2, i < 4);
         }
         n += g.n;
     }
@@ -421,10 +420,17 @@ DEV void pre_products(const AttParams &p, const PreShared &s, uint32_t tmem) {
 }
 
 // ---- softmax warps
-// One page's scores to probabilities: this thread's row, CN tokens from column c0 on.
-template <int CN>
-DEV void pre_softmax(uint32_t s_addr, uint32_t p_addr, float fk, float &m, float &l, float &alpha) {
-    constexpr int W = CN < 16 ? CN : 16;
+// A row's state: the reference, the sum relative to it (and without the first
+// page's V scale, 2^base).
+struct PreRow {
+    float ref, sum, base;
+};
+// One page's scores to probabilities: this thread's row, CN tokens.  `taken` is
+// called when the scores are read, `settle` before P is written, with what O has
+// to be multiplied by (1: nothing).
+template <int CN, typename Taken, typename Settle>
+DEV void pre_softmax(uint32_t s_addr, uint32_t p_addr, float fk, float lv, PreRow &w, const Taken &taken, const Settle &settle) {
+    constexpr int W = CN < 32 ? CN : 32;  // scores in registers at a time
     uint32_t r[W];
     float mx = -INFINITY;
 #pragma unroll
@@ -434,15 +440,24 @@ DEV void pre_softmax(uint32_t s_addr, uint32_t p_addr, float fk, float &m, float
 #pragma unroll
         for (int i = 0; i < W; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
     }
-    const float mn = fmaxf(m, mx * fk), mu = mn == -INFINITY ? 0.f : mn, off = 14.f - mu;
-    alpha = exp2_fast(m - mu);
-    m = mn;
+    // scales so far apart that P may be 0 where the sum is not: the sum's terms by themselves
+    const bool apart = !(fabsf(lv - w.base) <= 60.f);
+    if (CN == W && !apart) taken();
+    const float to = mx * fk + (lv == lv ? lv : w.base);  // a NaN scale makes outputs NaN, not the sum
+    float back = 1.f;
+    if (!(to <= w.ref + 8.f)) {  // (the first page; a NaN score leaves the reference)
+        back = to > w.ref ? exp2_fast(w.ref - to) : 1.f;
+        w.ref = to > w.ref ? to : w.ref;
+        w.sum *= back;
+    }
+    const float at = w.ref == -INFINITY ? 0.f : w.ref, off = lv + 7.f - at;
     float sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < CN; c += W) {
-        if (CN > W) {
+    for (int c = CN - W; c >= 0; c -= W) {  // the last part is in registers
+        if (c < CN - W) {
             pre_ld(s_addr + c, r);
             pre_wait_ld();
+            if (c == 0 && !apart) taken();
         }
         uint32_t h[W / 2];
 #pragma unroll
@@ -451,9 +466,25 @@ DEV void pre_softmax(uint32_t s_addr, uint32_t p_addr, float fk, float &m, float
             sum += a + b;
             h[i / 2] = half2_of(a, b);
         }
+        if (c == CN - W) settle(back);
         pre_st(p_addr + c / 2, h);
     }
-    l = fmaf(l, alpha, sum);
+    if (!apart) {
+        w.sum = fmaf(sum, exp2_fast(w.base - lv), w.sum);
+    } else {
+        sum = 0.f;
+        const float alone = w.base + 7.f - at;
+#pragma unroll 1
+        for (int c = 0; c < CN; c += 8) {
+            uint32_t t[8];
+            pre_ld(s_addr + c, t);
+            pre_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += exp2_fast(fmaf(__uint_as_float(t[i]), fk, alone));
+        }
+        w.sum += sum;
+        taken();
+    }
 }
 
 DEV void pre_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -468,33 +499,54 @@ DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
     int n = 0;  // pages before the segment
     uint32_t seg = 0;
     bool ok = true;  // a warp that gives up still takes its place at the barriers
+    if (lane == 0) mbar_arrive(&s.s_ready[x]);  // no scores before the first
     for (; walk.next(g); ++seg, n += g.n) {
         const int copies = g.copies(), each = PRE_ROWS / copies, copy = tid / each, rows = g.tile_rows();
-        if (x == 0) {  // the segment's queries
-            const int r = g.tile * PRE_ROWS + tid % each;
-            uint4 q[D / 8];
-            uint32_t big = 0;
-            const uint16_t *row = nullptr;
-            if (tid % each < rows) {
-                const int tok = r / p.group;
-                row = p.q + (int64_t)(g.q0 + tok) * p.qs_t + (int64_t)(g.h * p.group + r - tok * p.group) * p.qs_h;
+        if (x == 0) {  // the segment's queries: row by row to shared memory, then a row per lane
+            constexpr int LINE = D * 2 + 16;
+            uint8_t *stage = reinterpret_cast<uint8_t *>(s.merge) + warp * 32 * LINE;
+            const int row0 = g.tile * PRE_ROWS + (warp * 32) % each, there = rows - (warp * 32) % each;
+            constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;  // lanes to a row of 16-byte pieces
+            constexpr int BATCH = 8;
+#pragma unroll
+            for (int i = 0; i < 32; i += AT_ONCE * BATCH) {
+                uint4 q[BATCH];
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {  // (rows behind the last: it again, then zeros)
+                    const int r = row0 + max(0, min(i + k * AT_ONCE + lane / LANES, there - 1)), tok = r / p.group;
+                    q[k] = make_uint4(0, 0, 0, 0);
+                    if (there > 0)
+                        q[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)(g.q0 + tok) * p.qs_t + (int64_t)(g.h * p.group + r - tok * p.group) * p.qs_h) + lane % LANES);
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int mine = i + k * AT_ONCE + lane / LANES;
+                    *reinterpret_cast<uint4 *>(stage + mine * LINE + lane % LANES * 16) = mine < there ? q[k] : make_uint4(0, 0, 0, 0);
+                }
             }
+            __syncwarp();
+            const uint4 *row = reinterpret_cast<const uint4 *>(stage + lane * LINE);
+            uint32_t big = 0;
+            const auto most = [&](uint32_t w) { big = max(big, max((w << 16) & 0x7fffffffu, w & 0x7fff0000u)); };
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) q[i] = row ? __ldg(reinterpret_cast<const uint4 *>(row) + i) : make_uint4(0, 0, 0, 0);
-            const auto word = [&](int i) { return i % 4 == 0 ? q[i / 4].x : i % 4 == 1 ? q[i / 4].y : i % 4 == 2 ? q[i / 4].z : q[i / 4].w; };
-#pragma unroll
-            for (int i = 0; i < D / 2; ++i) big = max(big, max((word(i) << 16) & 0x7fffffffu, word(i) & 0x7fff0000u));
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 q = row[i];
+                most(q.x), most(q.y), most(q.z), most(q.w);
+            }
             // times 2^(14 - exponent): the row's largest value lands in [2^14, 2^15)
             const int up = min(max(268 - (int)(big >> 23), 1), 253);
             const float sc = __uint_as_float((uint32_t)up << 23);
+            const auto pair = [&](uint32_t w) { return half2_of(__uint_as_float(w << 16) * sc, __uint_as_float(w & 0xffff0000u) * sc); };
             if (seg > 0 && ok) ok = pre_wait_warp(p, s, s.q_empty, (seg - 1) & 1);
             pre_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 2; c += 16) {
                 uint32_t h[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    h[i] = half2_of(__uint_as_float(word(c + i) << 16) * sc, __uint_as_float(word(c + i) & 0xffff0000u) * sc);
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 q = row[c / 4 + i];
+                    h[4 * i] = pair(q.x), h[4 * i + 1] = pair(q.y), h[4 * i + 2] = pair(q.z), h[4 * i + 3] = pair(q.w);
+                }
                 pre_st(lanes + PRE_Q + c, h);
             }
             s.qf[tid] = big >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(254 - up) << 23);
@@ -511,43 +563,43 @@ DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
         }
         if (ok) ok = pre_wait_warp(p, s, s.q_full, seg & 1);
         const float qf = s.qf[tid] * p.scale_log2;
-        float m = -INFINITY, l = 0.f, o[D], later_alpha = 1.f, later_scale = 0.f;
-#pragma unroll
-        for (int i = 0; i < D; ++i) o[i] = 0.f;
-        // a page's output: added while the next one's is on its way
-        const auto add = [&](int k) {
-            ok = pre_wait_warp(p, s, &s.o_full[x], (k >> 1) & 1);
-            if (!ok) return;
+        PreRow w{-INFINITY, 0.f, 0.f};
+        int last = -1;  // the stream's page before
+        const auto taken = [&] {  // the scores' columns may be written again
+            pre_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.s_ready[x]);
+        };
+        // P's and O's earlier product is done; O relative to a new reference
+        const auto settle = [&](float back) {
+            if (last < 0) return;
+            ok = pre_wait_warp(p, s, &s.o_done[x], (last >> 1) & 1);
+            if (!ok || __all_sync(FULL, back == 1.f)) return;
             pre_fence_after();
-            if (!__all_sync(FULL, later_alpha == 1.f)) {
-#pragma unroll
-                for (int i = 0; i < D; ++i) o[i] *= later_alpha;
-            }
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
                 uint32_t r[16];
                 pre_ld(o_addr + c, r);
                 pre_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[c + i] = fmaf(__uint_as_float(r[i]), later_scale, o[c + i]);
+                for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * back);
+                pre_st(o_addr + c, r);
             }
-            pre_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.o_empty[x]);
         };
-        int last = -1;
         for (int k = n + ((n ^ x) & 1); k < n + g.n && ok; k += 2) {
-            ok = pre_wait_warp(p, s, &s.s_full[x], (k >> 1) & 1);
+            ok = pre_wait_warp(p, s, &s.s_done[x], (k >> 1) & 1);
             if (!ok) break;
             pre_fence_after();
             const float2 sc = s.scale[k & 3];
-            float alpha = 1.f;
             if (sc.x >= 0.f || sc.x != sc.x) {
                 const float fk = qf * sc.x;
-                if (copies == 1) pre_softmax<P>(s_addr, p_addr, fk, m, l, alpha);
-                else if (copies == 2) pre_softmax<P / 2>(s_addr + copy * (P / 2), p_addr + copy * (P / 4), fk, m, l, alpha);
-                else pre_softmax<P / 4>(s_addr + copy * (P / 4), p_addr + copy * (P / 8), fk, m, l, alpha);
+                if (w.ref == -INFINITY && w.sum == 0.f) w.base = sc.y == sc.y ? sc.y : 0.f;
+                if (copies == 1) pre_softmax<P>(s_addr, p_addr, fk, sc.y, w, taken, settle);
+                else if (copies == 2) pre_softmax<P / 2>(s_addr + copy * (P / 2), p_addr + copy * (P / 4), fk, sc.y, w, taken, settle);
+                else pre_softmax<P / 4>(s_addr + copy * (P / 4), p_addr + copy * (P / 8), fk, sc.y, w, taken, settle);
             } else {  // a page that is not loaded: as if its tokens were masked
+                taken();
+                settle(1.f);
                 const uint32_t zero[16] = {};
 #pragma unroll
                 for (int c = 0; c < P / 2; c += 16) pre_st(p_addr + c, zero);
@@ -555,51 +607,60 @@ DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
             pre_wait_st();
             pre_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&s.s_empty[x]);
-                mbar_arrive(&s.p_full[x]);
-            }
-            if (last >= 0) add(last);
+            if (lane == 0) mbar_arrive(&s.o_ready[x]);
             last = k;
-            later_alpha = alpha;
-            later_scale = sc.y;
         }
-        if (last >= 0 && ok) add(last);
+        if (last >= 0 && ok) ok = pre_wait_warp(p, s, &s.o_done[x], (last >> 1) & 1);
+        pre_fence_after();
+        // as attend.cu has them: the sum of 2^(s - m + 14), outputs relative to m
+        const float m = w.ref == -INFINITY ? -INFINITY : w.ref - w.base + 7.f, l = w.sum;
+        const float unscale = last >= 0 ? exp2_fast(w.base - 14.f) : 0.f;
 
         // join the copies of both streams, 32 dims at a time
+        constexpr int LD = 36;
         *reinterpret_cast<float2 *>(s.ml + threadIdx.x * 2) = make_float2(m, l);
         pre_bar();
         const int parts = 2 * copies;  // row r of the tile: threads r + i * each
         float big = -INFINITY;
         for (int i = 0; i < parts; ++i) big = fmaxf(big, s.ml[(tid % each + i * each) * 2]);
-        const float a = exp2_fast(m - (big == -INFINITY ? 0.f : big));
-        const size_t slot = ((size_t)blockIdx.x * 2 + (g.head ? 1 : 0)) * PRE_ROWS;
-        const auto at_row = [&](int r) {
-            const int rr = g.tile * PRE_ROWS + r;
-            return (((size_t)p.tokens + g.q0 + rr / p.group) * p.c.hkv + g.h) * p.group + rr % p.group;
-        };
+        const float part = last >= 0 ? exp2_fast(m - (big == -INFINITY ? 0.f : big)) * unscale : 0.f;
         if (threadIdx.x < rows) {  // (rows <= each: this thread's row is threadIdx.x)
             float sum = 0.f;
             for (int i = 0; i < parts; ++i) {
                 const float2 y = *reinterpret_cast<const float2 *>(s.ml + (threadIdx.x + i * each) * 2);
                 sum = fmaf(y.y, exp2_fast(y.x - (big == -INFINITY ? 0.f : big)), sum);
             }
-            float *to = g.whole ? p.row_ml + at_row(threadIdx.x) * 2 : p.pre_ml + (slot + threadIdx.x) * 2;
-            *reinterpret_cast<float2 *>(to) = make_float2(big, sum);
+            const int rr = g.tile * PRE_ROWS + threadIdx.x, tok = rr / p.group;
+            const size_t to = g.whole ? (((size_t)p.tokens + g.q0 + tok) * p.c.hkv + g.h) * p.group + rr - tok * p.group
+                                      : ((size_t)blockIdx.x * 2 + (g.head ? 1 : 0)) * PRE_ROWS + threadIdx.x;
+            *reinterpret_cast<float2 *>((g.whole ? p.row_ml : p.pre_ml) + to * 2) = make_float2(big, sum);
+            s.to[threadIdx.x] = (g.whole ? p.row_o : p.pre_o) + to * D;
         }
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
+            uint32_t r[32];
+            pre_ld(o_addr + c, r);
+            pre_wait_ld();
+            float4 *mine = reinterpret_cast<float4 *>(s.merge + threadIdx.x * LD);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s.merge[threadIdx.x * 33 + i] = o[c + i] * a;
+            for (int i = 0; i < 8; ++i) {
+                const auto o = [&](int j) { return last >= 0 ? __uint_as_float(r[4 * i + j]) * part : 0.f; };
+                mine[i] = make_float4(o(0), o(1), o(2), o(3));
+            }
             pre_bar();
-            for (int e = threadIdx.x; e < rows * 32; e += 256) {
-                const int r = e / 32, d = e % 32;
-                float sum = 0.f;
-                for (int i = 0; i < parts; ++i) sum += s.merge[(r + i * each) * 33 + d];
-                (g.whole ? p.row_o + at_row(r) * D : p.pre_o + (slot + r) * D)[c + d] = sum;
+            for (int e = threadIdx.x; e < rows * 8; e += 256) {
+                const float *from = s.merge + (e / 8) * LD + e % 8 * 4;
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int i = 0; i < parts; ++i) {
+                    const float4 y = *reinterpret_cast<const float4 *>(from + i * each * LD);
+                    sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+                }
+                *reinterpret_cast<float4 *>(s.to[e / 8] + c + e % 8 * 4) = sum;
             }
             pre_bar();
         }
+        pre_fence_before();
     }
 }
 
@@ -607,7 +668,7 @@ template <int D, int P>
 __global__ void __launch_bounds__(PRE_THREADS, 1) cache_prefix_kernel(const AttParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
     const PreShared s = pre_shared<D, P>(p);
-    const int tid = threadIdx.x, warp = tid / 32;
+    const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid / 32, 0);
     att_groups<P>(p, s.groups, blockIdx.x == 0);
     for (int g = tid; g < p.ngroups; g += PRE_THREADS) {
         const AttSeq q = att_unit<P, true>(p, s.groups, g, false);
@@ -616,19 +677,14 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) cache_prefix_kernel(const AttP
     }
     if (tid < p.pre_ring) {
         mbar_init(&s.full[tid], 1);
-        mbar_init(&s.empty[tid], 4);
+        mbar_init(&s.empty[tid], 8);
     }
     if (tid == 64) {
         for (int x = 0; x < 2; ++x) {
-            mbar_init(&s.k_full[x], 4);
-            mbar_init(&s.v_full[x], 4);
-            mbar_init(&s.k_empty[x], 1);
-            mbar_init(&s.v_empty[x], 1);
-            mbar_init(&s.s_full[x], 1);
-            mbar_init(&s.s_empty[x], 4);
-            mbar_init(&s.p_full[x], 4);
-            mbar_init(&s.o_full[x], 1);
-            mbar_init(&s.o_empty[x], 4);
+            mbar_init(&s.s_ready[x], 8);
+            mbar_init(&s.s_done[x], 1);
+            mbar_init(&s.o_ready[x], 8);
+            mbar_init(&s.o_done[x], 1);
         }
         mbar_init(s.q_full, 4);
         mbar_init(s.q_empty, 1);
@@ -636,7 +692,7 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) cache_prefix_kernel(const AttP
         s.ctrl[0] = 0;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (warp == 13) {
+    if (warp == PRE_ISSUER) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&s.ctrl[1])) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         pre_fence_before();
@@ -644,25 +700,22 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) cache_prefix_kernel(const AttP
     att_running(s.prefix, p.ngroups);
     pre_fence_after();
     const uint32_t tmem = (uint32_t)s.ctrl[1];
-    // registers: 4 x 128 threads were launched with 128 each; 2 x 184 + 2 x 72
-    if (tid < 256) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        if ((saddr(s.tiles) & 1023) == 0) pre_rows<D, P>(p, s, tmem);
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if ((saddr(s.tiles) & 1023) != 0) {
-            if (tid == 256) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, -1, -2, -1);
-        } else if (tid < 384) {
-            pre_convert<D, P>(p, s);
-        } else if (warp == 12) {
-            pre_produce<D, P>(p, s);
-        } else if (tid == 13 * 32) {
-            pre_products<D, P>(p, s, tmem);
-        }
+    if ((saddr(s.tiles) & 1023) != 0) {
+        if (tid == 0) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, -1, -2, -1);
+    } else if (warp < 8) {
+        pre_rows<D, P>(p, s, tmem);
+    } else if (warp < 12) {
+        pre_convert<D, P, false>(p, s);
+    } else if (warp < 16) {
+        pre_convert<D, P, true>(p, s);
+    } else if (warp == 16) {
+        pre_produce<D, P>(p, s);
+    } else if (warp == PRE_ISSUER) {
+        pre_products<D, P>(p, s, tmem);
     }
     __syncwarp();
     __syncthreads();
-    if (warp == 13) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    if (warp == PRE_ISSUER) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 int prefix_launch(const mk_cache_desc *cache, AttParams &p, cudaStream_t stream) {
