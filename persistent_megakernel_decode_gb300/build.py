@@ -16,12 +16,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIB_DIR, "libmk.so")
-SOURCES = ["interp.cu", "api.cpp", "planner.cpp", "cache.cu", "attend.cu", "prefix.cu", "sample.cu", "beam.cu", "pages.cpp"]
+SOURCES = ["interp.cu", "api.cpp", "planner.cpp", "cache.cu", "attend.cu", "shared.cu", "prefix.cu", "sample.cu",
+           "beam.cu", "pages.cpp"]
 HEADERS = ["mk_internal.h", "planner.h", "dev_common.cuh", "dev_ops.cuh", "dev_glm.cuh", "dev_tc.cuh", "dev_glm_tc.cuh",
-           "dev_serve.cuh", "dev_weigh.cuh", "dev_attend.cuh"]
+           "dev_serve.cuh", "dev_weigh.cuh", "dev_attend.cuh", "dev_attend_pages.cuh"]
 # the operators beside the interpreter: no file of its kernel or planner includes them
-SERVING = ["cache.cu", "attend.cu", "prefix.cu", "sample.cu", "beam.cu", "pages.cpp", "dev_serve.cuh", "dev_weigh.cuh",
-           "dev_attend.cuh"]
+SERVING = ["cache.cu", "attend.cu", "shared.cu", "prefix.cu", "sample.cu", "beam.cu", "pages.cpp", "dev_serve.cuh",
+           "dev_weigh.cuh", "dev_attend.cuh", "dev_attend_pages.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -27,9 +27,10 @@ struct AttParams {
     const int *groups, *shared;
     int ngroups;
     float *row_ml, *row_o;
-    // the groups' parts by tiles of 128 rows in a launch of their own (0 CTAs:
-    // none): its ring, and what its CTAs cut, like part_ml and part_o
-    int pre_ctas, pre_ring;
+    // The groups' pages are a launch of their own, on part of `sms` SMs: rows of
+    // its tiles (PRE_ROWS: prefix.cu's, else attend.cu's) and of the other one's,
+    // and what its CTAs cut, like part_ml and part_o.
+    int sms, pre_rt, rt;
     float *pre_ml, *pre_o;
 };
 
@@ -161,27 +162,30 @@ DEV void att_groups(const AttParams &p, const AttGroups &s, bool report) {
     }
     __syncthreads();
 }
-DEV int att_units(const AttParams &p, bool sh) { return sh ? p.ngroups + p.batch : p.batch; }
-// Unit v: a sequence, or with shared prefixes a group's rows over its pages
-// (every row sees all of them), or a sequence's rows over the pages behind.
-template <int P, bool SH>
+// What a launch is for: sequences by themselves; with shared prefixes, sequences
+// over the pages behind them; groups over the shared pages.
+enum AttKind { ATT_PLAIN, ATT_OWN, ATT_GROUPS };
+DEV int att_units(const AttParams &p, AttKind kind) { return kind == ATT_GROUPS ? p.ngroups : p.batch; }
+// Unit v: a sequence, or a group's rows over its pages (every row sees all).
+template <int P, AttKind KIND>
 DEV AttSeq att_unit(const AttParams &p, const AttGroups &s, int v, bool report) {
-    if constexpr (!SH) return att_seq<P>(p, v, report);
-    if (v >= p.ngroups) {
-        const int b = v - p.ngroups;
-        AttSeq q = att_seq<P>(p, b, report);
-        const int g = att_group_of(p, s, b);
+    if constexpr (KIND == ATT_PLAIN) {
+        return att_seq<P>(p, v, report);
+    } else if constexpr (KIND == ATT_OWN) {
+        AttSeq q = att_seq<P>(p, v, report);
+        const int g = att_group_of(p, s, v);
         q.gap = g < 0 ? 0 : min(s.lim[g], q.hi);
         return q;
+    } else {
+        AttSeq q{0, 0, 0, 0, 0, false};
+        if (s.lim[v] > 0 && s.lead[v] < p.batch) {
+            q.q0 = p.q_start ? p.q_start[s.grp[v]] : s.grp[v] * p.max_tokens;
+            q.cnt = (p.q_start ? p.q_start[s.grp[v + 1]] : s.grp[v + 1] * p.max_tokens) - q.q0;
+            q.hi = s.lim[v];
+            q.len = q.hi * P;
+        }
+        return q;
     }
-    AttSeq q{0, 0, 0, 0, 0, false};
-    if (s.lim[v] > 0 && s.lead[v] < p.batch) {
-        q.q0 = p.q_start ? p.q_start[s.grp[v]] : s.grp[v] * p.max_tokens;
-        q.cnt = (p.q_start ? p.q_start[s.grp[v + 1]] : s.grp[v + 1] * p.max_tokens) - q.q0;
-        q.hi = s.lim[v];
-        q.len = q.hi * P;
-    }
-    return q;
 }
 
 // Shared pages in a launch of their own (prefix.cu): tiles of 128 rows, and what
@@ -192,6 +196,63 @@ DEV long long pre_items(const AttParams &p, int cnt, int np) {
 }
 DEV int pre_used(long long total, int ctas) { return (int)max(1ll, min((long long)ctas, total)); }
 
+
+// Warps side by side on a tile of so many rows (tiles of rt rows, 8 or 16 a warp): 1, 2 or 4.
+__host__ __device__ constexpr int att_side_of(int rt, int rows) {
+    const int per = rt == 8 ? 8 : 16, need = ((rt < rows ? rt : rows) + per - 1) / per;
+    return need <= 1 ? 1 : need == 2 ? 2 : 4;
+}
+// What beginning and merging a unit costs a CTA, in items.  By the clock 4 to 5
+// thousand clocks, at 375 to 700 an item, with one tile a warp; 10 thousand, at
+// 525, with two.  Measured over six sets of lengths, 8 sequences of the 1B
+// shape / 13 with up to 9 drafted tokens: none 15.8 / 41 us, 4 and 8 items
+// 14.3 / 30, 12 and 24 13.3 / 26.6, 16 and 40 12.7 / 27.3.
+__host__ __device__ constexpr int att_fixed_items(int rt) { return rt == 8 ? 12 : 24; }
+// Work items of a sequence: of each unit the fixed ones, then its pages', each
+// as many as its tile has warps side by side.  All tiles but the last are full.
+DEV long long att_items_of(const AttParams &p, int rt, int cnt, int np) {
+    const int rows = cnt * p.group, tiles = (rows + rt - 1) / rt, fixed = att_fixed_items(rt);
+    if (tiles == 0 || np <= 0) return 0;
+    return p.c.hkv * ((tiles - 1) * ((long long)np * att_side_of(rt, rt) + fixed) +
+                      (long long)np * att_side_of(rt, rows - (tiles - 1) * rt) + fixed);
+}
+
+// Work items of a group.
+DEV long long att_group_items(const AttParams &p, int cnt, int np) {
+    return p.pre_rt == PRE_ROWS ? pre_items(p, cnt, np) : att_items_of(p, p.pre_rt, cnt, np);
+}
+// Both launches run beside each other, on SMs shared out by their work: the CTAs
+// of the groups' one.  A page through prefix.cu's tiles (0.9 us) takes about as
+// long as two items of attend.cu's.
+DEV int att_share(const AttParams &p, long long groups, long long own) {
+    if (groups == 0) return 0;
+    if (own == 0) return p.sms;
+    const long long a = groups * (p.pre_rt == PRE_ROWS ? 2 : 1), n = (a * p.sms + (a + own) / 2) / (a + own);
+    return (int)min((long long)p.sms - 1, max(1ll, n));
+}
+// Sum of v over the block, in *to (zeroed before a barrier; read after one).
+DEV void att_total(long long v, unsigned long long *to) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    if (threadIdx.x % 32 == 0 && v) atomicAdd(to, (unsigned long long)v);
+}
+// The other launch's items, summed over the block.
+template <int P, AttKind KIND>
+DEV void att_others(const AttParams &p, const AttGroups &s, unsigned long long *to) {
+    long long v = 0;
+    if constexpr (KIND == ATT_GROUPS) {
+        for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
+            const AttSeq q = att_unit<P, ATT_OWN>(p, s, b, false);
+            v += att_items_of(p, p.rt, q.cnt, q.hi - q.gap);
+        }
+    } else {
+        for (int g = threadIdx.x; g < p.ngroups; g += blockDim.x) {
+            const AttSeq q = att_unit<P, ATT_GROUPS>(p, s, g, false);
+            v += att_group_items(p, q.cnt, q.hi);
+        }
+    }
+    att_total(v, to);
+}
 
 // Work item x belongs to the last sequence b with prefix[b] <= x that has any.
 DEV int att_find(const long long *prefix, int batch, long long x) {

@@ -60,14 +60,15 @@ struct PreShared {
     // its product is.
     uint64_t *s_ready, *s_done, *o_ready, *o_done;
     uint64_t *q_full, *q_empty, *drain;
-    int *ctrl;          // [0] abort, [1] tensor memory address
+    int *ctrl;          // [0] abort, [1] tensor memory address, [2] CTAs that share the work
+    unsigned long long *total;  // items of the launch beside this one
     uint8_t *tiles;     // [2][K f16, V f16]
     uint8_t *ring;      // [ring][K page, V page]
 };
 
 __host__ __device__ constexpr int pre_fixed_bytes(int ngroups) {
     return (ngroups + 1) * 8 + ngroups * 16 + att_group_bytes(ngroups) + PRE_MAXRING * 8 + 4 * 8 + 128 * 4 + 128 * 8 + 256 * 8 +
-           256 * 36 * 4 + (2 * PRE_MAXRING + 4 * 2 + 3) * 8 + 8 + 64;
+           256 * 36 * 4 + (2 * PRE_MAXRING + 4 * 2 + 3) * 8 + 24 + 64;
 }
 
 template <int D, int P>
@@ -80,7 +81,7 @@ DEV PreShared pre_shared(const AttParams &p) {
         return x;
     };
     s.tiles = take(4 * P * D * 2);  // at 1024-byte boundaries: the dynamic shared memory starts at one (checked)
-    s.ring = take((size_t)p.pre_ring * 2 * P * D);
+    s.ring = take((size_t)p.ring * 2 * P * D);
     s.merge = reinterpret_cast<float *>(take(256 * 36 * 4));
     s.ml = reinterpret_cast<float *>(take(256 * 8));
     s.qf = reinterpret_cast<float *>(take(128 * 4));
@@ -98,7 +99,8 @@ DEV PreShared pre_shared(const AttParams &p) {
     s.q_empty = s.q_full + 1;
     s.drain = s.q_empty + 1;
     s.prefix = reinterpret_cast<long long *>(take((p.ngroups + 1) * 8));
-    s.ctrl = reinterpret_cast<int *>(take(8));
+    s.total = reinterpret_cast<unsigned long long *>(take(8));
+    s.ctrl = reinterpret_cast<int *>(take(16));
     s.groups = att_groups_at(at, p.ngroups);
     return s;
 }
@@ -205,7 +207,7 @@ struct PreWalk {
     int g;
     DEV PreWalk(const AttParams &p_, const PreShared &s_) : p(p_), s(s_) {
         const long long total = s.prefix[p.ngroups];
-        const int ctas = pre_used(total, p.pre_ctas);
+        const int ctas = pre_used(total, s.ctrl[2]);
         if ((int)blockIdx.x < ctas) {
             x = att_div((long long)blockIdx.x * total, ctas);
             end = att_div((long long)(blockIdx.x + 1) * total, ctas);
@@ -292,14 +294,14 @@ DEV void pre_produce(const AttParams &p, const PreShared &s) {
                 }
             }
             ok = __shfl_sync(FULL, ok, i);
-            if (ok && ++slot == p.pre_ring) {
+            if (ok && ++slot == p.ring) {
                 slot = 0;
                 ++round;
             }
         }
     }
     // the copies in flight land before the CTA ends, also where the warps that wanted them have given up
-    if (lane < p.pre_ring) {
+    if (lane < p.ring) {
         const uint32_t fills = round + (lane < slot ? 1 : 0);
         for (int i = 0; i < 200 && fills && !mbar_wait_hint(&s.full[lane], (fills - 1) & 1, 1000000); ++i) {
         }
@@ -363,7 +365,7 @@ DEV void pre_convert(const AttParams &p, const PreShared &s) {
             mbar_arrive(&ready[x]);
             mbar_arrive(&s.empty[slot]);
         }
-        if (++slot == p.pre_ring) {
+        if (++slot == p.ring) {
             slot = 0;
             ++round;
         }
@@ -507,7 +509,7 @@ DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
             uint8_t *stage = reinterpret_cast<uint8_t *>(s.merge) + warp * 32 * LINE;
             const int row0 = g.tile * PRE_ROWS + (warp * 32) % each, there = rows - (warp * 32) % each;
             constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;  // lanes to a row of 16-byte pieces
-            constexpr int BATCH = 8;
+            constexpr int BATCH = 32 / AT_ONCE;  // all at once: one round trip
 #pragma unroll
             for (int i = 0; i < 32; i += AT_ONCE * BATCH) {
                 uint4 q[BATCH];
@@ -669,13 +671,15 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) cache_prefix_kernel(const AttP
     asm volatile("griddepcontrol.launch_dependents;");
     const PreShared s = pre_shared<D, P>(p);
     const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid / 32, 0);
-    att_groups<P>(p, s.groups, blockIdx.x == 0);
+    if (tid == 0) *s.total = 0;
+    att_groups<P>(p, s.groups, false);
+    att_others<P, ATT_GROUPS>(p, s.groups, s.total);
     for (int g = tid; g < p.ngroups; g += PRE_THREADS) {
-        const AttSeq q = att_unit<P, true>(p, s.groups, g, false);
+        const AttSeq q = att_unit<P, ATT_GROUPS>(p, s.groups, g, false);
         s.unit[g] = make_int4(q.q0, q.cnt, q.hi, s.groups.lead[g]);
         s.prefix[g + 1] = pre_items(p, q.cnt, q.hi);
     }
-    if (tid < p.pre_ring) {
+    if (tid < p.ring) {
         mbar_init(&s.full[tid], 1);
         mbar_init(&s.empty[tid], 8);
     }
@@ -692,12 +696,16 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) cache_prefix_kernel(const AttP
         s.ctrl[0] = 0;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    att_running(s.prefix, p.ngroups);
+    const int ctas = att_share(p, s.prefix[p.ngroups], (long long)*s.total);
+    if ((int)blockIdx.x >= ctas) return;
+    if (tid == 0) s.ctrl[2] = ctas;
     if (warp == PRE_ISSUER) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&s.ctrl[1])) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         pre_fence_before();
     }
-    att_running(s.prefix, p.ngroups);
+    __syncthreads();
     pre_fence_after();
     const uint32_t tmem = (uint32_t)s.ctrl[1];
     if ((saddr(s.tiles) & 1023) != 0) {
@@ -721,13 +729,13 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) cache_prefix_kernel(const AttP
 int prefix_launch(const mk_cache_desc *cache, AttParams &p, cudaStream_t stream) {
     const int D = cache->head_dim, P = cache->page_tokens;
     const int fixed = pre_fixed_bytes(p.ngroups) + 4 * P * D * 2;
-    p.pre_ring = std::min(PRE_MAXRING, (SERVE_SMEM - fixed) / (2 * P * D));
-    const int smem = fixed + p.pre_ring * 2 * P * D;
+    p.ring = std::min(PRE_MAXRING, (SERVE_SMEM - fixed) / (2 * P * D));
+    const int smem = fixed + p.ring * 2 * P * D;
     void (*f)(const AttParams) = D == 64 ? (P == 32 ? cache_prefix_kernel<64, 32> : cache_prefix_kernel<64, 64>)
                                          : (P == 32 ? cache_prefix_kernel<128, 32> : cache_prefix_kernel<128, 64>);
     static std::atomic<uint32_t> ready[SERVE_MAX_DEVICES];
     if (int rc = serve_prepare(reinterpret_cast<const void *>(f), ready, (D == 128 ? 2 : 0) + (P == 64 ? 1 : 0), false)) return rc;
-    f<<<p.pre_ctas, PRE_THREADS, smem, stream>>>(p);
+    f<<<p.sms, PRE_THREADS, smem, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? MK_OK : serve_cuda_fail(e, "prefix attention launch");
 }
