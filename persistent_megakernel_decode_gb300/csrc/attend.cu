@@ -59,10 +59,15 @@ struct AttPlan {
 
 // Tiles of 8, 16, 32 or 64 rows: the least that takes so many.
 static int att_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
-// Rows of an average group and kv head from which prefix.cu's tiles are taken for its shared pages.
-#ifndef PRE_LEAST
-#define PRE_LEAST 96
-#endif
+// Rows of an average group and kv head from which prefix.cu's tiles are taken for
+// its shared pages.  64 sequences (256 rows) behind 16,000 tokens: 82 us, with
+// attend.cu's 120; 21 with drafted tokens in 3 groups (56 rows) 35 and 39; 4 x 8
+// beams (32 rows) 46 and 44.
+constexpr int PRE_LEAST = 48;
+// Pages of all sequences and kv heads, per SM, up to which nothing is shared: a
+// launch more costs as much as reading so few again.  4 beams of a prompt of 300
+// tokens (88 pages): 11 us, shared 16.
+constexpr int ALONE_PAGES = 4;
 
 // ngroups: 0 without shared prefixes
 static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, int ngroups, AttPlan &pl) {
@@ -88,14 +93,15 @@ static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, int ngroups
     pl.pre_rt = 0;
     if (ngroups) {
         const int64_t rows = ((int64_t)a->tokens + ngroups - 1) / ngroups * group;  // of an average group
-        pl.pre_rt = rows >= PRE_LEAST ? PRE_ROWS : att_tile(rows);
+        const bool alone = (int64_t)a->batch * a->table_width * c->kv_heads <= (int64_t)ALONE_PAGES * sms;
+        pl.pre_rt = alone ? 0 : rows >= PRE_LEAST ? PRE_ROWS : att_tile(rows);
         sms = std::max(sms, 2);  // both launches share them
     }
     pl.sms = sms;
     // no more CTAs than pages there can be (all tiles' together, each as many items as it has warps side by side)
     const int64_t side = pl.rt == 64 ? 4 : pl.rt == 32 ? 2 : 1;
     const int64_t tiles = a->batch + (int64_t)a->tokens * group / pl.rt;
-    pl.ctas = (int)std::min<int64_t>(sms, std::max<int64_t>(1, std::min<int64_t>(tiles * c->kv_heads, INT32_MAX) * (a->table_width * side + att_fixed_items(pl.rt))));
+    pl.ctas = (int)std::min<int64_t>(ngroups ? 2 * sms : sms, std::max<int64_t>(1, std::min<int64_t>(tiles * c->kv_heads, INT32_MAX) * (a->table_width * side + att_fixed_items(pl.rt))));
     pl.ml_bytes = ((uint64_t)pl.ctas * 2 * pl.rt * 8 + 255) / 256 * 256;
     pl.o_bytes = (uint64_t)pl.ctas * 2 * pl.rt * c->head_dim * 4;
     const uint64_t row_parts = ngroups ? 2ull * a->tokens * a->q_heads : 0;
@@ -109,8 +115,9 @@ static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, int ngroups
 // One launch of the kernel over `units` units, its tiles of rt rows.
 static int att_start(const mk_cache_desc *cache, AttParams &p, AttKind kind, int rt, int ctas, int units, bool after, cudaStream_t st) {
     const int D = cache->head_dim, P = cache->page_tokens;
-    const int fixed = att_fixed_bytes(D, att_nt(rt)) + att_seq_bytes(units, p.ngroups) + 128;
-    p.ring = std::min(ATT_MAXRING, (SERVE_SMEM - fixed) / (2 * P * D));
+    const int fixed = att_fixed_bytes(D, att_nt(rt), att_warps(kind)) + att_seq_bytes(units, p.ngroups) + 128;
+    const int smem = kind == ATT_OWN ? SERVE_SMEM / 2 - 512 : SERVE_SMEM;  // (a CTA takes 1024 bytes more)
+    p.ring = std::min(ATT_MAXRING, (smem - fixed) / (2 * P * D));
     p.ctas = ctas;
     const AttFn f = kind == ATT_PLAIN ? att_kernel_of<ATT_PLAIN>(D, P, rt) : att_shared_kernel(kind, D, P, rt);
     static std::atomic<uint32_t> ready[3][SERVE_MAX_DEVICES];
@@ -121,7 +128,7 @@ static int att_start(const mk_cache_desc *cache, AttParams &p, AttKind kind, int
     dep.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(ATT_THREADS);
+    cfg.blockDim = dim3(att_threads(kind));
     cfg.dynamicSmemBytes = fixed + p.ring * 2 * P * D;
     cfg.stream = st;
     cfg.attrs = &dep;
@@ -192,13 +199,13 @@ static int att_launch(const mk_cache_desc *cache, int layer, const mk_attend_des
         p.pre_o = reinterpret_cast<float *>(at + pl.pre_ml_bytes);
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (ngroups) {
+    if (pl.pre_rt) {
         const int rc = pl.pre_rt == PRE_ROWS ? prefix_launch(cache, p, st)
                                              : att_start(cache, p, ATT_GROUPS, pl.pre_rt, pl.sms, ngroups, false, st);
         if (rc) return rc;
     }
     // (with groups: on the SMs that their launch leaves)
-    if (int rc = att_start(cache, p, ngroups ? ATT_OWN : ATT_PLAIN, pl.rt, pl.ctas, p.batch, ngroups > 0, st)) return rc;
+    if (int rc = att_start(cache, p, ngroups ? ATT_OWN : ATT_PLAIN, pl.rt, pl.ctas, p.batch, pl.pre_rt > 0, st)) return rc;
     cudaLaunchAttribute dep{};
     dep.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     dep.val.programmaticStreamSerializationAllowed = 1;

@@ -424,8 +424,8 @@ __global__ void __launch_bounds__(COPY_THREADS) cache_copy_kernel(const __grid_c
 // parent's children one keeps that page (the parent itself, else the first) and
 // each other one takes the page of a beam without children, of which there are
 // exactly as many, and a copy of the tokens in it: nothing is allocated, and no
-// page is both read and written.  Bound by the copies' bytes.
-constexpr int REORDER_BEAMS = 64, REORDER_THREADS = 256;
+// page is both read and written.
+constexpr int REORDER_BEAMS = 64, REORDER_THREADS = 256, REORDER_CTAS = 2432;
 
 struct ReorderParams {
     CacheView c;
@@ -434,104 +434,120 @@ struct ReorderParams {
     int beams, width;
 };
 
-// CTA (row, 2 l + half): half 0 / 1 = K / V of layer l of the row's copy, if it
-// needs one; the last y row writes the table row.
+// CTA (row, y): of the row's parts y, y + gridDim.y, ...: part 2 l + half is the
+// copy, if it needs one, of K / V of layer l, the last one the table row.  Each
+// CTA finds out by itself which rows copy (masks of children, two dependent
+// loads), which is why it has several parts.  Measured: 64 beams in 36 layers of
+// the 8B shape 40 us, of which K takes 14 (4 pieces of a thread in flight; with 8
+// 47, a CTA a part 41); V's are pieces of 64-byte rows, whose 32-byte sectors the
+// tokens fill in part.
 template <int D, int P>
 __global__ void __launch_bounds__(REORDER_THREADS) cache_reorder_kernel(const ReorderParams p) {
-    __shared__ int s_parent[REORDER_BEAMS], s_extra[REORDER_BEAMS], s_free[REORDER_BEAMS];
-    __shared__ int s_bad;
-    const int tid = threadIdx.x, W = p.beams, row = blockIdx.x % W, l = blockIdx.y / 2;
+    __shared__ unsigned long long s_child[REORDER_BEAMS], s_extra, s_dead;
+    const int tid = threadIdx.x, W = p.beams, row = blockIdx.x % W;
     const int64_t row0 = blockIdx.x - row;
-    const bool names = l == p.c.layers, reports = names && row == 0;
+    const int parts = 2 * p.c.layers + 1;
+    const bool reports = row == 0 && (parts - 1) % gridDim.y == blockIdx.y;
     const int n = p.lens[row0];
-    if (tid == 0) s_bad = 0;
+    int parent = 0, wrong = 0;
+    if (tid < W) {
+        const int x = p.parents[row0 + tid], held = p.lens[row0 + tid];
+        wrong = x < -1 || x >= W || held != n || n < 0 || (int64_t)n > (int64_t)p.width * P;
+        if (wrong && reports) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, (int)(row0 + tid), held, -1);
+        parent = x == -1 ? tid : x;
+    }
+    if (tid < REORDER_BEAMS) s_child[tid] = 0;
+    if (tid == 0) s_extra = s_dead = 0;
+    const bool bad = __syncthreads_or(wrong);
+    const int t = bad ? 0 : n / P, part = bad ? 0 : n % P;
+    if (bad) parent = tid;  // each row stays as it is
+    if (tid < W) atomicOr(&s_child[parent], 1ull << tid);
     __syncthreads();
     if (tid < W) {
-        int x = p.parents[row0 + tid];
-        const bool wrong = x < -1 || x >= W || p.lens[row0 + tid] != n || n < 0 || (int64_t)n > (int64_t)p.width * P;
-        if (wrong) {
-            s_bad = 1;
-            if (reports) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, (int)(row0 + tid), p.lens[row0 + tid], -1);
-        }
-        s_parent[tid] = x == -1 ? tid : x;
+        const unsigned long long children = s_child[parent];
+        const int keeper = children >> parent & 1 ? parent : __ffsll((long long)children) - 1;
+        if (keeper != tid) atomicOr(&s_extra, 1ull << tid);
+        if (s_child[tid] == 0) atomicOr(&s_dead, 1ull << tid);
     }
     __syncthreads();
-    const bool bad = s_bad;
-    const int t = bad ? 0 : n / P, part = bad ? 0 : n % P;
-    bool extra = false, dead = true;
-    if (!bad && tid < W) {
-        const int mine = s_parent[tid];
-        bool older = false;  // the parent goes on itself, or has a child before this one
-        for (int i = 0; i < W; ++i) {
-            const int x = s_parent[i];
-            dead = dead && x != tid;
-            older = older || (x == mine && (i < tid || i == mine));
+    int mine = 0;  // the row's parent
+    while (!(s_child[mine] >> row & 1)) ++mine;
+    int tail = mine;  // the row whose page being filled this one goes on with
+    const bool copies = part && s_extra >> row & 1;
+    if (copies) {
+        unsigned long long dead = s_dead;
+        for (int k = __popcll(s_extra & ((1ull << row) - 1)); k > 0; --k) dead &= dead - 1;
+        tail = __ffsll((long long)dead) - 1;
+    }
+    const int *from = p.table + (row0 + mine) * p.width;
+    int src = -1, dst = -1;
+    if (part) {
+        src = from[t];
+        dst = p.table[(row0 + tail) * p.width + t];
+    }
+    const bool there = (unsigned)src < (unsigned)p.c.pages && (unsigned)dst < (unsigned)p.c.pages;
+    for (int y = blockIdx.y; y < parts; y += gridDim.y) {
+        if (y == parts - 1) {
+            const int *self = p.table + (row0 + row) * p.width;
+            for (int c = tid; c < p.width; c += REORDER_THREADS)
+                p.out[(row0 + row) * p.width + c] = c < t ? from[c] : c == t && part ? dst : self[c];
+            if (copies && !there && tid == 0)
+                note_failure(p.c.status, MK_ERR_DEVICE_CHECK, (int)(row0 + row), t * P, (unsigned)src >= (unsigned)p.c.pages ? src : dst);
+            continue;
         }
-        extra = mine != tid && older;
-        s_extra[tid] = extra;
-    }
-    __syncthreads();
-    if (!bad && tid < W && dead) {
-        int k = 0;
-        for (int i = 0; i < tid; ++i) {  // dead rows before this one
-            bool none = true;
-            for (int j = 0; j < W; ++j) none = none && s_parent[j] != i;
-            k += none;
+        if (!copies || !there || src == dst) continue;
+        // The pages' 16-byte pieces of all heads, U of a thread in flight; those
+        // behind the tokens are passed over.
+        const bool values = y % 2;
+        const size_t a = p.c.at(y / 2, src, 0), z = p.c.at(y / 2, dst, 0);
+        uint8_t *codes = values ? p.c.v : p.c.k;
+        float *scales = values ? p.c.vs : p.c.ks;
+        const uint4 *in = reinterpret_cast<const uint4 *>(codes + a * P * D);
+        uint4 *out = reinterpret_cast<uint4 *>(codes + z * P * D);
+        constexpr int U = 4, PIECES = P * D / 16;
+        const int all = p.c.hkv * PIECES;
+        // bytes of piece i that hold tokens: K's token i / (D / 16); V's tokens 16 (i % (P / 16)) ..
+        const auto bytes_of = [&](int i) {
+            return values ? min(max(part - i % (P / 16) * 16, 0), 16) : i % PIECES / (D / 16) < part ? 16 : 0;
+        };
+        for (int i0 = tid; i0 < all; i0 += U * REORDER_THREADS) {
+            uint4 x[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int i = i0 + k * REORDER_THREADS;
+                if (i < all && bytes_of(i)) x[k] = in[i];
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int i = i0 + k * REORDER_THREADS;
+                const int bytes = i < all ? bytes_of(i) : 0;
+                if (bytes == 0) continue;
+                if (bytes < 16) {  // the rest of these 16 stays: narrower stores (old bytes to mix in would have to be waited for)
+                    uint8_t *to = reinterpret_cast<uint8_t *>(out + i);
+                    uint32_t w = x[k].x;
+                    if (bytes & 8) {
+                        *reinterpret_cast<uint2 *>(to) = make_uint2(x[k].x, x[k].y);
+                        w = x[k].z;
+                        to += 8;
+                    }
+                    if (bytes & 4) {
+                        *reinterpret_cast<uint32_t *>(to) = w;
+                        w = bytes & 8 ? x[k].w : x[k].y;
+                        to += 4;
+                    }
+                    if (bytes & 2) {
+                        *reinterpret_cast<uint16_t *>(to) = (uint16_t)w;
+                        w >>= 16;
+                        to += 2;
+                    }
+                    if (bytes & 1) *to = (uint8_t)w;
+                    continue;
+                }
+                out[i] = x[k];
+            }
         }
-        s_free[k] = tid;
+        for (int h = tid; h < p.c.hkv; h += REORDER_THREADS) scales[z + h] = scales[a + h];
     }
-    __syncthreads();
-    const int parent = bad ? row : s_parent[row];
-    int tail = parent;  // the row whose page being filled this one goes on with
-    bool copies = false;
-    if (part && s_extra[row]) {
-        int k = 0;
-        for (int i = 0; i < row; ++i) k += s_extra[i];
-        tail = s_free[k];
-        copies = true;
-    }
-    const int *from = p.table + (row0 + parent) * p.width;
-    if (names) {
-        const int *self = p.table + (row0 + row) * p.width;
-        for (int c = tid; c < p.width; c += REORDER_THREADS)
-            p.out[(row0 + row) * p.width + c] =
-                c < t ? from[c] : c == t && part ? p.table[(row0 + tail) * p.width + t] : self[c];
-    }
-    if (!copies) return;
-    const int src = from[t], dst = p.table[(row0 + tail) * p.width + t];
-    if ((unsigned)src >= (unsigned)p.c.pages || (unsigned)dst >= (unsigned)p.c.pages) {
-        if (names && tid == 0)
-            note_failure(p.c.status, MK_ERR_DEVICE_CHECK, (int)(row0 + row), t * P, (unsigned)src >= (unsigned)p.c.pages ? src : dst);
-        return;
-    }
-    if (names || src == dst) return;
-    const size_t a = p.c.at(l, src, 0), z = p.c.at(l, dst, 0);
-    if (blockIdx.y % 2 == 0) {
-        const int per = part * (D / 16);  // 16-byte pieces of a head
-        for (int i = tid; i < per * p.c.hkv; i += REORDER_THREADS) {
-            const int h = i / per, x = i - h * per;
-            reinterpret_cast<uint4 *>(p.c.k + (z + h) * P * D)[x] = reinterpret_cast<const uint4 *>(p.c.k + (a + h) * P * D)[x];
-        }
-        for (int h = tid; h < p.c.hkv; h += REORDER_THREADS) p.c.ks[z + h] = p.c.ks[a + h];
-        return;
-    }
-    const int per = (part + 15) / 16, rest = part % 16;  // pieces of a dim's tokens, and what the last has of 16
-    for (int i = tid; i < per * D * p.c.hkv; i += REORDER_THREADS) {
-        const int rw = i / per, x = i - rw * per;
-        uint4 *to = reinterpret_cast<uint4 *>(p.c.v + z * P * D + (size_t)rw * P) + x;
-        uint4 y = reinterpret_cast<const uint4 *>(p.c.v + a * P * D + (size_t)rw * P)[x];
-        if (rest && x == per - 1) {
-            const uint4 old = *to;
-            const auto mix = [&](uint32_t nw, uint32_t od, int w) {
-                const int bytes = min(max(rest - 4 * w, 0), 4);
-                const uint32_t m = bytes == 4 ? ~0u : (1u << (8 * bytes)) - 1;
-                return (nw & m) | (od & ~m);
-            };
-            y = make_uint4(mix(y.x, old.x, 0), mix(y.y, old.y, 1), mix(y.z, old.z, 2), mix(y.w, old.w, 3));
-        }
-        *to = y;
-    }
-    for (int h = tid; h < p.c.hkv; h += REORDER_THREADS) p.c.vs[z + h] = p.c.vs[a + h];
 }
 
 static int move_params(const mk_cache_desc *cache, const mk_cache_rows *rows, const int32_t *table, int width,
@@ -677,7 +693,8 @@ int mk_cache_reorder(const mk_cache_desc *cache, const int32_t *table, const int
     const bool p32 = cache->page_tokens == 32;
     void (*f)(const ReorderParams) = cache->head_dim == 64 ? (p32 ? cache_reorder_kernel<64, 32> : cache_reorder_kernel<64, 64>)
                                                            : (p32 ? cache_reorder_kernel<128, 32> : cache_reorder_kernel<128, 64>);
-    f<<<dim3((unsigned)rows, 2 * cache->layers + 1), REORDER_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    const int64_t each = std::max<int64_t>(1, std::min<int64_t>(2 * cache->layers + 1, (REORDER_CTAS + rows - 1) / rows));
+    f<<<dim3((unsigned)rows, (unsigned)each), REORDER_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? MK_OK : serve_cuda_fail(e, "reorder launch");
 }

@@ -28,8 +28,9 @@ struct AttParams {
     int ngroups;
     float *row_ml, *row_o;
     // The groups' pages are a launch of their own, on part of `sms` SMs: rows of
-    // its tiles (PRE_ROWS: prefix.cu's, else attend.cu's) and of the other one's,
-    // and what its CTAs cut, like part_ml and part_o.
+    // its tiles (PRE_ROWS: prefix.cu's, else attend.cu's; 0: there is none, every
+    // sequence reads its pages) and of the other one's, and what its CTAs cut, like
+    // part_ml and part_o.
     int sms, pre_rt, rt;
     float *pre_ml, *pre_o;
 };
@@ -128,13 +129,14 @@ DEV int att_group_of(const AttParams &p, const AttGroups &s, int b) {
     }
     return b >= s.grp[a] && b < s.grp[a + 1] ? a : -1;
 }
-// By the whole block.  What `shared` says is a bound: only full pages, and of
+// By the whole block; returns sequence threadIdx.x (what fails there is reported
+// here).  What `shared` says is a bound: only full pages, and of
 // them those that every query of the group sees whole.
 template <int P>
-DEV void att_groups(const AttParams &p, const AttGroups &s, bool report) {
+DEV AttSeq att_groups(const AttParams &p, const AttGroups &s, bool report) {
     const int n = p.ngroups, tid = threadIdx.x, threads = blockDim.x;
     // the first of everything at once: one round trip
-    const AttSeq mine = tid < p.batch ? att_seq<P>(p, tid, false) : AttSeq{0, 0, 0, 0, 0, false};
+    const AttSeq mine = tid < p.batch ? att_seq<P>(p, tid, report) : AttSeq{0, 0, 0, 0, 0, false};
     const int share = tid < n ? p.shared[tid] : 0;
     bool bad = false;
     for (int g = tid; g <= n; g += threads) {
@@ -148,7 +150,7 @@ DEV void att_groups(const AttParams &p, const AttGroups &s, bool report) {
         const int x = g == tid ? share : p.shared[g];
         if (x < 0 && report) note_failure(p.c.status, MK_ERR_DEVICE_CHECK, s.grp[g], x, -1);
         s.lead[g] = INT_MAX;
-        s.lim[g] = bad || s.grp[g + 1] - s.grp[g] < 2 ? 0 : max(x, 0) / P;
+        s.lim[g] = bad || !p.pre_rt || s.grp[g + 1] - s.grp[g] < 2 ? 0 : max(x, 0) / P;
     }
     __syncthreads();
     for (int b = tid; b < p.batch && !bad; b += threads) {
@@ -161,18 +163,19 @@ DEV void att_groups(const AttParams &p, const AttGroups &s, bool report) {
         atomicMin(&s.lim[g], max(0, q.len - q.cnt + 1) / P);
     }
     __syncthreads();
+    return mine;
 }
 // What a launch is for: sequences by themselves; with shared prefixes, sequences
 // over the pages behind them; groups over the shared pages.
 enum AttKind { ATT_PLAIN, ATT_OWN, ATT_GROUPS };
 DEV int att_units(const AttParams &p, AttKind kind) { return kind == ATT_GROUPS ? p.ngroups : p.batch; }
-// Unit v: a sequence, or a group's rows over its pages (every row sees all).
+// Unit v: a sequence (`mine`: what att_groups returned), or a group's rows over its pages (every row sees all).
 template <int P, AttKind KIND>
-DEV AttSeq att_unit(const AttParams &p, const AttGroups &s, int v, bool report) {
+DEV AttSeq att_unit(const AttParams &p, const AttGroups &s, int v, bool report, const AttSeq *mine = nullptr) {
     if constexpr (KIND == ATT_PLAIN) {
         return att_seq<P>(p, v, report);
     } else if constexpr (KIND == ATT_OWN) {
-        AttSeq q = att_seq<P>(p, v, report);
+        AttSeq q = mine && v == (int)threadIdx.x ? *mine : att_seq<P>(p, v, report);
         const int g = att_group_of(p, s, v);
         q.gap = g < 0 ? 0 : min(s.lim[g], q.hi);
         return q;
@@ -219,7 +222,7 @@ DEV long long att_items_of(const AttParams &p, int rt, int cnt, int np) {
 
 // Work items of a group.
 DEV long long att_group_items(const AttParams &p, int cnt, int np) {
-    return p.pre_rt == PRE_ROWS ? pre_items(p, cnt, np) : att_items_of(p, p.pre_rt, cnt, np);
+    return np == 0 ? 0 : p.pre_rt == PRE_ROWS ? pre_items(p, cnt, np) : att_items_of(p, p.pre_rt, cnt, np);
 }
 // Both launches run beside each other, on SMs shared out by their work: the CTAs
 // of the groups' one.  A page through prefix.cu's tiles (0.9 us) takes about as
@@ -238,11 +241,11 @@ DEV void att_total(long long v, unsigned long long *to) {
 }
 // The other launch's items, summed over the block.
 template <int P, AttKind KIND>
-DEV void att_others(const AttParams &p, const AttGroups &s, unsigned long long *to) {
+DEV void att_others(const AttParams &p, const AttGroups &s, const AttSeq &mine, unsigned long long *to) {
     long long v = 0;
     if constexpr (KIND == ATT_GROUPS) {
         for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
-            const AttSeq q = att_unit<P, ATT_OWN>(p, s, b, false);
+            const AttSeq q = att_unit<P, ATT_OWN>(p, s, b, false, &mine);
             v += att_items_of(p, p.rt, q.cnt, q.hi - q.gap);
         }
     } else {

@@ -5,8 +5,10 @@
 
 namespace mk {
 
-constexpr int ATT_WARPS = 8;                        // consumer warps
-constexpr int ATT_THREADS = (ATT_WARPS + 4) * 32;   // + the producer's warpgroup, of which one warp works
+// Consumer warps of a CTA.  What sequences have behind a shared prefix is short:
+// two CTAs of four on an SM have two of those units in work.
+__host__ __device__ constexpr int att_warps(AttKind kind) { return kind == ATT_OWN ? 4 : 8; }
+__host__ __device__ constexpr int att_threads(AttKind kind) { return (att_warps(kind) + 4) * 32; }  // + the producer's warpgroup, of which one warp works
 constexpr int ATT_MAXRING = 32;                     // pages in the ring (one producer lane each)
 
 // Tiles of rt rows: 8 NT rows a warp, up to rt / (8 NT) warps side by side
@@ -39,14 +41,14 @@ struct AttShared {
     uint8_t *ring;      // [ring][K page, V page]
 };
 
-__host__ __device__ constexpr int att_fixed_bytes(int D, int nt) {
-    return ATT_WARPS * 8 * nt * (D + 4) * 4 + ATT_WARPS * 8 * nt * 2 * 4 + ATT_MAXRING * (8 + 32 + 8) + 16;
+__host__ __device__ constexpr int att_fixed_bytes(int D, int nt, int warps) {
+    return warps * 8 * nt * (D + 4) * 4 + warps * 8 * nt * 2 * 4 + ATT_MAXRING * (8 + 32 + 8) + 16;
 }
 __host__ __device__ constexpr int att_seq_bytes(int units, int ngroups) {
     return units * 16 + (units + 1) * 8 + att_group_bytes(ngroups);
 }
 
-template <int D, int NT>
+template <int D, int NT, int WARPS>
 DEV AttShared att_shared(const AttParams &p, int units) {
     AttShared s;
     uint8_t *at = mk_smem;
@@ -64,9 +66,9 @@ DEV AttShared att_shared(const AttParams &p, int units) {
     s.total = reinterpret_cast<unsigned long long *>(at + 8);
     at += 16;
     s.ml = reinterpret_cast<float *>(at);
-    at += ATT_WARPS * 8 * NT * 2 * 4;
+    at += WARPS * 8 * NT * 2 * 4;
     s.merge = reinterpret_cast<float *>(at);
-    at += ATT_WARPS * 8 * NT * (D + 4) * 4;
+    at += WARPS * 8 * NT * (D + 4) * 4;
     s.seq = reinterpret_cast<int4 *>(at);
     s.prefix = reinterpret_cast<long long *>(s.seq + units);
     s.groups = att_groups_at(s.prefix + units + 1, p.ngroups);
@@ -334,11 +336,12 @@ DEV float att_load_q(const uint16_t *row, int t, uint32_t (&qb)[D / 64][8]) {
 DEV void mbar_arrive_n(uint64_t *b, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(b)), "r"(n) : "memory");
 }
-DEV void att_consumer_bar() { asm volatile("bar.sync 1, %0;" ::"n"(ATT_WARPS * 32) : "memory"); }
+template <int WARPS>
+DEV void att_consumer_bar() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); }
 
 template <int D, int P, int RT, AttKind KIND>
 DEV void att_consume(const AttParams &p, const AttShared &s) {
-    constexpr int NT = att_nt(RT), WT = RT / (8 * NT);  // 8-row tiles a warp, warps for a full tile
+    constexpr int WARPS = att_warps(KIND), NT = att_nt(RT), WT = RT / (8 * NT);  // 8-row tiles a warp, warps for a full tile
     constexpr int PAGE = P * D, RUN = P / 4, NM = P / 16, ND = D / 16, LD = D + 4;
     constexpr bool QS = NT > 1;  // the query operand in shared memory (registers would spill)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g8 = lane / 4, t = lane % 4;
@@ -352,7 +355,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
         // as many warps side by side as the tile's rows need (1, 2 or 4), the
         // others on other pages: group grp takes every ng-th page of the range
         const int side = att_side<RT>(rows - g.tile * RT);
-        const int wt = warp % side, grp = warp / side, ng = ATT_WARPS / side;
+        const int wt = warp % side, grp = warp / side, ng = WARPS / side;
         const int row0 = g.tile * RT + wt * 8 * NT;
         int st = (before + grp) % p.ring;  // ring slot and phase of this warp's next page
         uint32_t ph = ((before + grp) / p.ring) & 1;
@@ -401,7 +404,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
         }
         all_hi = __reduce_min_sync(FULL, all_hi);
         all_lo = __reduce_max_sync(FULL, all_lo);
-        if constexpr (QS) att_consumer_bar();
+        if constexpr (QS) att_consumer_bar<WARPS>();
         for (int mine = before + grp; mine < before + g.n; mine += ng, st += ng, settle()) {
             const int pg = att_page(p, g.pg + mine - before, g.gap);
             if (ok) ok = att_wait(p, s, &s.has_k[st], mine, &s.full_k[st], ph);
@@ -598,7 +601,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
         }
         before += g.n;
         // merge the ng warps of each tile
-        if constexpr (QS) att_consumer_bar();  // the query operand lies where the sums go
+        if constexpr (QS) att_consumer_bar<WARPS>();  // the query operand lies where the sums go
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float *mo = s.merge + ((warp * NT + n) * 8 + 2 * t) * LD + g8;
@@ -616,8 +619,8 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                 if (g8 == 0) *reinterpret_cast<float2 *>(s.ml + ((warp * NT + n) * 8 + 2 * t + e) * 2) = make_float2(m[n][e], sum);
             }
         }
-        att_consumer_bar();
-        for (int i = threadIdx.x; i < RT * (D / 4); i += ATT_WARPS * 32) {
+        att_consumer_bar<WARPS>();
+        for (int i = threadIdx.x; i < RT * (D / 4); i += WARPS * 32) {
             const int row = i / (D / 4), d4 = i % (D / 4);
             const int rr = g.tile * RT + row;
             if (rr >= rows) continue;
@@ -656,23 +659,25 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                 if (d4 == 0) *reinterpret_cast<float2 *>((all ? p.pre_ml : p.part_ml) + slot * 2) = make_float2(big, sum);
             }
         }
-        att_consumer_bar();
+        att_consumer_bar<WARPS>();
     }
 }
 
 template <int D, int P, int RT, AttKind KIND>
-__global__ void __launch_bounds__(ATT_THREADS, 1) cache_attend_kernel(const AttParams p) {
+__global__ void __launch_bounds__(att_threads(KIND), KIND == ATT_OWN ? 2 : 1) cache_attend_kernel(const AttParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
-    const AttShared s = att_shared<D, att_nt(RT)>(p, att_units(p, KIND));
+    constexpr int WARPS = att_warps(KIND), THREADS = att_threads(KIND);
+    const AttShared s = att_shared<D, att_nt(RT), WARPS>(p, att_units(p, KIND));
     const int tid = threadIdx.x, units = att_units(p, KIND);
-    if constexpr (KIND != ATT_PLAIN) att_groups<P>(p, s.groups, KIND == ATT_OWN && blockIdx.x == 0);
-    for (int b = tid; b < units; b += ATT_THREADS) {
-        const AttSeq q = att_unit<P, KIND>(p, s.groups, b, KIND != ATT_GROUPS && blockIdx.x == 0);
+    AttSeq seq{0, 0, 0, 0, 0, false};
+    if constexpr (KIND != ATT_PLAIN) seq = att_groups<P>(p, s.groups, KIND == ATT_OWN && blockIdx.x == 0);
+    for (int b = tid; b < units; b += THREADS) {
+        const AttSeq q = att_unit<P, KIND>(p, s.groups, b, KIND != ATT_GROUPS && blockIdx.x == 0, &seq);
         s.prefix[b + 1] = att_items<RT>(p, q.cnt, q.hi - q.gap);
         s.seq[b] = make_int4(q.q0, q.cnt, q.len, q.gap);
     }
-    if (tid >= ATT_THREADS - 32 && tid - (ATT_THREADS - 32) < p.ring) {
-        const int i = tid - (ATT_THREADS - 32);
+    if (tid >= THREADS - 32 && tid - (THREADS - 32) < p.ring) {
+        const int i = tid - (THREADS - 32);
         s.has_k[i] = s.has_v[i] = -1;
         mbar_init(&s.full_k[i], 2);
         mbar_init(&s.full_v[i], 1);
@@ -683,23 +688,25 @@ __global__ void __launch_bounds__(ATT_THREADS, 1) cache_attend_kernel(const AttP
     if (tid == 0) s.ctrl[0] = 0, *s.total = 0;
     att_running(s.prefix, units);
     if constexpr (KIND != ATT_PLAIN) {
-        att_others<P, KIND>(p, s.groups, s.total);
+        att_others<P, KIND>(p, s.groups, seq, s.total);
         __syncthreads();
         const long long mine = s.prefix[units], others = (long long)*s.total;
-        const int share = KIND == ATT_GROUPS ? att_share(p, mine, others) : p.sms - att_share(p, others, mine);
+        const int share = KIND == ATT_GROUPS ? att_share(p, mine, others) : 2 * (p.sms - att_share(p, others, mine));
         if (tid == 0) s.ctrl[1] = min(p.ctas, share);
         __syncthreads();
         // (one CTA at least of the second of both: it ends after the first)
         if ((int)blockIdx.x >= max(s.ctrl[1], KIND == ATT_OWN ? 1 : 0)) return;
     }
-    // 3 x 128 threads were launched with 168 registers each (an SM's quarter holds
-    // three warps of that size): 2 x 216 + 72.  What does not fit goes to local
-    // memory, for which shared memory leaves hardly any L1 cache.
-    if (tid >= ATT_WARPS * 32) {
+    // Registers: 3 x 128 threads were launched with 168 each (an SM's quarter holds
+    // three warps of that size): 2 x 216 + 72; twice 2 x 128 with 128: 184 + 72.
+    // What does not fit goes to local memory, for which shared memory leaves hardly
+    // any L1 cache.
+    if (tid >= WARPS * 32) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (tid < (ATT_WARPS + 1) * 32) att_produce<D, P, RT, KIND>(p, s);
+        if (tid < (WARPS + 1) * 32) att_produce<D, P, RT, KIND>(p, s);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if constexpr (KIND == ATT_OWN) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         att_consume<D, P, RT, KIND>(p, s);
     }
     // the groups' launch, beside which this one ran, is done before this one is
@@ -719,9 +726,10 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
     const int tid = threadIdx.x, lane = tid % 32, heads = p.group * p.c.hkv, units = p.batch;
     constexpr bool SH = KIND != ATT_PLAIN;
     const AttGroups groups = att_groups_at(prefix + units + 1, p.ngroups);
-    if constexpr (SH) att_groups<P>(p, groups, false);
+    AttSeq seq{0, 0, 0, 0, 0, false};
+    if constexpr (SH) seq = att_groups<P>(p, groups, false);
     for (int b = tid; b < units; b += 256) {
-        const AttSeq q = att_unit<P, KIND>(p, groups, b, false);
+        const AttSeq q = att_unit<P, KIND>(p, groups, b, false, &seq);
         prefix[b + 1] = att_items<RT>(p, q.cnt, q.hi - q.gap);
     }
     att_running(prefix, units);
@@ -754,7 +762,7 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
     };
     const long long total = prefix[units];
     const int pre_ctas = SH ? att_share(p, before[p.ngroups], total) : 0;
-    const int ctas = att_used<RT>(total, SH ? min(p.ctas, p.sms - pre_ctas) : p.ctas);
+    const int ctas = att_used<RT>(total, SH ? min(p.ctas, 2 * (p.sms - pre_ctas)) : p.ctas);
     // of tiles of rt rows, a unit's first item being number `first`
     const auto part_of = [&](const AttSeq &s, int rt, long long first, long long all, int n, bool whole_pages) {
         Part x{s.hi - s.gap, 0, -1, 0};

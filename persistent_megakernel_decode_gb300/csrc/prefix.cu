@@ -672,8 +672,8 @@ __global__ void __launch_bounds__(PRE_THREADS, 1) cache_prefix_kernel(const AttP
     const PreShared s = pre_shared<D, P>(p);
     const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid / 32, 0);
     if (tid == 0) *s.total = 0;
-    att_groups<P>(p, s.groups, false);
-    att_others<P, ATT_GROUPS>(p, s.groups, s.total);
+    const AttSeq seq = att_groups<P>(p, s.groups, false);
+    att_others<P, ATT_GROUPS>(p, s.groups, seq, s.total);
     for (int g = tid; g < p.ngroups; g += PRE_THREADS) {
         const AttSeq q = att_unit<P, ATT_GROUPS>(p, s.groups, g, false);
         s.unit[g] = make_int4(q.q0, q.cnt, q.hi, s.groups.lead[g]);

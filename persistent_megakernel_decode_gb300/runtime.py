@@ -346,6 +346,9 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     return tokens, logprob
 
 
+_beam_sizes = {}  # workspace bytes by (batch, beams, vocabulary, num)
+
+
 def beam_select(logits, scores, num: Optional[int] = None, finished=None, end: int = 0, stream=None):
     """Beam search's selection: of all tokens after all beams of a prompt the ``num`` (default: as many as beams) with the
     largest score + log softmax(logits), ties to the lower beam, then the lower token (``mk_beam_desc`` in ``include/mk.h``
@@ -374,21 +377,29 @@ def beam_select(logits, scores, num: Optional[int] = None, finished=None, end: i
     stride, inner = logits.stride()
     if inner != 1 and v > 1:
         raise ValueError("logits must be contiguous along the vocabulary")
-    scores = scores.contiguous()
+    if not scores.is_contiguous():
+        scores = scores.contiguous()
     if finished is not None:
         check_tensor("finished", finished, index, torch.bool, (b, w))
-        finished = finished.contiguous()
+        if not finished.is_contiguous():
+            finished = finished.contiguous()
     num = w if num is None else c_int(num)
-    shape, device = (b, max(num, 0)), logits.device
-    out = torch.empty(shape, dtype=torch.float32, device=device)
-    parents, tokens = (torch.empty(shape, dtype=torch.int32, device=device) for _ in range(2))
+    device = logits.device
+    out = torch.empty((b, max(num, 0)), dtype=torch.float32, device=device)
+    parents = torch.empty((b, max(num, 0)), dtype=torch.int32, device=device)
+    tokens = torch.empty_like(parents)
     d = BeamDesc(logits.data_ptr(), stride if rows > 1 else v, b, w, v, logits.dtype is torch.bfloat16, num, c_int(end),
                  scores.data_ptr(), 0 if finished is None else finished.data_ptr(), out.data_ptr(), parents.data_ptr(),
                  tokens.data_ptr())
-    size = C.c_uint64()
-    _check(load().mk_beam_select_workspace(C.byref(d), C.byref(size)))
-    workspace = torch.empty(size.value, dtype=torch.uint8, device=device)
-    launch(index, None, load().mk_beam_select, C.byref(d), workspace.data_ptr(), size.value)
+    size = _beam_sizes.get((b, w, v, num))
+    if size is None:
+        need = C.c_uint64()
+        _check(load().mk_beam_select_workspace(C.byref(d), C.byref(need)))
+        if len(_beam_sizes) >= 1024:
+            _beam_sizes.clear()
+        size = _beam_sizes[b, w, v, num] = need.value
+    workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    launch(index, None, load().mk_beam_select, C.byref(d), workspace.data_ptr(), size)
     return out, parents, tokens
 
 
