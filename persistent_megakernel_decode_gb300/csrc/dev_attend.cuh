@@ -225,12 +225,14 @@ DEV long long att_group_items(const AttParams &p, int cnt, int np) {
     return np == 0 ? 0 : p.pre_rt == PRE_ROWS ? pre_items(p, cnt, np) : att_items_of(p, p.pre_rt, cnt, np);
 }
 // Both launches run beside each other, on SMs shared out by their work: the CTAs
-// of the groups' one.  A page through prefix.cu's tiles (0.9 us) takes about as
-// long as two items of attend.cu's.
+// of the groups' one.  By the clock a page through prefix.cu's tiles takes an SM as
+// long as 2.5 items of the sequences' launch, an item of attend.cu's for groups
+// 1.3 (0.95 and 0.5 us).
 DEV int att_share(const AttParams &p, long long groups, long long own) {
     if (groups == 0) return 0;
     if (own == 0) return p.sms;
-    const long long a = groups * (p.pre_rt == PRE_ROWS ? 2 : 1), n = (a * p.sms + (a + own) / 2) / (a + own);
+    const long long a = groups * (p.pre_rt == PRE_ROWS ? 15 : 8), all = a + 6 * own;
+    const long long n = (a * p.sms + all / 2) / all;
     return (int)min((long long)p.sms - 1, max(1ll, n));
 }
 // Sum of v over the block, in *to (zeroed before a barrier; read after one).
