@@ -13,13 +13,13 @@
 // land in to the swizzled tiles the products read; a row of Q is scaled by a
 // power of two into f16's range.
 //
-// One reference.  P and the sum are relative to a row's reference r, which is
-// the first page's largest s + log2(the page's V scale) and follows a larger
-// one only when that is 2^8 above it: then O is rescaled in tensor memory, and
-// else nothing is.  P = 2^(s + log2 vs - r + 7) holds the V scale, so that pages
-// of different scales add up in one accumulator; it stays below 2^15, and what
-// it rounds away is 2^-11 of itself or 2^-32 of the reference.  The sum takes the
-// page's P as they are in fp32, times a power of two that removes the scale.
+// One reference.  P and O are relative to a row's reference r, which is the
+// first page's largest s + log2(the page's V scale) and follows a larger one only
+// when that is 2^8 above it: then O is rescaled in tensor memory, and else nothing
+// is.  P = 2^(s + log2 vs - r + 7) holds the V scale, so that pages of different
+// scales add up in one accumulator; it stays below 2^15, and what it rounds away
+// is 2^-11 of itself or 2^-32 of the reference.  The sum is relative to the
+// largest s and takes the page's P as they are in fp32, without the scale.
 //
 // Fewer rows.  The tile's 128 lanes hold two copies of up to 64 rows, or four of
 // up to 32: each copy takes the softmax of its share of a page's tokens, the
@@ -29,6 +29,14 @@
 // Roles.  Two streams of four softmax warps take pages in turn, so that one's
 // products run during the other's softmax; four warps each expand K and V; one
 // producer (bulk copies); one warp issues the products.
+//
+// What bounds it: 0.9 us a page of 64 tokens and 128 dims and tile of 128 rows,
+// 4.7 TFLOP/s an SM.  The products alone are 512 clocks (measured: 64 for 128 x
+// 128 x 16); the rest is shared memory (a page's codes land, are read, and are
+// written twice as large, and the products read them: some 770 wavefronts of 128
+// bytes without conflicts) and the way of a page through scores, softmax and
+// outputs, of which tensor memory holds two.  Tried and slower: a third pair of tiles, all 64
+// scores in registers, V expanded by integer instructions, spinning waits.
 //
 // Work split.  As in attend.cu: the pages of all (group, tile, kv head) are one
 // axis cut into equal ranges, one per CTA; what a CTA boundary cuts is merged
@@ -422,10 +430,10 @@ DEV void pre_products(const AttParams &p, const PreShared &s, uint32_t tmem) {
 }
 
 // ---- softmax warps
-// A row's state: the reference, the sum relative to it (and without the first
-// page's V scale, 2^base).
+// A row's state: the reference of P and O (of s + log2 of V scales), the largest
+// s, and the sum of 2^s relative to that.
 struct PreRow {
-    float ref, sum, base;
+    float ref, top, sum;
 };
 // One page's scores to probabilities: this thread's row, CN tokens.  `taken` is
 // called when the scores are read, `settle` before P is written, with what O has
@@ -442,24 +450,28 @@ DEV void pre_softmax(uint32_t s_addr, uint32_t p_addr, float fk, float lv, PreRo
 #pragma unroll
         for (int i = 0; i < W; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
     }
-    // scales so far apart that P may be 0 where the sum is not: the sum's terms by themselves
-    const bool apart = !(fabsf(lv - w.base) <= 60.f);
-    if (CN == W && !apart) taken();
-    const float to = mx * fk + (lv == lv ? lv : w.base);  // a NaN scale makes outputs NaN, not the sum
+    mx *= fk;
+    const float top = fmaxf(w.top, mx), mu = top == -INFINITY ? 0.f : top;
+    w.sum *= exp2_fast(w.top - mu);
+    w.top = top;
+    const float to = mx + (lv == lv ? lv : 0.f);
     float back = 1.f;
     if (!(to <= w.ref + 8.f)) {  // (the first page; a NaN score leaves the reference)
         back = to > w.ref ? exp2_fast(w.ref - to) : 1.f;
         w.ref = to > w.ref ? to : w.ref;
-        w.sum *= back;
     }
     const float at = w.ref == -INFINITY ? 0.f : w.ref, off = lv + 7.f - at;
+    // scales so far apart that P may be 0 where the sum is not (or a NaN scale,
+    // which makes outputs NaN, not the sum): the sum's terms by themselves
+    const bool apart = !(to >= at - 60.f) || lv != lv, some = __any_sync(FULL, apart);
+    if (CN == W && !some) taken();
     float sum = 0.f;
 #pragma unroll
     for (int c = CN - W; c >= 0; c -= W) {  // the last part is in registers
         if (c < CN - W) {
             pre_ld(s_addr + c, r);
             pre_wait_ld();
-            if (c == 0 && !apart) taken();
+            if (c == 0 && !some) taken();
         }
         uint32_t h[W / 2];
 #pragma unroll
@@ -471,22 +483,20 @@ DEV void pre_softmax(uint32_t s_addr, uint32_t p_addr, float fk, float lv, PreRo
         if (c == CN - W) settle(back);
         pre_st(p_addr + c / 2, h);
     }
-    if (!apart) {
-        w.sum = fmaf(sum, exp2_fast(w.base - lv), w.sum);
-    } else {
-        sum = 0.f;
-        const float alone = w.base + 7.f - at;
+    const float here = sum * exp2_fast(-off - mu);
+    float alone = 0.f;
+    if (some) {
 #pragma unroll 1
         for (int c = 0; c < CN; c += 8) {
             uint32_t t[8];
             pre_ld(s_addr + c, t);
             pre_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += exp2_fast(fmaf(__uint_as_float(t[i]), fk, alone));
+            for (int i = 0; i < 8; ++i) alone += exp2_fast(fmaf(__uint_as_float(t[i]), fk, -mu));
         }
-        w.sum += sum;
         taken();
     }
+    w.sum += apart ? alone : here;
 }
 
 DEV void pre_bar() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -517,8 +527,8 @@ DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
                 for (int k = 0; k < BATCH; ++k) {  // (rows behind the last: it again, then zeros)
                     const int r = row0 + max(0, min(i + k * AT_ONCE + lane / LANES, there - 1)), tok = r / p.group;
                     q[k] = make_uint4(0, 0, 0, 0);
-                    if (there > 0)
-                        q[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)(g.q0 + tok) * p.qs_t + (int64_t)(g.h * p.group + r - tok * p.group) * p.qs_h) + lane % LANES);
+                    const int64_t at = (int64_t)(g.q0 + tok) * p.qs_t + (int64_t)(g.h * p.group + r - tok * p.group) * p.qs_h;
+                    if (there > 0) q[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + at) + lane % LANES);
                 }
 #pragma unroll
                 for (int k = 0; k < BATCH; ++k) {
@@ -565,7 +575,7 @@ DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
         }
         if (ok) ok = pre_wait_warp(p, s, s.q_full, seg & 1);
         const float qf = s.qf[tid] * p.scale_log2;
-        PreRow w{-INFINITY, 0.f, 0.f};
+        PreRow w{-INFINITY, -INFINITY, 0.f};
         int last = -1;  // the stream's page before
         const auto taken = [&] {  // the scores' columns may be written again
             pre_fence_before();
@@ -595,7 +605,6 @@ DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
             const float2 sc = s.scale[k & 3];
             if (sc.x >= 0.f || sc.x != sc.x) {
                 const float fk = qf * sc.x;
-                if (w.ref == -INFINITY && w.sum == 0.f) w.base = sc.y == sc.y ? sc.y : 0.f;
                 if (copies == 1) pre_softmax<P>(s_addr, p_addr, fk, sc.y, w, taken, settle);
                 else if (copies == 2) pre_softmax<P / 2>(s_addr + copy * (P / 2), p_addr + copy * (P / 4), fk, sc.y, w, taken, settle);
                 else pre_softmax<P / 4>(s_addr + copy * (P / 4), p_addr + copy * (P / 8), fk, sc.y, w, taken, settle);
@@ -614,9 +623,7 @@ DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
         }
         if (last >= 0 && ok) ok = pre_wait_warp(p, s, &s.o_done[x], (last >> 1) & 1);
         pre_fence_after();
-        // as attend.cu has them: the sum of 2^(s - m + 14), outputs relative to m
-        const float m = w.ref == -INFINITY ? -INFINITY : w.ref - w.base + 7.f, l = w.sum;
-        const float unscale = last >= 0 ? exp2_fast(w.base - 14.f) : 0.f;
+        const float m = w.top, l = w.sum * 0x1p14f;  // as attend.cu has them: the sum of 2^(s - m + 14), outputs relative to m
 
         // join the copies of both streams, 32 dims at a time
         constexpr int LD = 36;
@@ -625,7 +632,8 @@ DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
         const int parts = 2 * copies;  // row r of the tile: threads r + i * each
         float big = -INFINITY;
         for (int i = 0; i < parts; ++i) big = fmaxf(big, s.ml[(tid % each + i * each) * 2]);
-        const float part = last >= 0 ? exp2_fast(m - (big == -INFINITY ? 0.f : big)) * unscale : 0.f;
+        // O times 2^(ref - 7 - big), in two steps (a V scale may be 2^120)
+        const float part = exp2_fast(0.5f * (w.ref - 7.f - (big == -INFINITY ? 0.f : big)));
         if (threadIdx.x < rows) {  // (rows <= each: this thread's row is threadIdx.x)
             float sum = 0.f;
             for (int i = 0; i < parts; ++i) {
@@ -646,7 +654,7 @@ DEV void pre_rows(const AttParams &p, const PreShared &s, uint32_t tmem) {
             float4 *mine = reinterpret_cast<float4 *>(s.merge + threadIdx.x * LD);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const auto o = [&](int j) { return last >= 0 ? __uint_as_float(r[4 * i + j]) * part : 0.f; };
+                const auto o = [&](int j) { return last >= 0 ? __uint_as_float(r[4 * i + j]) * part * part : 0.f; };
                 mine[i] = make_float4(o(0), o(1), o(2), o(3));
             }
             pre_bar();
