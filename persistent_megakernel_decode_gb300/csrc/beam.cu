@@ -17,13 +17,19 @@
 // The largest without sorting: a bound that at least `num` threads' largest
 // values reach is found by bisection, one barrier and vote a step; the few
 // logits that reach it (at most as many per thread as it holds) are listed.
-// Later pieces of the part list what is above the bound; now and then the bound
-// rises to what the listed allow, and the list shrinks to it.  At the end the
-// list is ranked by comparing each with all.
+// Later pieces of the part list what is above the bound; when the list is full
+// the bound rises to what the listed allow, and the list shrinks to it (doing so
+// now and then, before, cost more than it saved: 31.6 us for 29.1 below).  At the
+// end the list is ranked by comparing each with all.
 //
 // Work split.  A CTA streams a part of a row, 4096 logits at a time in
 // registers, the next piece's loads in flight.  A second, dependent launch orders
-// a prompt's candidates, one CTA each.  Bytes bound it: each logit is read once.
+// a prompt's candidates, one CTA each.  Each logit is read once, so bytes bound
+// it: 64 x 8 beams of 151,936 logits take 58 us, 5.4 TB/s.  16 x 8 take 29, of
+// which the bytes are 10: the rest is the ramp of two launches, the bisection and
+// the rank of each part's list (barriers), and 26 instructions a logit.  Three
+// CTAs an SM in one wave are the best split (six: 36 us; one cluster a row, in
+// registers: 52-99).
 #include <algorithm>
 #include <climits>
 
@@ -155,9 +161,16 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
     const int pieces = (last - begin + BM_PIECE - 1) / BM_PIECE;
     uint4 raw[E / VEC];
     const auto load = [&](int piece) {
+        const int from = begin + piece * BM_PIECE;
+        if (from >= first && from + BM_PIECE <= last) {
+            const uint4 *z = reinterpret_cast<const uint4 *>(base + (size_t)from * SIZE) + tid;
+#pragma unroll
+            for (int i = 0; i < E / VEC; ++i) raw[i] = __ldcs(z + i * BM_THREADS);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < E / VEC; ++i) {
-            const int x = begin + piece * BM_PIECE + (i * BM_THREADS + tid) * VEC;
+            const int x = from + (i * BM_THREADS + tid) * VEC;
             if (x >= first && x + VEC <= last) {
                 raw[i] = __ldcs(reinterpret_cast<const uint4 *>(base + (size_t)x * SIZE));
             } else {
@@ -188,12 +201,13 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
     int ref = 0, room = p.cap;       // room: entries that the list has at least
     unsigned long long rest = 0;
     // 2^(x log2(e) - ref): x log2(e) = n + f, f good to 2^-26; e^-80 below the bound is nothing (-inf and NaN too)
+    constexpr float ROUND = 12582912.f;  // its bits shifted left by 23 are 0
+    float least = 0.f, round = ROUND;    // bound - 80, ROUND - ref
     const auto term = [&](float z) {
-        constexpr float ROUND = 12582912.f;  // its bits shifted left by 23 are 0
-        const float x = fmaxf(z, bound - 80.f);
-        const float t = fmaf(x, CH, ROUND), k = t - ROUND;
+        const float x = fmaxf(z, least);
+        const float t = fmaf(x, CH, round), k = t - round;
         const float f = fmaf(x, CL, fmaf(x, CH, -k));
-        return __int_as_float(__float_as_int(exp2_approx(f)) + (__float_as_int(t) << 23) - (ref << 23));
+        return __int_as_float(__float_as_int(exp2_approx(f)) + (__float_as_int(t) << 23));
     };
     const auto raise_to = [&](uint32_t o) {
         bound = ordered_value(o);
@@ -203,6 +217,8 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
             const int r = (int)ceilf(bound * CH);
             rest = r - ref < 64 ? rest >> max(r - ref, 0) : 0;  // (a first bound below 0: nothing is summed yet)
             ref = r;
+            least = bound - 80.f;
+            round = ROUND - (float)r;
         }
     };
     // A listed logit's key; the list holds the index alone until it is first looked through.
@@ -347,16 +363,14 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
         }
         if (!slow && strict) rest += __float2ull_rn((a[0] + a[1]) * 0x1p44f);
         room -= threads * E;
-        if (room < p.limit * E || (piece >= 3 && (piece & (piece + 1)) == 0)) {
+        if (room < p.limit * E) {
             __syncthreads();
-            if (room < p.limit * E || piece + 1 < pieces) {
-                shrink(false);
+            shrink(false);
+            room = p.cap - s.count;
+            if (room < p.limit * E) {
+                __syncthreads();  // the count is read
+                shrink(true);
                 room = p.cap - s.count;
-                if (room < p.limit * E) {
-                    __syncthreads();  // the count is read
-                    shrink(true);
-                    room = p.cap - s.count;
-                }
             }
         }
     }
@@ -434,7 +448,8 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const Beam
     double *s_add = reinterpret_cast<double *>(mk_smem);            // [64]: a beam's score less its log sum of exp(z - top)
     float *s_top = reinterpret_cast<float *>(s_add + BM_MAXBEAMS);  // [64]
     int *s_state = reinterpret_cast<int *>(s_top + BM_MAXBEAMS);    // [64]: 2 extended, 1 finished, 0 neither
-    uint32_t *s_table = reinterpret_cast<uint32_t *>(s_state + BM_MAXBEAMS);  // [32]
+    float *s_fast = reinterpret_cast<float *>(s_state + BM_MAXBEAMS);         // [64]: s_add in fp32
+    uint32_t *s_table = reinterpret_cast<uint32_t *>(s_fast + BM_MAXBEAMS);   // [32]
     uint32_t *s_red = s_table + 32;                                 // [32]
     unsigned long long *total = reinterpret_cast<unsigned long long *>(s_red + 32);  // [all]: ordered
     int *list = reinterpret_cast<int *>(total + all);               // [all]: those that reach the bound
@@ -456,7 +471,7 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const Beam
     for (int w = tid / 32; w < W; w += BM_MERGE_THREADS / 32) {
         const float score = p.scores[row0 + w];
         if (s_state[w] != 2) {
-            if (lane == 0) s_add[w] = score;
+            if (lane == 0) s_add[w] = s_fast[w] = score;
             continue;
         }
         const BeamPart *r = p.rows + (row0 + w) * S;
@@ -479,32 +494,76 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const Beam
         sum = warp_sum64(sum);
         if (lane == 0) {
             s_add[w] = sum ? (double)score - log_sum(sum, s_table) : 0.0;
+            s_fast[w] = (float)s_add[w];
             s_top[w] = top;
         }
     }
     __syncthreads();
-    uint32_t most = 0;  // the thread's largest total, to fp32, ordered
-    for (int i = tid; i < all; i += BM_MERGE_THREADS) {
-        const int w = i / per;
-        const unsigned long long k = i == tid ? ahead : key_of(i);
-        unsigned long long t = none;
-        if (k != KEY_NONE) {
-            const float z = key_value(k), top = s_top[w];
-            const double d = s_state[w] == 1 || z == top ? 0.0 : (double)z - (double)top;
-            const double sum = d + s_add[w];
-            t = ordered64(sum);
-            if (t > none) most = max(most, ordered_bits((float)sum));
+    // First in fp32: a total a with its error e, of which total[i] holds a - e and
+    // a + e, ordered (0: not a candidate).  FP64 is slow on this GPU, so it forms the
+    // few totals alone that may be among the first.
+    const auto exact = [&](int w, float z) {
+        const float top = s_top[w];
+        return (s_state[w] == 1 || z == top ? 0.0 : (double)z - (double)top) + s_add[w];
+    };
+    uint32_t most = 0;  // the thread's largest a - e
+    constexpr int U = 4;
+    for (int i0 = tid; i0 < all; i0 += U * BM_MERGE_THREADS) {
+        unsigned long long key[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * BM_MERGE_THREADS;
+            key[u] = i == tid ? ahead : i < all ? key_of(i) : KEY_NONE;
         }
-        total[i] = t;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * BM_MERGE_THREADS, w = i / per;
+            if (i >= all) continue;
+            uint32_t low = 0, high = 0;
+            if (key[u] != KEY_NONE) {
+                const float z = key_value(key[u]), top = s_top[w], c = s_fast[w];
+                const float d = s_state[w] == 1 || z == top ? 0.f : z - top;
+                float a = d + c, e = 0x1p-22f * (fabsf(d) + fabsf(c));  // (three roundings of 2^-24, and those of a - e and a + e)
+                if (!(fabsf(a) + e < INFINITY)) {
+                    const double t = exact(w, z);
+                    a = (float)t, e = 0.f;
+                    if (!(t > -INFINITY)) key[u] = KEY_NONE;
+                }
+                if (key[u] != KEY_NONE) low = ordered_bits(a - e), high = ordered_bits(a + e);
+            }
+            most = max(most, low);
+            total[i] = (unsigned long long)high << 32 | low;
+        }
     }
-    // a bound that num threads' largest reach: what reaches it is listed
+    // a bound that num threads' largest reach: what may reach it is listed
+    const int limit = K + K / 2 + 4;
     uint32_t lo = 1;
-    if (__syncthreads_count(most > 0) > K + K / 2 + 4) bisect<BM_MERGE_THREADS / 32>(most, lo, K, K + K / 2 + 4, s_red);
-    if (most >= lo)
-        for (int i = tid; i < all; i += BM_MERGE_THREADS)
-            if (total[i] > none && ordered_bits((float)unordered64(total[i])) >= lo) list[atomicAdd(&s_count, 1)] = i;
+    if (__syncthreads_count(most > 0) > limit) bisect<BM_MERGE_THREADS / 32>(most, lo, K, limit, s_red);
+    for (int i = tid; i < all; i += BM_MERGE_THREADS)
+        if ((uint32_t)(total[i] >> 32) >= lo) list[atomicAdd(&s_count, 1)] = i;
     __syncthreads();
-    const int n = s_count;
+    int n = s_count;
+    // The threads' candidates have like places in their parts' lists, so that many
+    // may be listed: once more among these.
+    if (n > 2 * limit) {
+        most = 0;
+        for (int x = tid; x < n; x += BM_MERGE_THREADS) most = max(most, (uint32_t)total[list[x]]);
+        if (__syncthreads_count(most >= lo) > limit) bisect<BM_MERGE_THREADS / 32>(most, lo, K, limit, s_red);
+        __syncthreads();
+        if (tid == 0) s_count = 0;
+        for (int x0 = 0; x0 < n; x0 += BM_MERGE_THREADS) {
+            const int i = x0 + tid < n ? list[x0 + tid] : -1;
+            __syncthreads();
+            if (i >= 0 && (uint32_t)(total[i] >> 32) >= lo) list[atomicAdd(&s_count, 1)] = i;
+        }
+        __syncthreads();
+        n = s_count;
+    }
+    for (int x = tid; x < n; x += BM_MERGE_THREADS) {
+        const int i = list[x];
+        total[i] = ordered64(exact(i / per, key_value(key_of(i))));
+    }
+    __syncthreads();
     // Of equal totals the lower beam comes first, and within a beam the key.
     for (int x = tid; x < n; x += BM_MERGE_THREADS) {
         const int i = list[x], w = i / per;
@@ -530,7 +589,7 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const Beam
 }
 
 // Parts of a row.  As many CTAs as the GPU holds at once (3 an SM; 128 rows of
-// 151,936 fp32 logits: 33.9 us, with twice as many 40.1, three times 44.2), no
+// 151,936 fp32 logits: 29.1 us, with twice as many 36.3), no
 // shorter parts than a piece, and no more candidates than the second launch
 // holds.
 static void beam_parts(const mk_beam_desc *d, int &parts, int &chunk) {
@@ -612,7 +671,7 @@ int mk_beam_select(const mk_beam_desc *d, void *workspace, uint64_t workspace_by
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)d->batch);
     cfg.blockDim = dim3(BM_MERGE_THREADS);
-    cfg.dynamicSmemBytes = BM_MAXBEAMS * 16 + 64 * 4 + p.beams * p.parts * p.num * 12 + 4;
+    cfg.dynamicSmemBytes = BM_MAXBEAMS * 20 + 64 * 4 + p.beams * p.parts * p.num * 12 + 4;
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
