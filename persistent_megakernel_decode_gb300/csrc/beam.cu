@@ -68,7 +68,7 @@ struct alignas(16) BeamShared {  // the lists lie behind it
     uint32_t table[32];
     unsigned long long red[2][BM_WARPS];
     uint32_t red_u[2 * BM_WARPS];
-    unsigned long long first;
+    unsigned long long first, dropped;  // dropped: what left the list, in units like `rest`
     int count, shrunk;
 };
 
@@ -102,15 +102,17 @@ DEV uint32_t block_sum(uint32_t v, uint32_t *red) {
     return sum;
 }
 
-// A bound from lo up that at least `num` and at most `limit` threads' values
-// (ordered) reach, given that more than `limit` reach lo; false: more than
-// `limit` reach the bound, fewer than `num` exceed it.  The middle is first
-// that of the values between the threads' least and largest, where logits lie
-// evenly enough to be done in some five steps; then that of the 32-bit integers.
-template <int WARPS>
-DEV bool bisect(uint32_t mine, uint32_t &lo, int num, int limit, uint32_t *red) {
+// A bound that at least `num` and at most `limit` values (ordered) reach, given
+// that more than `limit` do in all; false: more than `limit` reach the bound, fewer
+// than `num` exceed it.  hi and least: of the thread's values; count: of the
+// block's that reach a bound.  The middle is first that of the values between the
+// least and the largest, where logits lie evenly enough to be done in some five
+// steps; then that of the 32-bit integers.
+template <int WARPS, typename Count>
+DEV bool bisect_by(uint32_t hi, uint32_t least, uint32_t &lo, int num, int limit, uint32_t *red, const Count &count) {
     const int lane = threadIdx.x % 32;
-    uint32_t hi = __reduce_max_sync(FULL, mine), least = __reduce_min_sync(FULL, mine >= lo ? mine : ~0u);
+    hi = __reduce_max_sync(FULL, hi);
+    least = __reduce_min_sync(FULL, least);
     __syncthreads();
     if (lane == 0) {
         red[threadIdx.x / 32] = hi;
@@ -126,7 +128,7 @@ DEV bool bisect(uint32_t mine, uint32_t &lo, int num, int limit, uint32_t *red) 
     for (int step = 0; lo < hi; ++step) {
         uint32_t mid = lo + (hi - lo + 1) / 2;
         if (step < 10) mid = min(max(ordered_bits(0.5f * ordered_value(lo) + 0.5f * ordered_value(hi)), lo + 1), hi);
-        const int n = __syncthreads_count(mine >= mid);
+        const int n = count(mid);
         if (n > limit) {
             lo = mid;
         } else if (n >= num) {
@@ -137,6 +139,11 @@ DEV bool bisect(uint32_t mine, uint32_t &lo, int num, int limit, uint32_t *red) 
         }
     }
     return false;
+}
+// A value of each thread, of those that reach lo.
+template <int WARPS>
+DEV bool bisect(uint32_t mine, uint32_t &lo, int num, int limit, uint32_t *red) {
+    return bisect_by<WARPS>(mine, mine >= lo ? mine : ~0u, lo, num, limit, red, [&](uint32_t mid) { return __syncthreads_count(mine >= mid); });
 }
 
 constexpr uint32_t LEAST = 0x00800000u;  // the least value above -inf, ordered
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
     };
     load(0);
     if (tid < 32) s.table[tid] = c_table[tid];
-    if (tid == 0) s.count = 0;
+    if (tid == 0) s.count = 0, s.dropped = 0;
     constexpr float CH = 1.44269502162933349609375f, CL = 1.92596303350011e-08f;  // log2(e)
     // All of these are the same in every thread but `rest`.
     float bound = ordered_value(LEAST);
@@ -215,7 +222,9 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
         slow = slow || !(fabsf(bound) <= 1e5f);
         if (!slow) {
             const int r = (int)ceilf(bound * CH);
-            rest = r - ref < 64 ? rest >> max(r - ref, 0) : 0;  // (a first bound below 0: nothing is summed yet)
+            const auto shift = [&](unsigned long long x) { return r - ref < 64 ? x >> max(r - ref, 0) : 0; };
+            rest = shift(rest);  // (a first bound below 0: nothing is summed yet)
+            if (tid == 0) s.dropped = shift(s.dropped);
             ref = r;
             least = bound - 80.f;
             round = ROUND - (float)r;
@@ -243,15 +252,18 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
         }
         __syncthreads();
     };
-    // The bound up to what the threads' largest of the listed allow, the list
-    // down to it; `hard`: down to the num first, where few threads list them.
+    // The bound up to what the listed allow, the list down to it; `hard`: down to
+    // the num first, where many are equal.  Nothing here may depend on the order of
+    // the list, which is that of the atomics.
     const auto shrink = [&](bool hard) {
         const int n = s.count;
-        unsigned long long first_key = KEY_NONE;
+        const int most = p.num + p.num / 2 + 4;
+        uint32_t hi = 0, least = ~0u;
         for (int i = tid; i < n; i += BM_THREADS) {
             const unsigned long long key = key_at(i);
             cand[i] = key;
-            first_key = min(first_key, key);
+            hi = max(hi, ~(uint32_t)(key >> 32));
+            least = min(least, ~(uint32_t)(key >> 32));
         }
         if (tid == 0) s.shrunk = 0;
         hard = hard && n > p.num;
@@ -263,15 +275,16 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
                 if (ranks[i] == p.num - 1) s.red_u[0] = ~(uint32_t)(cand[i] >> 32);
             __syncthreads();
             raise_to(s.red_u[0]);
-        } else {
-            const uint32_t mine = first_key == KEY_NONE ? 0 : ~(uint32_t)(first_key >> 32);
-            if (__syncthreads_count(mine >= floor) > p.num) {
-                uint32_t lo = floor;
-                bisect<BM_WARPS>(mine, lo, p.num, p.num + p.num / 2 + 4, s.red_u);
-                if (lo > floor) raise_to(lo);
-            }
+        } else if (n > most) {
+            uint32_t lo = floor;
+            bisect_by<BM_WARPS>(hi, least, lo, p.num, most, s.red_u, [&](uint32_t mid) {
+                uint32_t c = 0;
+                for (int i = tid; i < n; i += BM_THREADS) c += ~(uint32_t)(cand[i] >> 32) >= mid;
+                return (int)block_sum(c, s.red_u);
+            });
+            if (lo > floor) raise_to(lo);
         }
-        float a = 0.f;
+        unsigned long long gone = 0;  // (as integers, and to one sum: which thread has which is not known)
         for (int i0 = 0; i0 < n; i0 += BM_THREADS) {
             const bool there = i0 + tid < n;
             const unsigned long long key = there ? cand[i0 + tid] : KEY_NONE;
@@ -280,10 +293,11 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
             if (there) {
                 const float z = key_value(key);
                 if (z >= bound && !out) cand[atomicAdd(&s.shrunk, 1)] = key;
-                else if (!slow) a += term(z);
+                else if (!slow) gone += __float2ull_rn(term(z) * 0x1p44f);
             }
         }
-        rest += __float2ull_rn(a * 0x1p44f);
+        gone = warp_sum64(gone);
+        if (lane == 0 && gone) atomicAdd(&s.dropped, gone);
         __syncthreads();
         if (tid == 0) s.count = s.shrunk;
         __syncthreads();
@@ -409,7 +423,7 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
         if (ranks[i] < p.num) to[ranks[i]] = cand[i];
     for (int i = kept + tid; i < p.num; i += BM_THREADS) to[i] = KEY_NONE;
     if (tid == 0) {
-        BeamPart r{top, ref, 0, 0};
+        BeamPart r{top, ref, 0, slow ? 0 : s.dropped};
         for (int i = 0; i < BM_WARPS; ++i) {
             r.list += s.red[0][i];
             r.rest += s.red[1][i];

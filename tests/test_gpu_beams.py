@@ -180,6 +180,22 @@ def test_select_sum_of_exponentials_is_good_to_a_few_2_28():
     assert wrong == 0
 
 
+@pytest.mark.parametrize("w, v, num", [(8, 40000, 128), (64, 300, 128), (8, 151936, 16), (2, 9000, 100)])
+@pytest.mark.parametrize("step", [0.0, 2.0 ** -21])
+def test_select_beams_that_are_almost_equal(w, v, num, step):
+    """The same logits after every beam, scores equal or an fp32 step at 4 to 8 apart: totals that fp32 would not tell apart."""
+    z = logits_of(1, v, seed=v).expand(w, v).contiguous()
+    check_select(z, -5 - step * torch.arange(w, dtype=torch.float32)[None], num)
+
+
+def test_select_totals_beyond_fp32():
+    """Differences of logits that overflow fp32: in order, and -inf only as their rounded score."""
+    z = torch.tensor([[3e38, -3e38, 0.0, -2e38], [1.0, 1.0, -3e38, 2.0]])
+    s, p, t = (x.cpu() for x in rt.beam_select(z.to(DEV), torch.tensor([[-1.0, -2.0]], device=DEV), 8))
+    assert p.tolist() == [[0, 1, 1, 1, 0, 1, 0, 0]] and t.tolist() == [[0, 3, 0, 1, 2, 2, 3, 1]]
+    assert s[0, 0] == -1 and s[0, 4] == s[0, 5] == torch.tensor(-3e38) and s[0, 6] == s[0, 7] == -math.inf
+
+
 def test_select_nothing_to_do():
     out = rt.beam_select(torch.zeros(0, 10, device=DEV), torch.zeros(0, 4, device=DEV), 4)
     assert [tuple(x.shape) for x in out] == [(0, 4)] * 3
