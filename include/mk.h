@@ -592,13 +592,15 @@ int mk_cache_attend(const mk_cache_desc *cache, int layer, const mk_attend_desc 
 typedef struct {
     uint64_t first;               /* device int32 [groups + 1], not falling, within 0 .. batch */
     uint64_t shared;              /* device int32 [groups] */
-    int groups;                   /* at most batch, and 1024 less it */
+    int groups;                   /* at most batch, and batch + groups at most 1024 */
 } mk_shared_desc;
 
 /* mk_cache_attend (the same results but for rounding: same masks, checks and
  * precision; window and sinks must be 0), with the pages that a group shares
- * read once for all of its rows (no counterpart on the pages).  A group list
- * that falls or leaves 0 .. batch, or a negative shared length, is a failed
+ * read once for all of its rows (no counterpart on the pages).  Where the rows
+ * of a group are many, a probability over its shared pages is rounded to 2^-11
+ * of itself or 2^-32 of the row's largest product of weight and V scale.  A
+ * group list that falls or leaves 0 .. batch, or a negative shared length, is a failed
  * check: nothing is shared then (in that group).  Workspace like
  * mk_cache_attend's, of its own size. */
 int mk_cache_attend_shared_workspace(const mk_cache_desc *cache, const mk_attend_desc *attend,

@@ -17,9 +17,10 @@
 // (each row split into two e4m3 halves at scales 1 and 1/16, one in row g and
 // one in row g + 8), needs no conversion in the source but executed 1460
 // instructions a page and warp against about 1000 here, and is less exact
-// (2^-8).  tcgen05 is not used: its tiles take 64 rows or more of an operand
-// from shared memory, a decode step has 4 to 16, and scores would cross tensor
-// memory between the two products; bytes bound a decode step either way.
+// (2^-8).  tcgen05 is not used here: its tiles take 64 rows or more of an
+// operand from shared memory, a decode step has 4 to 16, and scores would cross
+// tensor memory between the two products; bytes bound a decode step either way.
+// (prefix.cu uses it, for the pages that large groups of sequences share.)
 //
 // Token order.  A contraction may run over tokens in any order, so row (m, u,
 // g) of the score tile (16-row step m, half u, row g) is token (P/4)(g/2) + 4m
@@ -30,18 +31,28 @@
 // Work split.  The pages of all units (sequence, row tile, kv head) form one
 // axis, each weighted with the warps its tile occupies side by side, and with
 // a constant for beginning and merging a unit, cut into equal ranges, one per
-// CTA (one CTA per SM): ragged batches and single long sequences balance alike.  A producer warp streams the pages through a
-// shared-memory ring with bulk copies; the consumer warps take them in turn
-// (as many side by side as the tile's rows need) and merge in shared memory.
-// A page that a tile does not see, or whose number is out of range, takes its
-// turn in the ring without being loaded.
+// CTA (one CTA per SM): ragged batches and single long sequences balance alike.
+// A producer warp streams the pages through a shared-memory ring with bulk
+// copies; the consumer warps take them in turn (as many side by side as the
+// tile's rows need) and merge in shared memory.  A page that a tile does not
+// see, or whose number is out of range, takes its turn in the ring without
+// being loaded.  With sinks, a unit's pages are those of the sinks and those
+// from the window's first on; the pages between are no items at all.
 // A unit that one CTA covers is written at once; ranges cut by a CTA boundary
 // go to the workspace and a second small launch (dependent launch, so that its
 // start overlaps) merges them in order: results do not depend on timing.
 //
+// Shared prefixes.  Groups' shared pages are units of one launch (the page
+// kernel's tiles, or prefix.cu's), what sequences have behind them are units of
+// another, and the merge joins both.  The two run beside each other, on SMs that
+// the device shares out by the items of each at their measured costs
+// (dev_attend.cuh); an own part is short, so two CTAs of four warps take them on
+// an SM (64 sequences of 16,000 shared tokens and 100-2,000 of their own: 82 us,
+// with one CTA of eight warps 85; 4 x 8 beams: 43.7 and 45).
+//
 // Measured (one GB300, device time): 16 sequences of 16-32K tokens, 32 q / 8
-// kv heads of 128: 128 us, 6.1 TB/s, 90 % of the copy rate; 8 sequences of
-// 512-4096, heads of 64: 13.0 us, of which the bytes are 2.8
+// kv heads of 128: 125 us, 6.3 TB/s, 93 % of the copy rate; 8 sequences of
+// 512-4096, heads of 64: 13.5 us, of which the bytes are 2.8
 // (two launches, two dependent look-ups, the ramp of the loads and the merge
 // are the rest); 64 new tokens a sequence over 4000: 190 TFLOP/s, bound by the
 // instructions per product that a 16-row operand held in registers costs; a
@@ -101,7 +112,8 @@ static int att_plan(const mk_cache_desc *c, const mk_attend_desc *a, int ngroups
     // no more CTAs than pages there can be (all tiles' together, each as many items as it has warps side by side)
     const int64_t side = pl.rt == 64 ? 4 : pl.rt == 32 ? 2 : 1;
     const int64_t tiles = a->batch + (int64_t)a->tokens * group / pl.rt;
-    pl.ctas = (int)std::min<int64_t>(ngroups ? 2 * sms : sms, std::max<int64_t>(1, std::min<int64_t>(tiles * c->kv_heads, INT32_MAX) * (a->table_width * side + att_fixed_items(pl.rt))));
+    const int64_t items = std::min<int64_t>(tiles * c->kv_heads, INT32_MAX) * (a->table_width * side + att_fixed_items(pl.rt));
+    pl.ctas = (int)std::min<int64_t>(ngroups ? 2 * sms : sms, std::max<int64_t>(1, items));
     pl.ml_bytes = ((uint64_t)pl.ctas * 2 * pl.rt * 8 + 255) / 256 * 256;
     pl.o_bytes = (uint64_t)pl.ctas * 2 * pl.rt * c->head_dim * 4;
     const uint64_t row_parts = ngroups ? 2ull * a->tokens * a->q_heads : 0;

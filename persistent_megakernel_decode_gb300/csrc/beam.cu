@@ -19,15 +19,15 @@
 // logits that reach it (at most as many per thread as it holds) are listed.
 // Later pieces of the part list what is above the bound; when the list is full
 // the bound rises to what the listed allow, and the list shrinks to it (doing so
-// now and then, before, cost more than it saved: 31.6 us for 29.1 below).  At the
+// now and then, before, cost more than it saved: 31.6 us where 29.1 do).  At the
 // end the list is ranked by comparing each with all.
 //
 // Work split.  A CTA streams a part of a row, 4096 logits at a time in
 // registers, the next piece's loads in flight.  A second, dependent launch orders
 // a prompt's candidates, one CTA each.  Each logit is read once, so bytes bound
-// it: 64 x 8 beams of 151,936 logits take 58 us, 5.4 TB/s.  16 x 8 take 29, of
+// it: 64 x 8 beams of 151,936 logits take 59 us, 5.3 TB/s.  16 x 8 take 30, of
 // which the bytes are 10: the rest is the ramp of two launches, the bisection and
-// the rank of each part's list (barriers), and 26 instructions a logit.  Three
+// the rank of each part's list (barriers), and 22 instructions a logit.  Three
 // CTAs an SM in one wave are the best split (six: 36 us; one cluster a row, in
 // registers: 52-99).
 #include <algorithm>
@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
         } else if (n > most) {
             uint32_t lo = floor;
             bisect_by<BM_WARPS>(hi, least, lo, p.num, most, s.red_u, [&](uint32_t mid) {
+                if (n <= BM_THREADS) return __syncthreads_count(hi >= mid);
                 uint32_t c = 0;
                 for (int i = tid; i < n; i += BM_THREADS) c += ~(uint32_t)(cand[i] >> 32) >= mid;
                 return (int)block_sum(c, s.red_u);

@@ -8,7 +8,8 @@ namespace mk {
 // Consumer warps of a CTA.  What sequences have behind a shared prefix is short:
 // two CTAs of four on an SM have two of those units in work.
 __host__ __device__ constexpr int att_warps(AttKind kind) { return kind == ATT_OWN ? 4 : 8; }
-__host__ __device__ constexpr int att_threads(AttKind kind) { return (att_warps(kind) + 4) * 32; }  // + the producer's warpgroup, of which one warp works
+// + the producer's warpgroup, of which one warp works
+__host__ __device__ constexpr int att_threads(AttKind kind) { return (att_warps(kind) + 4) * 32; }
 constexpr int ATT_MAXRING = 32;                     // pages in the ring (one producer lane each)
 
 // Tiles of rt rows: 8 NT rows a warp, up to rt / (8 NT) warps side by side

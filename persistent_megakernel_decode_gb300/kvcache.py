@@ -134,10 +134,10 @@ class Kv8Cache:
         the last T of them are the queries.  ``q`` is bf16 [B, T, Hq, D], or with ``q_start`` (int32 [B + 1]) packed
         [total, Hq, D], sequence b's queries being rows q_start[b] .. q_start[b + 1] - 1 (``max_tokens``: the most of
         one sequence, a hint for the height of the tiles and so for the workspace; default: all rows).  ``window`` > 0:
-        a query sees that many last tokens, itself among them, and the sequence's first ``sinks`` ones.  Returns (out bf16 like q, lse fp32 without the last
-        axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8 tensor of at least
-        :meth:`attend_workspace` bytes, used by one call at a time; by default calls on the default stream share one
-        that the cache keeps, others allocate their own."""
+        a query sees that many last tokens, itself among them, and the sequence's first ``sinks`` ones.  Returns (out bf16
+        like q, lse fp32 without the last axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8 tensor of
+        at least :meth:`attend_workspace` bytes, used by one call at a time; by default calls on the default stream share
+        one that the cache keeps, others allocate their own."""
         if stream is not None and not rt.is_current(self.index, stream):
             return self._beside(stream, self.attend, q, table, lens, layer, q_start, max_tokens, scale, window, out, lse,
                                 workspace, None, sinks)
