@@ -712,7 +712,8 @@ int mk_sample(const mk_sample_desc *sample, void *stream);
  * behind the last where there are fewer.  NaN logits count as -inf; where the
  * largest logit is +inf, those that are share the probability.
  * Precision: totals are compared in 64 bits, with the sum of exponentials good
- * to about 2^-28 of itself; scores are rounded to fp32 at the end. */
+ * to 2^-27 of itself (repeated logits too); scores are rounded to fp32 at the
+ * end. */
 typedef struct {
     uint64_t logits;              /* device, [batch x beams, vocab], row stride below */
     int64_t row_stride;           /* elements, >= vocab */

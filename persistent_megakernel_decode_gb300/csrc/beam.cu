@@ -8,11 +8,19 @@
 //
 // The order between beams hangs on the sums: two totals closer than their
 // errors would change places.  Totals are therefore formed in 64 bits, and the
-// sum is kept to a few 2^-28 of itself: a part's largest logits (where single
-// rounding errors weigh) by the fixed-point weights of dev_weigh.cuh, the rest
-// as fp32 2^f after a two-part reduction of the argument, whose errors (2^-23
-// of a term, either way) average out; partial sums are joined as integers, so
-// no order of arrival changes anything.
+// sum is kept to 2^-27 of itself whatever the logits are: equal ones have equal
+// errors, which add up (rows of few values, masked tails, bf16), so no error may
+// be left to averages.  A part's largest logits are weighed by the fixed-point
+// weights of dev_weigh.cuh (2^-30).  The rest are fp32 w (1 + r), w a power of
+// 2^(1/32) from a table and r the rest of it from a polynomial: log2(e) in two
+// parts for the argument (Cody and Waite's reduction), a table with a short
+// polynomial (Tang's exponential).  What a product and a polynomial round away
+// is then 2^-24 of r, 2^-6.5 or less; the w are added with what each addition
+// loses (Dekker's sum of two).  In all 2^-28.6 a term, and 2^-28.7 for the chain
+// of eight small parts.  Partial sums are joined as integers, so no order of
+// arrival changes anything.  (With the hardware's 2^f, off by up to 2^-22, the
+// sum of a flat row was off by 2^-22.6 and of a normal one by 2^-26, and 16 x 8
+// beams took 29.7 us where they take 38.7.)
 //
 // The largest without sorting: a bound that at least `num` threads' largest
 // values reach is found by bisection, one barrier and vote a step; the few
@@ -25,11 +33,12 @@
 // Work split.  A CTA streams a part of a row, 4096 logits at a time in
 // registers, the next piece's loads in flight.  A second, dependent launch orders
 // a prompt's candidates, one CTA each.  Each logit is read once, so bytes bound
-// it: 64 x 8 beams of 151,936 logits take 59 us, 5.3 TB/s.  16 x 8 take 30, of
-// which the bytes are 10: the rest is the ramp of two launches, the bisection and
-// the rank of each part's list (barriers), and 22 instructions a logit.  Three
-// CTAs an SM in one wave are the best split (six: 36 us; one cluster a row, in
-// registers: 52-99).
+// it from below; 64 x 8 beams of 151,936 logits take 82 us, 3.4 TB/s, and 16 x 8
+// 39, of which the bytes are 10: 33 instructions a logit (multiplies and adds
+// above all; as instructions on register pairs throughout 40.6 us), the ramp of
+// two launches, the bisection and the rank of each part's list (barriers).  Three
+// CTAs an SM in one wave are the best split (with six, and a cheaper sum, 36 us
+// where three took 29; one cluster a row, in registers, 52-99).
 #include <algorithm>
 #include <climits>
 
@@ -66,6 +75,7 @@ struct BeamParams {
 
 struct alignas(16) BeamShared {  // the lists lie behind it
     uint32_t table[32];
+    uint2 powers[32];  // c_powers: the first's bits less j 2^18, the second's
     unsigned long long red[2][BM_WARPS];
     uint32_t red_u[2 * BM_WARPS];
     unsigned long long first, dropped;  // dropped: what left the list, in units like `rest`
@@ -84,11 +94,39 @@ DEV float beam_logit(float x) { return fmaxf(x, -INFINITY) + 0.f; }
 DEV float ordered_value(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o); }
 DEV float key_value(unsigned long long key) { return ordered_value(~(uint32_t)(key >> 32)); }
 
-DEV float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+// 2^(j/32): the nearest fp32, and how far the power is from it, relative to it.
+static __constant__ float2 c_powers[32] = {
+    {1.f, 0.f}, {0x1.059b0ep+0f, -4.7084576e-08f}, {0x1.0b5586p+0f, 4.628547e-08f}, {0x1.11301ep+0f, -5.5604225e-08f},
+    {0x1.172b84p+0f, -1.19921575e-08f}, {0x1.1d4874p+0f, -4.8776062e-08f}, {0x1.2387a6p+0f, 4.7297824e-08f}, {0x1.29e9ep+0f, -3.4814427e-08f},
+    {0x1.306fep+0f, 3.193418e-08f}, {0x1.371a74p+0f, -2.6886665e-08f}, {0x1.3dea64p+0f, 3.6210572e-08f}, {0x1.44e086p+0f, 1.118421e-09f},
+    {0x1.4bfdaep+0f, -3.099072e-08f}, {0x1.5342b6p+0f, -2.638301e-08f}, {0x1.5ab07ep+0f, -7.475213e-09f}, {0x1.6247ecp+0f, -4.2456357e-08f},
+    {0x1.6a09e6p+0f, 1.7114271e-08f}, {0x1.71f75ep+0f, 2.3001967e-08f}, {0x1.7a1148p+0f, -3.0476834e-08f}, {0x1.82589ap+0f, -1.6538538e-08f},
+    {0x1.8ace54p+0f, 5.233334e-09f}, {0x1.93737cp+0f, -3.5920646e-08f}, {0x1.9c4918p+0f, 6.1075918e-09f}, {0x1.a5503cp+0f, -3.1140544e-08f},
+    {0x1.ae89fap+0f, -1.4719605e-08f}, {0x1.b7f77p+0f, -2.8218102e-08f}, {0x1.c199bep+0f, -5.258795e-09f}, {0x1.cb720ep+0f, -6.3603873e-09f},
+    {0x1.d5818ep+0f, -6.1282597e-09f}, {0x1.dfc974p+0f, -2.4880409e-08f}, {0x1.ea4afap+0f, 5.1406093e-09f}, {0x1.f50766p+0f, -8.697267e-09f}};
+
+// Two fp32 numbers of a register pair, an instruction for both.
+struct Pair {
+    unsigned long long b;
+    DEV Pair() {}
+    DEV Pair(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(x), "f"(y)); }
+    DEV float2 both() const {
+        float2 f;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(b));
+        return f;
+    }
+};
+DEV Pair pair_fma(Pair x, Pair y, Pair z) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(x.b), "l"(y.b), "l"(z.b));
+    return r;
 }
+DEV Pair pair_add(Pair x, Pair y) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(x.b), "l"(y.b));
+    return r;
+}
+DEV Pair operator-(Pair x, Pair y) { return pair_fma(y, Pair(-1.f, -1.f), x); }  // (exact as a subtraction is)
 
 // Sum over the block (every thread gets it).
 DEV uint32_t block_sum(uint32_t v, uint32_t *red) {
@@ -198,7 +236,10 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
         }
     };
     load(0);
-    if (tid < 32) s.table[tid] = c_table[tid];
+    if (tid < 32) {
+        s.table[tid] = c_table[tid];
+        s.powers[tid] = make_uint2(__float_as_uint(c_powers[tid].x) - ((uint32_t)tid << 18), __float_as_uint(c_powers[tid].y));
+    }
     if (tid == 0) s.count = 0, s.dropped = 0;
     constexpr float CH = 1.44269502162933349609375f, CL = 1.92596303350011e-08f;  // log2(e)
     // All of these are the same in every thread but `rest`.
@@ -207,14 +248,49 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
     bool slow = false;               // logits too large for the products below
     int ref = 0, room = p.cap;       // room: entries that the list has at least
     unsigned long long rest = 0;
-    // 2^(x log2(e) - ref): x log2(e) = n + f, f good to 2^-26; e^-80 below the bound is nothing (-inf and NaN too)
-    constexpr float ROUND = 12582912.f;  // its bits shifted left by 23 are 0
-    float least = 0.f, round = ROUND;    // bound - 80, ROUND - ref
-    const auto term = [&](float z) {
-        const float x = fmaxf(z, least);
-        const float t = fmaf(x, CH, round), k = t - round;
-        const float f = fmaf(x, CL, fmaf(x, CH, -k));
-        return __int_as_float(__float_as_int(exp2_approx(f)) + (__float_as_int(t) << 23));
+    // 2^(x log2(e) - ref), as a power w of 2^(1/32) and how far it is from that,
+    // relative to w: x log2(e) 32 = k + g with an integer k, g in [-0.5, 0.5] from
+    // log2(e) in two parts, 2^(g/32) - 1 by its series (ln 2 / 32 and so on; the
+    // fourth term's mean is in the second's factor).  e^-42 below the bound is
+    // nothing (-inf and NaN too).
+    constexpr float ROUND = 12582912.f;  // 1.5 2^23: a sum with it is rounded to an integer; its bits shifted left by 18 are 0
+    float least = 0.f, round = ROUND;    // bound - 42, ROUND - 32 ref
+    const auto power = [&](float z, float &w, float &r) {
+        const float x = fmaxf(z, least), t = fmaf(x, 32.f * CH, round);
+        const float g = fmaf(x, 32.f * CL, fmaf(x, 32.f * CH, round - t));
+        const uint2 p = s.powers[__float_as_uint(t) & 31];
+        w = __uint_as_float(p.x + (__float_as_uint(t) << 18));
+        r = fmaf(g, fmaf(g, fmaf(g, 1.693851e-6f, 2.3459810e-4f), 0.02166084939f), __uint_as_float(p.y));
+    };
+    const auto term = [&](float z) {  // in 2^-44
+        float w, r;
+        power(z, w, r);
+        w *= 0x1p44f;
+        return (unsigned long long)(__float2ll_rn(w) + __float2ll_rn(w * r));
+    };
+    // The terms of v, of which the largest is `most`.  Sums of w next to 2^6 of
+    // that are exact with what each addition loses, which goes to the small parts'
+    // sum.  Both are joined in 32-bit units of the largest (a conversion to 64 bits
+    // is FP64's, which is slow).
+    const auto terms = [&](const float (&v)[E], float most) {
+        const float high = fmaf(fmaxf(fminf(most, bound), least), 32.f * CH, round);
+        const int n = __float_as_int(high) << 18 >> 23;  // below 2^(n + 1); -62 and more
+        const float c = __int_as_float((n + 133) << 23);
+        Pair big(c, c), small(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            float w0, w1, r0, r1;
+            power(v[i], w0, r0);
+            power(v[i + 1], w1, r1);
+            const Pair w(w0, w1), r(r0, r1), sum = pair_add(big, w);
+            small = pair_add(pair_fma(w, r, small), w - (sum - big));
+            big = sum;
+        }
+        const float2 a = big.both(), b = small.both();
+        const int first = __float2int_rn(((a.x - c) + (a.y - c)) * __int_as_float((144 - n) << 23));  // in 2^(n - 17): exact
+        const int second = __float2int_rn((b.x + b.y) * __int_as_float((157 - n) << 23));              // in 2^(n - 30)
+        const long long sum = (((long long)first << 13) + second) << 14;                               // in 2^(n - 44)
+        return (unsigned long long)((sum + ((1ll << -n) >> 1)) >> -n);
     };
     const auto raise_to = [&](uint32_t o) {
         bound = ordered_value(o);
@@ -226,8 +302,8 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
             rest = shift(rest);  // (a first bound below 0: nothing is summed yet)
             if (tid == 0) s.dropped = shift(s.dropped);
             ref = r;
-            least = bound - 80.f;
-            round = ROUND - (float)r;
+            least = bound - 42.f;
+            round = ROUND - 32.f * (float)r;
         }
     };
     // A listed logit's key; the list holds the index alone until it is first looked through.
@@ -294,7 +370,7 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
             if (there) {
                 const float z = key_value(key);
                 if (z >= bound && !out) cand[atomicAdd(&s.shrunk, 1)] = key;
-                else if (!slow) gone += __float2ull_rn(term(z) * 0x1p44f);
+                else if (!slow) gone += term(z);
             }
         }
         gone = warp_sum64(gone);
@@ -321,27 +397,18 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
         if (piece + 1 < pieces) load(piece + 1);
         const auto at = [&](int i) { return begin + piece * BM_PIECE + (i / VEC * BM_THREADS + tid) * VEC + i % VEC; };
         uint32_t want = 0;  // bit i: logit i is listed
-        float a[2] = {0.f, 0.f};
-        int threads = BM_THREADS;
-        if (strict) {
+        float most = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float e = term(v[i]);
-                if (v[i] > bound) want |= 1u << i;
-                else a[i % 2] += e;
-            }
-            threads = __syncthreads_count(want != 0);
-        }
+        for (int i = 0; i < E; ++i) most = fmaxf(most, v[i]);
+        int threads = strict ? __syncthreads_count(most > bound) : BM_THREADS;
+        float from = bound;  // logits above it are listed
         if (threads > p.limit || !strict) {  // the first piece, or one with many large logits: the bound from its own
-            float most = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < E; ++i) most = fmaxf(most, v[i]);
             const uint32_t mine = ordered_bits(beam_logit(most));
             uint32_t lo = ordered_bits(bound) + (strict ? 1 : 0);
-            int upto = INT_MAX;  // of the logits at the bound, those up to this index
+            bool found = true;
             threads = __syncthreads_count(mine >= lo);
             if (threads > p.limit) {
-                const bool found = bisect<BM_WARPS>(mine, lo, p.num, p.num + p.num / 2 + 4, s.red_u);
+                found = bisect<BM_WARPS>(mine, lo, p.num, p.num + p.num / 2 + 4, s.red_u);
                 raise_to(lo);
                 threads = p.limit;
                 if (!found) {  // many threads have the same largest logit
@@ -359,24 +426,30 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
                         if ((int)block_sum(n, s.red_u) >= need) z = mid;
                         else x = mid;
                     }
-                    upto = z;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const bool in = v[i] == bound && at(i) <= z;
+                        want |= (uint32_t)in << i;
+                        v[i] = in ? -INFINITY : v[i];
+                    }
                 }
             }
-            want = 0;
-            a[0] = a[1] = 0.f;
-            const float from = ordered_value(lo);
+            // those at the bound too: above the next value below it (of both zeros)
+            from = found ? ordered_value(lo - (lo == 0x80000000u ? 2 : 1)) : bound;
+        }
+        if (most > from) {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const bool in = v[i] > from || (v[i] == from && at(i) <= upto);
+                const bool in = v[i] > from;
                 want |= (uint32_t)in << i;
-                if (!in && strict) a[i % 2] += term(v[i]);  // (no bound yet: all that are finite are listed)
+                v[i] = in ? -INFINITY : v[i];  // no term
             }
         }
         if (want) {
             int to = atomicAdd(&s.count, __popc(want));
             for (; want; want &= want - 1) cand[to++] = (uint32_t)at(__ffs(want) - 1);
         }
-        if (!slow && strict) rest += __float2ull_rn((a[0] + a[1]) * 0x1p44f);
+        if (strict && !slow) rest += terms(v, most);  // (no bound yet: all that are finite are listed)
         room -= threads * E;
         if (room < p.limit * E) {
             __syncthreads();
@@ -443,6 +516,13 @@ DEV double unordered64(unsigned long long t) {
     return __longlong_as_double(t >> 63 ? t & 0x7fffffffffffffffull : ~t);
 }
 
+// x 2^(up - d), d >= 0 in 32.32 fixed point: to 2^-34 of itself, whatever d is.
+DEV unsigned long long octaves_below(unsigned long long x, long long d, int up, const uint32_t *table) {
+    const unsigned long long w = octave_weight(d & 0xffffffffll, table), hi = __umul64hi(x, w), lo = x * w;
+    const long long n = 44 - up + (d >> 32);  // 42 and more
+    return n < 64 ? hi << (64 - n) | lo >> n : n < 128 ? hi >> (n - 64) : 0;
+}
+
 // ln(sum 2^-44) for a sum of 1 and more of them: fp32's logarithm of the
 // fraction, corrected by how far its exponential is from it, so that no FP64
 // function is called (one warp's takes microseconds on this GPU).
@@ -499,12 +579,9 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const Beam
         unsigned long long sum = 0;
         for (int i = lane; i < S && top > -INFINITY; i += 32) {
             const BeamPart x = r[i];
-            const unsigned long long a = x.top > -INFINITY ? weigh(x.top) : 0;
-            sum += __umul64hi(x.list, a) << 20 | x.list * a >> 44;
-            if (x.rest) {  // 2^(ref - top log2(e)): the exponent is below 2
-                const unsigned long long b = octave_weight(max(0ll, octaves - ((long long)x.ref - 2) * (1ll << 32)), s_table);
-                sum += __umul64hi(x.rest, b) << 22 | x.rest * b >> 42;
-            }
+            if (x.top > -INFINITY) sum += octaves_below(x.list, weigh.distance(x.top, 126.f), 0, s_table);
+            // 2^(ref - top log2(e)): the exponent is below 2
+            if (x.rest) sum += octaves_below(x.rest, max(0ll, octaves - ((long long)x.ref - 2) * (1ll << 32)), 2, s_table);
         }
         sum = warp_sum64(sum);
         if (lane == 0) {

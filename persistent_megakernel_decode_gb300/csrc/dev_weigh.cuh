@@ -41,19 +41,23 @@ struct Weigher {
     float top, ch, cl;  // the row's maximum; log2(e) / temperature as a pair of fp32
     const uint32_t *table;
     DEV float octaves(float x) const { return (top - x) * ch; }  // d in fp32: monotone in x
-    // 2^44 2^-d, without branches, so that several weights overlap
-    DEV unsigned long long operator()(float x) const {
+    // d in 32.32 fixed point for d < most, else most + 1 (most: below 127)
+    DEV long long distance(float x, float most) const {
         const float dh = top - x;
         const float bp = dh - top;
         const float dl = (top - (dh - bp)) + (-x - bp);  // dh + dl = top - x exactly
-        const float t = fminf(dh * ch, 47.f);            // (NaN too) from 46 on the weight is 0
-        const float te = t < 46.f ? fmaf(dh, ch, -t) + fmaf(dh, cl, dl * ch) : 0.f;
+        const float t = fminf(dh * ch, most + 1.f);      // (NaN too)
+        const float te = t < most ? fmaf(dh, ch, -t) + fmaf(dh, cl, dl * ch) : 0.f;
         const int n = __float2int_rz(t);
-        // d in 32.32 fixed point; t - n is exact, te below 2^-17
+        // t - n is exact, te below 2^-16
         const long long d = max(0ll, ((long long)n << 32) + (long long)__float2uint_rz((t - (float)n) * 4294967296.f) +
                                          (long long)__float2int_rn(te * 4294967296.f));
-        const unsigned long long r = octave_weight(d, table);
-        return x == top ? 1ull << 44 : r;  // (the largest may be infinite)
+        return x == top ? 0 : d;  // (the largest may be infinite)
+    }
+    // 2^44 2^-d, without branches, so that several weights overlap; from d = 46 on it is 0
+    DEV unsigned long long operator()(float x) const {
+        const unsigned long long r = octave_weight(distance(x, 46.f), table);
+        return x == top ? 1ull << 44 : r;
     }
 };
 
