@@ -28,7 +28,9 @@
 // Later pieces of the part list what is above the bound; when the list is full
 // the bound rises to what the listed allow, and the list shrinks to it (doing so
 // now and then, before, cost more than it saved: 31.6 us where 29.1 do).  At the
-// end the list is ranked by comparing each with all.
+// end the list is ranked by comparing each with all; where very many are equal it
+// is cut by bisection first, here and in the second launch (4 equal flat rows of
+// 151,936 logits, 128 continuations: 0.45 ms, with comparisons alone 36).
 //
 // Work split.  A CTA streams a part of a row, 4096 logits at a time in
 // registers, the next piece's loads in flight.  A second, dependent launch orders
@@ -344,13 +346,18 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
         if (tid == 0) s.shrunk = 0;
         hard = hard && n > p.num;
         const uint32_t floor = ordered_bits(bound);
+        unsigned long long last = KEY_NONE;  // the num-th key: those behind it leave
         if (hard) {
             __syncthreads();
-            rank_all(n);
-            for (int i = tid; i < n; i += BM_THREADS)
-                if (ranks[i] == p.num - 1) s.red_u[0] = ~(uint32_t)(cand[i] >> 32);
-            __syncthreads();
-            raise_to(s.red_u[0]);
+            unsigned long long lo = 0;
+            while (lo < last) {
+                const unsigned long long mid = lo + (last - lo) / 2;
+                uint32_t c = 0;
+                for (int i = tid; i < n; i += BM_THREADS) c += cand[i] <= mid;
+                if ((int)block_sum(c, s.red_u) >= p.num) last = mid;
+                else lo = mid + 1;
+            }
+            raise_to(~(uint32_t)(last >> 32));
         } else if (n > most) {
             uint32_t lo = floor;
             bisect_by<BM_WARPS>(hi, least, lo, p.num, most, s.red_u, [&](uint32_t mid) {
@@ -365,11 +372,10 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
         for (int i0 = 0; i0 < n; i0 += BM_THREADS) {
             const bool there = i0 + tid < n;
             const unsigned long long key = there ? cand[i0 + tid] : KEY_NONE;
-            const bool out = hard && there && ranks[i0 + tid] >= p.num;
             __syncthreads();
             if (there) {
                 const float z = key_value(key);
-                if (z >= bound && !out) cand[atomicAdd(&s.shrunk, 1)] = key;
+                if (z >= bound && key <= last) cand[atomicAdd(&s.shrunk, 1)] = key;
                 else if (!slow) gone += term(z);
             }
         }
@@ -464,6 +470,10 @@ __global__ void __launch_bounds__(BM_THREADS, 3) beam_part_kernel(const BeamPara
     }
     __syncthreads();
     shrink(false);
+    if (s.count > 512) {  // many are equal: ranking them by comparing each with all would take longer
+        __syncthreads();
+        shrink(true);
+    }
     const int n = s.count, kept = min(n, p.num);
     rank_all(n);
     for (int i = tid; i < n; i += BM_THREADS)
@@ -537,6 +547,43 @@ DEV double log_sum(unsigned long long sum, const uint32_t *table) {
     return ((double)(lead - 44) * 0.6931471805599453 + (double)y) + (double)r;
 }
 
+// By the second launch's block: the list's n candidates down to those whose value
+// is at least the K-th largest, which it returns (n > K; one left of equal ones is
+// all of them).  64 steps of a barrier each; the values are formed again in each of
+// them (kept in registers, the rare case took half the time and the others 0.5 us more).
+template <typename Value>
+DEV unsigned long long narrow(int *list, int &n, int K, uint32_t *red, int &count, const Value &value) {
+    const int tid = threadIdx.x;
+    __syncthreads();  // `red` is read
+    if (tid < 3) red[tid] = 0;
+    __syncthreads();
+    unsigned long long lo = 0, hi = ~0ull;  // at least K reach lo
+    for (int step = 0; lo < hi; ++step) {
+        const unsigned long long mid = lo + (hi - lo) / 2 + 1;
+        uint32_t c = 0;
+#pragma unroll 1
+        for (int y = tid; y < n; y += BM_MERGE_THREADS) c += value(list[y]) >= mid;
+        c = __reduce_add_sync(FULL, c);
+        if (tid % 32 == 0 && c) atomicAdd(&red[step % 3], c);
+        __syncthreads();
+        if ((int)red[step % 3] >= K) lo = mid;
+        else hi = mid - 1;
+        if (tid == 0) red[(step + 2) % 3] = 0;  // the one that all have read
+    }
+    if (tid == 0) count = 0;
+    for (int y = 0; y < n; y += BM_MERGE_THREADS) {
+        const int i = y + tid < n ? list[y + tid] : -1;
+        __syncthreads();
+        if (i >= 0 && value(i) >= lo) list[atomicAdd(&count, 1)] = i;
+    }
+    __syncthreads();
+    n = count;
+    return lo;
+}
+
+// Candidates that a bound may let through.
+__host__ __device__ constexpr int beam_limit(int num) { return num + num / 2 + 4; }
+
 // One CTA per prompt: of all parts' candidates those with the largest totals.
 __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const BeamParams p) {
     const int tid = threadIdx.x, lane = tid % 32, W = p.beams, K = p.num, S = p.parts, per = S * K, all = W * per;
@@ -546,7 +593,9 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const Beam
     float *s_fast = reinterpret_cast<float *>(s_state + BM_MAXBEAMS);         // [64]: s_add in fp32
     uint32_t *s_table = reinterpret_cast<uint32_t *>(s_fast + BM_MAXBEAMS);   // [32]
     uint32_t *s_red = s_table + 32;                                 // [32]
-    unsigned long long *total = reinterpret_cast<unsigned long long *>(s_red + 32);  // [all]: ordered
+    const int limit = beam_limit(K);
+    unsigned long long *first = reinterpret_cast<unsigned long long *>(s_red + 32);  // [2 limit]: keys of the listed
+    unsigned long long *total = first + 2 * limit;                  // [all]: ordered
     int *list = reinterpret_cast<int *>(total + all);               // [all]: those that reach the bound
     int &s_count = list[all];
     const int64_t row0 = (int64_t)blockIdx.x * W;
@@ -628,7 +677,6 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const Beam
         }
     }
     // a bound that num threads' largest reach: what may reach it is listed
-    const int limit = K + K / 2 + 4;
     uint32_t lo = 1;
     if (__syncthreads_count(most > 0) > limit) bisect<BM_MERGE_THREADS / 32>(most, lo, K, limit, s_red);
     for (int i = tid; i < all; i += BM_MERGE_THREADS)
@@ -653,19 +701,32 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const Beam
     }
     for (int x = tid; x < n; x += BM_MERGE_THREADS) {
         const int i = list[x];
-        total[i] = ordered64(exact(i / per, key_value(key_of(i))));
+        const unsigned long long key = key_of(i);
+        total[i] = ordered64(exact(i / per, key_value(key)));
+        if (x < 2 * limit) first[x] = key;
     }
     __syncthreads();
-    // Of equal totals the lower beam comes first, and within a beam the key.
+    // Of equal totals the lower beam comes first, and within a beam the key.  Where
+    // that leaves many (flat rows), the list down to the K first by one after the
+    // other, each by bisection.
+    if (n > 2 * limit) {
+        const unsigned long long least = narrow(list, n, K, s_red, s_count, [&](int i) { return total[i]; });
+        const int beam = W - (int)narrow(list, n, K, s_red, s_count, [&](int i) {
+                             return total[i] > least ? ~0ull : (unsigned long long)(W - i / per);
+                         });
+        narrow(list, n, K, s_red, s_count, [&](int i) { return total[i] > least || i / per < beam ? ~0ull : ~key_of(i); });
+        for (int x = tid; x < n; x += BM_MERGE_THREADS) first[x] = key_of(list[x]);
+        __syncthreads();
+    }
     for (int x = tid; x < n; x += BM_MERGE_THREADS) {
         const int i = list[x], w = i / per;
-        const unsigned long long t = total[i], k = key_of(i);
+        const unsigned long long t = total[i], k = first[x];
         int rank = 0;
         for (int y = 0; y < n; ++y) {
             const int j = list[y];
             const unsigned long long u = total[j];
             rank += u > t;
-            if (u == t && i != j) rank += j / per < w || (j / per == w && key_of(j) < k);
+            if (u == t && i != j) rank += j / per < w || (j / per == w && first[y] < k);
         }
         if (rank >= K) continue;
         const int64_t to = (int64_t)blockIdx.x * K + rank;
@@ -763,7 +824,7 @@ int mk_beam_select(const mk_beam_desc *d, void *workspace, uint64_t workspace_by
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)d->batch);
     cfg.blockDim = dim3(BM_MERGE_THREADS);
-    cfg.dynamicSmemBytes = BM_MAXBEAMS * 20 + 64 * 4 + p.beams * p.parts * p.num * 12 + 4;
+    cfg.dynamicSmemBytes = BM_MAXBEAMS * 20 + 64 * 4 + 2 * beam_limit(p.num) * 8 + p.beams * p.parts * p.num * 12 + 4;
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
