@@ -54,6 +54,7 @@ constexpr int BM_MAXVOCAB = 622592;
 constexpr int BM_MAXBEAMS = 64, BM_MAXNUM = 128;
 constexpr int BM_CANDIDATES = 8192;                          // of a prompt at most: beams x parts x num
 constexpr int BM_MERGE_THREADS = 512;
+constexpr int BM_MAXSMS = 256;                               // that parts are planned for
 
 // What the second launch needs of a part beside its list.
 struct BeamPart {
@@ -741,26 +742,32 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const Beam
     }
 }
 
-// Parts of a row.  As many CTAs as the GPU holds at once (3 an SM; 128 rows of
-// 151,936 fp32 logits: 29.1 us, with twice as many 36.3), no
-// shorter parts than a piece, and no more candidates than the second launch
-// holds.
-static void beam_parts(const mk_beam_desc *d, int &parts, int &chunk) {
+// A piece lists all logits of as many threads as may reach its bound; the list takes two such pieces and more.
+static int beam_listers(int num) { return std::min(BM_THREADS, std::max(64, 2 * num)); }
+static int beam_cap(int num) { return beam_listers(num) * BM_PER * 3; }
+static int beam_smem(int num) { return (int)sizeof(BeamShared) + beam_cap(num) * 12; }
+// CTAs that an SM holds: 3 by their registers, fewer by the lists of many continuations (a CTA takes 1024 bytes more).
+static int beam_resident(int num) { return std::min(3, (SERVE_SMEM + 1024) / (beam_smem(num) + 1024)); }
+
+// Parts of a row.  As many CTAs as the GPU holds at once (128 rows of 151,936 fp32
+// logits, a cheaper sum: 29.1 us, with twice as many 36.3), no shorter parts than
+// a piece, and no more candidates than the second launch holds.
+static void beam_parts(const mk_beam_desc *d, int ctas, int &parts, int &chunk) {
     const int64_t rows = std::max<int64_t>(1, (int64_t)d->batch * d->beams);
-    int64_t n = std::max<int64_t>(1, 3 * 152 / rows);
+    int64_t n = std::max<int64_t>(1, ctas / rows);
     n = std::min<int64_t>(n, (d->vocab + BM_PIECE - 1) / BM_PIECE);
     n = std::min<int64_t>(n, BM_CANDIDATES / (d->beams * d->num));
     chunk = (int)(((d->vocab + n - 1) / n + 7) / 8 * 8);
     parts = (d->vocab + chunk - 1) / chunk;
 }
 
-static int beam_sizes(const mk_beam_desc *d, int &parts, int &chunk) {
+static int beam_sizes(const mk_beam_desc *d, int ctas, int &parts, int &chunk) {
     if (!d) return set_error(MK_ERR_INVALID, "null descriptor");
     if (d->batch < 0 || d->beams <= 0 || d->num <= 0 || d->vocab <= 0)
         return set_error(MK_ERR_INVALID, "batch negative, or beams, num or vocab not positive");
     if (d->beams > BM_MAXBEAMS || d->num > BM_MAXNUM) return set_error(MK_ERR_UNSUPPORTED, "more than 64 beams or 128 continuations");
     if (d->vocab > BM_MAXVOCAB) return set_error(MK_ERR_UNSUPPORTED, "vocab above 622592");
-    beam_parts(d, parts, chunk);
+    beam_parts(d, ctas, parts, chunk);
     if ((int64_t)d->batch * d->beams * parts > INT32_MAX) return set_error(MK_ERR_UNSUPPORTED, "too many rows");
     return MK_OK;
 }
@@ -774,8 +781,8 @@ extern "C" {
 
 int mk_beam_select_workspace(const mk_beam_desc *d, uint64_t *bytes) {
     if (!bytes) return set_error(MK_ERR_INVALID, "bytes is null");
-    int parts, chunk;
-    if (int rc = beam_sizes(d, parts, chunk)) return rc;
+    int parts, chunk;  // (on any device: fewer SMs make fewer parts)
+    if (int rc = beam_sizes(d, 3 * BM_MAXSMS, parts, chunk)) return rc;
     *bytes = beam_part_bytes(d, parts) + (uint64_t)d->batch * d->beams * parts * d->num * 8;
     return MK_OK;
 }
@@ -801,22 +808,25 @@ int mk_beam_select(const mk_beam_desc *d, void *workspace, uint64_t workspace_by
     p.scores = reinterpret_cast<const float *>(d->scores);
     p.finished = reinterpret_cast<const uint8_t *>(d->finished);
     p.end = d->end;
-    beam_parts(d, p.parts, p.chunk);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return serve_cuda_fail(e, "device query");
+    beam_parts(d, std::min(sms, BM_MAXSMS) * beam_resident(d->num), p.parts, p.chunk);
     p.rows = static_cast<BeamPart *>(workspace);
     p.keys = reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(workspace) + beam_part_bytes(d, p.parts));
     p.out = reinterpret_cast<float *>(d->out_scores);
     p.parents = reinterpret_cast<int *>(d->parents);
     p.tokens = reinterpret_cast<int *>(d->tokens);
-    // a piece lists all logits of as many threads as may reach its bound; the list takes two such pieces and more
-    p.limit = std::min(BM_THREADS, std::max(64, 2 * d->num));
-    p.cap = p.limit * BM_PER * 3;
+    p.limit = beam_listers(d->num);
+    p.cap = beam_cap(d->num);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     void (*f)(const BeamParams) = d->bf16 ? beam_part_kernel<true> : beam_part_kernel<false>;
     static std::atomic<uint32_t> ready[SERVE_MAX_DEVICES];
     if (int rc = serve_prepare(reinterpret_cast<const void *>(f), ready, d->bf16 ? 1 : 0, false)) return rc;
     if (int rc = serve_prepare(reinterpret_cast<const void *>(beam_merge_kernel), ready, 2, false)) return rc;
-    f<<<(unsigned)(rows * p.parts), BM_THREADS, sizeof(BeamShared) + p.cap * 12, st>>>(p);
-    cudaError_t e = cudaGetLastError();
+    f<<<(unsigned)(rows * p.parts), BM_THREADS, beam_smem(d->num), st>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return serve_cuda_fail(e, "beam selection launch");
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
