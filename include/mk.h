@@ -602,7 +602,7 @@ typedef struct {
  * of itself or 2^-32 of the row's largest product of weight and V scale.  A
  * group list that falls or leaves 0 .. batch, or a negative shared length, is a failed
  * check: nothing is shared then (in that group).  Workspace like
- * mk_cache_attend's, of its own size. */
+ * mk_cache_attend's, of its own size: enough for up to `groups` groups. */
 int mk_cache_attend_shared_workspace(const mk_cache_desc *cache, const mk_attend_desc *attend,
                                      const mk_shared_desc *shared, uint64_t *bytes);
 /* See mk_shared_desc (no counterpart on the pages). */

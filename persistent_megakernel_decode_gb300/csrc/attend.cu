@@ -266,7 +266,8 @@ int mk_cache_attend_shared_workspace(const mk_cache_desc *cache, const mk_attend
     AttPlan pl;
     if (!bytes) return set_error(MK_ERR_INVALID, "bytes is null");
     if (int rc = shared_check(attend, shared)) return rc;
-    if (int rc = att_plan(cache, attend, shared->groups, pl)) return rc;
+    // (of as many groups or fewer: one group's tiles are the tallest)
+    if (int rc = att_plan(cache, attend, shared->groups ? 1 : 0, pl)) return rc;
     *bytes = pl.bytes();
     return MK_OK;
 }

@@ -55,7 +55,7 @@ class Kv8Cache:
         self._lib = rt.load()
         self._kept = None  # the default stream's workspace
         self._lock = threading.Lock()  # of _kept, from its choice to the last launch that uses it
-        self._sizes = {}  # workspace bytes by (batch, table width, q heads, tokens, most tokens of a sequence, num_sms)
+        self._sizes = {}  # workspace bytes by (batch, table width, q heads, tokens, most tokens of a sequence, num_sms, any groups)
 
     @classmethod
     def empty(cls, layers: int, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
@@ -206,7 +206,7 @@ class Kv8Cache:
         else:
             call, args = self._lib.mk_cache_attend_shared, (self._ref, rt.c_int(layer), C.byref(a), C.byref(share))
         if own:
-            size = self._sizes.get((b, width, hq, total, most, self.num_sms, share.groups if share else None))
+            size = self._sizes.get((b, width, hq, total, most, self.num_sms, share is not None and share.groups > 0))
             if not size:
                 size = self._workspace(a, share) if share else self._workspace(a)
         else:
@@ -215,8 +215,8 @@ class Kv8Cache:
                 raise ValueError("workspace must be contiguous")
             size = workspace.numel()
         if own and torch._C._cuda_getCurrentRawStream(self.index) == 0:
-            # Calls on the default stream share a workspace.  One call is two launches, which another thread's must not
-            # come between; the stream orders the calls, and cannot be captured.
+            # Calls on the default stream share a workspace.  One call is two or three launches, which another thread's
+            # must not come between; the stream orders the calls, and cannot be captured.
             with self._lock:
                 if self._kept is None or self._kept.numel() < size:
                     self._kept = torch.empty(size, dtype=torch.uint8, device=self.device)
@@ -236,7 +236,8 @@ class Kv8Cache:
                 rt._check(self._lib.mk_cache_attend_shared_workspace(self._ref, C.byref(a), C.byref(share), C.byref(n)))
         if len(self._sizes) >= 1024:
             self._sizes.clear()
-        self._sizes[a.batch, a.table_width, a.q_heads, a.tokens, a.max_tokens, a.num_sms, share.groups if share else None] = n.value
+        self._sizes[a.batch, a.table_width, a.q_heads, a.tokens, a.max_tokens, a.num_sms,
+                    share is not None and share.groups > 0] = n.value
         return n.value
 
     def attend_workspace(self, batch: int, q_heads: int, max_tokens: int = 1, table_width: int = 1 << 20) -> int:
@@ -246,8 +247,8 @@ class Kv8Cache:
 
     def attend_shared_workspace(self, batch: int, q_heads: int, groups: int, max_tokens: int = 1,
                                 table_width: int = 1 << 20) -> int:
-        """Bytes of workspace :meth:`attend_shared` needs for up to ``batch`` sequences of up to ``max_tokens`` queries in
-        ``groups`` groups."""
+        """Bytes of workspace :meth:`attend_shared` needs for up to ``batch`` sequences of up to ``max_tokens`` queries in up
+        to ``groups`` groups (and ``table_width`` pages; packed queries: with that ``max_tokens`` as its hint)."""
         return self._workspace(self._sized(batch, q_heads, max_tokens, table_width), rt.SharedDesc(0, 0, rt.c_int(groups)))
 
     def _sized(self, batch, q_heads, max_tokens, table_width):
