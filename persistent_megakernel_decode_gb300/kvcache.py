@@ -21,6 +21,7 @@ from . import runtime as rt
 rt.need_torch()
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _I32, _BF16 = torch.int32, torch.bfloat16
+KEPT_BYTES = 64 << 20  # the largest workspace that a cache keeps (prompts that share a prefix need 2 rows of fp32 a query row)
 
 
 class Kv8Cache:
@@ -137,7 +138,7 @@ class Kv8Cache:
         a query sees that many last tokens, itself among them, and the sequence's first ``sinks`` ones.  Returns (out bf16
         like q, lse fp32 without the last axis); a query that sees nothing gets 0 and -inf.  ``workspace``: uint8 tensor of
         at least :meth:`attend_workspace` bytes, used by one call at a time; by default calls on the default stream share
-        one that the cache keeps, others allocate their own."""
+        one of up to 64 MB that the cache keeps, others allocate their own."""
         if stream is not None and not rt.is_current(self.index, stream):
             return self._beside(stream, self.attend, q, table, lens, layer, q_start, max_tokens, scale, window, out, lse,
                                 workspace, None, sinks)
@@ -214,7 +215,7 @@ class Kv8Cache:
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
             size = workspace.numel()
-        if own and torch._C._cuda_getCurrentRawStream(self.index) == 0:
+        if own and size <= KEPT_BYTES and torch._C._cuda_getCurrentRawStream(self.index) == 0:
             # Calls on the default stream share a workspace.  One call is two or three launches, which another thread's
             # must not come between; the stream orders the calls, and cannot be captured.
             with self._lock:
