@@ -597,8 +597,11 @@ typedef struct {
 
 /* mk_cache_attend (the same results but for rounding: same masks, checks and
  * precision; window and sinks must be 0), with the pages that a group shares
- * read once for all of its rows (no counterpart on the pages).  Where the rows
- * of a group are many, a probability over its shared pages is rounded to 2^-11
+ * read once for every tile of its rows (query tokens x q heads of a kv head),
+ * not for every sequence (no counterpart on the pages).  All groups have tiles
+ * of one height, 8 to 64 rows or 128, which follows the average group's rows
+ * (groups of one among them: they need not be listed).  Calls of few pages share
+ * nothing.  Where the rows of a group are many, a probability over its shared pages is rounded to 2^-11
  * of itself or 2^-32 of the row's largest product of weight and V scale.  A
  * group list that falls or leaves 0 .. batch, or a negative shared length, is a failed
  * check: nothing is shared then (in that group).  Workspace like

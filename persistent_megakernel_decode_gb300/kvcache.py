@@ -148,8 +148,9 @@ class Kv8Cache:
                       scale: Optional[float] = None, out=None, lse=None, workspace=None,
                       stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """:meth:`attend` (without a window) of sequences that share their first pages, as beams or samples of one prompt and
-        conversations behind one instruction do; the shared pages are read once for all rows of a group.  Group g is the
-        sequences groups[g] .. groups[g + 1] - 1 (``groups``: int32 [G + 1]), whose first ``shared[g]`` (int32 [G]) tokens lie
+        conversations behind one instruction do; the shared pages are read once for every tile of up to 128 rows of a group,
+        not for every sequence (the tiles' height follows the average group: sequences by themselves are best in none).
+        Group g is the sequences groups[g] .. groups[g + 1] - 1 (``groups``: int32 [G + 1]), whose first ``shared[g]`` (int32 [G]) tokens lie
         in the same pages; what is not a whole page of that counts as the sequences' own.  The table rows still name every
         page.  ``workspace``: at least :meth:`attend_shared_workspace` bytes."""
         if stream is not None and not rt.is_current(self.index, stream):
