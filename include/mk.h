@@ -634,7 +634,9 @@ int mk_cache_copy(const mk_cache_desc *cache, const int32_t *src, const int32_t 
  *   all further columns (and column t of a full len) stay the row's own: pages
  *     that it may fill later.
  * So a beam needs pages for all it may ever write, and no page is taken or
- * given back here.  table_out must not overlap table.  A prompt whose lens
+ * given back here: a full page is named by every row that goes on with it, and
+ * one of rows without children by none any more (with mk_pages_*: a reference
+ * for every entry of the new rows, then one less for every entry of the old).  table_out must not overlap table.  A prompt whose lens
  * differ or leave the table, or with a parent outside [-1, beams), is a failed
  * check: its rows stay as they are.  A copy between pages out of range is one
  * too, and not made.  At most 64 beams. */

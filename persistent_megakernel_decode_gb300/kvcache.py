@@ -280,8 +280,11 @@ class Kv8Cache:
         b W + w continues row b W + ``parent[b, w]`` (int32 [B, W], -1: itself) of ``table`` (int32 [B W, width]).
         ``lens`` (int32 [B W]): the tokens that the rows hold, the same for all beams of a prompt.  Full pages are shared
         from then on; the page being filled, which must be its row's own, is kept by one child and copied for the others
-        into the pages of beams without children, so the rows need pages for all that they may write from the beginning, and
-        the pages of a prompt's beams together stay the same ones (``mk_cache_reorder`` in ``include/mk.h``)."""
+        into the pages of beams without children, so the rows need pages for all that they may write from the beginning.
+        From the page being filled on, the pages of a prompt's beams together stay the same ones; full pages are named by
+        every row that goes on with them, and those of beams without children by none any more (``mk_cache_reorder`` in
+        ``include/mk.h``).  A ``PagePool`` with a reference for every entry of the rows follows by ``share(new entries)``,
+        then ``release(old entries)``, from host copies of the tables, after each call or once for many."""
         if stream is not None and not rt.is_current(self.index, stream):
             return self._beside(stream, self._reorder, table, lens, parent, out)[0]
         return self._reorder(table, lens, parent, out)[0]
