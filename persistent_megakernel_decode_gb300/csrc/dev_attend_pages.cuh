@@ -642,7 +642,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                 acc.z = fmaf(a, x.z, acc.z);
                 acc.w = fmaf(a, x.w, acc.w);
             }
-            if ((KIND == ATT_GROUPS || (KIND == ATT_OWN && g.gap > 0)) && g.whole) {  // (gap: the sequence shares pages)
+            if (KIND != ATT_PLAIN && g.whole) {
                 const size_t at_row = (((size_t)all * p.tokens + g.q0 + rr / p.group) * p.c.hkv + g.h) * p.group + rr % p.group;
                 *reinterpret_cast<float4 *>(p.row_o + at_row * D + 4 * d4) = acc;
                 if (d4 == 0) *reinterpret_cast<float2 *>(p.row_ml + at_row * 2) = make_float2(big, sum);
@@ -717,8 +717,8 @@ __global__ void __launch_bounds__(att_threads(KIND), KIND == ATT_OWN ? 2 : 1) ca
 
 // One warp per query row: rows that see nothing get zeros, rows whose pages
 // two or more CTAs shared are merged, in the order of the CTAs; the others
-// are written already.  Rows of sequences that share pages are all merged, the
-// own tokens' part first.  All that does not need the main kernel's results (the
+// are written already.  With shared prefixes all rows are merged, the own
+// tokens' part first.  All that does not need the main kernel's results (the
 // sequences' running page counts again, the row's sequence) runs while that
 // one still does.
 template <int D, int P, int RT, AttKind KIND>
@@ -798,8 +798,9 @@ __global__ void __launch_bounds__(256) cache_attend_merge(const AttParams p) {
                 pre = part_of(att_unit<P, ATT_GROUPS>(p, groups, g, false), p.pre_rt, before[g], all,
                               whole_pages ? pre_used(all, pre_ctas) : att_used_of(p.pre_rt, all, min(p.sms, pre_ctas)), whole_pages);
             }
+        } else {
+            todo = own.n == 0 || own.c0 <= own.c1;
         }
-        if (pre.n == 0) todo = own.n == 0 || own.c0 <= own.c1;
     }
     // every thread waits: this grid must not be done before the main kernel is
     asm volatile("griddepcontrol.wait;" ::: "memory");
