@@ -82,7 +82,7 @@ def test_prompts_through_a_window_with_sinks(T, window, sinks):
 
 @pytest.mark.parametrize("T, hq", [(1, 8), (3, 8), (40, 24)])
 def test_sequences_that_share_nothing_are_as_without_groups(T, hq):
-    """Groups of one, groups that share no whole page, and sequences in no group are written as `attend` writes them."""
+    """Groups of one, groups that share no whole page, and sequences in no group."""
     P, D, hkv, B = 64, 64, 2, 9
     lens = [T + 400 + 100 * b for b in range(B)]
     c, r, pages = shared_case(P, D, hq, hkv, [0, 3], [5 * P], lens, seed=5, poison=False)
