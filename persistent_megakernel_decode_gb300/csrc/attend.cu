@@ -140,7 +140,7 @@ static int att_start(const mk_cache_desc *cache, AttParams &p, AttKind kind, int
     dep.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(att_threads(kind));
+    cfg.blockDim = dim3(att_threads(kind, rt));
     cfg.dynamicSmemBytes = fixed + p.ring * 2 * P * D;
     cfg.stream = st;
     cfg.attrs = &dep;

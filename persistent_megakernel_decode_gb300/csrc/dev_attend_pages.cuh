@@ -8,8 +8,14 @@ namespace mk {
 // Consumer warps of a CTA.  What sequences have behind a shared prefix is short:
 // two CTAs of four on an SM have two of those units in work.
 __host__ __device__ constexpr int att_warps(AttKind kind) { return kind == ATT_OWN ? 4 : 8; }
-// + the producer's warpgroup, of which one warp works
-__host__ __device__ constexpr int att_threads(AttKind kind) { return (att_warps(kind) + 4) * 32; }
+// Are the registers shared out by warpgroups?  Tiles of 8 rows by themselves need
+// fewer than a thread of 9 warps has; starting the three idle warps of a producer's
+// warpgroup costs a short call more than they give (8 sequences of 512-4096, heads of
+// 64: 13.4 us, with them 13.6; window and sinks: 12.6 and 12.9).  Taller tiles would
+// spill without (36 rows of 128 dims: 27.1 us, without 28.5).
+__host__ __device__ constexpr bool att_split(AttKind kind, int rt) { return kind != ATT_PLAIN || rt > 8; }
+// + the producer, in a warpgroup of its own where registers are shared out
+__host__ __device__ constexpr int att_threads(AttKind kind, int rt) { return (att_warps(kind) + (att_split(kind, rt) ? 4 : 1)) * 32; }
 constexpr int ATT_MAXRING = 32;                     // pages in the ring (one producer lane each)
 
 // Tiles of rt rows: 8 NT rows a warp, up to rt / (8 NT) warps side by side
@@ -665,9 +671,9 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
 }
 
 template <int D, int P, int RT, AttKind KIND>
-__global__ void __launch_bounds__(att_threads(KIND), KIND == ATT_OWN ? 2 : 1) cache_attend_kernel(const AttParams p) {
+__global__ void __launch_bounds__(att_threads(KIND, RT), KIND == ATT_OWN ? 2 : 1) cache_attend_kernel(const AttParams p) {
     asm volatile("griddepcontrol.launch_dependents;");
-    constexpr int WARPS = att_warps(KIND), THREADS = att_threads(KIND);
+    constexpr int WARPS = att_warps(KIND), THREADS = att_threads(KIND, RT);
     const AttShared s = att_shared<D, att_nt(RT), WARPS>(p, att_units(p, KIND));
     const int tid = threadIdx.x, units = att_units(p, KIND);
     AttSeq seq{0, 0, 0, 0, 0, false};
@@ -703,11 +709,11 @@ __global__ void __launch_bounds__(att_threads(KIND), KIND == ATT_OWN ? 2 : 1) ca
     // What does not fit goes to local memory, for which shared memory leaves hardly
     // any L1 cache.
     if (tid >= WARPS * 32) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if constexpr (att_split(KIND, RT)) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (tid < (WARPS + 1) * 32) att_produce<D, P, RT, KIND>(p, s);
     } else {
         if constexpr (KIND == ATT_OWN) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        else if constexpr (att_split(KIND, RT)) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         att_consume<D, P, RT, KIND>(p, s);
     }
     // the groups' launch, beside which this one ran, is done before this one is
