@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) beam_merge_kernel(const Beam
         unsigned long long sum = 0;
         for (int i = lane; i < S && top > -INFINITY; i += 32) {
             const BeamPart x = r[i];
-            if (x.top > -INFINITY) sum += octaves_below(x.list, weigh.distance(x.top, 126.f), 0, s_table);
+            if (x.top > -INFINITY) sum += octaves_below(x.list, x.top == top ? 0 : weigh.distance(x.top, 126.f), 0, s_table);
             // 2^(ref - top log2(e)): the exponent is below 2
             if (x.rest) sum += octaves_below(x.rest, max(0ll, octaves - ((long long)x.ref - 2) * (1ll << 32)), 2, s_table);
         }

@@ -41,7 +41,7 @@ struct Weigher {
     float top, ch, cl;  // the row's maximum; log2(e) / temperature as a pair of fp32
     const uint32_t *table;
     DEV float octaves(float x) const { return (top - x) * ch; }  // d in fp32: monotone in x
-    // d in 32.32 fixed point for d < most, else most + 1 (most: below 127)
+    // d in 32.32 fixed point for d < most, else most + 1 (most: below 127); not for the largest itself, which may be infinite
     DEV long long distance(float x, float most) const {
         const float dh = top - x;
         const float bp = dh - top;
@@ -50,14 +50,13 @@ struct Weigher {
         const float te = t < most ? fmaf(dh, ch, -t) + fmaf(dh, cl, dl * ch) : 0.f;
         const int n = __float2int_rz(t);
         // t - n is exact, te below 2^-16
-        const long long d = max(0ll, ((long long)n << 32) + (long long)__float2uint_rz((t - (float)n) * 4294967296.f) +
+        return max(0ll, ((long long)n << 32) + (long long)__float2uint_rz((t - (float)n) * 4294967296.f) +
                                          (long long)__float2int_rn(te * 4294967296.f));
-        return x == top ? 0 : d;  // (the largest may be infinite)
     }
     // 2^44 2^-d, without branches, so that several weights overlap; from d = 46 on it is 0
     DEV unsigned long long operator()(float x) const {
         const unsigned long long r = octave_weight(distance(x, 46.f), table);
-        return x == top ? 1ull << 44 : r;
+        return x == top ? 1ull << 44 : r;  // (the largest may be infinite)
     }
 };
 
