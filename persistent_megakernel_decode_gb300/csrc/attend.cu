@@ -47,8 +47,9 @@
 // another, and the merge joins both.  The two run beside each other, on SMs that
 // the device shares out by the items of each at their measured costs
 // (dev_attend.cuh); an own part is short, so two CTAs of four warps take them on
-// an SM (64 sequences of 16,000 shared tokens and 100-2,000 of their own: 82 us,
-// with one CTA of eight warps 85; 4 x 8 beams: 43.7 and 45).
+// an SM (64 sequences of 16,000 shared tokens and 100-2,000 of their own: 82 us
+// when that was chosen, with one CTA of eight warps 85, now 77; 4 x 8 beams: 43.7
+// and 45).
 //
 // Measured (one GB300, device time): 16 sequences of 16-32K tokens, 32 q / 8
 // kv heads of 128: 125 us, 6.3 TB/s, 93 % of the copy rate; 8 sequences of
@@ -73,11 +74,11 @@ static int att_tile(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : row
 // Rows of an average group and kv head from which prefix.cu's tiles are taken for
 // its shared pages.  64 sequences (256 rows) behind 16,000 tokens: 82 us, with
 // attend.cu's 120; 21 with drafted tokens in 3 groups (56 rows) 35 and 39; 4 x 8
-// beams (32 rows) 46 and 44.
+// beams (32 rows) 46 and 44.  (Between 32 and 56 rows nothing was measured.)
 constexpr int PRE_LEAST = 48;
 // Pages of all sequences and kv heads, per SM, up to which nothing is shared: a
 // launch more costs as much as reading so few again.  4 beams of a prompt of 300
-// tokens (88 pages): 11 us, shared 16.
+// tokens (88 pages): 11 us, shared 16.  (The one such call measured.)
 constexpr int ALONE_PAGES = 4;
 
 // ngroups: 0 without shared prefixes

@@ -20,7 +20,7 @@
 // of eight small parts.  Partial sums are joined as integers, so no order of
 // arrival changes anything.  (With the hardware's 2^f, off by up to 2^-22, the
 // sum of a flat row was off by 2^-22.6 and of a normal one by 2^-26, and 16 x 8
-// beams took 29.7 us where they take 38.7.)
+// beams took 29.7 us where they take 38.2.)
 //
 // The largest without sorting: a bound that at least `num` threads' largest
 // values reach is found by bisection, one barrier and vote a step; the few
@@ -35,10 +35,11 @@
 // Work split.  A CTA streams a part of a row, 4096 logits at a time in
 // registers, the next piece's loads in flight.  A second, dependent launch orders
 // a prompt's candidates, one CTA each.  Each logit is read once, so bytes bound
-// it from below; 64 x 8 beams of 151,936 logits take 82 us, 3.4 TB/s, and 16 x 8
-// 39, of which the bytes are 10: 33 instructions a logit (multiplies and adds
-// above all; as instructions on register pairs throughout 40.6 us), the ramp of
-// two launches, the bisection and the rank of each part's list (barriers).  Three
+// it from below; 64 x 8 beams of 151,936 logits take 80 us, 3.5 TB/s, and 16 x 8
+// 38, of which the bytes are 10: 28 instructions a logit, half of them its term's
+// (as instructions on register pairs throughout 40.6 us; with the next piece's
+// loads behind the terms 42), and with the bisection and the rank of each part's
+// list 33; the barriers of these; the ramp of two launches.  Three
 // CTAs an SM in one wave are the best split (with six, and a cheaper sum, 36 us
 // where three took 29; one cluster a row, in registers, 52-99).
 #include <algorithm>

@@ -227,7 +227,7 @@ DEV long long att_group_items(const AttParams &p, int cnt, int np) {
 // Both launches run beside each other, on SMs shared out by their work: the CTAs
 // of the groups' one.  By the clock a page through prefix.cu's tiles takes an SM as
 // long as 2.5 items of the sequences' launch, an item of attend.cu's for groups
-// 1.3 (0.95 and 0.5 us).
+// 1.3 (0.95 and 0.5 us; with heads of 128 and pages of 64, taken for others too).
 DEV int att_share(const AttParams &p, long long groups, long long own) {
     if (groups == 0) return 0;
     if (own == 0) return p.sms;
