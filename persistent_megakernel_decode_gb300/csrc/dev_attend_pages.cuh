@@ -343,6 +343,14 @@ DEV float att_load_q(const uint16_t *row, int t, uint32_t (&qb)[D / 64][8]) {
 DEV void mbar_arrive_n(uint64_t *b, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(b)), "r"(n) : "memory");
 }
+// This thread's loads from shared memory come before copies that another thread
+// starts after an arrival behind this.  Copies are the async proxy's, loads the
+// generic one's: an arrival alone does not order them.  Without it a slot's next
+// page landed under the last loads once in some 10,000 calls with pages of 32 tokens
+// and heads of 128, whose rows conflict eight ways and wait longest in the load
+// queue.  (36 rows of 128 dims: 26.9 us, without 26.6; releasing K behind the
+// maxima instead, which need all of it, 27.2.)
+DEV void att_reads_done() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 template <int WARPS>
 DEV void att_consumer_bar() { asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory"); }
 
@@ -458,6 +466,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                                     att_mma(c[n][i], a0, a1, a2, a3, j ? qj[n].z : qj[n].x, j ? qj[n].w : qj[n].y);
                             }
                     }
+                att_reads_done();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_n(&s.empty_k[st], WT / side);  // K is read: the next one loads during the rest
                 const int first = pg * P + RUN * (g8 >> 1) + (g8 & 1);  // token of c[.][0][0]; [i][2u + e]: + 4 i + 2 u
@@ -603,6 +612,7 @@ DEV void att_consume(const AttParams &p, const AttShared &s) {
                 ok = att_wait(p, s, &s.has_v[st], mine, &s.full_v[st], ph);
                 ok = __all_sync(FULL, ok);
             }
+            att_reads_done();
             __syncwarp();
             if (ok && lane == 0) mbar_arrive_n(&s.empty_v[st], WT / side);
         }
