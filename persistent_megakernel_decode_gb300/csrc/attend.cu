@@ -36,7 +36,7 @@
 // copies; the consumer warps take them in turn (as many side by side as the
 // tile's rows need) and merge in shared memory.  A page that a tile does not
 // see, or whose number is out of range, takes its turn in the ring without
-// being loaded.  With sinks, a unit's pages are those of the sinks and those
+// being loaded.  A slot is released behind a proxy fence (att_reads_done).  With sinks, a unit's pages are those of the sinks and those
 // from the window's first on; the pages between are no items at all.
 // A unit that one CTA covers is written at once; ranges cut by a CTA boundary
 // go to the workspace and a second small launch (dependent launch, so that its
