@@ -29,3 +29,23 @@ def test_the_same_bits_every_time(P, D, times, B, hkv, group, n):
             wrong += (lse != want[1]).any() | (out != want[0]).any()
         assert wrong.item() == 0
     c.check()
+
+
+@pytest.mark.parametrize("P, D", [(32, 128), (64, 128), (32, 64), (64, 64)])
+@pytest.mark.parametrize("members, group", [(2, 2), (25, 4)])  # groups' tiles of 8 rows, and of 128
+def test_shared_pages_the_same_bits_every_time(P, D, members, group):
+    B, hkv, full, own, times = 100, 2, 700 // P, 300 // P + 1, 3000
+    groups = B // members
+    c, _ = by_hand(1, groups * full + B * own, hkv, P, D, seed=members)
+    table = table_of([list(range(b // members * full, b // members * full + full))
+                      + list(range(groups * full + b * own, groups * full + (b + 1) * own)) for b in range(B)])
+    lens = i32([full * P + 1 + (29 * b) % 290 for b in range(B)])
+    q = gen(B, 1, hkv * group, D, seed=1).to(DEV)
+    first, shared = i32(list(range(0, B + 1, members))), i32([full * P] * groups)
+    want = c.attend_shared(q, table, lens, first, shared)
+    wrong = torch.zeros((), dtype=torch.int64, device=DEV)
+    for _ in range(times):
+        out, lse = c.attend_shared(q, table, lens, first, shared)
+        wrong += (lse != want[1]).any() | (out != want[0]).any()
+    assert wrong.item() == 0
+    c.check()
